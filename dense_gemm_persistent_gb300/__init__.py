@@ -17,7 +17,10 @@ from ._lib import (ACT, B_KN, B_NK, BF16, E4M3, F32, QUANT, DgemmError, Epilogue
 
 __all__ = ["dgemm_bf16", "dgemm_fp8_scaled", "dgemm_fp8_rowquant_noalloc", "dgemm_workspace_size", "dgemm_plan",
            "dgemm_status_string", "dgemm_query_device_status", "set_overrides", "get_overrides", "overrides",
-           "DgemmError", "load", "lib_path"]
+           "DgemmError", "load", "lib_path",
+           "dgemm_route", "dgemm_route_workspace_size", "dgemm_combine", "dgemm_grouped_bf16",
+           "dgemm_grouped_fp8_scaled", "dgemm_grouped_int8_scaled", "dgemm_grouped_workspace_size",
+           "dgemm_int8_quantize", "dgemm_int8_scaled", "dgemm_int8_workspace_size"]
 
 
 def _torch():
@@ -264,3 +267,18 @@ class overrides:
         o = Overrides(**{k: int(v) for k, v in self.saved.items()})
         _check(load().dgemm_set_overrides(ctypes.byref(o)), "dgemm_set_overrides")
         return False
+
+
+# Routed-expert and 8-bit integer operators (imports torch on first use, as the
+# entry points above do).
+_EXPERTS = frozenset(name for name in __all__ if name.startswith(("dgemm_route", "dgemm_combine", "dgemm_grouped",
+                                                                  "dgemm_int8")))
+
+
+def __getattr__(name):
+    if name in _EXPERTS:
+        from . import experts
+        for n in _EXPERTS:
+            globals()[n] = getattr(experts, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

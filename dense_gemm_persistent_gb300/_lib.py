@@ -21,7 +21,7 @@ B_KN, B_NK = 0, 1
 ACT = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
 QUANT = {"none": 0, "e4m3_row_amax": 1}
 
-# Every symbol the header declares, with (restype, argtypes).
+# Every symbol the headers declare, with (restype, argtypes).
 _vp, _i64, _i32, _f32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 
 
@@ -61,6 +61,23 @@ SIGNATURES = {
     "dgemm_fp8_rowquant_noalloc": (_i32, [_vp, _vp, _i32, _vp, _vp, _vp, _i32, _vp, _i64, _i64, _i64, _f32, _f32,
                                           ctypes.POINTER(Epilogue), _vp]),
 }
+# include/dgemm_experts.h
+SIGNATURES.update({
+    "dgemm_route": (_i32, [_vp, _i32, _i64, _i64, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "dgemm_route_workspace_size": (_sz, [_i64, _i64, _i32]),
+    "dgemm_combine": (_i32, [_vp, _i64, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _i32, _vp]),
+    "dgemm_grouped_bf16": (_i32, [_vp, _i64, _vp, _vp, _i32, _vp, _i64, _vp, _i32, _i64, _i64, _i64, _f32, _vp, _i32,
+                                  _vp, _sz, _vp]),
+    "dgemm_grouped_fp8_scaled": (_i32, [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i32, _i64, _i64, _i64, _f32,
+                                        _vp, _i32, _vp, _sz, _vp]),
+    "dgemm_grouped_int8_scaled": (_i32, [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i32, _i64, _i64, _i64, _f32,
+                                         _vp, _i32, _vp, _sz, _vp]),
+    "dgemm_grouped_workspace_size": (_sz, [_i32, _i64, _i64, _i64, _i64, _i32]),
+    "dgemm_int8_quantize": (_i32, [_vp, _i32, _vp, _vp, _i64, _i64, _vp]),
+    "dgemm_int8_scaled": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i64, _i64, _i64, _f32, _f32, _vp, _i32,
+                                 _vp, _sz, _vp]),
+    "dgemm_int8_workspace_size": (_sz, [_i64, _i64, _i64]),
+})
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
 WS_STATUS_BYTES = 256
 

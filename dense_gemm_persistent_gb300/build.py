@@ -14,13 +14,14 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
+CSRC_EXPERTS = os.path.join(PKG, "csrc_experts")   # routed-expert and 8-bit integer operators
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libdgemm.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC",
-                     "-I", INCLUDE, "-I", CSRC]
+                     "-I", INCLUDE, "-I", CSRC, "-I", CSRC_EXPERTS]
 
 
 def nvcc() -> str:
@@ -31,12 +32,12 @@ def nvcc() -> str:
 
 
 def _sources():
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    return sorted(glob.glob(os.path.join(CSRC, "*.cu"))) + sorted(glob.glob(os.path.join(CSRC_EXPERTS, "*.cu")))
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
-        glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
+    headers = [os.path.join(d, pat) for d in (CSRC, CSRC_EXPERTS, INCLUDE) for pat in ("*.cuh", "*.h")]
+    return _sources() + [f for pat in headers for f in glob.glob(pat)] + [os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:

@@ -13,6 +13,7 @@
 #include <mutex>
 
 #include "dgemm.h"
+#include "host.h"
 #include "kernels.h"
 
 namespace {
@@ -865,6 +866,47 @@ dgemm_status_t run(int fp8, const void* A, const void* B, dgemm_b_layout_t bl, c
 }
 
 }  // namespace
+
+// ---- services for the expert operators (host.h)
+namespace dg {
+namespace host {
+
+dgemm_status_t current_device(Device* out) {
+    DeviceState* d = nullptr;
+    const dgemm_status_t st = device_state(&d, &out->id);
+    if (st != DGEMM_OK) return st;
+    out->num_sms = d->num_sms;
+    out->status = d->status;
+    return DGEMM_OK;
+}
+
+unsigned long long next_launch_epoch() { return next_epoch(); }
+
+bool encode_map(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, int rank, const uint64_t* dims,
+                const uint64_t* strides, const uint32_t* box) {
+    std::call_once(g_encode_once, init_encode);
+    if (!g_encode || rank < 2 || rank > 5) return false;
+    cuuint64_t d[5], st[4];
+    cuuint32_t b[5], es[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        es[i] = 1;
+        if (i + 1 < rank) st[i] = strides[i];
+    }
+    return g_encode(m, type, static_cast<cuuint32_t>(rank), const_cast<void*>(ptr), d, st, b, es,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+void wait_settings(uint64_t* wait_ns, long long* stall_after) {
+    const dgemm_overrides_t ov = overrides_now();
+    *wait_ns = ov.wait_limit_ns > 0 ? static_cast<uint64_t>(ov.wait_limit_ns) : dg::kWaitLimitNs;
+    *stall_after = ov.stall_after_loads;
+}
+
+}  // namespace host
+}  // namespace dg
 
 extern "C" {
 
