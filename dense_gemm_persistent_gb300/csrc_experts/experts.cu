@@ -9,10 +9,12 @@
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
+#include <algorithm>
 #include <atomic>
+#include <cstring>
 
 #include "dgemm_experts.h"
-#include "gemm_kernel.cuh"
+#include "experts_kernels.h"
 #include "host.h"
 
 namespace {
@@ -201,6 +203,16 @@ __global__ void __launch_bounds__(256, 1) expert_product(const ExpertParams p) {
 
 constexpr size_t SMEM = 1024 + TM * 128 + TN * 128 + TN * (TM + 1) * 4;
 
+using dg::experts::Variant;
+
+const Variant* find_variant(int fp8, int kn, int pair, int gather) {
+    int n = 0;
+    const Variant* v = fp8 ? dg::experts::variants_fp8(&n) : kn ? dg::experts::variants_bf16_kn(&n) : dg::experts::variants_bf16(&n);
+    for (int i = 0; i < n; ++i)
+        if (v[i].pair == pair && v[i].gather == gather) return v + i;
+    return nullptr;
+}
+
 struct Call {
     int type;
     const void* A;
@@ -240,6 +252,103 @@ dgemm_status_t check_sizes(int type, int64_t R, int64_t E, int64_t N, int64_t K,
     return DGEMM_OK;
 }
 
+// Launches the tensor-core variant for BF16 or E4M3 operands.
+dgemm_status_t run_mma(const Call& c, const dg::host::Device& dev) {
+    const int fp8 = c.type == DGEMM_GROUPED_FP8, kn = c.layout == DGEMM_B_KN, gated = c.act == DGEMM_ACT_SWIGLU;
+    const uint64_t esz = fp8 ? 1 : 2, sl = 128 / esz;
+    const uint64_t N = static_cast<uint64_t>(c.N), K = static_cast<uint64_t>(c.K), E = static_cast<uint64_t>(c.E);
+    // KN: both halves of a gated product start on 16 bytes
+    if (kn && gated && (N / 2) * esz % 16 != 0) return DGEMM_ERR_MISALIGNED;
+    // CTA pairs (256 channels, up to 256 rows a tile) where groups are long enough to
+    // share weights between two SMs; single CTAs (128 channels, up to 64 rows) where
+    // the calls read weights for few rows each.
+    const int pair = c.R > 48 * c.E;
+    const Variant* v = find_variant(fp8, kn, pair, c.a_rows != nullptr);
+    if (!v) return DGEMM_ERR_NOT_SUPPORTED;
+
+    dg::experts::Params p{};
+    p.offsets = c.offsets;
+    p.a_rows = c.a_rows;
+    p.A = c.A;
+    p.a_scale = c.a_scale;
+    p.b_scale = c.b_scale;
+    p.bias = c.bias;
+    p.D = c.D;
+    p.E = static_cast<int>(c.E);
+    p.R = static_cast<int>(c.R);
+    p.N = static_cast<int>(c.N);
+    p.K = static_cast<int>(c.K);
+    p.a_count = static_cast<int>(c.a_count);
+    p.gated = gated;
+    p.wide = gated ? p.N / 2 : p.N;
+    p.act = c.act;
+    p.d_f32 = c.d_dtype == DGEMM_F32;
+    const int tile_channels = (gated ? 64 : 128) * v->ctas;
+    p.ctiles = (p.wide + tile_channels - 1) / tile_channels;
+    p.kstages = static_cast<int>((K + 2 * sl - 1) / (2 * sl));
+    p.k_whole = K % sl == 0;
+    p.alpha = c.alpha;
+    p.status = dev.status;
+    p.epoch = dg::host::next_launch_epoch();
+    p.ws_status = c.ws && c.ws_bytes >= DGEMM_WS_STATUS_BYTES ? static_cast<unsigned long long*>(c.ws) : nullptr;
+    dg::host::wait_settings(&p.wait_ns, &p.stall_after);
+
+    // at most one partial tile per group
+    const int64_t most_tiles = ((c.R + v->bn - 1) / v->bn + std::min(c.E, c.R)) * p.ctiles;
+    if (most_tiles > INT32_MAX / 2) return DGEMM_ERR_NOT_SUPPORTED;
+    const int units = static_cast<int>(std::min<int64_t>(dev.num_sms / v->ctas, most_tiles));
+
+    alignas(64) CUtensorMap w, x, xs;
+    std::memset(&w, 0, sizeof w);
+    std::memset(&x, 0, sizeof x);
+    std::memset(&xs, 0, sizeof xs);
+    if (K > 0) {
+        const CUtensorMapDataType dt = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+        const uint32_t s = static_cast<uint32_t>(sl);
+        const uint64_t halves = gated ? 2 : 1, H = N / halves;
+        const uint32_t box_rows = gated ? 64 : 128, box_halves = static_cast<uint32_t>(halves);
+        bool ok;
+        if (kn) {
+            const uint64_t d[3] = {N, K, E}, st[2] = {N * esz, K * N * esz};
+            const uint32_t b[3] = {s, 2 * s, 1};
+            ok = dg::host::encode_map(&w, dt, c.B, 3, d, st, b);
+        } else if (p.k_whole) {
+            // a stage's two K slices, and the gate and up channels of a gated tile, in one copy
+            const uint64_t d[5] = {sl, H, halves, K / sl, E}, st[4] = {K * esz, H * K * esz, 128, N * K * esz};
+            const uint32_t b[5] = {s, box_rows, box_halves, 2, 1};
+            ok = dg::host::encode_map(&w, dt, c.B, 5, d, st, b);
+        } else {
+            const uint64_t d[4] = {K, H, halves, E}, st[3] = {K * esz, H * K * esz, N * K * esz};
+            const uint32_t b[4] = {s, box_rows, box_halves, 1};
+            ok = dg::host::encode_map(&w, dt, c.B, 4, d, st, b);
+        }
+        if (ok && !c.a_rows) {
+            const uint64_t rows = static_cast<uint64_t>(c.a_count);
+            const uint32_t big = static_cast<uint32_t>(v->bn_cta), few = static_cast<uint32_t>(v->small_rows);
+            if (p.k_whole) {
+                const uint64_t d[3] = {sl, rows, K / sl}, st[2] = {K * esz, 128};
+                const uint32_t b[3] = {s, big, 2}, bs[3] = {s, few, 1};
+                ok = dg::host::encode_map(&x, dt, c.A, 3, d, st, b) && dg::host::encode_map(&xs, dt, c.A, 3, d, st, bs);
+            } else {
+                const uint64_t d[2] = {K, rows}, st[1] = {K * esz};
+                const uint32_t b[2] = {s, big}, bs[2] = {s, few};
+                ok = dg::host::encode_map(&x, dt, c.A, 2, d, st, b) && dg::host::encode_map(&xs, dt, c.A, 2, d, st, bs);
+            }
+        }
+        if (!ok) return DGEMM_ERR_CUDA;
+    }
+    const size_t smem = v->smem_fixed + dg::experts::Schedule::bytes(p.E);
+    static std::atomic<unsigned char> ready[12][dg::host::kMaxDevices];
+    std::atomic<unsigned char>& flag = ready[(fp8 ? 8 : kn ? 4 : 0) + pair * 2 + (c.a_rows ? 1 : 0)][dev.id];
+    if (!flag.load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(v->func, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(v->smem_fixed + dg::experts::Schedule::bytes(DGEMM_MAX_EXPERTS))) != cudaSuccess)
+            return DGEMM_ERR_CUDA;
+        flag.store(1, std::memory_order_release);
+    }
+    return v->launch(w, x, xs, p, units * v->ctas, smem, c.stream) == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
+}
+
 dgemm_status_t run_experts(const Call& c) {
     const dgemm_status_t st = check_sizes(c.type, c.R, c.E, c.N, c.K, c.layout, c.act);
     if (st != DGEMM_OK) return st;
@@ -261,6 +370,7 @@ dgemm_status_t run_experts(const Call& c) {
     const dgemm_status_t ds = dg::host::current_device(&dev);
     if (ds != DGEMM_OK) return ds;
 
+    if (c.type != DGEMM_GROUPED_INT8) return run_mma(c, dev);
     ExpertParams p{};
     p.A = c.A;
     p.a_rows = c.a_rows;

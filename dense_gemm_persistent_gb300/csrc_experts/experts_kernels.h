@@ -1,0 +1,26 @@
+// experts_kernels.h -- the compiled variants of the expert products, for the host side.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "experts_common.cuh"
+
+namespace dg {
+namespace experts {
+
+struct Variant {
+    int fp8, kn, pair, gather;
+    int bn, bn_cta, ctas, small_rows, threads;
+    size_t smem_fixed;           // dynamic shared memory without the schedule
+    const void* func;
+    cudaError_t (*launch)(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& xs, const Params& p, int grid,
+                          size_t smem, cudaStream_t s);
+};
+
+const Variant* variants_bf16(int* count);
+const Variant* variants_bf16_kn(int* count);
+const Variant* variants_fp8(int* count);
+
+}  // namespace experts
+}  // namespace dg
