@@ -285,7 +285,8 @@ dgemm_status_t run_mma(const Call& c, const dg::host::Device& dev) {
     p.d_f32 = c.d_dtype == DGEMM_F32;
     const int tile_channels = (gated ? 64 : 128) * v->ctas;
     p.ctiles = (p.wide + tile_channels - 1) / tile_channels;
-    p.kstages = static_cast<int>((K + 2 * sl - 1) / (2 * sl));
+    const uint64_t ks = static_cast<uint64_t>(v->slices);
+    p.kstages = static_cast<int>((K + ks * sl - 1) / (ks * sl));
     p.k_whole = K % sl == 0;
     p.alpha = c.alpha;
     p.status = dev.status;
@@ -310,12 +311,12 @@ dgemm_status_t run_mma(const Call& c, const dg::host::Device& dev) {
         bool ok;
         if (kn) {
             const uint64_t d[3] = {N, K, E}, st[2] = {N * esz, K * N * esz};
-            const uint32_t b[3] = {s, 2 * s, 1};
+            const uint32_t b[3] = {s, static_cast<uint32_t>(ks) * s, 1};
             ok = dg::host::encode_map(&w, dt, c.B, 3, d, st, b);
         } else if (p.k_whole) {
-            // a stage's two K slices, and the gate and up channels of a gated tile, in one copy
+            // a stage's K slices, and the gate and up channels of a gated tile, in one copy
             const uint64_t d[5] = {sl, H, halves, K / sl, E}, st[4] = {K * esz, H * K * esz, 128, N * K * esz};
-            const uint32_t b[5] = {s, box_rows, box_halves, 2, 1};
+            const uint32_t b[5] = {s, box_rows, box_halves, static_cast<uint32_t>(ks), 1};
             ok = dg::host::encode_map(&w, dt, c.B, 5, d, st, b);
         } else {
             const uint64_t d[4] = {K, H, halves, E}, st[3] = {K * esz, H * K * esz, N * K * esz};

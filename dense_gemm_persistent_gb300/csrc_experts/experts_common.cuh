@@ -158,18 +158,32 @@ struct Cursor {
 
 __device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.0f + __expf(-v)); }
 
-__device__ __forceinline__ float activate(float v, int act) {
-    if (act == DGEMM_ACT_RELU) return fmaxf(v, 0.0f);
-    if (act == DGEMM_ACT_GELU) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
-    if (act == DGEMM_ACT_SILU) return silu(v);
-    return v;
-}
-
-__device__ __forceinline__ void store1(const Params& p, int64_t at, float v) {
-    if (p.d_f32)
-        static_cast<float*>(p.D)[at] = v;
-    else
-        static_cast<__nv_bfloat16*>(p.D)[at] = __float2bfloat16_rn(v);
+// Stores one channel's COLS values, one row of D each (lanes: consecutive channels; `at`: this
+// lane's first). BF16 rows of even length: neighbouring lanes swap one value of every two
+// rows, so that a lane stores two channels of one row and the warp two rows at once.
+template <int COLS>
+__device__ __forceinline__ void store_columns(const Params& p, int64_t at, const float (&v)[COLS], bool live, int valid) {
+    const int64_t wide = p.wide;
+    if (p.d_f32) {
+        float* d = static_cast<float*>(p.D) + at;
+#pragma unroll
+        for (int j = 0; j < COLS; ++j)
+            if (live && j < valid) d[j * wide] = v[j];
+    } else if ((p.wide & 1) == 0) {
+        const int odd = threadIdx.x & 1;
+        uint32_t* d = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.D) + at - odd + odd * wide);
+#pragma unroll
+        for (int j = 0; j < COLS; j += 2) {
+            const float got = __shfl_xor_sync(kAllLanes, odd ? v[j] : v[j + 1], 1);
+            // (an even row length: both channels of a lane pair are live or neither is)
+            if (live && j + odd < valid) d[(j / 2) * wide] = odd ? pack_bf16x2(got, v[j + 1]) : pack_bf16x2(v[j], got);
+        }
+    } else {
+        __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.D) + at;
+#pragma unroll
+        for (int j = 0; j < COLS; ++j)
+            if (live && j < valid) d[j * wide] = __float2bfloat16_rn(v[j]);
+    }
 }
 
 // Named barrier of the two warps that exchange gate and up halves; every thread
@@ -236,6 +250,14 @@ __device__ __forceinline__ bool tile_epilogue(const Params& p, const Tile& t, ui
     float* mine = exchange + ((part * 2 + (q & 1)) * 2 + (q >> 1)) * 512;
     const float* theirs = exchange + ((part * 2 + (q & 1)) * 2 + ((q >> 1) ^ 1)) * 512;
     const int chunks = (t.rows + 31) / 32;
+    // The accumulator goes back once its last columns are in registers (a relaxed
+    // arrive: its reads have completed, and the stores to come need no ordering).
+    auto hand_back = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) released();
+    };
+    if (part >= chunks) hand_back();
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c) {
         const int col0 = (c * COLS + part) * 32;
@@ -243,12 +265,18 @@ __device__ __forceinline__ bool tile_epilogue(const Params& p, const Tile& t, ui
         uint32_t r[32];
         tmem_ld32(acc + (static_cast<uint32_t>(q * 32) << 16) + col0, r);
         tmem_ld_wait();
+        if ((c + 1) * COLS + part >= chunks) hand_back();
         float v[32];
+        if (p.kstages == 0) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            float s = bs;
-            if (p.a_scale) s *= __shfl_sync(kAllLanes, as[c], j);
-            v[j] = p.kstages > 0 ? fmaf(__uint_as_float(r[j]), s, bias) : bias;
+            for (int j = 0; j < 32; ++j) v[j] = bias;
+        } else if (p.a_scale) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                v[j] = fmaf(__uint_as_float(r[j]), bs * __shfl_sync(kAllLanes, as[c], j), bias);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = fmaf(__uint_as_float(r[j]), bs, bias);
         }
         const int64_t at = static_cast<int64_t>(t.row0 + col0) * p.wide + ch;
         const int valid = t.rows - col0;
@@ -259,32 +287,30 @@ __device__ __forceinline__ bool tile_epilogue(const Params& p, const Tile& t, ui
 #pragma unroll
             for (int j = 0; j < 16; ++j) mine[j * 32 + lane] = up ? v[j] : v[16 + j];
             pair_sync(swap_id);
+            float y[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
                 const float x = theirs[j * 32 + lane];
-                const int col = up ? 16 + j : j;
-                const float y = up ? silu(x) * v[16 + j] : silu(v[j]) * x;
-                if (live && col < valid) store1(p, at + static_cast<int64_t>(col) * p.wide, y);
+                y[j] = up ? silu(x) * v[16 + j] : silu(v[j]) * x;
             }
+            const int skip = up ? 16 : 0;
+            store_columns<16>(p, at + static_cast<int64_t>(skip) * p.wide, y, live, valid - skip);
         } else {
+            if (p.C && live) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                if (!live || j >= valid) continue;
-                const int64_t o = at + static_cast<int64_t>(j) * p.wide;
-                float y = v[j];
-                if (p.C) {
+                for (int j = 0; j < 32; ++j) {
+                    if (j >= valid) continue;
+                    const int64_t o = at + static_cast<int64_t>(j) * p.wide;
                     const float x = p.c_f32 ? static_cast<const float*>(p.C)[o]
                                             : __bfloat162float(static_cast<const __nv_bfloat16*>(p.C)[o]);
-                    y = fmaf(p.beta, x, y);
+                    v[j] = fmaf(p.beta, x, v[j]);
                 }
-                store1(p, o, activate(y, p.act));
             }
+            activation32(v, p.act);
+            store_columns<32>(p, at, v, live, valid);
         }
     }
     if (p.gated && part < chunks) pair_sync(swap_id);        // before the next tile's first write
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) released();
     return true;
 }
 

@@ -11,7 +11,7 @@ namespace experts {
 
 struct Variant {
     int fp8, kn, pair, gather;
-    int bn, bn_cta, ctas, small_rows, threads;
+    int bn, bn_cta, ctas, slices, small_rows, threads;   // slices: 128-byte slices of K per stage
     size_t smem_fixed;           // dynamic shared memory without the schedule
     const void* func;
     cudaError_t (*launch)(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& xs, const Params& p, int grid,

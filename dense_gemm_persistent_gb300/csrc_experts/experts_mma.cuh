@@ -4,12 +4,23 @@
 // schedule. Warps of a CTA:
 //   0       TMA producer: weights, and token rows that are already in order
 //   1       MMA issuer (one thread), owner of the Tensor Memory
-//   2-3     idle (they complete the first warpgroup)
+//   2       gathering variants: announces gathered stages to the MMA issuer
+//   3       idle (completes the first warpgroup)
 //   4-11    epilogue
-//   12-15   gathering variants: token rows by index with cp.async into the
-//           swizzled slices the MMA reads
-// A stage of the ring holds two 128-byte slices of K of both operands. The output
-// channels are the MMA's rows, the token rows its columns, as many as the tile has.
+//   12-15   gathering variants: cp.async of token rows by index into the swizzled
+//           slices that the MMA reads
+// A stage of the ring holds two 128-byte slices of K of both operands; TMA brings
+// each operand's in one copy.
+//
+// The gather, for 16384 rows of 4096 x 4096 BF16 over 16 experts (355 us with rows in
+// order): TMA copies by index (four rows each) 1075 us, one per ~17 ns and 64 of
+// them per stage; cp.async waited for and announced by the copying warps 622 us; the
+// same with stages of one slice 933-1290 us, because each stage's arrive on the peer's
+// barrier, released at cluster scope, waited for all the thread's memory operations; with
+// a release at CTA scope 493 us; copies that arrive by themselves and a thread of its
+// own that announces them 424 us (one-slice stages: 440).
+// The output channels are the MMA's rows, the token rows its columns, as many as
+// the tile has.
 #pragma once
 
 #include "experts_common.cuh"
@@ -26,21 +37,22 @@ struct MmaCfg {
     static constexpr int BN_CTA = BN / CTAS;
     static constexpr int ESZ = FP8 ? 1 : 2;
     static constexpr int SL = 128 / ESZ;                 // K elements of a slice
-    static constexpr int KS = 2;                         // slices per stage
+    static constexpr int KS = 2;                          // slices per stage
     static constexpr int UK = 32 / ESZ;                  // K elements of one MMA
     static constexpr int SLICE_W = 128 * 128, SLICE_X = BN_CTA * 128;
     static constexpr int W_BYTES = KS * SLICE_W, X_BYTES = KS * SLICE_X, STAGE = W_BYTES + X_BYTES;
-    static constexpr int STAGES = PAIR ? 3 : 4;
+    static constexpr int ATOM = KS * SL * 128;           // KN weights: 64 channels of a stage's K rows
+    static constexpr int STAGES = (PAIR ? 6 : 8) / KS;
     static constexpr int SMALL_ROWS = 16;                // rows of a small copy of token rows
     static constexpr int EPI_WARPS = 8, EPI_WARP0 = 4, GATHER_WARP0 = 12, GATHER_WARPS = 4;
-    static constexpr int THREADS = 32 * (GATHER ? 16 : 12);
+    static constexpr int THREADS = 32 * (GATHER ? GATHER_WARP0 + GATHER_WARPS : EPI_WARP0 + EPI_WARPS);
     static constexpr int TMEM_COLS = 2 * BN;
     static constexpr int BAR_BYTES = 256;
     static constexpr int FIXED = 1024 + STAGES * STAGE + exchange_bytes<EPI_WARPS>() + BAR_BYTES;
     static constexpr uint32_t IDESC0 = make_idesc(FP8 ? 0u : 1u, KN, false, 128 * CTAS, 0);
     static_assert(!(FP8 && KN), "E4M3 weights are stored N x K");
     static_assert(FIXED + Schedule::bytes(DGEMM_MAX_EXPERTS) <= 232448, "shared memory");
-    static_assert((2 * STAGES + 5) * 8 + 8 <= BAR_BYTES, "barriers fit");
+    static_assert((3 * STAGES + 5) * 8 + 8 <= BAR_BYTES, "barriers fit");
 };
 
 template <class CF>
@@ -53,7 +65,8 @@ __global__ void __launch_bounds__(CF::THREADS, 1)
     float* exchange = reinterpret_cast<float*>(ring + S * CF::STAGE);
     uint64_t* full = reinterpret_cast<uint64_t*>(ring + S * CF::STAGE + exchange_bytes<CF::EPI_WARPS>());
     uint64_t* empty = full + S;
-    uint64_t* acc_full = empty + S;
+    uint64_t* landed = empty + S;                // gathered rows of a stage
+    uint64_t* acc_full = landed + S;
     uint64_t* acc_empty = acc_full + 2;
     uint64_t* drain = acc_empty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -67,7 +80,8 @@ __global__ void __launch_bounds__(CF::THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(&full[s], 1 + (CF::GATHER ? CF::GATHER_WARPS * CF::CTAS : 0));
+            mbar_init(&full[s], 1 + (CF::GATHER ? CF::CTAS : 0));
+            mbar_init(&landed[s], 32 * CF::GATHER_WARPS);
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -136,15 +150,15 @@ __global__ void __launch_bounds__(CF::THREADS, 1)
                     const uint32_t fb = CF::PAIR ? mapa_shared(smem_u32(&full[stage]), 0) : smem_u32(&full[stage]);
                     const int k0 = kb * CF::KS * CF::SL;
                     if constexpr (CF::KN) {
-                        // atoms of 64 channels, 128 K rows each
+                        // atoms of 64 channels, a stage's K rows each
                         const int second = p.gated ? p.N / 2 + chan : chan + 64;
                         tma_load_nd<CF::PAIR>(w, &tmW, fb, chan, k0, t.expert, pol);
-                        tma_load_nd<CF::PAIR>(w + CF::SLICE_W, &tmW, fb, second, k0, t.expert, pol);
+                        tma_load_nd<CF::PAIR>(w + CF::ATOM, &tmW, fb, second, k0, t.expert, pol);
                     } else if (p.k_whole) {
                         tma_load_nd<CF::PAIR>(w, &tmW, fb, 0, chan, 0, kb * CF::KS, t.expert, pol);
                     } else {
-                        tma_load_nd<CF::PAIR>(w, &tmW, fb, k0, chan, 0, t.expert, pol);
-                        tma_load_nd<CF::PAIR>(w + CF::SLICE_W, &tmW, fb, k0 + CF::SL, chan, 0, t.expert, pol);
+                        for (int s = 0; s < CF::KS; ++s)
+                            tma_load_nd<CF::PAIR>(w + s * CF::SLICE_W, &tmW, fb, k0 + s * CF::SL, chan, 0, t.expert, pol);
                     }
                     if constexpr (!CF::GATHER) {
                         const CUtensorMap* m = small ? &tmXs : &tmX;
@@ -187,7 +201,7 @@ __global__ void __launch_bounds__(CF::THREADS, 1)
         // ---------------------------------------------------------------- MMA issuer
         if (lane == 0 && rank == 0) {
             const uint32_t s0 = smem_u32(ring);
-            const uint64_t wd0 = smem_desc_sw128(s0, CF::KN ? CF::SLICE_W : 16, 1024);
+            const uint64_t wd0 = smem_desc_sw128(s0, CF::KN ? CF::ATOM : 16, 1024);
             const uint64_t xd0 = smem_desc_sw128(s0 + CF::W_BYTES, 16, 1024);
             constexpr int NK = CF::SL / CF::UK;                  // MMAs per slice
             constexpr uint32_t W_STEP = (CF::KN ? CF::UK * 128 : 32) >> 4;
@@ -256,37 +270,50 @@ __global__ void __launch_bounds__(CF::THREADS, 1)
             ok = tile_epilogue<CF::EPI_WARPS, CF::BN>(
                 p, t, tmem + static_cast<uint32_t>(buf * CF::BN), ew,
                 t.chan0 + static_cast<int>(rank) * (p.gated ? 64 : 128), exchange,
+                [&]() { return mbar_wait_warp(&acc_full[buf], (local >> 1) & 1, abort_flag, p.wait_ns); },
                 [&]() {
-                    return __all_sync(kAllLanes, mbar_wait(&acc_full[buf], (local >> 1) & 1, abort_flag, p.wait_ns)) != 0;
-                },
-                [&]() {
-                    if (CF::PAIR && rank != 0) mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[buf]), 0));
-                    else mbar_arrive(&acc_empty[buf]);
+                    if (CF::PAIR && rank != 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&acc_empty[buf]), 0));
+                    else mbar_arrive_relaxed(&acc_empty[buf]);
                 });
         }
         if (!ok) fail(p, ERR_TIMEOUT_EPILOGUE, abort_flag);
         __syncwarp();
+    } else if (CF::GATHER && warp == 2) {
+        // ---------------------------------------------------------------- announcer
+        // A stage whose copies have landed becomes visible to the tensor core's
+        // (asynchronous) reads by a proxy fence, then counts on its full barrier.
+        if (lane == 0) {
+            uint32_t stage = 0, phase = 0;
+            bool ok = true;
+            Cursor cur;
+            Tile t;
+            for (int item = unit; ok && cur.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, t); item += units) {
+                for (int kb = 0; kb < p.kstages; ++kb) {
+                    if (!mbar_wait(&landed[stage], phase, abort_flag, p.wait_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    fence_proxy_async_smem();
+                    if (CF::PAIR && rank != 0) mbar_arrive_peer(mapa_shared(smem_u32(&full[stage]), 0));
+                    else mbar_arrive(&full[stage]);
+                    if (++stage == S) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+            if (!ok) fail(p, ERR_TIMEOUT_PRODUCER, abort_flag);
+        }
+        __syncwarp();
     } else if (CF::GATHER && warp >= CF::GATHER_WARP0) {
         // ---------------------------------------------------------------- gather
-        // Eight lanes copy the 16-byte chunks of one row's slice. Copies of up to
-        // two stages are in flight; a stage is announced once its copies have landed
-        // and are visible to the tensor core's (asynchronous) reads.
+        // Eight lanes copy the 16-byte chunks of one row's slice, four rows a warp; every
+        // thread's copies arrive on the stage's landed barrier by themselves.
         constexpr int ROUNDS = CF::BN_CTA / 16;
-        const int gw = warp - CF::GATHER_WARP0, sub = lane >> 3, chunk = lane & 7;
+        const int sub = (warp - CF::GATHER_WARP0) * 4 + (lane >> 3), chunk = lane & 7;
         const int64_t pitch = static_cast<int64_t>(p.K) * CF::ESZ;
-        uint32_t stage = 0, phase = 0, ann = 0;      // next stage to fill / to announce
-        int pending = 0;                             // stages filled and not announced
+        uint32_t stage = 0, phase = 0;
         bool ok = true;
-        auto announce = [&]() {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                if (CF::PAIR && rank != 0) mbar_arrive_cluster(mapa_shared(smem_u32(&full[ann]), 0));
-                else mbar_arrive(&full[ann]);
-            }
-            if (++ann == S) ann = 0;
-            --pending;
-        };
         Cursor cur;
         Tile t;
         for (int item = unit; ok && cur.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, t); item += units) {
@@ -295,62 +322,41 @@ __global__ void __launch_bounds__(CF::THREADS, 1)
             const char* src[ROUNDS];
 #pragma unroll
             for (int i = 0; i < ROUNDS; ++i) {
-                const int row = i * 16 + gw * 4 + sub, r = first + row;
+                const int r = first + i * 16 + sub;
                 src[i] = nullptr;
-                if (row < xrows && r < t.rows) {
+                if (i * 16 + sub < xrows && r < t.rows) {
                     const int a = __ldg(p.a_rows + t.row0 + r);
                     if (a >= 0 && a < p.a_count) src[i] = static_cast<const char*>(p.A) + a * pitch;
                 }
             }
-            const int rounds = (xrows + 15) / 16;
-            for (int kb = 0; ok && kb < p.kstages; ++kb) {
-                if (!__all_sync(kAllLanes, mbar_test(&empty[stage], phase ^ 1))) {
-                    // nothing to fill yet: announce what has landed first
-                    if (pending == 2) {
-                        cp_async_wait<1>();
-                        announce();
-                    }
-                    if (pending == 1) {
-                        cp_async_wait<0>();
-                        announce();
-                    }
-                    if (!__all_sync(kAllLanes, mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.wait_ns))) {
-                        ok = false;
-                        break;
-                    }
+            const int rounds = xrows / 16;
+            for (int kb = 0; kb < p.kstages; ++kb) {
+                if (!mbar_wait_warp(&empty[stage], phase ^ 1, abort_flag, p.wait_ns)) {
+                    ok = false;
+                    break;
                 }
                 uint8_t* x = ring + stage * CF::STAGE + CF::W_BYTES;
 #pragma unroll
                 for (int s = 0; s < CF::KS; ++s) {
                     const int64_t kbyte = (static_cast<int64_t>(kb) * CF::KS + s) * 128 + chunk * 16;
-                    const bool inside = kbyte < pitch;
 #pragma unroll
                     for (int i = 0; i < ROUNDS; ++i) {
                         if (i >= rounds) break;
-                        const int row = i * 16 + gw * 4 + sub;
-                        const bool read = inside && src[i] != nullptr;
+                        const int row = i * 16 + sub;
+                        const bool read = kbyte < pitch && src[i] != nullptr;
                         cp_async_16(x + s * CF::SLICE_X + row * 128 + ((chunk ^ (row & 7)) << 4),
                                     read ? src[i] + kbyte : static_cast<const char*>(p.A), read ? 16u : 0u);
                     }
                 }
-                cp_async_commit();
-                ++pending;
+                cp_async_mbar_arrive(&landed[stage]);
                 if (++stage == S) {
                     stage = 0;
                     phase ^= 1;
                 }
-                if (pending == 3) {
-                    cp_async_wait<2>();
-                    announce();
-                }
             }
         }
-        if (pending == 2 && ok) {
-            cp_async_wait<1>();
-            announce();
-        }
-        cp_async_wait<0>();
-        if (pending == 1 && ok) announce();
+        cp_async_commit();
+        cp_async_wait<0>();      // nothing of this thread's is in flight when it leaves
         if (!ok) fail(p, ERR_TIMEOUT_PRODUCER, abort_flag);
         __syncwarp();
     }

@@ -30,6 +30,25 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
     }
 }
 
+// Arrive on a barrier of the pair's other CTA, releasing at CTA scope. What is
+// handed over lies in this CTA's own shared memory and is read by its own SM's
+// tensor core, so CTA scope orders it; a release at cluster scope waits for every
+// memory operation that the thread has outstanding (~0.9 us a stage, measured).
+__device__ __forceinline__ void mbar_arrive_peer(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// A wait by a whole warp, polled by one lane: every poll of a barrier by 32 lanes
+// takes 32 turns in the shared-memory unit that the tensor core's operands pass
+// through. The outcome is the same in every lane.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+    unsigned ok = 1;
+    if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort, limit_ns);
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    __syncwarp();
+    return ok != 0;
+}
+
 // 4-D and 5-D tiled loads global -> shared (coordinates innermost first), counted
 // in bytes on an mbarrier given by its shared::cluster address; PAIR: the barrier
 // may be in the peer CTA.
