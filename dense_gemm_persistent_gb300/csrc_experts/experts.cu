@@ -2,12 +2,8 @@
 //
 //     D[r,n] = act(alpha * as[a] * bs[e,n] * sum_k A[a,k] B_e[n,k] + beta * C[r,n] + bias[e,n])
 //
-// for the rows r of expert e, a = a_rows[r] or r. The output channels n run over the
-// 128 rows of the MMA and the token rows over its columns, so a group's few rows
-// cost few columns. The simplest form: every thread loads operands, converts them to
-// BF16 (exact for E4M3 and int8) and stores them swizzled; one thread multiplies.
-#include <cuda_bf16.h>
-#include <cuda_fp8.h>
+// for the rows r of expert e, a = a_rows[r] or r. Host side: checks, the choice of a
+// variant, tensor maps and the launch. The kernels are in experts_mma.cuh and experts_int8.cuh.
 
 #include <algorithm>
 #include <atomic>
@@ -19,197 +15,16 @@
 
 namespace {
 
-struct ExpertParams {
-    const void* A;
-    const int* a_rows;
-    const void* B;
-    const float* a_scale;
-    const float* b_scale;
-    const int* offsets;          // null: one group of R rows
-    const float* bias;
-    const void* C;
-    void* D;
-    int type, kn, E, R, N, K, a_count, act, d_f32, c_f32;
-    int wide;                    // columns of D: N, or N / 2 when gated
-    float alpha, beta;
-    unsigned* status;
-    unsigned long long* ws_status;
-    unsigned long long epoch;
-    uint64_t wait_ns;
-};
-
-constexpr int ACT_SWIGLU = DGEMM_ACT_SWIGLU;
-constexpr int TM = 128, TN = 64;
-
-__device__ __forceinline__ float load_value(const void* x, int type, int64_t i) {
-    if (type == DGEMM_GROUPED_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(x)[i]);
-    if (type == DGEMM_GROUPED_INT8) return static_cast<float>(static_cast<const int8_t*>(x)[i]);
-    return static_cast<float>(static_cast<const __nv_fp8_e4m3*>(x)[i]);
-}
-
-__device__ __forceinline__ void expert_error(const ExpertParams& p, unsigned bit) {
-    if (p.ws_status) atomicExch(p.ws_status, (p.epoch << 8) | bit);
-    else atomicOr(p.status, bit);
-}
-
-__device__ __forceinline__ float silu1(float v) { return __fdividef(v, 1.0f + __expf(-v)); }
-
-__device__ __forceinline__ float activation1(float v, int act) {
-    if (act == DGEMM_ACT_RELU) return fmaxf(v, 0.0f);
-    if (act == DGEMM_ACT_GELU) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
-    if (act == DGEMM_ACT_SILU) return silu1(v);
-    return v;
-}
-
-__global__ void __launch_bounds__(256, 1) expert_product(const ExpertParams p) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* sa = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* sb = sa + TM * 128;
-    float* sy = reinterpret_cast<float*>(sb + TN * 128);    // [TN][TM + 1]
-    __shared__ uint64_t done;
-    __shared__ uint32_t tmem_slot;
-    __shared__ int s_e, s_r0, s_r1, s_ok;
-    dg::grid_dependency_wait();
-    if (threadIdx.x == 0) dg::grid_launch_dependents();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) {
-        // which group's tile of token rows this CTA has
-        int left = blockIdx.y;
-        s_e = -1;
-        for (int e = 0; e < p.E; ++e) {
-            const int lo = p.offsets ? min(max(p.offsets[e], 0), p.R) : 0;
-            const int hi = p.offsets ? min(max(p.offsets[e + 1], lo), p.R) : p.R;
-            const int tiles = (hi - lo + TN - 1) / TN;
-            if (left < tiles) {
-                s_e = e;
-                s_r0 = lo + left * TN;
-                s_r1 = min(hi, s_r0 + TN);
-                break;
-            }
-            left -= tiles;
-        }
-        dg::mbar_init(&done, 1);
-        dg::fence_mbarrier_init();
-        s_ok = 1;
-    }
-    __syncthreads();
-    if (s_e < 0) return;
-    if (warp == 0) {
-        dg::tmem_alloc(&tmem_slot, 64);
-        dg::tmem_relinquish();
-    }
-    dg::tc_fence_before();
-    __syncthreads();
-    dg::tc_fence_after();
-    const int e = s_e, r0 = s_r0, rows = s_r1 - s_r0;
-    const bool gated = p.act == ACT_SWIGLU;
-    const int half = p.N / 2;
-    const int n0 = blockIdx.x * (gated ? TM / 2 : TM);
-    // MMA row i is this output channel (-1: none); gated: 64 of the gate, 64 of the up half
-    auto channel = [&](int i) {
-        const int n = gated ? n0 + (i & 63) : n0 + i;
-        if (n >= p.wide) return -1;
-        return gated && i >= 64 ? half + n : n;
-    };
-    const int64_t eb = static_cast<int64_t>(e) * p.N * p.K;
-    bool ok = true;
-    for (int k0 = 0; ok && k0 < p.K; k0 += 64) {
-        for (int c = threadIdx.x; c < (TM + TN) * 8; c += 256) {
-            const bool is_a = c < TM * 8;
-            const int i = is_a ? c % TM : (c - TM * 8) % TN, chunk = is_a ? c / TM : (c - TM * 8) / TN;
-            const int k = k0 + chunk * 8;
-            float v[8];
-            int64_t row = -1;
-            if (is_a) {
-                row = channel(i);
-            } else if (i < rows) {
-                row = p.a_rows ? p.a_rows[r0 + i] : r0 + i;
-                if (row < 0 || row >= p.a_count) row = -1;
-            }
-            for (int j = 0; j < 8; ++j) {
-                v[j] = 0.0f;
-                if (row >= 0 && k + j < p.K)
-                    v[j] = !is_a ? load_value(p.A, p.type, row * p.K + k + j)
-                           : p.kn ? load_value(p.B, p.type, eb + static_cast<int64_t>(k + j) * p.N + row)
-                                  : load_value(p.B, p.type, eb + row * p.K + k + j);
-            }
-            const uint4 w = make_uint4(dg::pack_bf16x2(v[0], v[1]), dg::pack_bf16x2(v[2], v[3]),
-                                       dg::pack_bf16x2(v[4], v[5]), dg::pack_bf16x2(v[6], v[7]));
-            *reinterpret_cast<uint4*>((is_a ? sa : sb) + i * 128 + ((chunk ^ (i & 7)) << 4)) = w;
-        }
-        dg::fence_proxy_async_smem();
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            dg::tc_fence_after();
-            const uint64_t ad = dg::smem_desc_sw128(dg::smem_u32(sa), 16, 1024);
-            const uint64_t bd = dg::smem_desc_sw128(dg::smem_u32(sb), 16, 1024);
-            const uint32_t idesc = dg::make_idesc(1u, false, false, TM, TN);
-            for (int s = 0; s < 4; ++s)
-                dg::mma_bf16(tmem_slot, ad + s * 2, bd + s * 2, idesc, (k0 > 0 || s > 0) ? 1u : 0u);
-            dg::mma_commit(&done);
-        }
-        ok = dg::mbar_wait(&done, (k0 / 64) & 1, nullptr, p.wait_ns);
-        if (!ok) s_ok = 0;
-        __syncthreads();
-        ok = s_ok != 0;
-    }
-    if (!ok && threadIdx.x == 0) expert_error(p, dg::ERR_TIMEOUT_MMA);
-    dg::tc_fence_after();
-    if (ok && warp < 4) {
-        const int i = warp * 32 + lane, ch = channel(i);
-        const float bs = p.alpha * (p.b_scale && ch >= 0 ? p.b_scale[static_cast<int64_t>(e) * p.N + ch] : 1.0f);
-        const float bias = p.bias && ch >= 0 ? p.bias[static_cast<int64_t>(e) * p.N + ch] : 0.0f;
-        for (int c0 = 0; c0 < TN; c0 += 32) {
-            uint32_t acc[32];
-            dg::tmem_ld32(tmem_slot + (static_cast<uint32_t>(warp * 32) << 16) + c0, acc);
-            dg::tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                const int c = c0 + j;
-                float v = 0.0f;
-                if (c < rows) {
-                    const int a = p.a_rows ? p.a_rows[r0 + c] : r0 + c;
-                    const float as = p.a_scale && a >= 0 && a < p.a_count ? p.a_scale[a] : p.a_scale ? 0.0f : 1.0f;
-                    v = (p.K > 0 ? __uint_as_float(acc[j]) : 0.0f) * as * bs + bias;
-                }
-                sy[c * (TM + 1) + i] = v;
-            }
-        }
-    }
-    dg::tc_fence_before();
-    __syncthreads();
-    if (ok) {
-        const int width = gated ? 64 : 128;
-        for (int c = threadIdx.x; c < rows * width; c += 256) {
-            const int r = c / width, i = c % width, n = n0 + i;
-            if (n >= p.wide) continue;
-            const int64_t at = static_cast<int64_t>(r0 + r) * p.wide + n;
-            float v = sy[r * (TM + 1) + i];
-            if (p.C) {
-                const float x = p.c_f32 ? static_cast<const float*>(p.C)[at]
-                                        : __bfloat162float(static_cast<const __nv_bfloat16*>(p.C)[at]);
-                v = fmaf(p.beta, x, v);
-            }
-            v = gated ? silu1(v) * sy[r * (TM + 1) + 64 + i] : activation1(v, p.act);
-            if (p.d_f32) static_cast<float*>(p.D)[at] = v;
-            else static_cast<__nv_bfloat16*>(p.D)[at] = __float2bfloat16_rn(v);
-        }
-    }
-    if (warp == 0) {
-        dg::tc_fence_after();
-        dg::tmem_dealloc(tmem_slot, 64);
-    }
-}
-
-constexpr size_t SMEM = 1024 + TM * 128 + TN * 128 + TN * (TM + 1) * 4;
-
 using dg::experts::Variant;
 
-const Variant* find_variant(int fp8, int kn, int pair, int gather) {
+const Variant* find_variant(int type, int kn, int pair, int gather) {
     int n = 0;
-    const Variant* v = fp8 ? dg::experts::variants_fp8(&n) : kn ? dg::experts::variants_bf16_kn(&n) : dg::experts::variants_bf16(&n);
+    const Variant* v = type == DGEMM_GROUPED_INT8  ? dg::experts::variants_int8(&n)
+                       : type == DGEMM_GROUPED_FP8 ? dg::experts::variants_fp8(&n)
+                       : kn                        ? dg::experts::variants_bf16_kn(&n)
+                                                   : dg::experts::variants_bf16(&n);
     for (int i = 0; i < n; ++i)
-        if (v[i].pair == pair && v[i].gather == gather) return v + i;
+        if (v[i].pair == pair && (v[i].gather == gather || v[i].gather < 0)) return v + i;
     return nullptr;
 }
 
@@ -252,10 +67,11 @@ dgemm_status_t check_sizes(int type, int64_t R, int64_t E, int64_t N, int64_t K,
     return DGEMM_OK;
 }
 
-// Launches the tensor-core variant for BF16 or E4M3 operands.
-dgemm_status_t run_mma(const Call& c, const dg::host::Device& dev) {
-    const int fp8 = c.type == DGEMM_GROUPED_FP8, kn = c.layout == DGEMM_B_KN, gated = c.act == DGEMM_ACT_SWIGLU;
-    const uint64_t esz = fp8 ? 1 : 2, sl = 128 / esz;
+// Picks the variant, encodes the tensor maps and launches.
+dgemm_status_t launch(const Call& c, const dg::host::Device& dev) {
+    const int kn = c.layout == DGEMM_B_KN, gated = c.act == DGEMM_ACT_SWIGLU;
+    const int int8 = c.type == DGEMM_GROUPED_INT8;   // (its token rows need no map: converted on the way)
+    const uint64_t esz = c.type == DGEMM_GROUPED_BF16 ? 2 : 1, sl = 128 / esz;
     const uint64_t N = static_cast<uint64_t>(c.N), K = static_cast<uint64_t>(c.K), E = static_cast<uint64_t>(c.E);
     // KN: both halves of a gated product start on 16 bytes
     if (kn && gated && (N / 2) * esz % 16 != 0) return DGEMM_ERR_MISALIGNED;
@@ -263,7 +79,7 @@ dgemm_status_t run_mma(const Call& c, const dg::host::Device& dev) {
     // share weights between two SMs; single CTAs (128 channels, up to 64 rows) where
     // the calls read weights for few rows each.
     const int pair = c.R > 48 * c.E;
-    const Variant* v = find_variant(fp8, kn, pair, c.a_rows != nullptr);
+    const Variant* v = find_variant(c.type, kn, pair, c.a_rows != nullptr);
     if (!v) return DGEMM_ERR_NOT_SUPPORTED;
 
     dg::experts::Params p{};
@@ -273,6 +89,9 @@ dgemm_status_t run_mma(const Call& c, const dg::host::Device& dev) {
     p.a_scale = c.a_scale;
     p.b_scale = c.b_scale;
     p.bias = c.bias;
+    p.C = c.beta != 0.0f ? c.C : nullptr;
+    p.c_f32 = c.c_dtype == DGEMM_F32;
+    p.beta = c.beta;
     p.D = c.D;
     p.E = static_cast<int>(c.E);
     p.R = static_cast<int>(c.R);
@@ -287,7 +106,7 @@ dgemm_status_t run_mma(const Call& c, const dg::host::Device& dev) {
     p.ctiles = (p.wide + tile_channels - 1) / tile_channels;
     const uint64_t ks = static_cast<uint64_t>(v->slices);
     p.kstages = static_cast<int>((K + ks * sl - 1) / (ks * sl));
-    p.k_whole = K % sl == 0;
+    p.k_whole = K % sl == 0 && !int8;
     p.alpha = c.alpha;
     p.status = dev.status;
     p.epoch = dg::host::next_launch_epoch();
@@ -304,7 +123,7 @@ dgemm_status_t run_mma(const Call& c, const dg::host::Device& dev) {
     std::memset(&x, 0, sizeof x);
     std::memset(&xs, 0, sizeof xs);
     if (K > 0) {
-        const CUtensorMapDataType dt = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+        const CUtensorMapDataType dt = esz == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
         const uint32_t s = static_cast<uint32_t>(sl);
         const uint64_t halves = gated ? 2 : 1, H = N / halves;
         const uint32_t box_rows = gated ? 64 : 128, box_halves = static_cast<uint32_t>(halves);
@@ -323,7 +142,7 @@ dgemm_status_t run_mma(const Call& c, const dg::host::Device& dev) {
             const uint32_t b[4] = {s, box_rows, box_halves, 1};
             ok = dg::host::encode_map(&w, dt, c.B, 4, d, st, b);
         }
-        if (ok && !c.a_rows) {
+        if (ok && !c.a_rows && !int8) {
             const uint64_t rows = static_cast<uint64_t>(c.a_count);
             const uint32_t big = static_cast<uint32_t>(v->bn_cta), few = static_cast<uint32_t>(v->small_rows);
             if (p.k_whole) {
@@ -339,8 +158,8 @@ dgemm_status_t run_mma(const Call& c, const dg::host::Device& dev) {
         if (!ok) return DGEMM_ERR_CUDA;
     }
     const size_t smem = v->smem_fixed + dg::experts::Schedule::bytes(p.E);
-    static std::atomic<unsigned char> ready[12][dg::host::kMaxDevices];
-    std::atomic<unsigned char>& flag = ready[(fp8 ? 8 : kn ? 4 : 0) + pair * 2 + (c.a_rows ? 1 : 0)][dev.id];
+    static std::atomic<unsigned char> ready[16][dg::host::kMaxDevices];
+    std::atomic<unsigned char>& flag = ready[c.type * 4 + (kn ? 12 : 0) + pair * 2 + (c.a_rows ? 1 : 0)][dev.id];
     if (!flag.load(std::memory_order_acquire)) {
         if (cudaFuncSetAttribute(v->func, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(v->smem_fixed + dg::experts::Schedule::bytes(DGEMM_MAX_EXPERTS))) != cudaSuccess)
@@ -371,46 +190,7 @@ dgemm_status_t run_experts(const Call& c) {
     const dgemm_status_t ds = dg::host::current_device(&dev);
     if (ds != DGEMM_OK) return ds;
 
-    if (c.type != DGEMM_GROUPED_INT8) return run_mma(c, dev);
-    ExpertParams p{};
-    p.A = c.A;
-    p.a_rows = c.a_rows;
-    p.B = c.B;
-    p.a_scale = c.a_scale;
-    p.b_scale = c.b_scale;
-    p.offsets = c.offsets;
-    p.bias = c.bias;
-    p.C = c.beta != 0.0f ? c.C : nullptr;
-    p.c_f32 = c.c_dtype == DGEMM_F32;
-    p.D = c.D;
-    p.type = c.type;
-    p.kn = c.layout == DGEMM_B_KN;
-    p.E = static_cast<int>(c.E);
-    p.R = static_cast<int>(c.R);
-    p.N = static_cast<int>(c.N);
-    p.K = static_cast<int>(c.K);
-    p.a_count = static_cast<int>(c.a_count);
-    p.act = c.act;
-    p.d_f32 = c.d_dtype == DGEMM_F32;
-    p.wide = c.act == DGEMM_ACT_SWIGLU ? p.N / 2 : p.N;
-    p.alpha = c.alpha;
-    p.beta = c.beta;
-    p.status = dev.status;
-    p.epoch = dg::host::next_launch_epoch();
-    p.ws_status = c.ws && c.ws_bytes >= DGEMM_WS_STATUS_BYTES ? static_cast<unsigned long long*>(c.ws) : nullptr;
-    long long stall;
-    dg::host::wait_settings(&p.wait_ns, &stall);
-    static std::atomic<unsigned char> ready[dg::host::kMaxDevices];
-    if (!ready[dev.id].load(std::memory_order_acquire)) {
-        if (cudaFuncSetAttribute(expert_product, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM) != cudaSuccess)
-            return DGEMM_ERR_CUDA;
-        ready[dev.id].store(1, std::memory_order_release);
-    }
-    const int step = c.act == DGEMM_ACT_SWIGLU ? TM / 2 : TM;
-    const int64_t tiles = (c.R + TN - 1) / TN + c.E - 1;     // at most: one partial tile per group
-    if (tiles > 65535) return DGEMM_ERR_NOT_SUPPORTED;
-    dg::host::Launch l(static_cast<unsigned>((p.wide + step - 1) / step), static_cast<unsigned>(tiles), 256, SMEM, c.stream);
-    return cudaLaunchKernelEx(&l.cfg, expert_product, p) == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
+    return launch(c, dev);
 }
 
 }  // namespace

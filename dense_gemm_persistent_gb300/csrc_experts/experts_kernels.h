@@ -10,7 +10,8 @@ namespace dg {
 namespace experts {
 
 struct Variant {
-    int fp8, kn, pair, gather;
+    int type, kn, pair;          // dgemm_grouped_type_t; weights K x N; CTA pairs
+    int gather;                  // 1: rows by index, 0: rows in order, -1: either
     int bn, bn_cta, ctas, slices, small_rows, threads;   // slices: 128-byte slices of K per stage
     size_t smem_fixed;           // dynamic shared memory without the schedule
     const void* func;
@@ -21,6 +22,7 @@ struct Variant {
 const Variant* variants_bf16(int* count);
 const Variant* variants_bf16_kn(int* count);
 const Variant* variants_fp8(int* count);
+const Variant* variants_int8(int* count);
 
 }  // namespace experts
 }  // namespace dg
