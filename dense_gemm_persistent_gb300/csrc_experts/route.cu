@@ -8,6 +8,7 @@
 // since a token has an expert at most once. Tokens are cut into chunks of
 // CHUNK; a chunk's pairs with expert e are the bits of a mask (bit = token),
 // so the count inside the chunk is a popcount -- no atomics whose order shows.
+// One launch for up to a chunk of tokens, two beyond.
 //
 // What bounds it: T x E logits in, 16 bytes per pair out; a long prompt is bound by
 // HBM and by the two passes over the chunk counts, a decoding call by its launch.
@@ -30,8 +31,8 @@ struct RouteParams {
     int* offsets;
     int* row_token;
     int* slot_row;
-    unsigned* counts;           // [chunks][E]
-    int chunks;
+    uint8_t* counts;            // [chunks][E rounded up to 4]: at most CHUNK each
+    int chunks, pitch;
 };
 
 // Order-preserving map of a finite float to unsigned (0 is below every one).
@@ -107,12 +108,60 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int t, int lan
     }
 }
 
-// Selects the experts of one chunk of tokens and counts them; with one chunk in all
-// (and `last` set) it also writes the grouping.
+// Exclusive scan of total[0 .. E) over the experts in place, by all threads of the CTA
+// (each one or two experts of a run); returns the sum.
+__device__ __forceinline__ int scan_experts(int* total, int E) {
+    __shared__ int warp_sum[32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int per = (E + static_cast<int>(blockDim.x) - 1) / static_cast<int>(blockDim.x);
+    const int first = threadIdx.x * per, last = min(first + per, E);
+    int mine = 0;
+    for (int e = first; e < last; ++e) mine += total[e];
+    int inc = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    int before = inc - mine, all = 0;
+    for (int w = 0; w < warps; ++w) {
+        if (w < warp) before += warp_sum[w];
+        all += warp_sum[w];
+    }
+    for (int e = first; e < last; ++e) {
+        const int v = total[e];
+        total[e] = before;
+        before += v;
+    }
+    __syncthreads();
+    return all;
+}
+
+// Places the pairs of one chunk: base[e] is the first row of expert e, before[e] (null: none)
+// the pairs with e in earlier chunks, mask[e] the chunk's tokens with e.
+__device__ __forceinline__ void place_chunk(const RouteParams& p, int t0, int n, const unsigned long long* mask,
+                                            const int* base, const int* before, int all) {
+    for (int i = threadIdx.x; i < n * p.k; i += blockDim.x) {
+        const int64_t at = static_cast<int64_t>(t0) * p.k + i;
+        const int e = p.ids[at], tok = i / p.k;
+        int row = -1;
+        if (e >= 0) {
+            row = base[e] + (before ? before[e] : 0) + __popcll(mask[e] & ((1ull << tok) - 1));
+            p.row_token[row] = t0 + tok;
+        }
+        p.slot_row[at] = row;
+        if (at >= all) p.row_token[at] = -1;
+    }
+}
+
+// Selects the experts of one chunk of tokens and counts them. A call of one chunk is
+// placed here as well: one launch.
 template <int VPL>
 __global__ void __launch_bounds__(32 * WARPS) route_select(const RouteParams p) {
     extern __shared__ unsigned long long mask[];            // [E]
-    int* sid = reinterpret_cast<int*>(mask + p.E);          // [CHUNK][k]
+    int* total = reinterpret_cast<int*>(mask + p.E);        // [E] (one chunk)
+    int* sid = total + p.E;                                 // [CHUNK][k]
     dg::grid_dependency_wait();
     if (threadIdx.x == 0) dg::grid_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -125,37 +174,55 @@ __global__ void __launch_bounds__(32 * WARPS) route_select(const RouteParams p) 
         if (lane < p.k && sid[i * p.k + lane] >= 0) atomicOr(&mask[sid[i * p.k + lane]], 1ull << i);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < p.E; e += blockDim.x)
-        p.counts[static_cast<int64_t>(blockIdx.x) * p.E + e] = __popcll(mask[e]);
+    if (p.chunks > 1) {
+        for (int e = threadIdx.x; e < p.pitch; e += blockDim.x)
+            p.counts[static_cast<int64_t>(blockIdx.x) * p.pitch + e] =
+                e < p.E ? static_cast<uint8_t>(__popcll(mask[e])) : 0;
+        return;
+    }
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) total[e] = __popcll(mask[e]);
+    __syncthreads();
+    const int all = scan_experts(total, p.E);
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) p.offsets[e] = total[e];
+    if (threadIdx.x == 0) p.offsets[p.E] = all;
+    place_chunk(p, t0, n, mask, total, nullptr, all);
 }
 
 // Rows of one chunk's pairs: every CTA sums the counts of the chunks before its own
-// and of all chunks, scans the totals over the experts, and places its pairs.
+// and of all chunks (four experts a load, all loads of a thread in flight together),
+// scans the totals over the experts, and places its pairs.
 __global__ void __launch_bounds__(1024) route_place(const RouteParams p) {
     extern __shared__ unsigned long long mask[];            // [E]
-    int* before = reinterpret_cast<int*>(mask + p.E);       // [E] pairs of e in earlier chunks
-    int* base = before + p.E;                               // [E] first row of e
-    __shared__ int warp_sum[32];
+    int* before = reinterpret_cast<int*>(mask + p.E);       // [pitch] pairs of e in earlier chunks
+    int* base = before + p.pitch;                           // [pitch] first row of e
     dg::grid_dependency_wait();
     if (threadIdx.x == 0) dg::grid_launch_dependents();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
-        mask[e] = 0;
+    for (int e = threadIdx.x; e < p.pitch; e += blockDim.x) {
+        if (e < p.E) mask[e] = 0;
         before[e] = 0;
         base[e] = 0;
     }
     __syncthreads();
-    const int span = blockDim.x / p.E > 0 ? blockDim.x / p.E : 1;   // threads per expert
-    for (int w = threadIdx.x; w < p.E * span; w += blockDim.x) {
-        const int e = w % p.E, part = w / p.E;
-        int sum = 0, pre = 0;
-        for (int c = part; c < p.chunks; c += span) {
-            const int v = static_cast<int>(p.counts[static_cast<int64_t>(c) * p.E + e]);
-            sum += v;
-            if (c < static_cast<int>(blockIdx.x)) pre += v;
+    const int quads = p.pitch / 4, parts = max(1, static_cast<int>(blockDim.x) / quads);
+    const int quad = threadIdx.x % quads, part = threadIdx.x / quads;
+    const int mine = static_cast<int>(blockIdx.x);
+    if (part < parts) {
+        int sum[4] = {0, 0, 0, 0}, pre[4] = {0, 0, 0, 0};
+#pragma unroll 8
+        for (int c = part; c < p.chunks; c += parts) {
+            const uint32_t v = *reinterpret_cast<const uint32_t*>(p.counts + static_cast<int64_t>(c) * p.pitch + quad * 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int x = (v >> (8 * i)) & 0xFF;
+                sum[i] += x;
+                if (c < mine) pre[i] += x;
+            }
         }
-        if (sum) atomicAdd(&base[e], sum);                  // integers: any order
-        if (pre) atomicAdd(&before[e], pre);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (sum[i]) atomicAdd(&base[quad * 4 + i], sum[i]);     // integers: any order
+            if (pre[i]) atomicAdd(&before[quad * 4 + i], pre[i]);
+        }
     }
     const int t0 = blockIdx.x * CHUNK, n = min(CHUNK, p.T - t0);
     for (int i = threadIdx.x; i < n * p.k; i += blockDim.x) {
@@ -163,43 +230,12 @@ __global__ void __launch_bounds__(1024) route_place(const RouteParams p) {
         if (e >= 0) atomicOr(&mask[e], 1ull << (i / p.k));
     }
     __syncthreads();
-    // exclusive scan of the totals over the experts (E <= 1024 = blockDim)
-    const int mine = static_cast<int>(threadIdx.x) < p.E ? base[threadIdx.x] : 0;
-    int inc = mine;
-    for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
+    const int all = scan_experts(base, p.E);
+    if (blockIdx.x == 0) {
+        for (int e = threadIdx.x; e < p.E; e += blockDim.x) p.offsets[e] = base[e];
+        if (threadIdx.x == 0) p.offsets[p.E] = all;
     }
-    if (lane == 31) warp_sum[warp] = inc;
-    __syncthreads();
-    if (warp == 0) {
-        int s = warp_sum[lane];
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += v;
-        }
-        warp_sum[lane] = s;
-    }
-    __syncthreads();
-    const int first = inc - mine + (warp ? warp_sum[warp - 1] : 0);
-    const int all = warp_sum[31];
-    if (static_cast<int>(threadIdx.x) < p.E) {
-        base[threadIdx.x] = first;
-        if (blockIdx.x == 0) p.offsets[threadIdx.x] = first;
-    }
-    if (blockIdx.x == 0 && threadIdx.x == 0) p.offsets[p.E] = all;
-    __syncthreads();
-    for (int i = threadIdx.x; i < n * p.k; i += blockDim.x) {
-        const int64_t at = static_cast<int64_t>(t0) * p.k + i;
-        const int e = p.ids[at], tok = i / p.k;
-        int row = -1;
-        if (e >= 0) {
-            row = base[e] + before[e] + __popcll(mask[e] & ((1ull << tok) - 1));
-            p.row_token[row] = t0 + tok;
-        }
-        p.slot_row[at] = row;
-        if (at >= all) p.row_token[at] = -1;
-    }
+    place_chunk(p, t0, n, mask, base, before, all);
 }
 
 dgemm_status_t route_sizes(int64_t T, int64_t E, int k) {
@@ -211,7 +247,7 @@ dgemm_status_t route_sizes(int64_t T, int64_t E, int k) {
 
 template <int VPL>
 cudaError_t launch_select(const RouteParams& p, cudaStream_t s) {
-    dg::host::Launch l(static_cast<unsigned>(p.chunks), 1, 32 * WARPS, static_cast<size_t>(p.E) * 8 + CHUNK * p.k * 4, s);
+    dg::host::Launch l(static_cast<unsigned>(p.chunks), 1, 32 * WARPS, static_cast<size_t>(p.E) * 12 + CHUNK * p.k * 4, s);
     return cudaLaunchKernelEx(&l.cfg, route_select<VPL>, p);
 }
 
@@ -219,7 +255,8 @@ cudaError_t launch_select(const RouteParams& p, cudaStream_t s) {
 
 extern "C" size_t dgemm_route_workspace_size(int64_t T, int64_t E, int k) {
     if (route_sizes(T, E, k) != DGEMM_OK) return 0;
-    return static_cast<size_t>((T + CHUNK - 1) / CHUNK) * static_cast<size_t>(E) * 4;
+    const size_t chunks = static_cast<size_t>((T + CHUNK - 1) / CHUNK);
+    return chunks > 1 ? chunks * ((static_cast<size_t>(E) + 3) / 4 * 4) : 0;
 }
 
 extern "C" dgemm_status_t dgemm_route(const void* logits, dgemm_dtype_t logits_dtype, int64_t T, int64_t E, int k,
@@ -254,7 +291,8 @@ extern "C" dgemm_status_t dgemm_route(const void* logits, dgemm_dtype_t logits_d
     p.offsets = offsets;
     p.row_token = row_token;
     p.slot_row = slot_row;
-    p.counts = static_cast<unsigned*>(ws);
+    p.counts = static_cast<uint8_t*>(ws);
+    p.pitch = (p.E + 3) / 4 * 4;
     p.chunks = static_cast<int>((T + CHUNK - 1) / CHUNK);
     cudaError_t e;
     if (E <= 64) e = launch_select<2>(p, s);
@@ -263,6 +301,7 @@ extern "C" dgemm_status_t dgemm_route(const void* logits, dgemm_dtype_t logits_d
     else if (E <= 512) e = launch_select<16>(p, s);
     else e = launch_select<32>(p, s);
     if (e != cudaSuccess) return DGEMM_ERR_CUDA;
-    dg::host::Launch l(static_cast<unsigned>(p.chunks), 1, 1024, static_cast<size_t>(E) * 16, s);
+    if (p.chunks == 1) return DGEMM_OK;
+    dg::host::Launch l(static_cast<unsigned>(p.chunks), 1, 1024, static_cast<size_t>(p.pitch) * 16, s);
     return cudaLaunchKernelEx(&l.cfg, route_place, p) == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
 }

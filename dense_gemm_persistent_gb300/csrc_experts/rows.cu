@@ -16,53 +16,174 @@ __device__ __forceinline__ float load1(const void* x, int f32, int64_t i) {
 // ---------------------------------------------------------------- combine
 
 // out[t,h] = add[t,h] + sum_j w[t,j] Y[slot_row[t,j],h], j ascending, in FP32.
-__global__ void __launch_bounds__(256)
-    combine_rows(const __nv_bfloat16* Y, int64_t R, const int* slot_row, const float* weights,
-                 const __nv_bfloat16* add, void* out, int out_f32, int64_t H, int k) {
+//
+// VEC: a thread sums 8 columns (16 bytes of each row), eight rows in flight. One pass
+// over the rows is all there is: the bytes of T x k rows bound it.
+struct CombineParams {
+    const __nv_bfloat16* Y;
+    const int* slot_row;
+    const float* weights;
+    const __nv_bfloat16* add;
+    void* out;
+    int64_t R, H;
+    int out_f32, k;
+    unsigned blocks;        // CTAs per token
+};
+
+template <bool VEC>
+__global__ void __launch_bounds__(256) combine_rows(const CombineParams p) {
+    constexpr int W = VEC ? 8 : 1, BATCH = 8;
     dg::grid_dependency_wait();
     if (threadIdx.x == 0) dg::grid_launch_dependents();
-    const int64_t t = blockIdx.x;
-    for (int64_t h = blockIdx.y * 256 + threadIdx.x; h < H; h += gridDim.y * 256) {
-        float acc = 0.0f;
-        for (int j = 0; j < k; ++j) {
-            const int r = slot_row[t * k + j];
-            if (r >= 0 && r < R) acc = fmaf(weights[t * k + j], __bfloat162float(Y[r * H + h]), acc);
+    const int64_t t = blockIdx.x / p.blocks;
+    const int64_t h = (static_cast<int64_t>(blockIdx.x % p.blocks) * 256 + threadIdx.x) * W;
+    if (h >= p.H) return;
+    const int* slots = p.slot_row + t * p.k;
+    const float* weights = p.weights + t * p.k;
+    float acc[W];
+    uint4 a = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < W; ++i) acc[i] = 0.0f;
+    if constexpr (VEC)
+        if (p.add) a = *reinterpret_cast<const uint4*>(p.add + t * p.H + h);
+    for (int j0 = 0; j0 < p.k; j0 += BATCH) {
+        int row[BATCH];
+        float w[BATCH];
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+            row[j] = j0 + j < p.k ? __ldg(slots + j0 + j) : -1;
+            w[j] = j0 + j < p.k ? __ldg(weights + j0 + j) : 0.0f;
         }
-        if (add) acc += __bfloat162float(add[t * H + h]);
-        if (out_f32)
-            static_cast<float*>(out)[t * H + h] = acc;
-        else
-            static_cast<__nv_bfloat16*>(out)[t * H + h] = __float2bfloat16_rn(acc);
+        uint4 y[BATCH];
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+            y[j] = make_uint4(0, 0, 0, 0);
+            if (row[j] >= 0 && row[j] < p.R) {
+                const __nv_bfloat16* src = p.Y + row[j] * p.H + h;
+                if constexpr (VEC) y[j] = __ldcs(reinterpret_cast<const uint4*>(src));
+                else y[j].x = __bfloat16_as_ushort(*src);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < BATCH; ++j) {
+            if (row[j] < 0 || row[j] >= p.R) continue;       // adds nothing, whatever its weight
+            const uint32_t u[4] = {y[j].x, y[j].y, y[j].z, y[j].w};
+#pragma unroll
+            for (int i = 0; i < W; ++i) acc[i] = fmaf(w[j], (i & 1) ? dg::bf16_hi(u[i / 2]) : dg::bf16_lo(u[i / 2]), acc[i]);
+        }
+    }
+    const int64_t at = t * p.H + h;
+    if constexpr (VEC) {
+        if (p.add) {
+            const uint32_t u[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int i = 0; i < W; ++i) acc[i] += (i & 1) ? dg::bf16_hi(u[i / 2]) : dg::bf16_lo(u[i / 2]);
+        }
+        if (p.out_f32) {
+            float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at);
+            o[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            o[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        } else {
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at) =
+                make_uint4(dg::pack_bf16x2(acc[0], acc[1]), dg::pack_bf16x2(acc[2], acc[3]),
+                           dg::pack_bf16x2(acc[4], acc[5]), dg::pack_bf16x2(acc[6], acc[7]));
+        }
+    } else {
+        if (p.add) acc[0] += __bfloat162float(p.add[at]);
+        if (p.out_f32) static_cast<float*>(p.out)[at] = acc[0];
+        else static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(acc[0]);
     }
 }
 
 // ---------------------------------------------------------------- int8 codes
 
-// The code of x for scale s: x / s to the nearest integer, ties to even; NaN 0.
-__device__ __forceinline__ int8_t int8_code(float x, float s) {
-    const float q = rintf(__fdiv_rn(x, s));
-    return x != x ? 0 : static_cast<int8_t>(fminf(fmaxf(q, -127.0f), 127.0f));
+// The code of x for scale s: x / s to the nearest integer, ties to even; NaN 0. The
+// product with 1 / s is within 2^-15 of the quotient (|quotient| <= 127), so only
+// quotients that near a half are divided.
+__device__ __forceinline__ int int8_code(float x, float s, float inv) {
+    const float t = x * inv;
+    float q = rintf(t);
+    if (!(fabsf(t - q) < 0.4999f)) q = rintf(__fdiv_rn(x, s));   // (and what is not finite)
+    return x != x ? 0 : static_cast<int>(fminf(fmaxf(q, -127.0f), 127.0f));
 }
 
-// One CTA per row: maximum of the finite magnitudes, then the codes.
-__global__ void __launch_bounds__(512) quantize_rows(const void* X, int f32, int8_t* q, float* scale, int64_t K) {
-    __shared__ unsigned part[16];
-    dg::grid_dependency_wait();
-    if (threadIdx.x == 0) dg::grid_launch_dependents();
-    const int64_t at = static_cast<int64_t>(blockIdx.x) * K;
-    unsigned m = 0;                       // magnitudes order as their bits
-    for (int64_t i = threadIdx.x; i < K; i += blockDim.x) {
-        const unsigned u = __float_as_uint(load1(X, f32, at + i)) & 0x7FFFFFFFu;
-        if (u < 0x7F800000u) m = max(m, u);
-    }
+__device__ __forceinline__ unsigned finite_magnitude(float x) {   // magnitudes order as their bits
+    const unsigned u = __float_as_uint(x) & 0x7FFFFFFFu;
+    return u < 0x7F800000u ? u : 0u;
+}
+
+// The row's scale from every thread's maximum; all threads of the CTA take part.
+__device__ __forceinline__ float row_scale(unsigned m, float* scale) {
+    __shared__ unsigned part[32];
     m = __reduce_max_sync(0xffffffffu, m);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
     __syncthreads();
-    for (int w = 0; w < 16; ++w) m = max(m, part[w]);
+    for (unsigned w = 0; w < blockDim.x / 32; ++w) m = max(m, part[w]);
     float s = __fdiv_rn(__uint_as_float(m), 127.0f);
     if (s == 0.0f) s = 1.0f;              // a row of zeros (or one whose scale underflows)
-    if (threadIdx.x == 0) scale[blockIdx.x] = s;
-    for (int64_t i = threadIdx.x; i < K; i += blockDim.x) q[at + i] = int8_code(load1(X, f32, at + i), s);
+    if (threadIdx.x == 0) *scale = s;
+    return s;
+}
+
+// One CTA per row of up to 8 x CHUNKS x blockDim values, held in registers between the
+// maximum and the codes: the row is read once.
+template <bool F32, int CHUNKS>
+__global__ void __launch_bounds__(256) quantize_held(const void* X, int8_t* q, float* scale, int K) {
+    dg::grid_dependency_wait();
+    if (threadIdx.x == 0) dg::grid_launch_dependents();
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * K;
+    float x[CHUNKS][8];
+    unsigned m = 0;
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) {
+        const int k = (c * blockDim.x + threadIdx.x) * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[c][i] = 0.0f;
+        if (k < K) {
+            if constexpr (F32) {
+                const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(X) + at + k);
+                const float4 a = src[0], b = src[1];
+                x[c][0] = a.x, x[c][1] = a.y, x[c][2] = a.z, x[c][3] = a.w;
+                x[c][4] = b.x, x[c][5] = b.y, x[c][6] = b.z, x[c][7] = b.w;
+            } else {
+                const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(X) + at + k);
+                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[c][i] = (i & 1) ? dg::bf16_hi(u[i / 2]) : dg::bf16_lo(u[i / 2]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, finite_magnitude(x[c][i]));
+    }
+    const float s = row_scale(m, scale + blockIdx.x), inv = __frcp_rn(s);
+#pragma unroll
+    for (int c = 0; c < CHUNKS; ++c) {
+        const int k = (c * blockDim.x + threadIdx.x) * 8;
+        if (k >= K) continue;
+        uint32_t w[2] = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i / 4] |= (int8_code(x[c][i], s, inv) & 0xFFu) << (8 * (i % 4));
+        *reinterpret_cast<uint2*>(q + at + k) = make_uint2(w[0], w[1]);
+    }
+}
+
+// Rows of any length and alignment, read twice.
+__global__ void __launch_bounds__(512) quantize_rows(const void* X, int f32, int8_t* q, float* scale, int64_t K) {
+    dg::grid_dependency_wait();
+    if (threadIdx.x == 0) dg::grid_launch_dependents();
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * K;
+    unsigned m = 0;
+    for (int64_t i = threadIdx.x; i < K; i += blockDim.x) m = max(m, finite_magnitude(load1(X, f32, at + i)));
+    const float s = row_scale(m, scale + blockIdx.x), inv = __frcp_rn(s);
+    for (int64_t i = threadIdx.x; i < K; i += blockDim.x) q[at + i] = static_cast<int8_t>(int8_code(load1(X, f32, at + i), s, inv));
+}
+
+template <bool F32>
+cudaError_t launch_held(const void* X, int8_t* q, float* scale, int64_t M, int K, cudaStream_t s) {
+    dg::host::Launch l(static_cast<unsigned>(M), 1, 256, 0, s);
+    if (K <= 2048) return cudaLaunchKernelEx(&l.cfg, quantize_held<F32, 1>, X, q, scale, K);
+    if (K <= 4096) return cudaLaunchKernelEx(&l.cfg, quantize_held<F32, 2>, X, q, scale, K);
+    return cudaLaunchKernelEx(&l.cfg, quantize_held<F32, 4>, X, q, scale, K);
 }
 
 }  // namespace
@@ -81,10 +202,14 @@ extern "C" dgemm_status_t dgemm_combine(const void* Y, int64_t R, const int32_t*
     dg::host::Device dev;
     const dgemm_status_t ds = dg::host::current_device(&dev);
     if (ds != DGEMM_OK) return ds;
-    dg::host::Launch l(static_cast<unsigned>(T), 1, 256, 0, reinterpret_cast<cudaStream_t>(stream));
+    CombineParams p{static_cast<const __nv_bfloat16*>(Y), slot_row, weights, static_cast<const __nv_bfloat16*>(add), out,
+                    R, H, out_dtype == DGEMM_F32 ? 1 : 0, k, 0};
+    const bool vec = H % 8 == 0;       // rows on 16 bytes
+    p.blocks = static_cast<unsigned>((H / (vec ? 8 : 1) + 255) / 256);
+    if (T * p.blocks > INT32_MAX) return DGEMM_ERR_NOT_SUPPORTED;
+    dg::host::Launch l(static_cast<unsigned>(T * p.blocks), 1, 256, 0, reinterpret_cast<cudaStream_t>(stream));
     const cudaError_t e =
-        cudaLaunchKernelEx(&l.cfg, combine_rows, static_cast<const __nv_bfloat16*>(Y), R, static_cast<const int*>(slot_row),
-                           weights, static_cast<const __nv_bfloat16*>(add), out, out_dtype == DGEMM_F32 ? 1 : 0, H, k);
+        vec ? cudaLaunchKernelEx(&l.cfg, combine_rows<true>, p) : cudaLaunchKernelEx(&l.cfg, combine_rows<false>, p);
     return e == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
 }
 
@@ -100,7 +225,14 @@ extern "C" dgemm_status_t dgemm_int8_quantize(const void* X, dgemm_dtype_t x_dty
     dg::host::Device dev;
     const dgemm_status_t ds = dg::host::current_device(&dev);
     if (ds != DGEMM_OK) return ds;
-    dg::host::Launch l(static_cast<unsigned>(M), 1, 512, 0, reinterpret_cast<cudaStream_t>(stream));
-    const cudaError_t e = cudaLaunchKernelEx(&l.cfg, quantize_rows, X, x_dtype == DGEMM_F32 ? 1 : 0, q, scale, K);
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (K % 8 == 0 && K > 0 && K <= 8192) {
+        e = x_dtype == DGEMM_F32 ? launch_held<true>(X, q, scale, M, static_cast<int>(K), st)
+                                 : launch_held<false>(X, q, scale, M, static_cast<int>(K), st);
+    } else {
+        dg::host::Launch l(static_cast<unsigned>(M), 1, 512, 0, st);
+        e = cudaLaunchKernelEx(&l.cfg, quantize_rows, X, x_dtype == DGEMM_F32 ? 1 : 0, q, scale, K);
+    }
     return e == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
 }
