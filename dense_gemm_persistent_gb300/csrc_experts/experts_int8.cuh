@@ -12,11 +12,12 @@
 // Warps of a CTA:
 //   0       TMA producer of weight codes: 128 channels x 128 K, 128B swizzle
 //   1       MMA issuer (one thread), owner of the Tensor Memory
-//   2-3     idle (they complete the first warpgroup)
+//   2-3     token copiers: rows by index or in order with cp.async
 //   4-7     epilogue
 //   8-11    weight converters: one channel a thread, 128 codes a stage
-//   12-15   token converters: each thread copies (cp.async, a few stages ahead) and
-//           converts its own 16-code chunks, so only the converted stage is shared
+//   12-15   token converters
+// (Copying in the converting threads was slower: their fence before each hand-over
+// waits for the copies that they have in flight, 1.15 us a stage.)
 #pragma once
 
 #include "experts_common.cuh"
@@ -37,17 +38,17 @@ struct Int8Cfg {
     static constexpr int SLICE_X = BN_CTA * 128;         // 64 FP16 of K
     static constexpr int X_CONV = 2 * SLICE_X, CONV_STAGES = 2;
     static constexpr int A_COLS = KB / 2;                // TMEM columns of a converted weight stage
-    static constexpr int EPI_WARPS = 4, EPI_WARP0 = 4, W_WARP0 = 8, X_WARP0 = 12;
+    static constexpr int COPY_WARP0 = 2, EPI_WARPS = 4, EPI_WARP0 = 4, W_WARP0 = 8, X_WARP0 = 12;
     static constexpr int THREADS = 512;
     static constexpr int ACC_COLS = 2 * BN;
     static constexpr int TMEM_COLS = ACC_COLS + CONV_STAGES * A_COLS <= 256 ? 256 : 512;
-    static constexpr int BAR_BYTES = 256;
+    static constexpr int BAR_BYTES = 384;
     static constexpr int BUFFERS = W_STAGES * W_RAW + CONV_STAGES * X_CONV + X_STAGES * X_RAW;
     static constexpr int FIXED = 1024 + BUFFERS + exchange_bytes<EPI_WARPS>() + BAR_BYTES;
     static constexpr uint32_t IDESC0 = make_idesc(0u, false, false, 128 * CTAS, 0);   // FP16 operands
     static_assert(ACC_COLS + CONV_STAGES * A_COLS <= 512, "Tensor Memory");
     static_assert(FIXED + Schedule::bytes(DGEMM_MAX_EXPERTS) <= 232448, "shared memory");
-    static_assert((2 * W_STAGES + 2 * CONV_STAGES + 5) * 8 + 8 <= BAR_BYTES, "barriers fit");
+    static_assert((2 * W_STAGES + 2 * X_STAGES + 2 * CONV_STAGES + 5) * 8 + 8 <= BAR_BYTES, "barriers fit");
 };
 
 // Four int8 codes to four FP16 numbers.
@@ -67,7 +68,9 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
     float* exchange = reinterpret_cast<float*>(wraw + CF::BUFFERS);
     uint64_t* w_full = reinterpret_cast<uint64_t*>(wraw + CF::BUFFERS + exchange_bytes<CF::EPI_WARPS>());
     uint64_t* w_empty = w_full + CF::W_STAGES;
-    uint64_t* full = w_empty + CF::W_STAGES;             // converted stages
+    uint64_t* x_full = w_empty + CF::W_STAGES;
+    uint64_t* x_empty = x_full + CF::X_STAGES;
+    uint64_t* full = x_empty + CF::X_STAGES;             // converted stages
     uint64_t* empty = full + CF::CONV_STAGES;
     uint64_t* acc_full = empty + CF::CONV_STAGES;
     uint64_t* acc_empty = acc_full + 2;
@@ -85,6 +88,10 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
         for (int s = 0; s < CF::W_STAGES; ++s) {
             mbar_init(&w_full[s], 1);
             mbar_init(&w_empty[s], 4);                   // every weight converter warp
+        }
+        for (int s = 0; s < CF::X_STAGES; ++s) {
+            mbar_init(&x_full[s], 64);                   // every copier's own copies
+            mbar_init(&x_empty[s], 4);                   // every token converter warp
         }
         for (int s = 0; s < CF::CONV_STAGES; ++s) {
             mbar_init(&full[s], 8 * CF::CTAS);           // every converter warp of the pair
@@ -209,6 +216,50 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
             if (!mbar_wait(drain, 0, nullptr, p.wait_ns)) fail(p, ERR_TIMEOUT_DRAIN, abort_flag);
         }
         __syncwarp();
+    } else if (warp >= CF::COPY_WARP0 && warp < CF::EPI_WARP0) {
+        // ---------------------------------------------------------------- token copiers
+        // Eight lanes copy one row's 128 codes; a thread's copies arrive by themselves.
+        constexpr int ROUNDS = CF::BN_CTA / 8;
+        const int sub = (threadIdx.x - CF::COPY_WARP0 * 32) >> 3, chunk = lane & 7;
+        uint32_t stage = 0, phase = 0;
+        for (int item = unit; ok && cur.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, t); item += units) {
+            const int xrows = t.n / CF::CTAS, first = static_cast<int>(rank) * xrows, rounds = xrows / 8;
+            int src[ROUNDS];
+#pragma unroll
+            for (int i = 0; i < ROUNDS; ++i) {
+                const int r = first + i * 8 + sub;
+                src[i] = -1;
+                if (i < rounds && r < t.rows) {
+                    const int a = p.a_rows ? __ldg(p.a_rows + t.row0 + r) : t.row0 + r;
+                    if (a >= 0 && a < p.a_count) src[i] = a;
+                }
+            }
+            for (int kb = 0; kb < p.kstages; ++kb) {
+                if (!mbar_wait_warp(&x_empty[stage], phase ^ 1, abort_flag, p.wait_ns)) {
+                    ok = false;
+                    break;
+                }
+                const int k = kb * CF::KB + chunk * 16;
+                const char* base = static_cast<const char*>(p.A) + k;
+                uint8_t* dst = xraw + stage * CF::X_RAW + sub * 128 + chunk * 16;
+#pragma unroll
+                for (int i = 0; i < ROUNDS; ++i) {
+                    if (i >= rounds) break;
+                    const bool read = k < p.K && src[i] >= 0;
+                    cp_async_16(dst + i * 1024, read ? base + static_cast<int64_t>(src[i]) * p.K : static_cast<const char*>(p.A),
+                                read ? 16u : 0u);
+                }
+                cp_async_mbar_arrive(&x_full[stage]);
+                if (++stage == CF::X_STAGES) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        cp_async_commit();
+        cp_async_wait<0>();      // nothing of this thread's is in flight when it leaves
+        if (!ok) fail(p, ERR_TIMEOUT_PRODUCER, abort_flag);
+        __syncwarp();
     } else if (warp >= CF::EPI_WARP0 && warp < CF::W_WARP0) {
         // ---------------------------------------------------------------- epilogue
         int local = 0;
@@ -276,87 +327,57 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
         __syncwarp();
     } else if (warp >= CF::X_WARP0) {
         // ---------------------------------------------------------------- token converters
-        // Chunk c (16 codes) of row r belongs to thread (8 r + c) % 128, which alone touches
-        // its copy. Stages are walked twice: the copies run X_STAGES - 1 stages ahead.
+        // Eight threads convert one row's 128 codes, 16 each.
         constexpr int ROUNDS = CF::BN_CTA / 16;
         const int tid = threadIdx.x - CF::X_WARP0 * 32, sub = tid >> 3, chunk = tid & 7;
-        Cursor ahead;
-        Tile ta;
-        int a_item = unit, a_kb = 0, a_slot = 0, slot = 0;
-        bool a_live = p.kstages > 0 && ahead.at<CF::BN, CF::CTAS>(p, sched, a_item, tile_channels, ta);
-        const char* src[ROUNDS];
-        auto point = [&]() {                                 // the rows of the tile that is copied from
-            const int xrows = ta.n / CF::CTAS, first = static_cast<int>(rank) * xrows;
-#pragma unroll
-            for (int i = 0; i < ROUNDS; ++i) {
-                const int r = first + i * 16 + sub;
-                src[i] = nullptr;
-                if (i * 16 + sub < xrows && r < ta.rows) {
-                    const int a = p.a_rows ? __ldg(p.a_rows + ta.row0 + r) : ta.row0 + r;
-                    if (a >= 0 && a < p.a_count) src[i] = static_cast<const char*>(p.A) + static_cast<int64_t>(a) * p.K;
-                }
-            }
-        };
-        auto copy_one = [&]() {                              // the copies of one stage (an empty group past the end)
-            if (a_live) {
-                if (a_kb == 0) point();
-                const int rounds = ta.n / CF::CTAS / 16;
-                const int k = a_kb * CF::KB + chunk * 16;
-#pragma unroll
-                for (int i = 0; i < ROUNDS; ++i) {
-                    if (i >= rounds) break;
-                    const bool read = k < p.K && src[i] != nullptr;
-                    cp_async_16(xraw + a_slot * CF::X_RAW + (i * 128 + tid) * 16,
-                                read ? src[i] + k : static_cast<const char*>(p.A), read ? 16u : 0u);
-                }
-                if (++a_kb == p.kstages) {
-                    a_kb = 0;
-                    a_item += units;
-                    a_live = ahead.at<CF::BN, CF::CTAS>(p, sched, a_item, tile_channels, ta);
-                }
-            }
-            if (++a_slot == CF::X_STAGES) a_slot = 0;
-            cp_async_commit();
-        };
-        for (int s = 0; s < CF::X_STAGES - 1; ++s) copy_one();
-        uint32_t stage = 0, phase = 0;
+        // a thread's 32 bytes of FP16 are two 16-byte chunks of one slice; threads of the second
+        // slice write theirs in the other order, so that the eight of a row meet different banks
+        const int j = (chunk & 3) * 2, flip = chunk >> 2;
+        const int at0 = (((j + flip) ^ (sub & 7)) << 4), at1 = (((j + 1 - flip) ^ (sub & 7)) << 4);
+        uint32_t raw = 0, raw_phase = 0, stage = 0, phase = 0;
         for (int item = unit; ok && cur.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, t); item += units) {
             const int rounds = t.n / CF::CTAS / 16;
             for (int kb = 0; kb < p.kstages; ++kb) {
-                copy_one();
-                cp_async_wait<CF::X_STAGES - 1>();           // this stage's copies (this thread's own) have landed
+                if (!mbar_wait_warp(&x_full[raw], raw_phase, abort_flag, p.wait_ns)) {
+                    ok = false;
+                    break;
+                }
+                uint4 codes[ROUNDS];
+#pragma unroll
+                for (int i = 0; i < ROUNDS; ++i)
+                    if (i < rounds)
+                        codes[i] = *reinterpret_cast<const uint4*>(xraw + raw * CF::X_RAW + (i * 16 + sub) * 128 + chunk * 16);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&x_empty[raw]);   // the codes are in registers
                 if (!mbar_wait_warp(&empty[stage], phase ^ 1, abort_flag, p.wait_ns)) {
                     ok = false;
                     break;
                 }
-                uint8_t* slice = xconv + stage * CF::X_CONV + (chunk >> 2) * CF::SLICE_X;
+                uint8_t* slice = xconv + stage * CF::X_CONV + (chunk >> 2) * CF::SLICE_X + sub * 128;
 #pragma unroll
                 for (int i = 0; i < ROUNDS; ++i) {
                     if (i >= rounds) break;
-                    const int row = i * 16 + sub;
-                    const uint4 c = *reinterpret_cast<const uint4*>(xraw + slot * CF::X_RAW + (i * 128 + tid) * 16);
                     uint4 lo, hi;
-                    int8x4_to_f16(c.x, lo.x, lo.y);
-                    int8x4_to_f16(c.y, lo.z, lo.w);
-                    int8x4_to_f16(c.z, hi.x, hi.y);
-                    int8x4_to_f16(c.w, hi.z, hi.w);
-                    // the two 16-byte chunks; threads of the second slice write theirs in the
-                    // other order, so that the eight of a row meet different banks
-                    const int j = (chunk & 3) * 2, flip = chunk >> 2;
-                    *reinterpret_cast<uint4*>(slice + row * 128 + (((j + flip) ^ (row & 7)) << 4)) = flip ? hi : lo;
-                    *reinterpret_cast<uint4*>(slice + row * 128 + (((j + 1 - flip) ^ (row & 7)) << 4)) = flip ? lo : hi;
+                    int8x4_to_f16(codes[i].x, lo.x, lo.y);
+                    int8x4_to_f16(codes[i].y, lo.z, lo.w);
+                    int8x4_to_f16(codes[i].z, hi.x, hi.y);
+                    int8x4_to_f16(codes[i].w, hi.z, hi.w);
+                    *reinterpret_cast<uint4*>(slice + i * 2048 + at0) = flip ? hi : lo;
+                    *reinterpret_cast<uint4*>(slice + i * 2048 + at1) = flip ? lo : hi;
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) converted(stage);
-                if (++slot == CF::X_STAGES) slot = 0;
+                if (++raw == CF::X_STAGES) {
+                    raw = 0;
+                    raw_phase ^= 1;
+                }
                 if (++stage == CF::CONV_STAGES) {
                     stage = 0;
                     phase ^= 1;
                 }
             }
         }
-        cp_async_wait<0>();
         if (!ok) fail(p, ERR_TIMEOUT_PRODUCER, abort_flag);
         __syncwarp();
     }

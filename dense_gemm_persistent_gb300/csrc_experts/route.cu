@@ -14,6 +14,9 @@
 // HBM and by the two passes over the chunk counts, a decoding call by its launch.
 #include <cuda_bf16.h>
 
+#include <algorithm>
+#include <cfloat>
+
 #include "dgemm_experts.h"
 #include "host.h"
 #include "ptx.cuh"
@@ -21,7 +24,6 @@
 namespace {
 
 constexpr int CHUNK = 64;       // tokens per chunk: one 64-bit mask per expert
-constexpr int WARPS = 16;       // warps per CTA
 
 struct RouteParams {
     const void* logits;
@@ -44,58 +46,84 @@ __device__ __forceinline__ float unordered(unsigned o) {
     return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
 }
 
-// One token by one warp: lane l holds entries l, l + 32, ... as ordered keys; 0 marks a
-// masked or chosen one.
-template <int VPL>
-__device__ __forceinline__ void route_token(const RouteParams& p, int t, int lane, int* sid) {
-    unsigned key[VPL];
+// One token by one warp: lane l holds entries l, l + 32, ... as order-preserving keys; 0
+// marks a masked or chosen one. Each round takes the warp's largest key. BF16: a
+// key is the value's 16 bits over the complement of the index, so keys differ and
+// one reduction names the winner. FP32: the value's 32 bits; a ballot names the
+// winner, and where several lanes hold that value the lowest index wins.
+template <int VPL, bool BF16>
+__device__ __forceinline__ void load_keys(const RouteParams& p, int t, int lane, unsigned (&key)[VPL]) {
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
         const int e = lane + 32 * i;
         key[i] = 0;
         if (e < p.E) {
             const int64_t at = static_cast<int64_t>(t) * p.E + e;
-            float x = p.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.logits)[at])
-                             : static_cast<const float*>(p.logits)[at];
+            const float x = BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.logits)[at])
+                                 : static_cast<const float*>(p.logits)[at];
             // masked: NaN and -inf; +inf counts as the largest finite number; -0 equals 0
-            if (x > -INFINITY) key[i] = ordered(fminf(x, 3.402823466e38f) + 0.0f);
+            if (x > -INFINITY) {
+                const unsigned o = ordered((BF16 ? x : fminf(x, FLT_MAX)) + 0.0f);
+                key[i] = BF16 ? (o & 0xFFFF0000u) | (0xFFFFu - static_cast<unsigned>(e)) : o;
+            }
         }
     }
-    unsigned best = 0;
+}
+
+template <bool BF16>
+__device__ __forceinline__ float key_value(unsigned key) {
+    // (a negative BF16's ordered bits are complemented, so its low half reads back as ones)
+    const unsigned o = BF16 ? (key & 0x80000000u ? key & 0xFFFF0000u : key | 0x0000FFFFu) : key;
+    return fminf(unordered(o), FLT_MAX);
+}
+
+template <int VPL, bool BF16>
+__device__ __forceinline__ void route_token(const RouteParams& p, int t, int lane, unsigned (&key)[VPL], int* sid) {
+    // this lane's largest key and, for FP32, its slot (the first of equals); no branches, so
+    // that a round costs little more than its reduction
+    unsigned best;
+    int best_i = 0;
+    auto scan = [&]() {
+        best = key[0];
+        best_i = 0;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) best = max(best, key[i]);
+        for (int i = 1; i < VPL; ++i) {
+            if (!BF16) best_i = key[i] > best ? i : best_i;
+            best = max(best, key[i]);
+        }
+    };
+    scan();
     const unsigned top = __reduce_max_sync(0xffffffffu, best);
-    const float xmax = unordered(top);
+    const float xmax = key_value<BF16>(top);
     float total = 0.0f;
     if (!p.renorm) {
 #pragma unroll
         for (int i = 0; i < VPL; ++i)
-            if (key[i]) total += expf(unordered(key[i]) - xmax);
+            if (key[i]) total += expf(key_value<BF16>(key[i]) - xmax);
         for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     }
     int my_id = -1;             // lane j keeps the j-th choice
-    float my_p = 0.0f;
+    unsigned my_key = 0;
     for (int j = 0; j < p.k; ++j) {
-        const unsigned m = __reduce_max_sync(0xffffffffu, best);
+        const unsigned m = j == 0 ? top : __reduce_max_sync(0xffffffffu, best);
         if (m == 0) break;      // nothing unmasked is left
-        unsigned at = 0xffffffffu;
-#pragma unroll
-        for (int i = VPL - 1; i >= 0; --i)
-            if (key[i] == m) at = static_cast<unsigned>(lane + 32 * i);
-        const unsigned e = __reduce_min_sync(0xffffffffu, at);
-        if (lane == j) {
-            my_id = static_cast<int>(e);
-            my_p = expf(unordered(m) - xmax);
+        int e;
+        if constexpr (BF16) {
+            e = static_cast<int>(0xFFFFu - (m & 0xFFFFu));
+        } else {
+            const unsigned who = __ballot_sync(0xffffffffu, best == m);
+            const int mine = lane + 32 * best_i;
+            e = (who & (who - 1)) == 0
+                    ? __shfl_sync(0xffffffffu, mine, __ffs(who) - 1)
+                    : static_cast<int>(__reduce_min_sync(0xffffffffu, best == m ? static_cast<unsigned>(mine) : 0xffffffffu));
         }
-        if (at == e) {
-            best = 0;
+        my_id = lane == j ? e : my_id;
+        my_key = lane == j ? m : my_key;
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                if (lane + 32 * i == static_cast<int>(e)) key[i] = 0;
-                best = max(best, key[i]);
-            }
-        }
+        for (int i = 0; i < VPL; ++i) key[i] = (BF16 ? key[i] == m : lane + 32 * i == e) ? 0 : key[i];
+        scan();
     }
+    float my_p = my_id >= 0 ? expf(key_value<BF16>(my_key) - xmax) : 0.0f;
     if (p.renorm) {
         total = my_p;
         for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
@@ -138,38 +166,23 @@ __device__ __forceinline__ int scan_experts(int* total, int E) {
     return all;
 }
 
-// Places the pairs of one chunk: base[e] is the first row of expert e, before[e] (null: none)
-// the pairs with e in earlier chunks, mask[e] the chunk's tokens with e.
-__device__ __forceinline__ void place_chunk(const RouteParams& p, int t0, int n, const unsigned long long* mask,
-                                            const int* base, const int* before, int all) {
-    for (int i = threadIdx.x; i < n * p.k; i += blockDim.x) {
-        const int64_t at = static_cast<int64_t>(t0) * p.k + i;
-        const int e = p.ids[at], tok = i / p.k;
-        int row = -1;
-        if (e >= 0) {
-            row = base[e] + (before ? before[e] : 0) + __popcll(mask[e] & ((1ull << tok) - 1));
-            p.row_token[row] = t0 + tok;
-        }
-        p.slot_row[at] = row;
-        if (at >= all) p.row_token[at] = -1;
-    }
-}
-
 // Selects the experts of one chunk of tokens and counts them. A call of one chunk is
 // placed here as well: one launch.
-template <int VPL>
-__global__ void __launch_bounds__(32 * WARPS) route_select(const RouteParams p) {
+template <int VPL, bool BF16>
+__global__ void __launch_bounds__(VPL <= 8 ? 1024 : 512, VPL <= 8 ? 2 : 1) route_select(const RouteParams p) {
     extern __shared__ unsigned long long mask[];            // [E]
     int* total = reinterpret_cast<int*>(mask + p.E);        // [E] (one chunk)
     int* sid = total + p.E;                                 // [CHUNK][k]
     dg::grid_dependency_wait();
     if (threadIdx.x == 0) dg::grid_launch_dependents();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int t0 = blockIdx.x * CHUNK, n = min(CHUNK, p.T - t0);
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) mask[e] = 0;
     __syncthreads();
-    for (int i = warp; i < n; i += WARPS) {
-        route_token<VPL>(p, t0 + i, lane, sid + i * p.k);
+    for (int i = warp; i < n; i += warps) {
+        unsigned key[VPL];
+        load_keys<VPL, BF16>(p, t0 + i, lane, key);
+        route_token<VPL, BF16>(p, t0 + i, lane, key, sid + i * p.k);
         __syncwarp();
         if (lane < p.k && sid[i * p.k + lane] >= 0) atomicOr(&mask[sid[i * p.k + lane]], 1ull << i);
     }
@@ -185,27 +198,47 @@ __global__ void __launch_bounds__(32 * WARPS) route_select(const RouteParams p) 
     const int all = scan_experts(total, p.E);
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) p.offsets[e] = total[e];
     if (threadIdx.x == 0) p.offsets[p.E] = all;
-    place_chunk(p, t0, n, mask, total, nullptr, all);
+    for (int i = threadIdx.x; i < n * p.k; i += blockDim.x) {
+        const int e = sid[i], tok = i / p.k;
+        int row = -1;
+        if (e >= 0) {
+            row = total[e] + __popcll(mask[e] & ((1ull << tok) - 1));
+            p.row_token[row] = tok;
+        }
+        p.slot_row[i] = row;
+        if (i >= all) p.row_token[i] = -1;
+    }
 }
 
 // Rows of one chunk's pairs: every CTA sums the counts of the chunks before its own
-// and of all chunks (four experts a load, all loads of a thread in flight together),
-// scans the totals over the experts, and places its pairs.
-__global__ void __launch_bounds__(1024) route_place(const RouteParams p) {
-    extern __shared__ unsigned long long mask[];            // [E]
-    int* before = reinterpret_cast<int*>(mask + p.E);       // [pitch] pairs of e in earlier chunks
-    int* base = before + p.pitch;                           // [pitch] first row of e
+// and of all chunks (four experts a load, a thread's loads in flight together), scans
+// the totals over the experts, and places its pairs.
+constexpr int PLACE_THREADS = 1024;
+constexpr int PLACE_PAIRS = CHUNK * DGEMM_MAX_TOPK / PLACE_THREADS;   // pairs of one thread, at most
+
+// Threads that share a quad of experts.
+__host__ __device__ inline int place_parts(int pitch) {
+    const int n = PLACE_THREADS / (pitch / 4);
+    return n < 1 ? 1 : n > 32 ? 32 : n;
+}
+
+__global__ void __launch_bounds__(PLACE_THREADS, 2) route_place(const RouteParams p) {
+    extern __shared__ unsigned long long mask[];            // [pitch]
+    int* before = reinterpret_cast<int*>(mask + p.pitch);   // [parts][pitch] pairs of e in earlier chunks
+    const int quads = p.pitch / 4, parts = place_parts(p.pitch);
+    int* base = before + parts * p.pitch;                   // [parts][pitch] pairs of e; then first row of e
     dg::grid_dependency_wait();
     if (threadIdx.x == 0) dg::grid_launch_dependents();
-    for (int e = threadIdx.x; e < p.pitch; e += blockDim.x) {
-        if (e < p.E) mask[e] = 0;
-        before[e] = 0;
-        base[e] = 0;
-    }
-    __syncthreads();
-    const int quads = p.pitch / 4, parts = max(1, static_cast<int>(blockDim.x) / quads);
-    const int quad = threadIdx.x % quads, part = threadIdx.x / quads;
     const int mine = static_cast<int>(blockIdx.x);
+    const int t0 = mine * CHUNK, pairs = min(CHUNK, p.T - t0) * p.k;
+    int id[PLACE_PAIRS];
+#pragma unroll
+    for (int i = 0; i < PLACE_PAIRS; ++i) {
+        const int at = threadIdx.x + i * PLACE_THREADS;
+        id[i] = at < pairs ? p.ids[static_cast<int64_t>(t0) * p.k + at] : -1;
+    }
+    for (int e = threadIdx.x; e < p.E; e += PLACE_THREADS) mask[e] = 0;
+    const int quad = threadIdx.x % quads, part = threadIdx.x / quads;
     if (part < parts) {
         int sum[4] = {0, 0, 0, 0}, pre[4] = {0, 0, 0, 0};
 #pragma unroll 8
@@ -218,24 +251,42 @@ __global__ void __launch_bounds__(1024) route_place(const RouteParams p) {
                 if (c < mine) pre[i] += x;
             }
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (sum[i]) atomicAdd(&base[quad * 4 + i], sum[i]);     // integers: any order
-            if (pre[i]) atomicAdd(&before[quad * 4 + i], pre[i]);
-        }
+        *reinterpret_cast<int4*>(base + part * p.pitch + quad * 4) = make_int4(sum[0], sum[1], sum[2], sum[3]);
+        *reinterpret_cast<int4*>(before + part * p.pitch + quad * 4) = make_int4(pre[0], pre[1], pre[2], pre[3]);
     }
-    const int t0 = blockIdx.x * CHUNK, n = min(CHUNK, p.T - t0);
-    for (int i = threadIdx.x; i < n * p.k; i += blockDim.x) {
-        const int e = p.ids[static_cast<int64_t>(t0) * p.k + i];
-        if (e >= 0) atomicOr(&mask[e], 1ull << (i / p.k));
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < PLACE_PAIRS; ++i)
+        if (id[i] >= 0) atomicOr(&mask[id[i]], 1ull << ((threadIdx.x + i * PLACE_THREADS) / p.k));
+    for (int e = threadIdx.x; e < p.E; e += PLACE_THREADS) {
+        int s = base[e], b = before[e];
+        for (int q = 1; q < parts; ++q) {
+            s += base[q * p.pitch + e];
+            b += before[q * p.pitch + e];
+        }
+        base[e] = s;
+        before[e] = b;
     }
     __syncthreads();
     const int all = scan_experts(base, p.E);
-    if (blockIdx.x == 0) {
-        for (int e = threadIdx.x; e < p.E; e += blockDim.x) p.offsets[e] = base[e];
+    if (mine == 0) {
+        for (int e = threadIdx.x; e < p.E; e += PLACE_THREADS) p.offsets[e] = base[e];
         if (threadIdx.x == 0) p.offsets[p.E] = all;
     }
-    place_chunk(p, t0, n, mask, base, before, all);
+#pragma unroll
+    for (int i = 0; i < PLACE_PAIRS; ++i) {
+        const int pair = threadIdx.x + i * PLACE_THREADS;
+        if (pair >= pairs) continue;
+        const int64_t at = static_cast<int64_t>(t0) * p.k + pair;
+        const int e = id[i], tok = pair / p.k;
+        int row = -1;
+        if (e >= 0) {
+            row = base[e] + before[e] + __popcll(mask[e] & ((1ull << tok) - 1));
+            p.row_token[row] = t0 + tok;
+        }
+        p.slot_row[at] = row;
+        if (at >= all) p.row_token[at] = -1;
+    }
 }
 
 dgemm_status_t route_sizes(int64_t T, int64_t E, int k) {
@@ -247,8 +298,12 @@ dgemm_status_t route_sizes(int64_t T, int64_t E, int k) {
 
 template <int VPL>
 cudaError_t launch_select(const RouteParams& p, cudaStream_t s) {
-    dg::host::Launch l(static_cast<unsigned>(p.chunks), 1, 32 * WARPS, static_cast<size_t>(p.E) * 12 + CHUNK * p.k * 4, s);
-    return cudaLaunchKernelEx(&l.cfg, route_select<VPL>, p);
+    // a warp per token as far as registers allow (two CTAs an SM up to 256 experts), and
+    // threads enough for the per-expert steps
+    const int most = VPL <= 8 ? 32 : 16, warps = std::max(std::min(most, p.T), std::min(most, (p.E + 31) / 32));
+    dg::host::Launch l(static_cast<unsigned>(p.chunks), 1, 32u * warps, static_cast<size_t>(p.E) * 12 + CHUNK * p.k * 4, s);
+    return p.bf16 ? cudaLaunchKernelEx(&l.cfg, route_select<VPL, true>, p)
+                  : cudaLaunchKernelEx(&l.cfg, route_select<VPL, false>, p);
 }
 
 }  // namespace
@@ -302,6 +357,7 @@ extern "C" dgemm_status_t dgemm_route(const void* logits, dgemm_dtype_t logits_d
     else e = launch_select<32>(p, s);
     if (e != cudaSuccess) return DGEMM_ERR_CUDA;
     if (p.chunks == 1) return DGEMM_OK;
-    dg::host::Launch l(static_cast<unsigned>(p.chunks), 1, 1024, static_cast<size_t>(p.pitch) * 16, s);
+    const size_t parts = static_cast<size_t>(place_parts(p.pitch));
+    dg::host::Launch l(static_cast<unsigned>(p.chunks), 1, PLACE_THREADS, static_cast<size_t>(p.E) * 8 + parts * p.pitch * 8, s);
     return cudaLaunchKernelEx(&l.cfg, route_place, p) == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
 }

@@ -447,3 +447,12 @@ def test_int8_in_place_and_no_depth():
     D = C.to(dev())
     dg.dgemm_int8_scaled(A[:, :0].contiguous().to(dev()), B[:, :0].contiguous().to(dev()), one(50), one(70), D, C=D, beta=0.5)
     assert torch.equal(D.cpu(), 0.5 * C)
+
+
+def test_route_bf16_infinity_beside_the_largest_number():
+    """+inf is read as the largest FP32 number, above the largest BF16 one."""
+    x = torch.zeros(70, 9)
+    x[:, 2] = 3.3895313892515355e38
+    x[:, 6] = float("inf")
+    run_route(x, 3, True, BF)
+    run_route(x, 3, False, BF)
