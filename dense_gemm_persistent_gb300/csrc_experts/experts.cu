@@ -164,6 +164,10 @@ dgemm_status_t launch(const Call& c, const dg::host::Device& dev) {
         if (cudaFuncSetAttribute(v->func, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(v->smem_fixed + dg::experts::Schedule::bytes(DGEMM_MAX_EXPERTS))) != cudaSuccess)
             return DGEMM_ERR_CUDA;
+        // a register split that adds up to more than the launch holds would wait forever
+        cudaFuncAttributes fa{};
+        if (v->launch_regs > 0 && (cudaFuncGetAttributes(&fa, v->func) != cudaSuccess || fa.numRegs < v->launch_regs))
+            return DGEMM_ERR_CUDA;
         flag.store(1, std::memory_order_release);
     }
     return v->launch(w, x, xs, p, units * v->ctas, smem, c.stream) == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;

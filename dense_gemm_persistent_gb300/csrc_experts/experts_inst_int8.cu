@@ -17,7 +17,7 @@ cudaError_t launch_int8(const CUtensorMap& w, const CUtensorMap&, const CUtensor
 
 template <class CF>
 Variant make_int8() {
-    return Variant{DGEMM_GROUPED_INT8, 0, CF::PAIR, -1, CF::BN, CF::BN_CTA, CF::CTAS, 1, 0, CF::THREADS, CF::FIXED,
+    return Variant{DGEMM_GROUPED_INT8, 0, CF::PAIR, -1, CF::BN, CF::BN_CTA, CF::CTAS, 1, 0, CF::THREADS, CF::LAUNCH_REGS, CF::FIXED,
                    reinterpret_cast<const void*>(&expert_int8<CF>), &launch_int8<CF>};
 }
 

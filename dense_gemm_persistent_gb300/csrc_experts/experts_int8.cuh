@@ -6,18 +6,20 @@
 // with u = b + 128 (a flipped sign bit), the bits 0x6400 | u are 1024 + u, less 1152.
 //
 // The weights are the MMA's A operand and go from shared memory through
-// registers into Tensor Memory, the token rows are its B operand and go back
-// to shared memory. (Both through shared memory would move 192 bytes a clock through
-// a unit that moves 128: raw in and out, converted in, and the MMA's reads.)
+// registers into Tensor Memory; the token rows are its B operand and go from global
+// memory through registers to shared memory. What bounds a prompt is shared memory's 128
+// bytes a clock: a stage of 128 K and 192 rows moves 80 KB through it (weights in and out,
+// rows in, the MMA's reads) in the 768 clocks that the tensor core needs; with the weights
+// converted back into shared memory it would be 112 KB, with raw rows staged there 104 KB.
 // Warps of a CTA:
 //   0       TMA producer of weight codes: 128 channels x 128 K, 128B swizzle
 //   1       MMA issuer (one thread), owner of the Tensor Memory
-//   2-3     token copiers: rows by index or in order with cp.async
+//   2-3     idle (they complete the first warpgroup)
 //   4-7     epilogue
-//   8-11    weight converters: one channel a thread, 128 codes a stage
-//   12-15   token converters
-// (Copying in the converting threads was slower: their fence before each hand-over
-// waits for the copies that they have in flight, 1.15 us a stage.)
+//   8-15    weight converters, two teams: one channel a thread, 128 codes a stage
+//   16-23   token converters, two teams: rows by index or in order
+// The teams take alternate stages: a stage passes through a chain of waits and
+// conversions that is longer than the tensor core takes for it.
 #pragma once
 
 #include "experts_common.cuh"
@@ -33,22 +35,32 @@ struct Int8Cfg {
     static constexpr int BN = PAIR ? 192 : 64;           // most token rows of a tile
     static constexpr int BN_CTA = BN / CTAS;
     static constexpr int KB = 128;                       // codes of K per stage
-    static constexpr int W_RAW = 128 * KB, W_STAGES = PAIR ? 4 : 8;
-    static constexpr int X_RAW = BN_CTA * KB, X_STAGES = 4;
+    static constexpr int W_RAW = 128 * KB, W_STAGES = PAIR ? 5 : 8;
     static constexpr int SLICE_X = BN_CTA * 128;         // 64 FP16 of K
-    static constexpr int X_CONV = 2 * SLICE_X, CONV_STAGES = 2;
+    static constexpr int X_CONV = 2 * SLICE_X;
+    static constexpr int A_STAGES = 2, C_STAGES = 3;     // converted weights (Tensor Memory), converted rows
+    // Converted stage g counts on barriers g % STAGE_BARS, whatever slots it lies in: full by both
+    // converters, done by the MMAs (one commit: a second one cost ~250 clocks a stage).
+    // The weights' slot is free when stage g - A_STAGES is done, the rows' when g - C_STAGES
+    // is; each barrier's next completion needs stage g, so no phase can be missed.
+    static constexpr int STAGE_BARS = 4;
+    static_assert(A_STAGES < STAGE_BARS && C_STAGES < STAGE_BARS, "stage barriers");
     static constexpr int A_COLS = KB / 2;                // TMEM columns of a converted weight stage
-    static constexpr int COPY_WARP0 = 2, EPI_WARPS = 4, EPI_WARP0 = 4, W_WARP0 = 8, X_WARP0 = 12;
-    static constexpr int THREADS = 512;
+    static constexpr int EPI_WARPS = 4, EPI_WARP0 = 4, W_WARP0 = 8, X_WARP0 = 16, TEAMS = 2;
+    static constexpr int THREADS = 768;
+    // registers per thread: at launch, and of the warpgroups after the split
+    static constexpr int LAUNCH_REGS = 80, REGS_CONTROL = 48, REGS_EPILOGUE = 128, REGS_WEIGHTS = 72, REGS_TOKENS = 80;
+    static_assert(REGS_CONTROL + REGS_EPILOGUE + TEAMS * (REGS_WEIGHTS + REGS_TOKENS) <= THREADS / 128 * LAUNCH_REGS,
+                  "register split exceeds the launch allocation");
     static constexpr int ACC_COLS = 2 * BN;
-    static constexpr int TMEM_COLS = ACC_COLS + CONV_STAGES * A_COLS <= 256 ? 256 : 512;
+    static constexpr int TMEM_COLS = ACC_COLS + A_STAGES * A_COLS <= 256 ? 256 : 512;
     static constexpr int BAR_BYTES = 384;
-    static constexpr int BUFFERS = W_STAGES * W_RAW + CONV_STAGES * X_CONV + X_STAGES * X_RAW;
+    static constexpr int BUFFERS = W_STAGES * W_RAW + C_STAGES * X_CONV;
     static constexpr int FIXED = 1024 + BUFFERS + exchange_bytes<EPI_WARPS>() + BAR_BYTES;
     static constexpr uint32_t IDESC0 = make_idesc(0u, false, false, 128 * CTAS, 0);   // FP16 operands
-    static_assert(ACC_COLS + CONV_STAGES * A_COLS <= 512, "Tensor Memory");
+    static_assert(ACC_COLS + A_STAGES * A_COLS <= 512, "Tensor Memory");
     static_assert(FIXED + Schedule::bytes(DGEMM_MAX_EXPERTS) <= 232448, "shared memory");
-    static_assert((2 * W_STAGES + 2 * X_STAGES + 2 * CONV_STAGES + 5) * 8 + 8 <= BAR_BYTES, "barriers fit");
+    static_assert((2 * W_STAGES + 2 * STAGE_BARS + 5) * 8 + 8 <= BAR_BYTES, "barriers fit");
 };
 
 // Four int8 codes to four FP16 numbers.
@@ -64,15 +76,12 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
     extern __shared__ uint8_t smem_raw[];
     uint8_t* wraw = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* xconv = wraw + CF::W_STAGES * CF::W_RAW;
-    uint8_t* xraw = xconv + CF::CONV_STAGES * CF::X_CONV;
     float* exchange = reinterpret_cast<float*>(wraw + CF::BUFFERS);
     uint64_t* w_full = reinterpret_cast<uint64_t*>(wraw + CF::BUFFERS + exchange_bytes<CF::EPI_WARPS>());
     uint64_t* w_empty = w_full + CF::W_STAGES;
-    uint64_t* x_full = w_empty + CF::W_STAGES;
-    uint64_t* x_empty = x_full + CF::X_STAGES;
-    uint64_t* full = x_empty + CF::X_STAGES;             // converted stages
-    uint64_t* empty = full + CF::CONV_STAGES;
-    uint64_t* acc_full = empty + CF::CONV_STAGES;
+    uint64_t* full = w_empty + CF::W_STAGES;             // converted stages
+    uint64_t* done = full + CF::STAGE_BARS;
+    uint64_t* acc_full = done + CF::STAGE_BARS;
     uint64_t* acc_empty = acc_full + 2;
     uint64_t* drain = acc_empty + 2;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -89,13 +98,9 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
             mbar_init(&w_full[s], 1);
             mbar_init(&w_empty[s], 4);                   // every weight converter warp
         }
-        for (int s = 0; s < CF::X_STAGES; ++s) {
-            mbar_init(&x_full[s], 64);                   // every copier's own copies
-            mbar_init(&x_empty[s], 4);                   // every token converter warp
-        }
-        for (int s = 0; s < CF::CONV_STAGES; ++s) {
-            mbar_init(&full[s], 8 * CF::CTAS);           // every converter warp of the pair
-            mbar_init(&empty[s], 1);
+        for (int s = 0; s < CF::STAGE_BARS; ++s) {
+            mbar_init(&full[s], 8 * CF::CTAS);           // a team's warps of both converters, of both CTAs
+            mbar_init(&done[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
@@ -126,14 +131,23 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     // converter warps: counts a converted stage in at the pair's leader
-    auto converted = [&](uint32_t stage) {
-        if (CF::PAIR && rank != 0) mbar_arrive_peer(mapa_shared(smem_u32(&full[stage]), 0));
-        else mbar_arrive(&full[stage]);
+    auto converted = [&](uint32_t g) {
+        uint64_t* bar = &full[g % CF::STAGE_BARS];
+        if (CF::PAIR && rank != 0) mbar_arrive_peer(mapa_shared(smem_u32(bar), 0));
+        else mbar_arrive(bar);
+    };
+    // ... and wait until the slot of stage g is free in a ring of `slots`
+    auto slot_free = [&](uint32_t g, uint32_t slots) {
+        if (g < slots) return true;
+        const uint32_t last = g - slots;
+        return mbar_wait_warp(&done[last % CF::STAGE_BARS], (last / CF::STAGE_BARS) & 1, abort_flag, p.wait_ns);
     };
 
     Cursor cur;
     Tile t;
     bool ok = true;
+    if (warp < CF::EPI_WARP0) {
+    regs_dec<CF::REGS_CONTROL>();
     if (warp == 0) {
         // ---------------------------------------------------------------- TMA producer
         if (lane == 0) {
@@ -148,7 +162,7 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
                         stalled = true;
                         break;
                     }
-                    if (!mbar_wait(&w_empty[stage], phase ^ 1, abort_flag, p.wait_ns)) {
+                    if (!mbar_poll(&w_empty[stage], phase ^ 1, abort_flag, p.wait_ns)) {
                         ok = false;
                         break;
                     }
@@ -174,7 +188,7 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
         // ---------------------------------------------------------------- MMA issuer
         if (lane == 0 && rank == 0) {
             const uint64_t xd0 = smem_desc_sw128(smem_u32(xconv), 16, 1024);
-            uint32_t stage = 0, phase = 0;
+            uint32_t g = 0, cs = 0;                      // stages so far; the rows' slot
             int local = 0;
             for (int item = unit; ok && cur.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, t); item += units, ++local) {
                 const int buf = local & 1;
@@ -186,25 +200,24 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
                 const uint32_t acc = tmem + static_cast<uint32_t>(buf * CF::BN);
                 const uint32_t idesc = CF::IDESC0 | (static_cast<uint32_t>(t.n >> 3) << 17);
                 for (int kb = 0; kb < p.kstages; ++kb) {
-                    const bool got = CF::PAIR ? mbar_wait_cluster(&full[stage], phase, abort_flag, p.wait_ns)
-                                              : mbar_wait(&full[stage], phase, abort_flag, p.wait_ns);
+                    const uint32_t bar = g % CF::STAGE_BARS, phase = (g / CF::STAGE_BARS) & 1;
+                    const bool got = CF::PAIR ? mbar_wait_cluster(&full[bar], phase, abort_flag, p.wait_ns)
+                                              : mbar_wait(&full[bar], phase, abort_flag, p.wait_ns);
                     if (!got) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t a = tmem + CF::ACC_COLS + stage * CF::A_COLS;
-                    const uint64_t xd = xd0 + stage * (CF::X_CONV >> 4);
+                    const uint32_t a = tmem + CF::ACC_COLS + g % CF::A_STAGES * CF::A_COLS;
+                    const uint64_t xd = xd0 + cs * (CF::X_CONV >> 4);
 #pragma unroll
                     for (int k = 0; k < CF::KB / 16; ++k)
                         mma_f16_tmem_a<CF::PAIR>(acc, a + k * 8, xd + (k / 4) * (CF::SLICE_X >> 4) + (k % 4) * 2, idesc,
                                                  (kb > 0 || k > 0) ? 1u : 0u);
-                    if constexpr (CF::PAIR) mma_commit_pair(&empty[stage], 3);
-                    else mma_commit(&empty[stage]);
-                    if (++stage == CF::CONV_STAGES) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
+                    if constexpr (CF::PAIR) mma_commit_pair(&done[bar], 3);
+                    else mma_commit(&done[bar]);
+                    ++g;
+                    if (++cs == CF::C_STAGES) cs = 0;
                 }
                 if (!ok) break;
                 if constexpr (CF::PAIR) mma_commit_pair(&acc_full[buf], 3);
@@ -216,52 +229,10 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
             if (!mbar_wait(drain, 0, nullptr, p.wait_ns)) fail(p, ERR_TIMEOUT_DRAIN, abort_flag);
         }
         __syncwarp();
-    } else if (warp >= CF::COPY_WARP0 && warp < CF::EPI_WARP0) {
-        // ---------------------------------------------------------------- token copiers
-        // Eight lanes copy one row's 128 codes; a thread's copies arrive by themselves.
-        constexpr int ROUNDS = CF::BN_CTA / 8;
-        const int sub = (threadIdx.x - CF::COPY_WARP0 * 32) >> 3, chunk = lane & 7;
-        uint32_t stage = 0, phase = 0;
-        for (int item = unit; ok && cur.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, t); item += units) {
-            const int xrows = t.n / CF::CTAS, first = static_cast<int>(rank) * xrows, rounds = xrows / 8;
-            int src[ROUNDS];
-#pragma unroll
-            for (int i = 0; i < ROUNDS; ++i) {
-                const int r = first + i * 8 + sub;
-                src[i] = -1;
-                if (i < rounds && r < t.rows) {
-                    const int a = p.a_rows ? __ldg(p.a_rows + t.row0 + r) : t.row0 + r;
-                    if (a >= 0 && a < p.a_count) src[i] = a;
-                }
-            }
-            for (int kb = 0; kb < p.kstages; ++kb) {
-                if (!mbar_wait_warp(&x_empty[stage], phase ^ 1, abort_flag, p.wait_ns)) {
-                    ok = false;
-                    break;
-                }
-                const int k = kb * CF::KB + chunk * 16;
-                const char* base = static_cast<const char*>(p.A) + k;
-                uint8_t* dst = xraw + stage * CF::X_RAW + sub * 128 + chunk * 16;
-#pragma unroll
-                for (int i = 0; i < ROUNDS; ++i) {
-                    if (i >= rounds) break;
-                    const bool read = k < p.K && src[i] >= 0;
-                    cp_async_16(dst + i * 1024, read ? base + static_cast<int64_t>(src[i]) * p.K : static_cast<const char*>(p.A),
-                                read ? 16u : 0u);
-                }
-                cp_async_mbar_arrive(&x_full[stage]);
-                if (++stage == CF::X_STAGES) {
-                    stage = 0;
-                    phase ^= 1;
-                }
-            }
-        }
-        cp_async_commit();
-        cp_async_wait<0>();      // nothing of this thread's is in flight when it leaves
-        if (!ok) fail(p, ERR_TIMEOUT_PRODUCER, abort_flag);
-        __syncwarp();
-    } else if (warp >= CF::EPI_WARP0 && warp < CF::W_WARP0) {
+    }
+    } else if (warp < CF::W_WARP0) {
         // ---------------------------------------------------------------- epilogue
+        regs_inc<CF::REGS_EPILOGUE>();
         int local = 0;
         for (int item = unit; ok && cur.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, t); item += units, ++local) {
             const int buf = local & 1;
@@ -276,107 +247,142 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
         }
         if (!ok) fail(p, ERR_TIMEOUT_EPILOGUE, abort_flag);
         __syncwarp();
-    } else if (warp >= CF::W_WARP0 && warp < CF::X_WARP0) {
+    } else if (warp < CF::X_WARP0) {
         // ---------------------------------------------------------------- weight converters
-        const int row = (warp - CF::W_WARP0) * 32 + lane;    // TMEM lane: the warp's own quarter
+        regs_dec<CF::REGS_WEIGHTS>();
+        const int team = (warp - CF::W_WARP0) >> 2;
+        const int row = (warp & 3) * 32 + lane;              // TMEM lane: the warp's own quarter
         const uint32_t a_base = tmem + CF::ACC_COLS + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        uint32_t raw = 0, raw_phase = 0, stage = 0, phase = 0;
+        uint32_t raw = 0, raw_phase = 0, g = 0;
         for (int item = unit; ok && cur.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, t); item += units) {
-            for (int kb = 0; kb < p.kstages; ++kb) {
-                if (!mbar_wait_warp(&w_full[raw], raw_phase, abort_flag, p.wait_ns)) {
-                    ok = false;
-                    break;
-                }
-                const uint8_t* src = wraw + raw * CF::W_RAW + row * 128;
-                uint4 codes[8];
+            for (int kb = 0; kb < p.kstages; ++kb, ++g) {
+                if (static_cast<int>(g % CF::TEAMS) == team) {
+                    if (!mbar_wait_warp(&w_full[raw], raw_phase, abort_flag, p.wait_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint8_t* src = wraw + raw * CF::W_RAW + row * 128;
+                    uint4 codes[8];
 #pragma unroll
-                for (int c = 0; c < 8; ++c) codes[c] = *reinterpret_cast<const uint4*>(src + ((c ^ (row & 7)) << 4));
-                uint32_t h[2][32];
+                    for (int c = 0; c < 8; ++c) codes[c] = *reinterpret_cast<const uint4*>(src + ((c ^ (row & 7)) << 4));
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&w_empty[raw]);   // the codes are in registers
+                    uint32_t h[32];
+                    auto convert = [&](int half) {
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    uint32_t* d = &h[c >> 2][(c & 3) * 8];
-                    int8x4_to_f16(codes[c].x, d[0], d[1]);
-                    int8x4_to_f16(codes[c].y, d[2], d[3]);
-                    int8x4_to_f16(codes[c].z, d[4], d[5]);
-                    int8x4_to_f16(codes[c].w, d[6], d[7]);
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t* d = h + c * 8;
+                            int8x4_to_f16(codes[half * 4 + c].x, d[0], d[1]);
+                            int8x4_to_f16(codes[half * 4 + c].y, d[2], d[3]);
+                            int8x4_to_f16(codes[half * 4 + c].z, d[4], d[5]);
+                            int8x4_to_f16(codes[half * 4 + c].w, d[6], d[7]);
+                        }
+                    };
+                    convert(0);
+                    if (!slot_free(g, CF::A_STAGES)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a = a_base + g % CF::A_STAGES * CF::A_COLS;
+                    tmem_st32(a, h);
+                    convert(1);
+                    tmem_st32(a + 32, h);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) converted(g);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&w_empty[raw]);   // the codes are in registers
-                if (!mbar_wait_warp(&empty[stage], phase ^ 1, abort_flag, p.wait_ns)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                tmem_st32(a_base + stage * CF::A_COLS, h[0]);
-                tmem_st32(a_base + stage * CF::A_COLS + 32, h[1]);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) converted(stage);
                 if (++raw == CF::W_STAGES) {
                     raw = 0;
                     raw_phase ^= 1;
-                }
-                if (++stage == CF::CONV_STAGES) {
-                    stage = 0;
-                    phase ^= 1;
                 }
             }
         }
         if (!ok) fail(p, ERR_TIMEOUT_PRODUCER, abort_flag);
         __syncwarp();
-    } else if (warp >= CF::X_WARP0) {
+    } else {
         // ---------------------------------------------------------------- token converters
-        // Eight threads convert one row's 128 codes, 16 each.
+        // Eight threads load and convert one row's 128 codes, 16 each; a team's next stage is
+        // being loaded while it converts this one.
+        regs_dec<CF::REGS_TOKENS>();
         constexpr int ROUNDS = CF::BN_CTA / 16;
-        const int tid = threadIdx.x - CF::X_WARP0 * 32, sub = tid >> 3, chunk = tid & 7;
+        const int team = (warp - CF::X_WARP0) >> 2;
+        const int tid = threadIdx.x & 127, sub = tid >> 3, chunk = tid & 7;
         // a thread's 32 bytes of FP16 are two 16-byte chunks of one slice; threads of the second
         // slice write theirs in the other order, so that the eight of a row meet different banks
         const int j = (chunk & 3) * 2, flip = chunk >> 2;
         const int at0 = (((j + flip) ^ (sub & 7)) << 4), at1 = (((j + 1 - flip) ^ (sub & 7)) << 4);
-        uint32_t raw = 0, raw_phase = 0, stage = 0, phase = 0;
-        for (int item = unit; ok && cur.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, t); item += units) {
-            const int rounds = t.n / CF::CTAS / 16;
-            for (int kb = 0; kb < p.kstages; ++kb) {
-                if (!mbar_wait_warp(&x_full[raw], raw_phase, abort_flag, p.wait_ns)) {
-                    ok = false;
-                    break;
-                }
-                uint4 codes[ROUNDS];
+        int item = unit, kb = team, rounds = 0, src[ROUNDS];
+        bool live = p.kstages > 0 && cur.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, t);
+        auto point = [&]() {                                 // the rows of tile t
+            const int xrows = t.n / CF::CTAS, first = static_cast<int>(rank) * xrows;
+            rounds = xrows / 16;
 #pragma unroll
-                for (int i = 0; i < ROUNDS; ++i)
-                    if (i < rounds)
-                        codes[i] = *reinterpret_cast<const uint4*>(xraw + raw * CF::X_RAW + (i * 16 + sub) * 128 + chunk * 16);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&x_empty[raw]);   // the codes are in registers
-                if (!mbar_wait_warp(&empty[stage], phase ^ 1, abort_flag, p.wait_ns)) {
-                    ok = false;
-                    break;
-                }
-                uint8_t* slice = xconv + stage * CF::X_CONV + (chunk >> 2) * CF::SLICE_X + sub * 128;
-#pragma unroll
-                for (int i = 0; i < ROUNDS; ++i) {
-                    if (i >= rounds) break;
-                    uint4 lo, hi;
-                    int8x4_to_f16(codes[i].x, lo.x, lo.y);
-                    int8x4_to_f16(codes[i].y, lo.z, lo.w);
-                    int8x4_to_f16(codes[i].z, hi.x, hi.y);
-                    int8x4_to_f16(codes[i].w, hi.z, hi.w);
-                    *reinterpret_cast<uint4*>(slice + i * 2048 + at0) = flip ? hi : lo;
-                    *reinterpret_cast<uint4*>(slice + i * 2048 + at1) = flip ? lo : hi;
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) converted(stage);
-                if (++raw == CF::X_STAGES) {
-                    raw = 0;
-                    raw_phase ^= 1;
-                }
-                if (++stage == CF::CONV_STAGES) {
-                    stage = 0;
-                    phase ^= 1;
+            for (int i = 0; i < ROUNDS; ++i) {
+                const int r = first + i * 16 + sub;
+                src[i] = -1;
+                if (i < rounds && r < t.rows) {
+                    const int a = p.a_rows ? __ldg(p.a_rows + t.row0 + r) : t.row0 + r;
+                    if (a >= 0 && a < p.a_count) src[i] = a;
                 }
             }
+        };
+        auto settle = [&]() {                                // kb into its tile
+            bool moved = false;
+            while (live && kb >= p.kstages) {
+                kb -= p.kstages;
+                item += units;
+                live = cur.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, t);
+                moved = true;
+            }
+            if (live && moved) point();
+        };
+        uint4 next[ROUNDS];
+        auto load = [&]() {
+            const int k = kb * CF::KB + chunk * 16;
+            const char* base = static_cast<const char*>(p.A) + k;
+#pragma unroll
+            for (int i = 0; i < ROUNDS; ++i) {
+                next[i] = make_uint4(0, 0, 0, 0);
+                if (live && src[i] >= 0 && k < p.K)
+                    next[i] = __ldg(reinterpret_cast<const uint4*>(base + static_cast<int64_t>(src[i]) * p.K));
+            }
+        };
+        if (live) point();
+        settle();
+        load();
+        uint32_t g = team, cs = team;
+        while (live) {
+            uint4 codes[ROUNDS];
+#pragma unroll
+            for (int i = 0; i < ROUNDS; ++i) codes[i] = next[i];
+            const int now = rounds;
+            kb += CF::TEAMS;
+            settle();
+            load();
+            if (!slot_free(g, CF::C_STAGES)) {
+                ok = false;
+                break;
+            }
+            uint8_t* slice = xconv + cs * CF::X_CONV + (chunk >> 2) * CF::SLICE_X + sub * 128;
+#pragma unroll
+            for (int i = 0; i < ROUNDS; ++i) {
+                if (i >= now) break;
+                uint4 lo, hi;
+                int8x4_to_f16(codes[i].x, lo.x, lo.y);
+                int8x4_to_f16(codes[i].y, lo.z, lo.w);
+                int8x4_to_f16(codes[i].z, hi.x, hi.y);
+                int8x4_to_f16(codes[i].w, hi.z, hi.w);
+                *reinterpret_cast<uint4*>(slice + i * 2048 + at0) = flip ? hi : lo;
+                *reinterpret_cast<uint4*>(slice + i * 2048 + at1) = flip ? lo : hi;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) converted(g);
+            g += CF::TEAMS;
+            cs += CF::TEAMS;
+            if (cs >= CF::C_STAGES) cs -= CF::C_STAGES;
         }
         if (!ok) fail(p, ERR_TIMEOUT_PRODUCER, abort_flag);
         __syncwarp();

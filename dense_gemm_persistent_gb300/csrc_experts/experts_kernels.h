@@ -13,6 +13,7 @@ struct Variant {
     int type, kn, pair;          // dgemm_grouped_type_t; weights K x N; CTA pairs
     int gather;                  // 1: rows by index, 0: rows in order, -1: either
     int bn, bn_cta, ctas, slices, small_rows, threads;   // slices: 128-byte slices of K per stage
+    int launch_regs;             // registers per thread that the kernel's register split assumes (0: none)
     size_t smem_fixed;           // dynamic shared memory without the schedule
     const void* func;
     cudaError_t (*launch)(const CUtensorMap& w, const CUtensorMap& x, const CUtensorMap& xs, const Params& p, int grid,

@@ -17,7 +17,7 @@ cudaError_t launch_mma(const CUtensorMap& w, const CUtensorMap& x, const CUtenso
 
 template <class CF>
 Variant make_variant() {
-    return Variant{CF::FP8 ? DGEMM_GROUPED_FP8 : DGEMM_GROUPED_BF16, CF::KN, CF::PAIR, CF::GATHER, CF::BN, CF::BN_CTA, CF::CTAS, CF::KS, CF::SMALL_ROWS, CF::THREADS,
+    return Variant{CF::FP8 ? DGEMM_GROUPED_FP8 : DGEMM_GROUPED_BF16, CF::KN, CF::PAIR, CF::GATHER, CF::BN, CF::BN_CTA, CF::CTAS, CF::KS, CF::SMALL_ROWS, CF::THREADS, 0,
                    CF::FIXED, reinterpret_cast<const void*>(&expert_mma<CF>), &launch_mma<CF>};
 }
 
