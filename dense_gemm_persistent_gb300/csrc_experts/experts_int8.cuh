@@ -13,7 +13,7 @@
 // columns, and its stages left room for 192 columns only (4096 x 11008 x 4096: 402 us).
 // Warps of a CTA:
 //   0       TMA producer of weight codes: 128 channels x 128 K, 128B swizzle
-//   1       MMA issuer (one thread), owner of the Tensor Memory
+//   1       MMA issuer, owner of the Tensor Memory
 //   2-3     idle (they complete the first warpgroup)
 //   4-7     epilogue
 //   8-15    weight converters, one channel a thread; two teams

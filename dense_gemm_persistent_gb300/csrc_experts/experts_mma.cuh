@@ -3,7 +3,7 @@
 // One persistent CTA per SM (or CTA pair per two SMs) walks the tiles of the
 // schedule. Warps of a CTA:
 //   0       TMA producer: weights, and token rows that are already in order
-//   1       MMA issuer (one thread), owner of the Tensor Memory
+//   1       MMA issuer, owner of the Tensor Memory
 //   2       gathering variants: announces gathered stages to the MMA issuer
 //   3       idle (completes the first warpgroup)
 //   4-11    epilogue
@@ -199,8 +199,9 @@ __global__ void __launch_bounds__(CF::THREADS, 1)
         __syncwarp();
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issuer
-        if (lane == 0 && rank == 0) {
-            const uint32_t s0 = smem_u32(ring);
+        if (rank == 0) {
+            // (values and branches that the compiler knows to be the warp's stay in uniform registers)
+            const uint32_t s0 = smem_u32(ring), tmem_u = __shfl_sync(kAllLanes, tmem, 0);
             const uint64_t wd0 = smem_desc_sw128(s0, CF::KN ? CF::ATOM : 16, 1024);
             const uint64_t xd0 = smem_desc_sw128(s0 + CF::W_BYTES, 16, 1024);
             constexpr int NK = CF::SL / CF::UK;                  // MMAs per slice
@@ -210,52 +211,57 @@ __global__ void __launch_bounds__(CF::THREADS, 1)
             bool ok = true;
             Cursor cur;
             Tile t;
-            for (int item = unit; ok && cur.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, t); item += units, ++local) {
+            for (int item = unit; ok && __all_sync(kAllLanes, cur.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, t));
+                 item += units, ++local) {
                 const int buf = local & 1;
-                if (!mbar_wait(&acc_empty[buf], ((local >> 1) & 1) ^ 1, abort_flag, p.wait_ns)) {
-                    ok = false;
-                    break;
-                }
+                ok = __all_sync(kAllLanes, mbar_wait(&acc_empty[buf], ((local >> 1) & 1) ^ 1, abort_flag, p.wait_ns));
+                if (!ok) break;
                 tc_fence_after();
-                const uint32_t acc = tmem + static_cast<uint32_t>(buf * CF::BN);
-                const uint32_t idesc = CF::IDESC0 | (static_cast<uint32_t>(t.n >> 3) << 17);
+                const uint32_t acc = tmem_u + static_cast<uint32_t>(buf * CF::BN);
+                const uint32_t idesc = CF::IDESC0 | (static_cast<uint32_t>(__shfl_sync(kAllLanes, t.n, 0) >> 3) << 17);
                 for (int kb = 0; kb < p.kstages; ++kb) {
                     const bool got = CF::PAIR && CF::GATHER ? mbar_wait_cluster(&full[stage], phase, abort_flag, p.wait_ns)
                                                             : mbar_wait(&full[stage], phase, abort_flag, p.wait_ns);
-                    if (!got) {
-                        ok = false;
-                        break;
-                    }
+                    ok = __all_sync(kAllLanes, got);
+                    if (!ok) break;
                     tc_fence_after();
                     const uint64_t wd = wd0 + stage * (CF::STAGE >> 4), xd = xd0 + stage * (CF::STAGE >> 4);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < CF::KS * NK; ++k) {
-                        const uint32_t more = (kb > 0 || k > 0) ? 1u : 0u;
-                        const uint64_t a = wd + (CF::KN ? k * W_STEP : (k / NK) * (CF::SLICE_W >> 4) + (k % NK) * W_STEP);
-                        const uint64_t b = xd + (k / NK) * (CF::SLICE_X >> 4) + (k % NK) * 2;
-                        if constexpr (CF::PAIR) {
-                            if constexpr (CF::FP8) mma_f8_pair(acc, a, b, idesc, more);
-                            else mma_bf16_pair(acc, a, b, idesc, more);
-                        } else {
-                            if constexpr (CF::FP8) mma_f8(acc, a, b, idesc, more);
-                            else mma_bf16(acc, a, b, idesc, more);
+                        for (int k = 0; k < CF::KS * NK; ++k) {
+                            const uint32_t more = (kb > 0 || k > 0) ? 1u : 0u;
+                            const uint64_t a = wd + (CF::KN ? k * W_STEP : (k / NK) * (CF::SLICE_W >> 4) + (k % NK) * W_STEP);
+                            const uint64_t b = xd + (k / NK) * (CF::SLICE_X >> 4) + (k % NK) * 2;
+                            if constexpr (CF::PAIR) {
+                                if constexpr (CF::FP8) mma_f8_pair(acc, a, b, idesc, more);
+                                else mma_bf16_pair(acc, a, b, idesc, more);
+                            } else {
+                                if constexpr (CF::FP8) mma_f8(acc, a, b, idesc, more);
+                                else mma_bf16(acc, a, b, idesc, more);
+                            }
                         }
+                        if constexpr (CF::PAIR) mma_commit_pair(&empty[stage], 3);
+                        else mma_commit(&empty[stage]);
                     }
-                    if constexpr (CF::PAIR) mma_commit_pair(&empty[stage], 3);
-                    else mma_commit(&empty[stage]);
+                    __syncwarp();
                     if (++stage == S) {
                         stage = 0;
                         phase ^= 1;
                     }
                 }
                 if (!ok) break;
-                if constexpr (CF::PAIR) mma_commit_pair(&acc_full[buf], 3);
-                else mma_commit(&acc_full[buf]);
+                if (elect_one()) {
+                    if constexpr (CF::PAIR) mma_commit_pair(&acc_full[buf], 3);
+                    else mma_commit(&acc_full[buf]);
+                }
+                __syncwarp();
             }
-            if (!ok) fail(p, ERR_TIMEOUT_MMA, abort_flag);
-            if constexpr (CF::PAIR) mma_commit_pair(drain, 1);
-            else mma_commit(drain);
-            if (!mbar_wait(drain, 0, nullptr, p.wait_ns)) fail(p, ERR_TIMEOUT_DRAIN, abort_flag);
+            if (elect_one()) {
+                if (!ok) fail(p, ERR_TIMEOUT_MMA, abort_flag);
+                if constexpr (CF::PAIR) mma_commit_pair(drain, 1);
+                else mma_commit(drain);
+                if (!mbar_wait(drain, 0, nullptr, p.wait_ns)) fail(p, ERR_TIMEOUT_DRAIN, abort_flag);
+            }
         }
         __syncwarp();
     } else if (warp >= CF::EPI_WARP0 && warp < CF::EPI_WARP0 + CF::EPI_WARPS) {
