@@ -142,40 +142,37 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
     regs_dec<CF::REGS_CONTROL>();
     if (warp == 0) {
         // ---------------------------------------------------------------- TMA producer
-        if (lane == 0) {
-            const uint64_t pol = policy_evict_last();
-            uint32_t stage = 0, phase = 0;
-            int64_t issued = 0;
-            bool stalled = false;
-            for (int item = unit; ok && !stalled && cur.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, t); item += units) {
-                const int chan = t.chan0 + static_cast<int>(rank) * (p.gated ? 64 : 128);
-                for (int kb = 0; kb < p.kstages; ++kb) {
-                    if (issued == p.stall_after) {
-                        stalled = true;
-                        break;
-                    }
-                    if (!mbar_poll(&w_empty[stage], phase ^ 1, abort_flag, p.wait_ns)) {
-                        ok = false;
-                        break;
-                    }
+        const uint64_t pol = policy_evict_last();
+        uint32_t stage = 0, phase = 0;
+        int64_t issued = 0;
+        bool stalled = false;
+        for (int item = unit; ok && !stalled && __all_sync(kAllLanes, cur.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, t));
+             item += units) {
+            const int chan = t.chan0 + static_cast<int>(rank) * (p.gated ? 64 : 128);
+            for (int kb = 0; kb < p.kstages; ++kb) {
+                stalled = issued == p.stall_after;
+                if (stalled) break;
+                ok = mbar_wait_warp(&w_empty[stage], phase ^ 1, abort_flag, p.wait_ns);
+                if (!ok) break;
+                if (elect_one()) {
                     mbar_arrive_expect_tx(&w_full[stage], CF::W_RAW);
                     tma_load_nd<false>(wraw + stage * CF::W_RAW, &tmW, smem_u32(&w_full[stage]), kb * CF::KB, chan, 0,
                                        t.expert, pol);
-                    ++issued;
-                    if (++stage == CF::W_STAGES) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
+                }
+                __syncwarp();
+                ++issued;
+                if (++stage == CF::W_STAGES) {
+                    stage = 0;
+                    phase ^= 1;
                 }
             }
-            if (!ok) fail(p, ERR_TIMEOUT_PRODUCER, abort_flag);
-            for (int s = 0; s < CF::W_STAGES; ++s) {     // every copy issued lands before the CTA may exit
-                const int64_t cnt = issued > s ? (issued - s + CF::W_STAGES - 1) / CF::W_STAGES : 0;
-                if (cnt > 0 && !mbar_wait(&w_full[s], static_cast<uint32_t>((cnt - 1) & 1), nullptr, p.wait_ns))
-                    fail(p, ERR_TIMEOUT_DRAIN, abort_flag);
-            }
         }
-        __syncwarp();
+        if (!ok && lane == 0) fail(p, ERR_TIMEOUT_PRODUCER, abort_flag);
+        for (int s = 0; s < CF::W_STAGES; ++s) {         // every copy issued lands before the CTA may exit
+            const int64_t cnt = issued > s ? (issued - s + CF::W_STAGES - 1) / CF::W_STAGES : 0;
+            if (cnt > 0 && !mbar_wait_warp(&w_full[s], static_cast<uint32_t>((cnt - 1) & 1), nullptr, p.wait_ns) && lane == 0)
+                fail(p, ERR_TIMEOUT_DRAIN, abort_flag);
+        }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issuer
         if (rank == 0) {
@@ -188,16 +185,14 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
             for (int item = unit; ok && __all_sync(kAllLanes, cur.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, t));
                  item += units, ++local) {
                 const int buf = local & 1;
-                ok = __all_sync(kAllLanes, mbar_wait(&acc_empty[buf], ((local >> 1) & 1) ^ 1, abort_flag, p.wait_ns));
+                ok = mbar_wait_warp(&acc_empty[buf], ((local >> 1) & 1) ^ 1, abort_flag, p.wait_ns);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t acc = tmem_u + static_cast<uint32_t>(buf * CF::BN);
                 const uint32_t idesc = CF::IDESC0 | (static_cast<uint32_t>(__shfl_sync(kAllLanes, t.n, 0) >> 3) << 17);
                 for (int kc = 0; kc < 2 * p.kstages; ++kc, ++g) {
                     const uint32_t slot = g % CF::C_STAGES, phase = (g / CF::C_STAGES) & 1;
-                    const bool got = CF::PAIR ? mbar_wait_cluster(&full[slot], phase, abort_flag, p.wait_ns)
-                                              : mbar_wait(&full[slot], phase, abort_flag, p.wait_ns);
-                    ok = __all_sync(kAllLanes, got);
+                    ok = mbar_wait_warp_at<CF::PAIR>(&full[slot], phase, abort_flag, p.wait_ns);
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t wd = wd0 + slot * (CF::CONV >> 4), xd = xd0 + slot * (CF::CONV >> 4);

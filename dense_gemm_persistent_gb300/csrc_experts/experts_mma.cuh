@@ -121,29 +121,26 @@ __global__ void __launch_bounds__(CF::THREADS, 1)
 
     if (warp == 0) {
         // ---------------------------------------------------------------- TMA producer
-        if (lane == 0) {
-            const uint64_t pol = policy_evict_last();
-            uint32_t stage = 0, phase = 0;
-            int64_t issued = 0;
-            bool ok = true, stalled = false;
-            Cursor cur;
-            Tile t;
-            for (int item = unit; ok && !stalled && cur.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, t); item += units) {
-                const int chan = t.chan0 + static_cast<int>(rank) * (p.gated ? 64 : 128);
-                const int xrows = t.n / CF::CTAS;                              // token rows of this CTA
-                const int x0 = t.row0 + static_cast<int>(rank) * xrows;
-                // few rows: copies of 16; else one copy of the whole box (rows beyond the tile are not used)
-                const int small = xrows <= 2 * CF::SMALL_ROWS ? (xrows + CF::SMALL_ROWS - 1) / CF::SMALL_ROWS : 0;
-                const uint32_t xbytes = CF::GATHER ? 0 : small ? small * CF::SMALL_ROWS * 128 * CF::KS : CF::X_BYTES;
-                for (int kb = 0; kb < p.kstages; ++kb) {
-                    if (issued == p.stall_after) {
-                        stalled = true;
-                        break;
-                    }
-                    if (!mbar_wait(&empty[stage], phase ^ 1, abort_flag, p.wait_ns)) {
-                        ok = false;
-                        break;
-                    }
+        const uint64_t pol = policy_evict_last();
+        uint32_t stage = 0, phase = 0;
+        int64_t issued = 0;
+        bool ok = true, stalled = false;
+        Cursor cur;
+        Tile t;
+        for (int item = unit; ok && !stalled && __all_sync(kAllLanes, cur.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, t));
+             item += units) {
+            const int chan = t.chan0 + static_cast<int>(rank) * (p.gated ? 64 : 128);
+            const int xrows = __shfl_sync(kAllLanes, t.n, 0) / CF::CTAS;   // token rows of this CTA
+            const int x0 = t.row0 + static_cast<int>(rank) * xrows;
+            // few rows: copies of 16; else one copy of the whole box (rows beyond the tile are not used)
+            const int small = xrows <= 2 * CF::SMALL_ROWS ? (xrows + CF::SMALL_ROWS - 1) / CF::SMALL_ROWS : 0;
+            const uint32_t xbytes = CF::GATHER ? 0 : small ? small * CF::SMALL_ROWS * 128 * CF::KS : CF::X_BYTES;
+            for (int kb = 0; kb < p.kstages; ++kb) {
+                stalled = issued == p.stall_after;
+                if (stalled) break;
+                ok = mbar_wait_warp(&empty[stage], phase ^ 1, abort_flag, p.wait_ns);
+                if (!ok) break;
+                if (elect_one()) {
                     uint8_t* w = ring + stage * CF::STAGE;
                     uint8_t* x = w + CF::W_BYTES;
                     if (rank == 0) mbar_arrive_expect_tx(&full[stage], CF::CTAS * (CF::W_BYTES + xbytes));
@@ -179,24 +176,24 @@ __global__ void __launch_bounds__(CF::THREADS, 1)
                             }
                         }
                     }
-                    ++issued;
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
+                }
+                __syncwarp();
+                ++issued;
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1;
                 }
             }
-            if (!ok) fail(p, ERR_TIMEOUT_PRODUCER, abort_flag);
-            // Drain: every copy issued has landed before the CTA may exit (the peer
-            // of a pair signals the leader's barriers, so it waits for the MMA's release).
-            for (int s = 0; s < S; ++s) {
-                const int64_t cnt = issued > s ? (issued - s + S - 1) / S : 0;
-                uint64_t* bar = (CF::PAIR && rank != 0) ? &empty[s] : &full[s];
-                if (cnt > 0 && !mbar_wait(bar, static_cast<uint32_t>((cnt - 1) & 1), nullptr, p.wait_ns))
-                    fail(p, ERR_TIMEOUT_DRAIN, abort_flag);
-            }
         }
-        __syncwarp();
+        if (!ok && lane == 0) fail(p, ERR_TIMEOUT_PRODUCER, abort_flag);
+        // Drain: every copy issued has landed before the CTA may exit (the peer of a pair
+        // signals the leader's barriers, so it waits for the MMA's release).
+        for (int s = 0; s < S; ++s) {
+            const int64_t cnt = issued > s ? (issued - s + S - 1) / S : 0;
+            uint64_t* bar = (CF::PAIR && rank != 0) ? &empty[s] : &full[s];
+            if (cnt > 0 && !mbar_wait_warp(bar, static_cast<uint32_t>((cnt - 1) & 1), nullptr, p.wait_ns) && lane == 0)
+                fail(p, ERR_TIMEOUT_DRAIN, abort_flag);
+        }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issuer
         if (rank == 0) {
@@ -214,15 +211,13 @@ __global__ void __launch_bounds__(CF::THREADS, 1)
             for (int item = unit; ok && __all_sync(kAllLanes, cur.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, t));
                  item += units, ++local) {
                 const int buf = local & 1;
-                ok = __all_sync(kAllLanes, mbar_wait(&acc_empty[buf], ((local >> 1) & 1) ^ 1, abort_flag, p.wait_ns));
+                ok = mbar_wait_warp(&acc_empty[buf], ((local >> 1) & 1) ^ 1, abort_flag, p.wait_ns);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t acc = tmem_u + static_cast<uint32_t>(buf * CF::BN);
                 const uint32_t idesc = CF::IDESC0 | (static_cast<uint32_t>(__shfl_sync(kAllLanes, t.n, 0) >> 3) << 17);
                 for (int kb = 0; kb < p.kstages; ++kb) {
-                    const bool got = CF::PAIR && CF::GATHER ? mbar_wait_cluster(&full[stage], phase, abort_flag, p.wait_ns)
-                                                            : mbar_wait(&full[stage], phase, abort_flag, p.wait_ns);
-                    ok = __all_sync(kAllLanes, got);
+                    ok = mbar_wait_warp_at<CF::PAIR && CF::GATHER>(&full[stage], phase, abort_flag, p.wait_ns);
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t wd = wd0 + stage * (CF::STAGE >> 4), xd = xd0 + stage * (CF::STAGE >> 4);
@@ -288,29 +283,27 @@ __global__ void __launch_bounds__(CF::THREADS, 1)
         // ---------------------------------------------------------------- announcer
         // A stage whose copies have landed becomes visible to the tensor core's
         // (asynchronous) reads by a proxy fence, then counts on its full barrier.
-        if (lane == 0) {
-            uint32_t stage = 0, phase = 0;
-            bool ok = true;
-            Cursor cur;
-            Tile t;
-            for (int item = unit; ok && cur.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, t); item += units) {
-                for (int kb = 0; kb < p.kstages; ++kb) {
-                    if (!mbar_wait(&landed[stage], phase, abort_flag, p.wait_ns)) {
-                        ok = false;
-                        break;
-                    }
-                    fence_proxy_async_smem();
+        uint32_t stage = 0, phase = 0;
+        bool ok = true;
+        Cursor cur;
+        Tile t;
+        for (int item = unit; ok && cur.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, t); item += units) {
+            for (int kb = 0; kb < p.kstages; ++kb) {
+                ok = mbar_wait_warp(&landed[stage], phase, abort_flag, p.wait_ns);
+                if (!ok) break;
+                fence_proxy_async_smem();
+                if (elect_one()) {
                     if (CF::PAIR && rank != 0) mbar_arrive_peer(mapa_shared(smem_u32(&full[stage]), 0));
                     else mbar_arrive(&full[stage]);
-                    if (++stage == S) {
-                        stage = 0;
-                        phase ^= 1;
-                    }
+                }
+                __syncwarp();
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1;
                 }
             }
-            if (!ok) fail(p, ERR_TIMEOUT_PRODUCER, abort_flag);
         }
-        __syncwarp();
+        if (!ok && lane == 0) fail(p, ERR_TIMEOUT_PRODUCER, abort_flag);
     } else if (CF::GATHER && warp >= CF::GATHER_WARP0) {
         // ---------------------------------------------------------------- gather
         // Eight lanes copy the 16-byte chunks of one row's slice, four rows a warp; every

@@ -51,29 +51,16 @@ __device__ __forceinline__ void mbar_arrive_peer(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-// A bounded wait that polls with test_wait. (try_wait, which may suspend the thread,
-// costs more where many warps of a CTA wait: with eight converter warps polling, the
-// MMA issuer took 1300 clocks a stage instead of 1060.)
-__device__ __forceinline__ bool mbar_poll(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
-    if (mbar_test(bar, parity)) return true;
-    const uint64_t t0 = globaltimer();
-    while (true) {
-#pragma unroll 1
-        for (int i = 0; i < 64; ++i)
-            if (mbar_test(bar, parity)) return true;
-        if (abort != nullptr && *abort) return false;
-        if (globaltimer() - t0 > limit_ns) return false;
-    }
-}
-
-// A wait by a whole warp, polled by one lane (32 polling lanes take 32 turns in the
-// shared-memory unit). The outcome is the same in every lane.
+// Waits by a whole converged warp: the outcome is the same in every lane. (Polling by one
+// lane and broadcasting cost 200 clocks even on a completed barrier: the int8 product of
+// one row took 50 us instead of 42, a gathered prompt 406 instead of 385.)
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
-    unsigned ok = 1;
-    if ((threadIdx.x & 31) == 0) ok = mbar_poll(bar, parity, abort, limit_ns);
-    ok = __shfl_sync(0xffffffffu, ok, 0);
-    __syncwarp();
-    return ok != 0;
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, limit_ns)) != 0;
+}
+template <bool CLUSTER>
+__device__ __forceinline__ bool mbar_wait_warp_at(uint64_t* bar, uint32_t parity, volatile int* abort, uint64_t limit_ns) {
+    return __all_sync(0xffffffffu, CLUSTER ? mbar_wait_cluster(bar, parity, abort, limit_ns)
+                                           : mbar_wait(bar, parity, abort, limit_ns)) != 0;
 }
 
 // 4-D and 5-D tiled loads global -> shared (coordinates innermost first), counted
