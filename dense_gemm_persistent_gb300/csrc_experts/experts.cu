@@ -67,21 +67,8 @@ dgemm_status_t check_sizes(int type, int64_t R, int64_t E, int64_t N, int64_t K,
     return DGEMM_OK;
 }
 
-// Picks the variant, encodes the tensor maps and launches.
-dgemm_status_t launch(const Call& c, const dg::host::Device& dev) {
-    const int kn = c.layout == DGEMM_B_KN, gated = c.act == DGEMM_ACT_SWIGLU;
-    const int int8 = c.type == DGEMM_GROUPED_INT8;   // (its token rows need no map: converted on the way)
-    const uint64_t esz = c.type == DGEMM_GROUPED_BF16 ? 2 : 1, sl = 128 / esz;
-    const uint64_t N = static_cast<uint64_t>(c.N), K = static_cast<uint64_t>(c.K), E = static_cast<uint64_t>(c.E);
-    // KN: both halves of a gated product start on 16 bytes
-    if (kn && gated && (N / 2) * esz % 16 != 0) return DGEMM_ERR_MISALIGNED;
-    // CTA pairs (256 channels, up to 256 rows a tile) where groups are long enough to
-    // share weights between two SMs; single CTAs (128 channels, up to 64 rows) where
-    // the calls read weights for few rows each.
-    const int pair = c.R > 48 * c.E;
-    const Variant* v = find_variant(c.type, kn, pair, c.a_rows != nullptr);
-    if (!v) return DGEMM_ERR_NOT_SUPPORTED;
-
+// What every kernel of a call is given.
+dg::experts::Params make_params(const Call& c, const dg::host::Device& dev) {
     dg::experts::Params p{};
     p.offsets = c.offsets;
     p.a_rows = c.a_rows;
@@ -98,20 +85,81 @@ dgemm_status_t launch(const Call& c, const dg::host::Device& dev) {
     p.N = static_cast<int>(c.N);
     p.K = static_cast<int>(c.K);
     p.a_count = static_cast<int>(c.a_count);
-    p.gated = gated;
-    p.wide = gated ? p.N / 2 : p.N;
+    p.gated = c.act == DGEMM_ACT_SWIGLU;
+    p.wide = p.gated ? p.N / 2 : p.N;
     p.act = c.act;
     p.d_f32 = c.d_dtype == DGEMM_F32;
-    const int tile_channels = (gated ? 64 : 128) * v->ctas;
-    p.ctiles = (p.wide + tile_channels - 1) / tile_channels;
-    const uint64_t ks = static_cast<uint64_t>(v->slices);
-    p.kstages = static_cast<int>((K + ks * sl - 1) / (ks * sl));
-    p.k_whole = K % sl == 0 && !int8;
     p.alpha = c.alpha;
     p.status = dev.status;
     p.epoch = dg::host::next_launch_epoch();
     p.ws_status = c.ws && c.ws_bytes >= DGEMM_WS_STATUS_BYTES ? static_cast<unsigned long long*>(c.ws) : nullptr;
     dg::host::wait_settings(&p.wait_ns, &p.stall_after);
+    return p;
+}
+
+// Shared memory of the kernels of few rows: the rows, and the schedule.
+constexpr size_t kFewSharedBytes = 74 * 1024;     // three CTAs an SM
+constexpr int kFewRows = 4;
+
+// Rows of a tile of the few-rows kernel for an int8 call, 0 where the tensor-core kernel
+// takes it: the first's work grows with the rows, the second's hardly does. Over 64 experts of
+// 2048 x 4096 a mean of 4 rows took 117 us against 141, a mean of 8 169 against 171, of 12 240
+// against 174.
+int few_rows(const Call& c) {
+    if (c.type != DGEMM_GROUPED_INT8 || c.K == 0 || c.K > 131071) return 0;
+    const int64_t mean = (c.R + c.E - 1) / c.E;
+    for (int rows = 1; rows <= kFewRows; rows *= 2)
+        if (mean <= rows && rows * static_cast<size_t>(c.K) + dg::experts::Schedule::bytes(static_cast<int>(c.E)) <=
+                                kFewSharedBytes)
+            return rows;
+    return 0;
+}
+
+dgemm_status_t launch_few(const Call& c, const dg::host::Device& dev, int rows) {
+    int n = 0, at = 0;
+    const dg::experts::FewVariant* v = dg::experts::variants_few(&n);
+    while (at < n && v[at].rows != rows) ++at;
+    if (at == n) return DGEMM_ERR_NOT_SUPPORTED;
+    v += at;
+    dg::experts::Params p = make_params(c, dev);
+    const int tile_channels = p.gated ? v->tile / 2 : v->tile;
+    p.ctiles = (p.wide + tile_channels - 1) / tile_channels;
+    const int64_t most_tiles = ((c.R + rows - 1) / rows + std::min(c.E, c.R)) * p.ctiles;
+    if (most_tiles > INT32_MAX / 2) return DGEMM_ERR_NOT_SUPPORTED;
+    const int grid = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(dev.num_sms) * v->ctas_per_sm, most_tiles));
+    static std::atomic<unsigned char> ready[3][dg::host::kMaxDevices];
+    std::atomic<unsigned char>& flag = ready[at][dev.id];
+    if (!flag.load(std::memory_order_acquire)) {
+        if (cudaFuncSetAttribute(v->func, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(kFewSharedBytes)) != cudaSuccess)
+            return DGEMM_ERR_CUDA;
+        flag.store(1, std::memory_order_release);
+    }
+    const size_t smem = rows * static_cast<size_t>(c.K) + dg::experts::Schedule::bytes(p.E);
+    return v->launch(c.B, p, grid, smem, c.stream) == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
+}
+
+// Picks the variant, encodes the tensor maps and launches.
+dgemm_status_t launch(const Call& c, const dg::host::Device& dev) {
+    const int kn = c.layout == DGEMM_B_KN, gated = c.act == DGEMM_ACT_SWIGLU;
+    const int int8 = c.type == DGEMM_GROUPED_INT8;   // (its token rows need no map: converted on the way)
+    const uint64_t esz = c.type == DGEMM_GROUPED_BF16 ? 2 : 1, sl = 128 / esz;
+    const uint64_t N = static_cast<uint64_t>(c.N), K = static_cast<uint64_t>(c.K), E = static_cast<uint64_t>(c.E);
+    // KN: both halves of a gated product start on 16 bytes
+    if (kn && gated && (N / 2) * esz % 16 != 0) return DGEMM_ERR_MISALIGNED;
+    // CTA pairs (256 channels, up to 256 rows a tile) where groups are long enough to
+    // share weights between two SMs; single CTAs (128 channels, up to 64 rows) where
+    // the calls read weights for few rows each.
+    const int pair = c.R > 48 * c.E;
+    const Variant* v = find_variant(c.type, kn, pair, c.a_rows != nullptr);
+    if (!v) return DGEMM_ERR_NOT_SUPPORTED;
+
+    dg::experts::Params p = make_params(c, dev);
+    const int tile_channels = (gated ? 64 : 128) * v->ctas;
+    p.ctiles = (p.wide + tile_channels - 1) / tile_channels;
+    const uint64_t ks = static_cast<uint64_t>(v->slices);
+    p.kstages = static_cast<int>((K + ks * sl - 1) / (ks * sl));
+    p.k_whole = K % sl == 0 && !int8;
 
     // at most one partial tile per group
     const int64_t most_tiles = ((c.R + v->bn - 1) / v->bn + std::min(c.E, c.R)) * p.ctiles;
@@ -194,7 +242,8 @@ dgemm_status_t run_experts(const Call& c) {
     const dgemm_status_t ds = dg::host::current_device(&dev);
     if (ds != DGEMM_OK) return ds;
 
-    return launch(c, dev);
+    const int rows = few_rows(c);
+    return rows ? launch_few(c, dev, rows) : launch(c, dev);
 }
 
 }  // namespace

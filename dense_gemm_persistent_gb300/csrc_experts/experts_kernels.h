@@ -25,5 +25,13 @@ const Variant* variants_bf16_kn(int* count);
 const Variant* variants_fp8(int* count);
 const Variant* variants_int8(int* count);
 
+// Few rows a group (int8).
+struct FewVariant {
+    int rows, tile, ctas_per_sm;   // rows of a tile; weight rows of a tile
+    const void* func;
+    cudaError_t (*launch)(const void* B, const Params& p, int grid, size_t smem, cudaStream_t s);
+};
+const FewVariant* variants_few(int* count);
+
 }  // namespace experts
 }  // namespace dg

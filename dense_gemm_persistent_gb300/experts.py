@@ -27,12 +27,37 @@ _I32 = (torch.int32,)
 _BF16 = (torch.bfloat16,)
 _CODES8 = (torch.float8_e4m3fn, torch.uint8)
 _INT8 = (torch.int8,)
+_current_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _need(t, name, shape, dtypes):
+    # the common case in few steps; anything else is looked at, and named, below
+    if t is not None and t.dtype in dtypes and t.is_cuda and (shape is None or t.shape == shape) and t.is_contiguous():
+        return
     if t is None:
         raise ValueError(f"{name} is required")
     _dg._require(t, name, shape, dtypes)
+
+
+def _maybe(t, name, shape, dtypes):
+    if t is not None:
+        _need(t, name, shape, dtypes)
+
+
+def _stream(stream, t):
+    """The raw stream: the given one, else the current one of t's device."""
+    if stream is None and t.is_cuda:
+        return _current_raw_stream(t.get_device())
+    return _dg._stream(stream)
+
+
+def _workspace(ws):
+    """(pointer, bytes) of the workspace tensor, or of none."""
+    if ws is None:
+        return None, 0
+    if not (ws.is_cuda and ws.is_contiguous()):
+        _dg._require(ws, "ws")
+    return ws.data_ptr(), ws.nbytes
 
 
 def _matrix(t, name, dtypes, dims=2):
@@ -43,10 +68,6 @@ def _matrix(t, name, dtypes, dims=2):
 
 def _float_code(t) -> int:
     return F32 if t.dtype == torch.float32 else BF16
-
-
-def _bytes(ws) -> int:
-    return 0 if ws is None else ws.numel() * ws.element_size()
 
 
 def _act(act) -> int:
@@ -74,10 +95,9 @@ def dgemm_route(logits, k, ids, weights, offsets, row_token, slot_row, *, renorm
     _need(offsets, "offsets", (E + 1,), _I32)
     _need(row_token, "row_token", (T * k,), _I32)
     _need(slot_row, "slot_row", (T, k), _I32)
-    _dg._require(ws, "ws")
     code = _dg.load().dgemm_route(logits.data_ptr(), _float_code(logits), T, E, k, int(bool(renormalize)), ids.data_ptr(),
                                   weights.data_ptr(), offsets.data_ptr(), row_token.data_ptr(), slot_row.data_ptr(),
-                                  _dg._ptr(ws), _bytes(ws), _dg._stream(stream))
+                                  *_workspace(ws), _stream(stream, logits))
     _dg._check(code, "dgemm_route")
 
 
@@ -97,14 +117,14 @@ def dgemm_combine(Y, slot_row, weights, out, *, add=None, stream=None):
     T, k = slot_row.shape
     _need(weights, "weights", (T, k), _F32)
     _need(out, "out", (T, H), _FLOATS)
-    _dg._require(add, "add", (T, H), _BF16)
+    _maybe(add, "add", (T, H), _BF16)
     code = _dg.load().dgemm_combine(Y.data_ptr(), R, slot_row.data_ptr(), weights.data_ptr(), _dg._ptr(add),
-                                    out.data_ptr(), _float_code(out), T, H, k, _dg._stream(stream))
+                                    out.data_ptr(), _float_code(out), T, H, k, _stream(stream, Y))
     _dg._check(code, "dgemm_combine")
     return out
 
 
-def _grouped_sizes(A, B, offsets, D, a_rows, b_layout, bias, act, ws, dtypes):
+def _grouped_sizes(A, B, offsets, D, a_rows, b_layout, bias, act, dtypes):
     _matrix(A, "A", dtypes)
     _matrix(B, "B", dtypes, 3)
     if b_layout == "nk":
@@ -125,8 +145,7 @@ def _grouped_sizes(A, B, offsets, D, a_rows, b_layout, bias, act, ws, dtypes):
     code = _act(act)
     _need(offsets, "offsets", (E + 1,), _I32)
     _need(D, "D", (R, N // 2 if act == "swiglu" else N), _FLOATS)
-    _dg._require(bias, "bias", (E, N), _F32)
-    _dg._require(ws, "ws")
+    _maybe(bias, "bias", (E, N), _F32)
     return E, R, N, K, count, code
 
 
@@ -140,22 +159,22 @@ def dgemm_grouped_bf16(A, B, offsets, D, *, a_rows=None, b_layout="nk", bias=Non
     gate's channels first in B). Rows outside every group are not written.
     ws: optional uint8 workspace (dgemm_grouped_workspace_size). Returns D.
     """
-    E, R, N, K, count, code = _grouped_sizes(A, B, offsets, D, a_rows, b_layout, bias, act, ws, _BF16)
+    E, R, N, K, count, code = _grouped_sizes(A, B, offsets, D, a_rows, b_layout, bias, act, _BF16)
     st = _dg.load().dgemm_grouped_bf16(A.data_ptr(), count, _dg._ptr(a_rows), B.data_ptr(),
                                        B_KN if b_layout == "kn" else B_NK, offsets.data_ptr(), E, D.data_ptr(),
-                                       _float_code(D), R, N, K, float(alpha), _dg._ptr(bias), code, _dg._ptr(ws),
-                                       _bytes(ws), _dg._stream(stream))
+                                       _float_code(D), R, N, K, float(alpha), _dg._ptr(bias), code, *_workspace(ws),
+                                       _stream(stream, A))
     _dg._check(st, "dgemm_grouped_bf16")
     return D
 
 
 def _grouped_scaled(name, dtypes, Aq, Bq, a_scale, b_scale, offsets, D, a_rows, bias, act, alpha, ws, stream):
-    E, R, N, K, count, code = _grouped_sizes(Aq, Bq, offsets, D, a_rows, "nk", bias, act, ws, dtypes)
+    E, R, N, K, count, code = _grouped_sizes(Aq, Bq, offsets, D, a_rows, "nk", bias, act, dtypes)
     _need(a_scale, "a_scale", (count,), _F32)
     _need(b_scale, "b_scale", (E, N), _F32)
     st = getattr(_dg.load(), name)(Aq.data_ptr(), count, _dg._ptr(a_rows), Bq.data_ptr(), a_scale.data_ptr(),
                                    b_scale.data_ptr(), offsets.data_ptr(), E, D.data_ptr(), _float_code(D), R, N, K,
-                                   float(alpha), _dg._ptr(bias), code, _dg._ptr(ws), _bytes(ws), _dg._stream(stream))
+                                   float(alpha), _dg._ptr(bias), code, *_workspace(ws), _stream(stream, Aq))
     _dg._check(st, name)
     return D
 
@@ -189,7 +208,7 @@ def dgemm_int8_quantize(X, q, scale, *, stream=None):
     _need(q, "q", (M, K), _INT8)
     _need(scale, "scale", (M,), _F32)
     code = _dg.load().dgemm_int8_quantize(X.data_ptr(), _float_code(X), q.data_ptr(), scale.data_ptr(), M, K,
-                                          _dg._stream(stream))
+                                          _stream(stream, X))
     _dg._check(code, "dgemm_int8_quantize")
     return q, scale
 
@@ -215,12 +234,11 @@ def dgemm_int8_scaled(Aq, Bq, a_scale, b_scale, D, *, C=None, alpha=1.0, beta=0.
     _need(D, "D", (M, N), _FLOATS)
     if beta != 0.0:   # C is read only then (and may be None otherwise)
         _need(C, "C", (M, N), _FLOATS)
-    _dg._require(bias, "bias", (N,), _F32)
-    _dg._require(ws, "ws")
+    _maybe(bias, "bias", (N,), _F32)
     code = _dg.load().dgemm_int8_scaled(Aq.data_ptr(), Bq.data_ptr(), a_scale.data_ptr(), b_scale.data_ptr(),
                                         _dg._ptr(C), _float_code(C) if C is not None else F32, D.data_ptr(),
                                         _float_code(D), M, N, K, float(alpha), float(beta), _dg._ptr(bias), ACT[act],
-                                        _dg._ptr(ws), _bytes(ws), _dg._stream(stream))
+                                        *_workspace(ws), _stream(stream, Aq))
     _dg._check(code, "dgemm_int8_scaled")
     return D
 

@@ -456,3 +456,26 @@ def test_route_bf16_infinity_beside_the_largest_number():
     x[:, 6] = float("inf")
     run_route(x, 3, True, BF)
     run_route(x, 3, False, BF)
+
+
+# ------------------------------------------------------------------ int8, few rows a group
+
+@pytest.mark.parametrize("sizes", [[1], [2], [3, 0, 1], [4, 4], [5, 8, 0, 7], [16], [9, 23, 0, 1], [1] * 40, [40, 0, 0, 0]])
+@pytest.mark.parametrize("K,N,act", [(16, 3, "none"), (528, 70, "swiglu"), (1040, 33, "gelu"), (4096, 130, "none")])
+def test_grouped_int8_few_rows(sizes, K, N, act):
+    check("int8", sizes, K, N, act, gather=len(sizes) > 1, with_bias=True, out=F32)
+    check("int8", sizes, K, N, act)
+
+
+@pytest.mark.parametrize("M", [1, 2, 3, 4, 7, 8, 12, 16])
+def test_int8_few_rows_exact(M):
+    """Integers at the ends of their range: the sums are exact whatever their size."""
+    K, N = 6000, 37
+    g = gen(M)
+    A = randint(g, 0, 1, M, K).mul(255).sub(128).to(I8)      # -128 or 127
+    B = torch.full((N, K), -128, dtype=I8)
+    one = lambda n: torch.ones(n, device=dev())
+    D = torch.empty(M, N, device=dev())
+    dg.dgemm_int8_scaled(A.to(dev()), B.to(dev()), one(M), one(N), D)
+    want = A.to(torch.float64) @ B.to(torch.float64).t()
+    assert torch.equal(D.cpu(), want.to(F32))
