@@ -5,12 +5,13 @@
 // the FP32 sum. A byte b becomes FP16 with one byte permute and one subtraction:
 // with u = b + 128 (a flipped sign bit), the bits 0x6400 | u are 1024 + u, less 1152.
 //
-// Weights come by TMA as codes, are read back, converted and stored to the slices that
-// the MMA reads; token rows go from global memory through registers to theirs.
-// Shared memory moves 160 KB for 128 K of a 256 x 256 tile of a CTA pair (1250 of its
-// clocks, with 1375 at the tensor core's sustained rate). Converted weights in Tensor Memory
-// instead (112 KB) were slower: an MMA with A there took 140-165 clocks whatever its
-// columns, and its stages left room for 192 columns only (4096 x 11008 x 4096: 402 us).
+// Weights come by TMA as codes and go through registers into Tensor Memory, where the
+// MMA takes its A operand from; token rows go from global memory through registers to
+// shared memory, its B operand. 128 K of a 256 x 192 tile of a CTA pair move 80 KB through
+// each SM's shared memory; with the converted weights there too (256 x 256 tiles) it
+// was 160 KB, 78 % of what shared memory can move in the time taken: 4096 x 11008 x 4096
+// 367 us against 333, 768 rows over 64 experts of 2048 x 4096 162 against 150. Three teams of weight
+// converters were slower (351, 159): fewer registers each.
 // Warps of a CTA:
 //   0       TMA producer of weight codes: 128 channels x 128 K, 128B swizzle
 //   1       MMA issuer, owner of the Tensor Memory
@@ -18,8 +19,8 @@
 //   4-7     epilogue
 //   8-15    weight converters, one channel a thread; two teams
 //   16-23   token converters, rows by index or in order; two teams
-// A converted stage is 64 K; team 0 makes the even ones, team 1 the odd ones, since a
-// stage passes through a chain of waits and conversions longer than its MMAs.
+// A converted stage is 64 K; the teams take them in turn, since a stage passes through a
+// chain of waits and conversions (~1500 clocks) longer than its MMAs (~700).
 #pragma once
 
 #include "experts_common.cuh"
@@ -32,21 +33,23 @@ template <bool PAIR_>
 struct Int8Cfg {
     static constexpr bool PAIR = PAIR_;
     static constexpr int CTAS = PAIR ? 2 : 1;
-    static constexpr int BN = PAIR ? 256 : 64;           // most token rows of a tile
+    static constexpr int BN = PAIR ? 192 : 64;           // most token rows of a tile
     static constexpr int BN_CTA = BN / CTAS;
     static constexpr int KB = 128, KC = 64;              // K of a raw and of a converted stage
-    static constexpr int W_RAW = 128 * KB, W_STAGES = PAIR ? 4 : 6;
-    static constexpr int W_CONV = 128 * KC * 2, X_CONV = BN_CTA * KC * 2, CONV = W_CONV + X_CONV;
-    static constexpr int C_STAGES = 4;
-    static constexpr int EPI_WARPS = 4, EPI_WARP0 = 4, W_WARP0 = 8, X_WARP0 = 16, TEAMS = 2;
-    static constexpr int THREADS = 768;
+    static constexpr int W_RAW = 128 * KB, W_STAGES = 8;
+    static constexpr int X_CONV = BN_CTA * KC * 2;       // a converted stage: rows here, weights in Tensor Memory
+    static constexpr int A_COLS = KC / 2, C_STAGES = 4;
+    static constexpr int ACC_COLS = 2 * BN;
+    static constexpr int EPI_WARPS = 4, EPI_WARP0 = 4, W_WARP0 = 8, W_TEAMS = 2, X_WARP0 = W_WARP0 + 4 * W_TEAMS, X_TEAMS = 2;
+    static constexpr int THREADS = 32 * (X_WARP0 + 4 * X_TEAMS);
     // registers per thread: at launch, and of the warpgroups after the split
     static constexpr int LAUNCH_REGS = 80, REGS_CONTROL = 48, REGS_EPILOGUE = 128, REGS_WEIGHTS = 72, REGS_TOKENS = 80;
-    static_assert(REGS_CONTROL + REGS_EPILOGUE + TEAMS * (REGS_WEIGHTS + REGS_TOKENS) <= THREADS / 128 * LAUNCH_REGS,
+    static_assert(REGS_CONTROL + REGS_EPILOGUE + W_TEAMS * REGS_WEIGHTS + X_TEAMS * REGS_TOKENS <= THREADS / 128 * LAUNCH_REGS,
                   "register split exceeds the launch allocation");
-    static constexpr int TMEM_COLS = 2 * BN;
+    static constexpr int TMEM_COLS = ACC_COLS + C_STAGES * A_COLS;
+    static_assert(TMEM_COLS == 256 || TMEM_COLS == 512, "Tensor Memory");
     static constexpr int BAR_BYTES = 384;
-    static constexpr int BUFFERS = W_STAGES * W_RAW + C_STAGES * CONV;
+    static constexpr int BUFFERS = W_STAGES * W_RAW + C_STAGES * X_CONV;
     static constexpr int FIXED = 1024 + BUFFERS + exchange_bytes<EPI_WARPS>() + BAR_BYTES;
     static constexpr uint32_t IDESC0 = make_idesc(0u, false, false, 128 * CTAS, 0);   // FP16 operands
     static_assert(FIXED + Schedule::bytes(DGEMM_MAX_EXPERTS) <= 232448, "shared memory");
@@ -65,7 +68,7 @@ template <class CF>
 __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_constant__ CUtensorMap tmW, const Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* wraw = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* conv = wraw + CF::W_STAGES * CF::W_RAW;     // converted stages: weights, then rows
+    uint8_t* conv = wraw + CF::W_STAGES * CF::W_RAW;     // converted rows
     float* exchange = reinterpret_cast<float*>(wraw + CF::BUFFERS);
     uint64_t* w_full = reinterpret_cast<uint64_t*>(wraw + CF::BUFFERS + exchange_bytes<CF::EPI_WARPS>());
     uint64_t* w_empty = w_full + CF::W_STAGES;
@@ -86,7 +89,7 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
     if (threadIdx.x == 0) {
         for (int s = 0; s < CF::W_STAGES; ++s) {
             mbar_init(&w_full[s], 1);
-            mbar_init(&w_empty[s], 8);                   // every weight converter warp
+            mbar_init(&w_empty[s], 8);                   // the teams that convert its two halves
         }
         for (int s = 0; s < CF::C_STAGES; ++s) {
             mbar_init(&full[s], 8 * CF::CTAS);           // a team's warps of both converters, of both CTAs
@@ -122,7 +125,6 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
     const uint32_t tmem = *tmem_slot;
     // converter warps: their part of converted stage g is in place ...
     auto converted = [&](uint32_t g) {
-        fence_proxy_async_smem();
         __syncwarp();
         uint64_t* bar = &full[g % CF::C_STAGES];
         if (lane == 0) {
@@ -176,8 +178,7 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issuer
         if (rank == 0) {
-            const uint64_t wd0 = smem_desc_sw128(smem_u32(conv), 16, 1024);
-            const uint64_t xd0 = smem_desc_sw128(smem_u32(conv) + CF::W_CONV, 16, 1024);
+            const uint64_t xd0 = smem_desc_sw128(smem_u32(conv), 16, 1024);
             uint32_t g = 0;                              // converted stages so far
             int local = 0;
             const uint32_t tmem_u = __shfl_sync(kAllLanes, tmem, 0);   // (values and branches that the compiler knows to
@@ -195,13 +196,13 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
                     ok = mbar_wait_warp_at<CF::PAIR>(&full[slot], phase, abort_flag, p.wait_ns);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint64_t wd = wd0 + slot * (CF::CONV >> 4), xd = xd0 + slot * (CF::CONV >> 4);
+                    const uint32_t a = tmem_u + CF::ACC_COLS + slot * CF::A_COLS;
+                    const uint64_t xd = xd0 + slot * (CF::X_CONV >> 4);
                     if (elect_one()) {
 #pragma unroll
                         for (int k = 0; k < CF::KC / 16; ++k) {
                             const uint32_t more = (kc > 0 || k > 0) ? 1u : 0u;
-                            if constexpr (CF::PAIR) mma_bf16_pair(acc, wd + k * 2, xd + k * 2, idesc, more);
-                            else mma_bf16(acc, wd + k * 2, xd + k * 2, idesc, more);
+                            mma_16_tmem_a<CF::PAIR>(acc, a + k * 8, xd + k * 2, idesc, more);
                         }
                         if constexpr (CF::PAIR) mma_commit_pair(&done[slot], 3);
                         else mma_commit(&done[slot]);
@@ -245,49 +246,48 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
         // ---------------------------------------------------------------- weight converters
         regs_dec<CF::REGS_WEIGHTS>();
         const int team = (warp - CF::W_WARP0) >> 2;
-        const int row = threadIdx.x & 127;
-        uint32_t raw = 0, raw_phase = 0, g = team;
+        const int row = threadIdx.x & 127;                   // TMEM lane: the warp's own quarter
+        const uint32_t a_base = tmem + CF::ACC_COLS + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        uint32_t g = 0;
+        int turn = team;                                     // stages until this team's next
         for (int item = unit; ok && cur.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, t); item += units) {
-            for (int kb = 0; kb < p.kstages; ++kb, g += CF::TEAMS) {
-                if (!mbar_wait_warp(&w_full[raw], raw_phase, abort_flag, p.wait_ns)) {
-                    ok = false;
-                    break;
-                }
+            for (int kc = 0; kc < 2 * p.kstages; ++kc, ++g) {
+                if (turn-- > 0) continue;
+                turn = CF::W_TEAMS - 1;
+                const uint32_t raw = (g >> 1) % CF::W_STAGES, half = g & 1;
+                ok = mbar_wait_warp(&w_full[raw], ((g >> 1) / CF::W_STAGES) & 1, abort_flag, p.wait_ns);
+                if (!ok) break;
                 const uint8_t* src = wraw + raw * CF::W_RAW + row * 128;
                 uint4 codes[4];
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
-                    codes[c] = *reinterpret_cast<const uint4*>(src + (((team * 4 + c) ^ (row & 7)) << 4));
+                    codes[c] = *reinterpret_cast<const uint4*>(src + (((half * 4 + c) ^ (row & 7)) << 4));
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&w_empty[raw]);   // the codes are in registers
-                uint4 h[8];
+                uint32_t h[32];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    int8x4_to_f16(codes[c].x, h[2 * c].x, h[2 * c].y);
-                    int8x4_to_f16(codes[c].y, h[2 * c].z, h[2 * c].w);
-                    int8x4_to_f16(codes[c].z, h[2 * c + 1].x, h[2 * c + 1].y);
-                    int8x4_to_f16(codes[c].w, h[2 * c + 1].z, h[2 * c + 1].w);
+                    int8x4_to_f16(codes[c].x, h[8 * c], h[8 * c + 1]);
+                    int8x4_to_f16(codes[c].y, h[8 * c + 2], h[8 * c + 3]);
+                    int8x4_to_f16(codes[c].z, h[8 * c + 4], h[8 * c + 5]);
+                    int8x4_to_f16(codes[c].w, h[8 * c + 6], h[8 * c + 7]);
                 }
-                if (!slot_free(g)) {
-                    ok = false;
-                    break;
-                }
-                uint8_t* dst = conv + g % CF::C_STAGES * CF::CONV + row * 128;
-#pragma unroll
-                for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(dst + ((c ^ (row & 7)) << 4)) = h[c];
+                ok = slot_free(g);
+                if (!ok) break;
+                tc_fence_after();
+                tmem_st32(a_base + g % CF::C_STAGES * CF::A_COLS, h);
+                tmem_st_wait();
+                tc_fence_before();
                 converted(g);
-                if (++raw == CF::W_STAGES) {
-                    raw = 0;
-                    raw_phase ^= 1;
-                }
             }
         }
         if (!ok) fail(p, ERR_TIMEOUT_PRODUCER, abort_flag);
         __syncwarp();
     } else {
         // ---------------------------------------------------------------- token converters
-        // Four threads load and convert a row's 64 codes, 16 each; a team's next stage is
-        // being loaded while it converts this one.
+        // Four threads load and convert a row's 64 codes, 16 each; a team's next two stages are
+        // being loaded while it converts one (in two register sets whose loads are waited
+        // for apart).
         regs_dec<CF::REGS_TOKENS>();
         constexpr int ROUNDS = CF::BN_CTA / 32;
         const int team = (warp - CF::X_WARP0) >> 2;
@@ -308,48 +308,58 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
                 }
             }
         };
-        uint4 next[ROUNDS];
-        auto load = [&]() {
+        struct Held {
+            uint4 codes[ROUNDS];
+            int rounds;                                      // 0: past the last stage
+        };
+        auto load = [&](Held& h) {                           // the team's next stage
+            h.rounds = live ? rounds : 0;
+            if (!live) return;
             const int k = kb * CF::KB + team * CF::KC + chunk * 16;
             const char* base = static_cast<const char*>(p.A) + k;
 #pragma unroll
             for (int i = 0; i < ROUNDS; ++i) {
-                next[i] = make_uint4(0, 0, 0, 0);
-                if (live && src[i] >= 0 && k < p.K)
-                    next[i] = __ldg(reinterpret_cast<const uint4*>(base + static_cast<int64_t>(src[i]) * p.K));
+                h.codes[i] = make_uint4(0, 0, 0, 0);
+                if (src[i] >= 0 && k < p.K)
+                    h.codes[i] = __ldg(reinterpret_cast<const uint4*>(base + static_cast<int64_t>(src[i]) * p.K));
             }
-        };
-        if (live) point();
-        load();
-        for (uint32_t g = team; live; g += CF::TEAMS) {
-            uint4 codes[ROUNDS];
-#pragma unroll
-            for (int i = 0; i < ROUNDS; ++i) codes[i] = next[i];
-            const int now = rounds;
             if (++kb == p.kstages) {
                 kb = 0;
                 item += units;
                 live = cur.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, t);
                 if (live) point();
             }
-            load();
-            if (!slot_free(g)) {
-                ok = false;
-                break;
-            }
-            uint8_t* dst = conv + g % CF::C_STAGES * CF::CONV + CF::W_CONV + sub * 128;
+        };
+        uint32_t g = team;
+        auto convert = [&](const Held& h) {
+            if (!slot_free(g)) return false;
+            uint8_t* dst = conv + g % CF::C_STAGES * CF::X_CONV + sub * 128;
 #pragma unroll
             for (int i = 0; i < ROUNDS; ++i) {
-                if (i >= now) break;
+                if (i >= h.rounds) break;
                 uint4 lo, hi;
-                int8x4_to_f16(codes[i].x, lo.x, lo.y);
-                int8x4_to_f16(codes[i].y, lo.z, lo.w);
-                int8x4_to_f16(codes[i].z, hi.x, hi.y);
-                int8x4_to_f16(codes[i].w, hi.z, hi.w);
+                int8x4_to_f16(h.codes[i].x, lo.x, lo.y);
+                int8x4_to_f16(h.codes[i].y, lo.z, lo.w);
+                int8x4_to_f16(h.codes[i].z, hi.x, hi.y);
+                int8x4_to_f16(h.codes[i].w, hi.z, hi.w);
                 *reinterpret_cast<uint4*>(dst + i * 4096 + at0) = lo;
                 *reinterpret_cast<uint4*>(dst + i * 4096 + at1) = hi;
             }
+            fence_proxy_async_smem();
             converted(g);
+            g += CF::X_TEAMS;
+            return true;
+        };
+        Held even, odd;
+        if (live) point();
+        load(even);
+        load(odd);
+        while (ok && even.rounds > 0) {
+            ok = convert(even);
+            load(even);
+            if (!ok || odd.rounds == 0) break;
+            ok = convert(odd);
+            load(odd);
         }
         if (!ok) fail(p, ERR_TIMEOUT_PRODUCER, abort_flag);
         __syncwarp();
