@@ -214,11 +214,10 @@ __host__ __device__ constexpr int exchange_bytes() { return EPI_WARPS / 2 * 2 * 
 // channel swap 16 columns each through shared memory, so both do half of the products.
 //   acc      TMEM address of the accumulator (lane 0)
 //   ready()  waits for it; released() hands it back after the last read
-template <int EPI_WARPS, int MAX_N, class Ready, class Released>
+template <int EPI_WARPS, class Ready, class Released>
 __device__ __forceinline__ bool tile_epilogue(const Params& p, const Tile& t, uint32_t acc, int ew, int cta_chan0,
                                               float* exchange, Ready ready, Released released) {
     constexpr int COLS = EPI_WARPS / 4;                      // warps that share a lane quarter
-    constexpr int CHUNKS = (MAX_N / 32 + COLS - 1) / COLS;   // chunks of 32 columns a warp may have
     const int lane = threadIdx.x & 31, q = ew & 3, part = ew >> 2;
     const int i = q * 32 + lane;                             // accumulator lane
     const int ch = cta_chan0 + (p.gated ? (i & 63) : i);     // channel of D
@@ -230,18 +229,14 @@ __device__ __forceinline__ bool tile_epilogue(const Params& p, const Tile& t, ui
         if (p.b_scale) bs *= __ldg(p.b_scale + en);
         if (p.bias) bias = __ldg(p.bias + en);
     }
-    float as[CHUNKS];                                        // lane j: the scale of column j of the chunk
-    if (p.a_scale) {
-#pragma unroll
-        for (int c = 0; c < CHUNKS; ++c) {
-            const int col = (c * COLS + part) * 32 + lane;
-            as[c] = 0.0f;
-            if (col < t.rows) {
-                const int a = p.a_rows ? __ldg(p.a_rows + t.row0 + col) : t.row0 + col;
-                if (a >= 0 && a < p.a_count) as[c] = __ldg(p.a_scale + a);
-            }
-        }
-    }
+    // lane j: the scale of column j of a chunk
+    auto column_scale = [&](int c) {
+        const int col = (c * COLS + part) * 32 + lane;
+        if (!p.a_scale || col >= t.rows) return 0.0f;
+        const int a = p.a_rows ? __ldg(p.a_rows + t.row0 + col) : t.row0 + col;
+        return a >= 0 && a < p.a_count ? __ldg(p.a_scale + a) : 0.0f;
+    };
+    float as_next = column_scale(0);
     bool ok = ready();
     const int swap_id = 1 + part * 2 + (q & 1);              // barrier of warps q and q ^ 2
     if (p.gated) ok = pair_all(swap_id, ok);
@@ -258,10 +253,13 @@ __device__ __forceinline__ bool tile_epilogue(const Params& p, const Tile& t, ui
         if (lane == 0) released();
     };
     if (part >= chunks) hand_back();
-#pragma unroll
-    for (int c = 0; c < CHUNKS; ++c) {
+    // (one copy of the loop's code: unrolled, it pushed the other warps' loops out of the
+    // instruction cache)
+#pragma unroll 1
+    for (int c = 0; c * COLS + part < chunks; ++c) {
         const int col0 = (c * COLS + part) * 32;
-        if (c * COLS + part >= chunks) break;
+        const float as = as_next;
+        as_next = column_scale(c + 1);
         uint32_t r[32];
         tmem_ld32(acc + (static_cast<uint32_t>(q * 32) << 16) + col0, r);
         tmem_ld_wait();
@@ -273,7 +271,7 @@ __device__ __forceinline__ bool tile_epilogue(const Params& p, const Tile& t, ui
         } else if (p.a_scale) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-                v[j] = fmaf(__uint_as_float(r[j]), bs * __shfl_sync(kAllLanes, as[c], j), bias);
+                v[j] = fmaf(__uint_as_float(r[j]), bs * __shfl_sync(kAllLanes, as, j), bias);
         } else {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = fmaf(__uint_as_float(r[j]), bs, bias);

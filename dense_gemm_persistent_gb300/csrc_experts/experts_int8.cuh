@@ -37,6 +37,7 @@ struct Int8Cfg {
     static constexpr int BN_CTA = BN / CTAS;
     static constexpr int KB = 128, KC = 64;              // K of a raw and of a converted stage
     static constexpr int W_RAW = 128 * KB, W_STAGES = 8;
+    static constexpr int AHEAD = 2;           // stages that a token converter team loads ahead
     static constexpr int X_CONV = BN_CTA * KC * 2;       // a converted stage: rows here, weights in Tensor Memory
     static constexpr int A_COLS = KC / 2, C_STAGES = 4;
     static constexpr int ACC_COLS = 2 * BN;
@@ -231,7 +232,7 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
         int local = 0;
         for (int item = unit; ok && cur.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, t); item += units, ++local) {
             const int buf = local & 1;
-            ok = tile_epilogue<CF::EPI_WARPS, CF::BN>(
+            ok = tile_epilogue<CF::EPI_WARPS>(
                 p, t, tmem + static_cast<uint32_t>(buf * CF::BN), warp - CF::EPI_WARP0,
                 t.chan0 + static_cast<int>(rank) * (p.gated ? 64 : 128), exchange,
                 [&]() { return mbar_wait_warp(&acc_full[buf], (local >> 1) & 1, abort_flag, p.wait_ns); },
@@ -285,9 +286,8 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
         __syncwarp();
     } else {
         // ---------------------------------------------------------------- token converters
-        // Four threads load and convert a row's 64 codes, 16 each; a team's next two stages are
-        // being loaded while it converts one (in two register sets whose loads are waited
-        // for apart).
+        // Four threads load and convert a row's 64 codes, 16 each, AHEAD of the team's stages
+        // ahead of their conversion.
         regs_dec<CF::REGS_TOKENS>();
         constexpr int ROUNDS = CF::BN_CTA / 32;
         const int team = (warp - CF::X_WARP0) >> 2;
@@ -350,16 +350,19 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
             g += CF::X_TEAMS;
             return true;
         };
-        Held even, odd;
+        Held held[CF::AHEAD];
         if (live) point();
-        load(even);
-        load(odd);
-        while (ok && even.rounds > 0) {
-            ok = convert(even);
-            load(even);
-            if (!ok || odd.rounds == 0) break;
-            ok = convert(odd);
-            load(odd);
+#pragma unroll
+        for (int i = 0; i < CF::AHEAD; ++i) load(held[i]);
+        bool more = true;
+        while (ok && more) {
+#pragma unroll
+            for (int i = 0; i < CF::AHEAD; ++i) {
+                more = more && held[i].rounds > 0;
+                if (!more || !ok) break;
+                ok = convert(held[i]);
+                load(held[i]);
+            }
         }
         if (!ok) fail(p, ERR_TIMEOUT_PRODUCER, abort_flag);
         __syncwarp();

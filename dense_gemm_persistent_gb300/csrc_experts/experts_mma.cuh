@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(CF::THREADS, 1)
         Tile t;
         for (int item = unit; ok && cur.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, t); item += units, ++local) {
             const int buf = local & 1;
-            ok = tile_epilogue<CF::EPI_WARPS, CF::BN>(
+            ok = tile_epilogue<CF::EPI_WARPS>(
                 p, t, tmem + static_cast<uint32_t>(buf * CF::BN), ew,
                 t.chan0 + static_cast<int>(rank) * (p.gated ? 64 : 128), exchange,
                 [&]() { return mbar_wait_warp(&acc_full[buf], (local >> 1) & 1, abort_flag, p.wait_ns); },
