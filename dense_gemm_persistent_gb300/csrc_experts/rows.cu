@@ -119,7 +119,7 @@ __device__ __forceinline__ float row_scale(unsigned m, float* scale) {
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
     __syncthreads();
     for (unsigned w = 0; w < blockDim.x / 32; ++w) m = max(m, part[w]);
-    float s = __fdiv_rn(__uint_as_float(m), 127.0f);
+    float s = __fmul_rn(__uint_as_float(m), 1.0f / 127.0f);
     if (s == 0.0f) s = 1.0f;              // a row of zeros (or one whose scale underflows)
     if (threadIdx.x == 0) *scale = s;
     return s;

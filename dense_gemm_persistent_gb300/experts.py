@@ -201,8 +201,8 @@ def dgemm_grouped_workspace_size(type, R, E, N, K, *, act="none") -> int:
 
 
 def dgemm_int8_quantize(X, q, scale, *, stream=None):
-    """Per-row int8 codes: scale [M] = max|X[m]| / 127, q [M,K] = X / scale rounded to
-    nearest even. X [M,K] bf16 or fp32. Returns (q, scale)."""
+    """Per-row int8 codes: scale [M] = max|X[m]| * (1 / 127) in fp32, q [M,K] = X / scale
+    rounded to nearest even. X [M,K] bf16 or fp32. Returns (q, scale)."""
     _matrix(X, "X", _FLOATS)
     M, K = X.shape
     _need(q, "q", (M, K), _INT8)

@@ -116,8 +116,9 @@ dgemm_status_t dgemm_grouped_int8_scaled(const void* Aq, int64_t a_count, const 
 /* Workspace bytes a grouped call with these sizes can use; 0 for invalid ones. */
 size_t dgemm_grouped_workspace_size(dgemm_grouped_type_t type, int64_t R, int64_t E, int64_t N, int64_t K, int act);
 
-/* Per-token quantisation: scale[m] = max_k |X[m,k]| / 127 (1 for a row of zeros)
- * and q[m,k] = X[m,k] / scale[m] rounded to the nearest integer, ties to even.
+/* Per-token quantisation: scale[m] = max_k |X[m,k]| * (1 / 127), with 1 / 127 rounded
+ * to FP32 (1 for a row of zeros), and q[m,k] = X[m,k] / scale[m], the FP32 quotient
+ * rounded to the nearest integer, ties to even.
  * The maximum is taken over finite values; infinities saturate to +-127 and NaN
  * becomes 0. X [M,K] BF16 or F32; q [M,K] int8; scale [M] F32. K any. */
 dgemm_status_t dgemm_int8_quantize(const void* X, dgemm_dtype_t x_dtype, int8_t* q, float* scale, int64_t M, int64_t K,

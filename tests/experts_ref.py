@@ -111,10 +111,12 @@ def combine(Y, slot_row, weights, add=None):
 
 
 def quantize(X):
-    """int8 codes and scales: the scale and the quotient are FP32 numbers by definition."""
+    """int8 codes and scales: the scale, a product with the FP32 number 1 / 127, and the
+    quotient are FP32 numbers by definition."""
     x = X.to(torch.float32)
     finite = torch.where(torch.isfinite(x), x.abs(), torch.zeros_like(x))
-    s = (finite.amax(1) if x.shape[1] else torch.zeros(x.shape[0])) / 127.0
+    inv127 = torch.tensor(1.0) / torch.tensor(127.0)
+    s = (finite.amax(1) if x.shape[1] else torch.zeros(x.shape[0])) * inv127
     s = torch.where(s == 0, torch.ones_like(s), s)
     q = torch.round(x / s[:, None])
     q = torch.where(torch.isnan(x), torch.zeros_like(q), torch.clamp(q, -127, 127))
