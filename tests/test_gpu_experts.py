@@ -458,6 +458,39 @@ def test_route_bf16_infinity_beside_the_largest_number():
     run_route(x, 3, False, BF)
 
 
+# ------------------------------------------------------------------ bounded waits
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("sizes,gather", [([20, 9, 14], False), ([20, 9, 14], True), ([300, 150], False), ([300, 150], True)])
+def test_grouped_wait_that_runs_out_is_reported(kind, sizes, gather):
+    """The weight producer stops after two copies (it issues nothing more): the waits for the
+    next stage run out, the call reports it on its own status word, and the next call is right."""
+    g = gen(31)
+    K, N = 2048, 300
+    a = make(kind, g, sizes, K, N, gather=gather, ints=True)
+    R = sum(sizes)
+    ws = torch.full((max(256, dg.dgemm_grouped_workspace_size(kind, R, len(sizes), N, K)),), 0x5A, dtype=torch.uint8, device=dev())
+    on = {k: (v.to(dev()) if v is not None else None) for k, v in a.items()}
+    D = torch.zeros(R, N, dtype=F32, device=dev())
+
+    def one():
+        if kind == "bf16":
+            dg.dgemm_grouped_bf16(on["A"], on["B"], on["offsets"], D, a_rows=on["a_rows"], ws=ws)
+        else:
+            f = dg.dgemm_grouped_fp8_scaled if kind == "fp8" else dg.dgemm_grouped_int8_scaled
+            f(on["A"], on["B"], on["a_scale"], on["b_scale"], on["offsets"], D, a_rows=on["a_rows"], ws=ws)
+
+    with dg.overrides(stall_after_loads=2, wait_limit_ns=20_000_000):
+        one()
+        assert dg.dgemm_query_device_status(ws) == 6      # DGEMM_ERR_DEVICE_TIMEOUT
+    assert status_ok(ws)                                  # the query cleared it; the device word is untouched
+    one()
+    assert status_ok(ws)
+    want, _ = ref.grouped(a["A"], a["B"], a["offsets"].tolist(), a_rows=a["a_rows"], a_scale=a["a_scale"], b_scale=a["b_scale"],
+                          out_dtype=F32)
+    assert torch.equal(D.cpu(), want.to(F32))
+
+
 # ------------------------------------------------------------------ int8, few rows a group
 
 @pytest.mark.parametrize("sizes", [[1], [2], [3, 0, 1], [4, 4], [5, 8, 0, 7], [16], [9, 23, 0, 1], [1] * 40, [40, 0, 0, 0]])
