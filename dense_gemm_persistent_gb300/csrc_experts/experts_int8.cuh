@@ -36,8 +36,8 @@ struct Int8Cfg {
     static constexpr int BN = PAIR ? 192 : 64;           // most token rows of a tile
     static constexpr int BN_CTA = BN / CTAS;
     static constexpr int KB = 128, KC = 64;              // K of a raw and of a converted stage
-    static constexpr int W_RAW = 128 * KB, W_STAGES = 8;
-    static constexpr int AHEAD = 2;           // stages that a token converter team loads ahead
+    static constexpr int W_RAW = 128 * KB, W_STAGES = 7 + PAIR;
+    static constexpr int AHEAD = PAIR ? 2 : 4;         // stages that a token converter team loads ahead
     static constexpr int X_CONV = BN_CTA * KC * 2;       // a converted stage: rows here, weights in Tensor Memory
     static constexpr int A_COLS = KC / 2, C_STAGES = 4;
     static constexpr int ACC_COLS = 2 * BN;
@@ -50,7 +50,8 @@ struct Int8Cfg {
     static constexpr int TMEM_COLS = ACC_COLS + C_STAGES * A_COLS;
     static_assert(TMEM_COLS == 256 || TMEM_COLS == 512, "Tensor Memory");
     static constexpr int BAR_BYTES = 384;
-    static constexpr int BUFFERS = W_STAGES * W_RAW + C_STAGES * X_CONV;
+    static constexpr int X_RAW = PAIR ? 0 : BN_CTA * KC;   // copies of codes
+    static constexpr int BUFFERS = W_STAGES * W_RAW + C_STAGES * X_CONV + X_TEAMS * AHEAD * X_RAW;
     static constexpr int FIXED = 1024 + BUFFERS + exchange_bytes<EPI_WARPS>() + BAR_BYTES;
     static constexpr uint32_t IDESC0 = make_idesc(0u, false, false, 128 * CTAS, 0);   // FP16 operands
     static_assert(FIXED + Schedule::bytes(DGEMM_MAX_EXPERTS) <= 232448, "shared memory");
@@ -286,83 +287,146 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
         __syncwarp();
     } else {
         // ---------------------------------------------------------------- token converters
-        // Four threads load and convert a row's 64 codes, 16 each, AHEAD of the team's stages
-        // ahead of their conversion.
+        // Four threads load and convert a row's 64 codes, 16 each; AHEAD of the team's stages are
+        // on their way before one is converted.
         regs_dec<CF::REGS_TOKENS>();
         constexpr int ROUNDS = CF::BN_CTA / 32;
         const int team = (warp - CF::X_WARP0) >> 2;
         const int tid = threadIdx.x & 127, sub = tid >> 2, chunk = tid & 3;
         const int at0 = ((2 * chunk) ^ (sub & 7)) << 4, at1 = ((2 * chunk + 1) ^ (sub & 7)) << 4;
         int item = unit, kb = 0, rounds = 0, src[ROUNDS];
-        bool live = p.kstages > 0 && cur.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, t);
-        auto point = [&]() {                                 // the rows of tile t
-            const int xrows = t.n / CF::CTAS, first = static_cast<int>(rank) * xrows;
+        Cursor ahead;
+        Tile ta;                                             // the tile that is loaded from
+        bool live = p.kstages > 0 && ahead.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, ta);
+        auto point = [&]() {                                 // the rows of tile ta
+            const int xrows = ta.n / CF::CTAS, first = static_cast<int>(rank) * xrows;
             rounds = (xrows + 31) / 32;
 #pragma unroll
             for (int i = 0; i < ROUNDS; ++i) {
                 const int row = i * 32 + sub, r = first + row;
                 src[i] = -1;
-                if (row < xrows && r < t.rows) {
-                    const int a = p.a_rows ? __ldg(p.a_rows + t.row0 + r) : t.row0 + r;
+                if (row < xrows && r < ta.rows) {
+                    const int a = p.a_rows ? __ldg(p.a_rows + ta.row0 + r) : ta.row0 + r;
                     if (a >= 0 && a < p.a_count) src[i] = a;
                 }
             }
         };
-        struct Held {
-            uint4 codes[ROUNDS];
-            int rounds;                                      // 0: past the last stage
-        };
-        auto load = [&](Held& h) {                           // the team's next stage
-            h.rounds = live ? rounds : 0;
-            if (!live) return;
-            const int k = kb * CF::KB + team * CF::KC + chunk * 16;
-            const char* base = static_cast<const char*>(p.A) + k;
-#pragma unroll
-            for (int i = 0; i < ROUNDS; ++i) {
-                h.codes[i] = make_uint4(0, 0, 0, 0);
-                if (src[i] >= 0 && k < p.K)
-                    h.codes[i] = __ldg(reinterpret_cast<const uint4*>(base + static_cast<int64_t>(src[i]) * p.K));
+        if constexpr (CF::PAIR) {
+            // Two stages in two register sets.
+            struct Held {
+                uint4 codes[ROUNDS];
+                int rounds;                                      // 0: past the last stage
+            };
+            auto load = [&](Held& h) {                           // the team's next stage
+                h.rounds = live ? rounds : 0;
+                if (!live) return;
+                const int k = kb * CF::KB + team * CF::KC + chunk * 16;
+                const char* base = static_cast<const char*>(p.A) + k;
+    #pragma unroll
+                for (int i = 0; i < ROUNDS; ++i) {
+                    h.codes[i] = make_uint4(0, 0, 0, 0);
+                    if (src[i] >= 0 && k < p.K)
+                        h.codes[i] = __ldg(reinterpret_cast<const uint4*>(base + static_cast<int64_t>(src[i]) * p.K));
+                }
+                if (++kb == p.kstages) {
+                    kb = 0;
+                    item += units;
+                    live = ahead.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, ta);
+                    if (live) point();
+                }
+            };
+            uint32_t g = team;
+            auto convert = [&](const Held& h) {
+                if (!slot_free(g)) return false;
+                uint8_t* dst = conv + g % CF::C_STAGES * CF::X_CONV + sub * 128;
+    #pragma unroll
+                for (int i = 0; i < ROUNDS; ++i) {
+                    if (i >= h.rounds) break;
+                    uint4 lo, hi;
+                    int8x4_to_f16(h.codes[i].x, lo.x, lo.y);
+                    int8x4_to_f16(h.codes[i].y, lo.z, lo.w);
+                    int8x4_to_f16(h.codes[i].z, hi.x, hi.y);
+                    int8x4_to_f16(h.codes[i].w, hi.z, hi.w);
+                    *reinterpret_cast<uint4*>(dst + i * 4096 + at0) = lo;
+                    *reinterpret_cast<uint4*>(dst + i * 4096 + at1) = hi;
+                }
+                fence_proxy_async_smem();
+                converted(g);
+                g += CF::X_TEAMS;
+                return true;
+            };
+            Held held[CF::AHEAD];
+            if (live) point();
+    #pragma unroll
+            for (int i = 0; i < CF::AHEAD; ++i) load(held[i]);
+            bool more = true;
+            while (ok && more) {
+    #pragma unroll
+                for (int i = 0; i < CF::AHEAD; ++i) {
+                    more = more && held[i].rounds > 0;
+                    if (!more || !ok) break;
+                    ok = convert(held[i]);
+                    load(held[i]);
+                }
             }
-            if (++kb == p.kstages) {
-                kb = 0;
-                item += units;
-                live = cur.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, t);
-                if (live) point();
+        } else {
+            // A thread's own places in shared memory, AHEAD stages of ROUNDS x 16 bytes: copies
+            // are waited for stage by stage, where registers in flight all wait for the last.
+            // (768 rows over 64 experts of 2048 x 4096: 133 us against 151. For pairs the extra
+            // traffic and the fence behind the copies cost more: 4096 x 11008 x 4096 358 against 313.)
+            uint8_t* place = conv + CF::C_STAGES * CF::X_CONV + team * CF::AHEAD * CF::X_RAW + tid * 16;
+            int slot_in = 0, slot_out = 0;
+            auto load = [&]() {                                  // the team's next stage (an empty group past the last)
+                if (live) {
+                    const int k = kb * CF::KB + team * CF::KC + chunk * 16;
+                    const char* base = static_cast<const char*>(p.A) + k;
+    #pragma unroll
+                    for (int i = 0; i < ROUNDS; ++i) {
+                        if (i >= rounds) break;
+                        const bool read = src[i] >= 0 && k < p.K;
+                        cp_async_16(place + slot_in * CF::X_RAW + i * 2048,
+                                    read ? base + static_cast<int64_t>(src[i]) * p.K : static_cast<const char*>(p.A), read ? 16u : 0u);
+                    }
+                    if (++kb == p.kstages) {
+                        kb = 0;
+                        item += units;
+                        live = ahead.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, ta);
+                        if (live) point();
+                    }
+                }
+                cp_async_commit();
+                if (++slot_in == CF::AHEAD) slot_in = 0;
+            };
+            if (live) point();
+    #pragma unroll 1
+            for (int i = 0; i < CF::AHEAD - 1; ++i) load();
+            uint32_t g = team;
+            for (int at = unit; ok && cur.at<CF::BN, CF::CTAS>(p, sched, at, tile_channels, t); at += units) {
+                const int now = (t.n / CF::CTAS + 31) / 32;
+                for (int n = 0; n < p.kstages; ++n, g += CF::X_TEAMS) {
+                    load();
+                    cp_async_wait<CF::AHEAD - 1>();              // this stage's copies (this thread's own) have landed
+                    ok = slot_free(g);
+                    if (!ok) break;
+                    uint8_t* dst = conv + g % CF::C_STAGES * CF::X_CONV + sub * 128;
+    #pragma unroll
+                    for (int i = 0; i < ROUNDS; ++i) {
+                        if (i >= now) break;
+                        const uint4 c = *reinterpret_cast<const uint4*>(place + slot_out * CF::X_RAW + i * 2048);
+                        uint4 lo, hi;
+                        int8x4_to_f16(c.x, lo.x, lo.y);
+                        int8x4_to_f16(c.y, lo.z, lo.w);
+                        int8x4_to_f16(c.z, hi.x, hi.y);
+                        int8x4_to_f16(c.w, hi.z, hi.w);
+                        *reinterpret_cast<uint4*>(dst + i * 4096 + at0) = lo;
+                        *reinterpret_cast<uint4*>(dst + i * 4096 + at1) = hi;
+                    }
+                    fence_proxy_async_smem();
+                    converted(g);
+                    if (++slot_out == CF::AHEAD) slot_out = 0;
+                }
             }
-        };
-        uint32_t g = team;
-        auto convert = [&](const Held& h) {
-            if (!slot_free(g)) return false;
-            uint8_t* dst = conv + g % CF::C_STAGES * CF::X_CONV + sub * 128;
-#pragma unroll
-            for (int i = 0; i < ROUNDS; ++i) {
-                if (i >= h.rounds) break;
-                uint4 lo, hi;
-                int8x4_to_f16(h.codes[i].x, lo.x, lo.y);
-                int8x4_to_f16(h.codes[i].y, lo.z, lo.w);
-                int8x4_to_f16(h.codes[i].z, hi.x, hi.y);
-                int8x4_to_f16(h.codes[i].w, hi.z, hi.w);
-                *reinterpret_cast<uint4*>(dst + i * 4096 + at0) = lo;
-                *reinterpret_cast<uint4*>(dst + i * 4096 + at1) = hi;
-            }
-            fence_proxy_async_smem();
-            converted(g);
-            g += CF::X_TEAMS;
-            return true;
-        };
-        Held held[CF::AHEAD];
-        if (live) point();
-#pragma unroll
-        for (int i = 0; i < CF::AHEAD; ++i) load(held[i]);
-        bool more = true;
-        while (ok && more) {
-#pragma unroll
-            for (int i = 0; i < CF::AHEAD; ++i) {
-                more = more && held[i].rounds > 0;
-                if (!more || !ok) break;
-                ok = convert(held[i]);
-                load(held[i]);
-            }
+            cp_async_wait<0>();                                  // nothing of this thread's is in flight when it leaves
         }
         if (!ok) fail(p, ERR_TIMEOUT_PRODUCER, abort_flag);
         __syncwarp();
