@@ -125,6 +125,26 @@ __device__ __forceinline__ float row_scale(unsigned m, float* scale) {
     return s;
 }
 
+// Four codes in a word, without conversions: x / s + 1.5 x 2^23 holds the rounded quotient in its
+// low byte (two's complement), and the rest of the product says how near a half it was.
+// Quotients near a half, and values that are not finite, take int8_code.
+__device__ __forceinline__ uint32_t int8_codes4(const float* x, float s, float inv) {
+    constexpr float MAGIC = 12582912.0f;
+    uint32_t b[4];
+    bool far = true;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float m = fmaf(x[i], inv, MAGIC), r = m - MAGIC;
+        far = far && fabsf(fmaf(x[i], inv, -r)) < 0.4999f;
+        b[i] = __float_as_uint(m);
+    }
+    if (!far) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) b[i] = static_cast<uint32_t>(int8_code(x[i], s, inv));
+    }
+    return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+}
+
 // One CTA per row of up to 8 x CHUNKS x blockDim values, held in registers between the
 // maximum and the codes: the row is read once.
 template <bool F32, int CHUNKS>
@@ -160,10 +180,7 @@ __global__ void __launch_bounds__(256) quantize_held(const void* X, int8_t* q, f
     for (int c = 0; c < CHUNKS; ++c) {
         const int k = (c * blockDim.x + threadIdx.x) * 8;
         if (k >= K) continue;
-        uint32_t w[2] = {0, 0};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[i / 4] |= (int8_code(x[c][i], s, inv) & 0xFFu) << (8 * (i % 4));
-        *reinterpret_cast<uint2*>(q + at + k) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2*>(q + at + k) = make_uint2(int8_codes4(x[c], s, inv), int8_codes4(x[c] + 4, s, inv));
     }
 }
 
