@@ -240,16 +240,24 @@ __global__ void __launch_bounds__(PLACE_THREADS, 2) route_place(const RouteParam
     for (int e = threadIdx.x; e < p.E; e += PLACE_THREADS) mask[e] = 0;
     const int quad = threadIdx.x % quads, part = threadIdx.x / quads;
     if (part < parts) {
+        // two 16-bit sums in a word: at most 512 counts of up to CHUNK each between foldings
         int sum[4] = {0, 0, 0, 0}, pre[4] = {0, 0, 0, 0};
+        for (int c0 = part; c0 < p.chunks; c0 += 512 * parts) {
+            const int c1 = static_cast<int>(min(static_cast<int64_t>(p.chunks), c0 + static_cast<int64_t>(512) * parts));
+            uint32_t s02 = 0, s13 = 0, p02 = 0, p13 = 0;
+            const uint8_t* at = p.counts + static_cast<int64_t>(c0) * p.pitch + quad * 4;
+            const int64_t step = static_cast<int64_t>(parts) * p.pitch;
 #pragma unroll 8
-        for (int c = part; c < p.chunks; c += parts) {
-            const uint32_t v = *reinterpret_cast<const uint32_t*>(p.counts + static_cast<int64_t>(c) * p.pitch + quad * 4);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int x = (v >> (8 * i)) & 0xFF;
-                sum[i] += x;
-                if (c < mine) pre[i] += x;
+            for (int c = c0; c < c1; c += parts, at += step) {
+                const uint32_t v = *reinterpret_cast<const uint32_t*>(at);
+                const uint32_t a = v & 0x00FF00FFu, b = (v >> 8) & 0x00FF00FFu;
+                s02 += a;
+                s13 += b;
+                p02 += c < mine ? a : 0;
+                p13 += c < mine ? b : 0;
             }
+            sum[0] += s02 & 0xFFFF, sum[2] += s02 >> 16, sum[1] += s13 & 0xFFFF, sum[3] += s13 >> 16;
+            pre[0] += p02 & 0xFFFF, pre[2] += p02 >> 16, pre[1] += p13 & 0xFFFF, pre[3] += p13 >> 16;
         }
         *reinterpret_cast<int4*>(base + part * p.pitch + quad * 4) = make_int4(sum[0], sum[1], sum[2], sum[3]);
         *reinterpret_cast<int4*>(before + part * p.pitch + quad * 4) = make_int4(pre[0], pre[1], pre[2], pre[3]);

@@ -112,13 +112,19 @@ __device__ __forceinline__ unsigned finite_magnitude(float x) {   // magnitudes 
     return u < 0x7F800000u ? u : 0u;
 }
 
-// The row's scale from every thread's maximum; all threads of the CTA take part.
-__device__ __forceinline__ float row_scale(unsigned m, float* scale) {
+// The largest of every thread's value; all threads of the CTA take part.
+__device__ __forceinline__ unsigned row_max(unsigned m) {
     __shared__ unsigned part[32];
     m = __reduce_max_sync(0xffffffffu, m);
+    __syncthreads();                      // (an earlier call's values have been read)
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
     __syncthreads();
     for (unsigned w = 0; w < blockDim.x / 32; ++w) m = max(m, part[w]);
+    return m;
+}
+
+// The row's scale from the bits of its largest finite magnitude.
+__device__ __forceinline__ float row_scale(unsigned m, float* scale) {
     float s = __fmul_rn(__uint_as_float(m), 1.0f / 127.0f);
     if (s == 0.0f) s = 1.0f;              // a row of zeros (or one whose scale underflows)
     if (threadIdx.x == 0) *scale = s;
@@ -152,35 +158,42 @@ __global__ void __launch_bounds__(256) quantize_held(const void* X, int8_t* q, f
     dg::grid_dependency_wait();
     if (threadIdx.x == 0) dg::grid_launch_dependents();
     const int64_t at = static_cast<int64_t>(blockIdx.x) * K;
-    float x[CHUNKS][8];
-    unsigned m = 0;
+    constexpr int WORDS = F32 ? 8 : 4;    // of 8 values
+    uint32_t v[CHUNKS][WORDS];
+    auto value = [&](int c, int i) {
+        return F32 ? __uint_as_float(v[c][i % WORDS]) : (i & 1) ? dg::bf16_hi(v[c][i / 2]) : dg::bf16_lo(v[c][i / 2]);
+    };
+    unsigned m = 0;                       // F32: the largest magnitude; BF16: two of them
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c) {
         const int k = (c * blockDim.x + threadIdx.x) * 8;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[c][i] = 0.0f;
-        if (k < K) {
-            if constexpr (F32) {
-                const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(X) + at + k);
-                const float4 a = src[0], b = src[1];
-                x[c][0] = a.x, x[c][1] = a.y, x[c][2] = a.z, x[c][3] = a.w;
-                x[c][4] = b.x, x[c][5] = b.y, x[c][6] = b.z, x[c][7] = b.w;
-            } else {
-                const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(X) + at + k);
-                const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[c][i] = (i & 1) ? dg::bf16_hi(u[i / 2]) : dg::bf16_lo(u[i / 2]);
-            }
+        for (int i = 0; i < WORDS; i += 4) {
+            uint4 w = make_uint4(0, 0, 0, 0);
+            if (k < K) w = *reinterpret_cast<const uint4*>(static_cast<const char*>(X) + (at + k) * (F32 ? 4 : 2) + i * 4);
+            v[c][i] = w.x, v[c][i + 1] = w.y, v[c][i + 2] = w.z, v[c][i + 3] = w.w;
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, finite_magnitude(x[c][i]));
+        for (int i = 0; i < WORDS; ++i) m = F32 ? max(m, v[c][i] & 0x7FFFFFFFu) : __vmaxu2(m, v[c][i] & 0x7FFF7FFFu);
+    }
+    m = row_max(F32 ? m : max(m << 16, m & 0xFFFF0000u));
+    if (m >= 0x7F800000u) {               // infinities or NaN in the row: its finite values only
+        m = 0;
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = max(m, finite_magnitude(value(c, i)));
+        m = row_max(m);
     }
     const float s = row_scale(m, scale + blockIdx.x), inv = __frcp_rn(s);
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c) {
         const int k = (c * blockDim.x + threadIdx.x) * 8;
         if (k >= K) continue;
-        *reinterpret_cast<uint2*>(q + at + k) = make_uint2(int8_codes4(x[c], s, inv), int8_codes4(x[c] + 4, s, inv));
+        float x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = value(c, i);
+        *reinterpret_cast<uint2*>(q + at + k) = make_uint2(int8_codes4(x, s, inv), int8_codes4(x + 4, s, inv));
     }
 }
 
@@ -191,7 +204,7 @@ __global__ void __launch_bounds__(512) quantize_rows(const void* X, int f32, int
     const int64_t at = static_cast<int64_t>(blockIdx.x) * K;
     unsigned m = 0;
     for (int64_t i = threadIdx.x; i < K; i += blockDim.x) m = max(m, finite_magnitude(load1(X, f32, at + i)));
-    const float s = row_scale(m, scale + blockIdx.x), inv = __frcp_rn(s);
+    const float s = row_scale(row_max(m), scale + blockIdx.x), inv = __frcp_rn(s);
     for (int64_t i = threadIdx.x; i < K; i += blockDim.x) q[at + i] = static_cast<int8_t>(int8_code(load1(X, f32, at + i), s, inv));
 }
 

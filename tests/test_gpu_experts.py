@@ -512,3 +512,40 @@ def test_int8_few_rows_exact(M):
     dg.dgemm_int8_scaled(A.to(dev()), B.to(dev()), one(M), one(N), D)
     want = A.to(torch.float64) @ B.to(torch.float64).t()
     assert torch.equal(D.cpu(), want.to(F32))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("K", [64, 2048, 4096, 8192])
+def test_int8_quantize_rows_with_infinities(K, dtype):
+    """Rows held in registers: infinities and NaN beside finite values, and rows of nothing else."""
+    g = gen(K)
+    X = randn(g, 6, K).to(dtype)
+    X[0, 3], X[0, K - 1] = float("inf"), -float("inf")
+    X[1, 5] = float("nan")
+    X[2] = float("nan")
+    X[3] = float("inf")
+    X[4, ::2] = -float("inf")
+    q = torch.full((6, K), 99, dtype=I8, device=dev())
+    s = torch.full((6,), -1.0, device=dev())
+    dg.dgemm_int8_quantize(X.to(dev()), q, s)
+    want_q, want_s = ref.quantize(X)
+    assert torch.equal(s.cpu(), want_s) and torch.equal(q.cpu(), want_q)
+
+
+def test_route_many_chunks():
+    """More chunks of tokens than one folding of the packed counts takes."""
+    g = gen(77)
+    T, E, k = 40000, 5, 2
+    x = randint(g, 0, 3, T, E).float().to(dev())
+    ids = torch.empty(T, k, dtype=torch.int32, device=dev())
+    w, offsets = torch.empty(T, k, device=dev()), torch.empty(E + 1, dtype=torch.int32, device=dev())
+    row_token, slot_row = torch.empty(T * k, dtype=torch.int32, device=dev()), torch.empty(T, k, dtype=torch.int32, device=dev())
+    ws = torch.empty(dg.dgemm_route_workspace_size(T, E, k), dtype=torch.uint8, device=dev())
+    dg.dgemm_route(x, k, ids, w, offsets, row_token, slot_row, ws=ws)
+    want = torch.sort(x.cpu(), dim=1, descending=True, stable=True).indices[:, :k]
+    assert torch.equal(ids.cpu().long(), want)
+    flat = want.reshape(-1)
+    order = torch.sort(flat, stable=True).indices
+    assert torch.equal(row_token.cpu().long(), order // k)
+    assert torch.equal(slot_row.cpu().long().reshape(-1)[order], torch.arange(T * k))
+    assert offsets.cpu().tolist() == [int((flat < e).sum()) for e in range(E + 1)]
