@@ -7,7 +7,7 @@
 //   2       gathering variants: announces gathered stages to the MMA issuer
 //   3       idle (completes the first warpgroup)
 //   4-11    epilogue
-//   12-15   gathering variants: cp.async of token rows by index into the swizzled
+//   12-..   gathering variants (4 warps, 8 of a pair's CTA): cp.async of token rows by index into the swizzled
 //           slices that the MMA reads
 // A stage of the ring holds two 128-byte slices of K of both operands; TMA brings
 // each operand's in one copy.
@@ -18,7 +18,9 @@
 // same with stages of one slice 933-1290 us, because each stage's arrive on the peer's
 // barrier, released at cluster scope, waited for all the thread's memory operations; with
 // a release at CTA scope 493 us; copies that arrive by themselves and a thread of its
-// own that announces them 424 us (one-slice stages: 440).
+// own that announces them 424 us (one-slice stages: 440); waits by converged warps 384;
+// eight copying warps in each CTA of a pair 376 (for single CTAs four are better: 64 us against 66
+// for 64 rows over 64 experts).
 // The output channels are the MMA's rows, the token rows its columns, as many as
 // the tile has.
 #pragma once
@@ -44,7 +46,7 @@ struct MmaCfg {
     static constexpr int ATOM = KS * SL * 128;           // KN weights: 64 channels of a stage's K rows
     static constexpr int STAGES = (PAIR ? 6 : 8) / KS;
     static constexpr int SMALL_ROWS = 16;                // rows of a small copy of token rows
-    static constexpr int EPI_WARPS = 8, EPI_WARP0 = 4, GATHER_WARP0 = 12, GATHER_WARPS = 4;
+    static constexpr int EPI_WARPS = 8, EPI_WARP0 = 4, GATHER_WARP0 = 12, GATHER_WARPS = PAIR ? 8 : 4;
     static constexpr int THREADS = 32 * (GATHER ? GATHER_WARP0 + GATHER_WARPS : EPI_WARP0 + EPI_WARPS);
     static constexpr int TMEM_COLS = 2 * BN;
     static constexpr int BAR_BYTES = 256;
@@ -306,9 +308,9 @@ __global__ void __launch_bounds__(CF::THREADS, 1)
         if (!ok && lane == 0) fail(p, ERR_TIMEOUT_PRODUCER, abort_flag);
     } else if (CF::GATHER && warp >= CF::GATHER_WARP0) {
         // ---------------------------------------------------------------- gather
-        // Eight lanes copy the 16-byte chunks of one row's slice, four rows a warp; every
+        // Eight lanes copy the 16-byte chunks of one row's slice, four rows a warp at a time; every
         // thread's copies arrive on the stage's landed barrier by themselves.
-        constexpr int ROUNDS = CF::BN_CTA / 16;
+        constexpr int STEP = 4 * CF::GATHER_WARPS, ROUNDS = CF::BN_CTA / STEP;
         const int sub = (warp - CF::GATHER_WARP0) * 4 + (lane >> 3), chunk = lane & 7;
         const int64_t pitch = static_cast<int64_t>(p.K) * CF::ESZ;
         uint32_t stage = 0, phase = 0;
@@ -321,14 +323,14 @@ __global__ void __launch_bounds__(CF::THREADS, 1)
             const char* src[ROUNDS];
 #pragma unroll
             for (int i = 0; i < ROUNDS; ++i) {
-                const int r = first + i * 16 + sub;
+                const int r = first + i * STEP + sub;
                 src[i] = nullptr;
-                if (i * 16 + sub < xrows && r < t.rows) {
+                if (i * STEP + sub < xrows && r < t.rows) {
                     const int a = __ldg(p.a_rows + t.row0 + r);
                     if (a >= 0 && a < p.a_count) src[i] = static_cast<const char*>(p.A) + a * pitch;
                 }
             }
-            const int rounds = xrows / 16;
+            const int rounds = (xrows + STEP - 1) / STEP;
             for (int kb = 0; kb < p.kstages; ++kb) {
                 if (!mbar_wait_warp(&empty[stage], phase ^ 1, abort_flag, p.wait_ns)) {
                     ok = false;
@@ -341,7 +343,7 @@ __global__ void __launch_bounds__(CF::THREADS, 1)
 #pragma unroll
                     for (int i = 0; i < ROUNDS; ++i) {
                         if (i >= rounds) break;
-                        const int row = i * 16 + sub;
+                        const int row = i * STEP + sub;
                         const bool read = kbyte < pitch && src[i] != nullptr;
                         cp_async_16(x + s * CF::SLICE_X + row * 128 + ((chunk ^ (row & 7)) << 4),
                                     read ? src[i] + kbyte : static_cast<const char*>(p.A), read ? 16u : 0u);

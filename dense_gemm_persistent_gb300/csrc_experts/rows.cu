@@ -160,9 +160,6 @@ __global__ void __launch_bounds__(256) quantize_held(const void* X, int8_t* q, f
     const int64_t at = static_cast<int64_t>(blockIdx.x) * K;
     constexpr int WORDS = F32 ? 8 : 4;    // of 8 values
     uint32_t v[CHUNKS][WORDS];
-    auto value = [&](int c, int i) {
-        return F32 ? __uint_as_float(v[c][i % WORDS]) : (i & 1) ? dg::bf16_hi(v[c][i / 2]) : dg::bf16_lo(v[c][i / 2]);
-    };
     unsigned m = 0;                       // F32: the largest magnitude; BF16: two of them
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c) {
@@ -176,6 +173,9 @@ __global__ void __launch_bounds__(256) quantize_held(const void* X, int8_t* q, f
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) m = F32 ? max(m, v[c][i] & 0x7FFFFFFFu) : __vmaxu2(m, v[c][i] & 0x7FFF7FFFu);
     }
+    auto value = [&](int c, int i) {
+        return F32 ? __uint_as_float(v[c][i % WORDS]) : (i & 1) ? dg::bf16_hi(v[c][i / 2]) : dg::bf16_lo(v[c][i / 2]);
+    };
     m = row_max(F32 ? m : max(m << 16, m & 0xFFFF0000u));
     if (m >= 0x7F800000u) {               // infinities or NaN in the row: its finite values only
         m = 0;
