@@ -549,3 +549,21 @@ def test_route_many_chunks():
     assert torch.equal(row_token.cpu().long(), order // k)
     assert torch.equal(slot_row.cpu().long().reshape(-1)[order], torch.arange(T * k))
     assert offsets.cpu().tolist() == [int((flat < e).sum()) for e in range(E + 1)]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("K", [48, 64, 80, 112, 128, 144, 176, 192, 208, 240, 256, 272, 304, 336, 400])
+def test_grouped_depths_around_whole_slices(kind, K):
+    """Depths that end inside, at and after a 128-byte slice, and after one or two slices of a
+    pipeline stage, for short and long groups; NaN rows around the group show a read past a row."""
+    for sizes in ([5, 60], [230, 90]):
+        g = gen(K + sum(sizes))
+        a = make(kind, g, sizes, K, 72)
+        if kind == "bf16":
+            a["A"][sizes[0]:] = float("nan")       # the second group's rows follow the first's
+        want, tol = ref.grouped(a["A"], a["B"], a["offsets"].tolist(), a_scale=a["a_scale"], b_scale=a["b_scale"], out_dtype=F32)
+        D = torch.full((sum(sizes), 72), 7.0, dtype=F32, device=dev())
+        call(kind, a, D)
+        first = slice(0, sizes[0]) if kind == "bf16" else slice(None)
+        assert bool(torch.isfinite(D[first]).all())
+        close(D[first], want[first], tol[first])
