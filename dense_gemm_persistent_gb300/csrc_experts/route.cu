@@ -23,7 +23,9 @@
 
 namespace {
 
-constexpr int CHUNK = 64;       // tokens per chunk: one 64-bit mask per expert
+constexpr int CHUNK = 64;       // most tokens of a chunk: one 64-bit mask per expert
+
+constexpr int kMoreChunks = 64;  // chunks beyond the fewest that a call may be cut into (workspace)
 
 struct RouteParams {
     const void* logits;
@@ -34,7 +36,7 @@ struct RouteParams {
     int* row_token;
     int* slot_row;
     uint8_t* counts;            // [chunks][E rounded up to 4]: at most CHUNK each
-    int chunks, pitch;
+    int chunks, pitch, chunk;   // tokens of a chunk
 };
 
 // Order-preserving map of a finite float to unsigned (0 is below every one).
@@ -48,9 +50,10 @@ __device__ __forceinline__ float unordered(unsigned o) {
 
 // One token by one warp: lane l holds entries l, l + 32, ... as order-preserving keys; 0
 // marks a masked or chosen one. Each round takes the warp's largest key. BF16: a
-// key is the value's 16 bits over the complement of the index, so keys differ and
-// one reduction names the winner. FP32: the value's 32 bits; a ballot names the
-// winner, and where several lanes hold that value the lowest index wins.
+// key is the value's 16 bits over the complement of the index, so keys differ, one
+// reduction names the winner, and up to 8 keys a lane are sorted first, so that a round
+// looks at the first and moves the winner's up. FP32: the value's 32 bits; a ballot
+// names the winner, and where several lanes hold that value the lowest index wins.
 template <int VPL, bool BF16>
 __device__ __forceinline__ void load_keys(const RouteParams& p, int t, int lane, unsigned (&key)[VPL]) {
 #pragma unroll
@@ -79,6 +82,22 @@ __device__ __forceinline__ float key_value(unsigned key) {
 
 template <int VPL, bool BF16>
 __device__ __forceinline__ void route_token(const RouteParams& p, int t, int lane, unsigned (&key)[VPL], int* sid) {
+    constexpr bool SORTED = BF16 && VPL <= 8;
+    if constexpr (SORTED) {     // odd-even merge sort, largest first
+#pragma unroll
+        for (int p2 = 1; p2 < VPL; p2 *= 2)
+#pragma unroll
+            for (int d = p2; d >= 1; d /= 2)
+#pragma unroll
+                for (int j = d % p2; j + d < VPL; j += 2 * d)
+#pragma unroll
+                    for (int i = 0; i < d; ++i)
+                        if (i + j + d < VPL && (i + j) / (2 * p2) == (i + j + d) / (2 * p2)) {
+                            const unsigned hi = max(key[i + j], key[i + j + d]), lo = min(key[i + j], key[i + j + d]);
+                            key[i + j] = hi;
+                            key[i + j + d] = lo;
+                        }
+    }
     // this lane's largest key and, for FP32, its slot (the first of equals); no branches, so
     // that a round costs little more than its reduction
     unsigned best;
@@ -86,6 +105,7 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int t, int lan
     auto scan = [&]() {
         best = key[0];
         best_i = 0;
+        if (SORTED) return;
 #pragma unroll
         for (int i = 1; i < VPL; ++i) {
             if (!BF16) best_i = key[i] > best ? i : best_i;
@@ -119,8 +139,14 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int t, int lan
         }
         my_id = lane == j ? e : my_id;
         my_key = lane == j ? m : my_key;
+        if constexpr (SORTED) {
+            const bool won = key[0] == m;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) key[i] = (BF16 ? key[i] == m : lane + 32 * i == e) ? 0 : key[i];
+            for (int i = 0; i < VPL; ++i) key[i] = won ? (i + 1 < VPL ? key[i + 1] : 0) : key[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) key[i] = (BF16 ? key[i] == m : lane + 32 * i == e) ? 0 : key[i];
+        }
         scan();
     }
     float my_p = my_id >= 0 ? expf(key_value<BF16>(my_key) - xmax) : 0.0f;
@@ -176,7 +202,7 @@ __global__ void __launch_bounds__(VPL <= 8 ? 1024 : 512, VPL <= 8 ? 2 : 1) route
     dg::grid_dependency_wait();
     if (threadIdx.x == 0) dg::grid_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int t0 = blockIdx.x * CHUNK, n = min(CHUNK, p.T - t0);
+    const int t0 = blockIdx.x * p.chunk, n = min(p.chunk, p.T - t0);
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) mask[e] = 0;
     __syncthreads();
     for (int i = warp; i < n; i += warps) {
@@ -230,7 +256,7 @@ __global__ void __launch_bounds__(PLACE_THREADS, 2) route_place(const RouteParam
     dg::grid_dependency_wait();
     if (threadIdx.x == 0) dg::grid_launch_dependents();
     const int mine = static_cast<int>(blockIdx.x);
-    const int t0 = mine * CHUNK, pairs = min(CHUNK, p.T - t0) * p.k;
+    const int t0 = mine * p.chunk, pairs = min(p.chunk, p.T - t0) * p.k;
     int id[PLACE_PAIRS];
 #pragma unroll
     for (int i = 0; i < PLACE_PAIRS; ++i) {
@@ -308,7 +334,7 @@ template <int VPL>
 cudaError_t launch_select(const RouteParams& p, cudaStream_t s) {
     // a warp per token as far as registers allow (two CTAs an SM up to 256 experts), and
     // threads enough for the per-expert steps
-    const int most = VPL <= 8 ? 32 : 16, warps = std::max(std::min(most, p.T), std::min(most, (p.E + 31) / 32));
+    const int most = VPL <= 8 ? 32 : 16, warps = std::max(std::min(most, p.chunk), std::min(most, (p.E + 31) / 32));
     dg::host::Launch l(static_cast<unsigned>(p.chunks), 1, 32u * warps, static_cast<size_t>(p.E) * 12 + CHUNK * p.k * 4, s);
     return p.bf16 ? cudaLaunchKernelEx(&l.cfg, route_select<VPL, true>, p)
                   : cudaLaunchKernelEx(&l.cfg, route_select<VPL, false>, p);
@@ -318,8 +344,8 @@ cudaError_t launch_select(const RouteParams& p, cudaStream_t s) {
 
 extern "C" size_t dgemm_route_workspace_size(int64_t T, int64_t E, int k) {
     if (route_sizes(T, E, k) != DGEMM_OK) return 0;
-    const size_t chunks = static_cast<size_t>((T + CHUNK - 1) / CHUNK);
-    return chunks > 1 ? chunks * ((static_cast<size_t>(E) + 3) / 4 * 4) : 0;
+    const size_t chunks = static_cast<size_t>((T + CHUNK - 1) / CHUNK) + kMoreChunks;
+    return T > CHUNK ? chunks * ((static_cast<size_t>(E) + 3) / 4 * 4) : 0;
 }
 
 extern "C" dgemm_status_t dgemm_route(const void* logits, dgemm_dtype_t logits_dtype, int64_t T, int64_t E, int k,
@@ -356,7 +382,11 @@ extern "C" dgemm_status_t dgemm_route(const void* logits, dgemm_dtype_t logits_d
     p.slot_row = slot_row;
     p.counts = static_cast<uint8_t*>(ws);
     p.pitch = (p.E + 3) / 4 * 4;
-    p.chunks = static_cast<int>((T + CHUNK - 1) / CHUNK);
+    // As many chunks as fill the last wave of two CTAs an SM, at most kMoreChunks more.
+    const int64_t fewest = (T + CHUNK - 1) / CHUNK, wave = 2 * dev.num_sms;
+    const int64_t want = T <= CHUNK ? 1 : std::min((fewest + wave - 1) / wave * wave, fewest + kMoreChunks);
+    p.chunk = static_cast<int>((T + want - 1) / want);
+    p.chunks = static_cast<int>((T + p.chunk - 1) / p.chunk);
     cudaError_t e;
     if (E <= 64) e = launch_select<2>(p, s);
     else if (E <= 128) e = launch_select<4>(p, s);
