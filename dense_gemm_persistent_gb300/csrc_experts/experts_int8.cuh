@@ -294,23 +294,31 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
         const int team = (warp - CF::X_WARP0) >> 2;
         const int tid = threadIdx.x & 127, sub = tid >> 2, chunk = tid & 3;
         const int at0 = ((2 * chunk) ^ (sub & 7)) << 4, at1 = ((2 * chunk + 1) ^ (sub & 7)) << 4;
-        int item = unit, kb = 0, rounds = 0, src[ROUNDS];
+        int item = unit, kb = 0, rounds = 0, src[ROUNDS], next[ROUNDS];
         Cursor ahead;
-        Tile ta;                                             // the tile that is loaded from
-        bool live = p.kstages > 0 && ahead.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, ta);
-        auto point = [&]() {                                 // the rows of tile ta
+        Tile ta;                                             // the tile after the one that is loaded from
+        bool more = p.kstages > 0 && ahead.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, ta), live = false;
+        auto look = [&]() {                                  // its row indexes, a tile before they are needed
             const int xrows = ta.n / CF::CTAS, first = static_cast<int>(rank) * xrows;
-            rounds = (xrows + 31) / 32;
 #pragma unroll
             for (int i = 0; i < ROUNDS; ++i) {
                 const int row = i * 32 + sub, r = first + row;
-                src[i] = -1;
-                if (row < xrows && r < ta.rows) {
-                    const int a = p.a_rows ? __ldg(p.a_rows + ta.row0 + r) : ta.row0 + r;
-                    if (a >= 0 && a < p.a_count) src[i] = a;
-                }
+                next[i] = -1;
+                if (row < xrows && r < ta.rows) next[i] = p.a_rows ? __ldg(p.a_rows + ta.row0 + r) : ta.row0 + r;
             }
         };
+        auto advance = [&]() {                               // on to that tile
+            live = more;
+            if (!more) return;
+            rounds = (ta.n / CF::CTAS + 31) / 32;
+#pragma unroll
+            for (int i = 0; i < ROUNDS; ++i) src[i] = next[i] < p.a_count ? next[i] : -1;
+            item += units;
+            more = ahead.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, ta);
+            if (more) look();
+        };
+        if (more) look();
+        advance();
         if constexpr (CF::PAIR) {
             // Two stages in two register sets.
             struct Held {
@@ -330,9 +338,7 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
                 }
                 if (++kb == p.kstages) {
                     kb = 0;
-                    item += units;
-                    live = ahead.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, ta);
-                    if (live) point();
+                    advance();
                 }
             };
             uint32_t g = team;
@@ -356,15 +362,14 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
                 return true;
             };
             Held held[CF::AHEAD];
-            if (live) point();
     #pragma unroll
             for (int i = 0; i < CF::AHEAD; ++i) load(held[i]);
-            bool more = true;
-            while (ok && more) {
+            bool left = true;
+            while (ok && left) {
     #pragma unroll
                 for (int i = 0; i < CF::AHEAD; ++i) {
-                    more = more && held[i].rounds > 0;
-                    if (!more || !ok) break;
+                    left = left && held[i].rounds > 0;
+                    if (!left || !ok) break;
                     ok = convert(held[i]);
                     load(held[i]);
                 }
@@ -389,15 +394,12 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
                     }
                     if (++kb == p.kstages) {
                         kb = 0;
-                        item += units;
-                        live = ahead.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, ta);
-                        if (live) point();
+                        advance();
                     }
                 }
                 cp_async_commit();
                 if (++slot_in == CF::AHEAD) slot_in = 0;
             };
-            if (live) point();
     #pragma unroll 1
             for (int i = 0; i < CF::AHEAD - 1; ++i) load();
             uint32_t g = team;

@@ -317,20 +317,26 @@ __global__ void __launch_bounds__(CF::THREADS, 1)
         bool ok = true;
         Cursor cur;
         Tile t;
-        for (int item = unit; ok && cur.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, t); item += units) {
-            const int xrows = t.n / CF::CTAS;
-            const int first = static_cast<int>(rank) * xrows;
-            const char* src[ROUNDS];
+        int item = unit, next[ROUNDS];                       // next: row indexes of tile t, loaded a tile ahead
+        bool live = cur.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, t);
+        auto look = [&]() {
+            const int xrows = t.n / CF::CTAS, first = static_cast<int>(rank) * xrows;
 #pragma unroll
             for (int i = 0; i < ROUNDS; ++i) {
                 const int r = first + i * STEP + sub;
-                src[i] = nullptr;
-                if (i * STEP + sub < xrows && r < t.rows) {
-                    const int a = __ldg(p.a_rows + t.row0 + r);
-                    if (a >= 0 && a < p.a_count) src[i] = static_cast<const char*>(p.A) + a * pitch;
-                }
+                next[i] = i * STEP + sub < xrows && r < t.rows ? __ldg(p.a_rows + t.row0 + r) : -1;
             }
-            const int rounds = (xrows + STEP - 1) / STEP;
+        };
+        if (live) look();
+        while (ok && live) {
+            const char* src[ROUNDS];
+#pragma unroll
+            for (int i = 0; i < ROUNDS; ++i)
+                src[i] = next[i] >= 0 && next[i] < p.a_count ? static_cast<const char*>(p.A) + next[i] * pitch : nullptr;
+            const int rounds = (t.n / CF::CTAS + STEP - 1) / STEP;
+            item += units;
+            live = cur.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, t);
+            if (live) look();
             for (int kb = 0; kb < p.kstages; ++kb) {
                 if (!mbar_wait_warp(&empty[stage], phase ^ 1, abort_flag, p.wait_ns)) {
                     ok = false;
