@@ -159,30 +159,44 @@ struct Cursor {
 __device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.0f + __expf(-v)); }
 
 // Stores one channel's COLS values, one row of D each (lanes: consecutive channels; `at`: this
-// lane's first). BF16 rows of even length: neighbouring lanes swap one value of every two
-// rows, so that a lane stores two channels of one row and the warp two rows at once.
+// lane's first). BF16 rows of even length: neighbouring lanes swap their packed pairs of rows,
+// so that a lane stores two channels of one row and the warp two rows at once. The values are
+// ready before any store, and the swap is a permute by a constant of the lane: choosing
+// between packings cost a divergent branch per pair, 35 of 77 us for 16384 x 4096 x 256.
 template <int COLS>
 __device__ __forceinline__ void store_columns(const Params& p, int64_t at, const float (&v)[COLS], bool live, int valid) {
     const int64_t wide = p.wide;
     if (p.d_f32) {
+        if (!live) return;
         float* d = static_cast<float*>(p.D) + at;
 #pragma unroll
-        for (int j = 0; j < COLS; ++j)
-            if (live && j < valid) d[j * wide] = v[j];
+        for (int j = 0; j < COLS; ++j, d += wide)
+            if (j < valid) *d = v[j];
     } else if ((p.wide & 1) == 0) {
         const int odd = threadIdx.x & 1;
-        uint32_t* d = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.D) + at - odd + odd * wide);
+        const uint32_t pick = odd ? 0x3276u : 0x5410u;    // (partner's row j + 1, own), or (own row j, partner's)
+        uint32_t w[COLS / 2];
 #pragma unroll
-        for (int j = 0; j < COLS; j += 2) {
-            const float got = __shfl_xor_sync(kAllLanes, odd ? v[j] : v[j + 1], 1);
-            // (an even row length: both channels of a lane pair are live or neither is)
-            if (live && j + odd < valid) d[(j / 2) * wide] = odd ? pack_bf16x2(got, v[j + 1]) : pack_bf16x2(v[j], got);
+        for (int j = 0; j < COLS / 2; ++j) {
+            const uint32_t own = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+            w[j] = __byte_perm(own, __shfl_xor_sync(kAllLanes, own, 1), pick);
+        }
+        if (!live) return;                                // (an even row length: both lanes of a pair are live or neither)
+        uint32_t* d = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.D) + at - odd + odd * wide);
+        if (valid >= COLS) {
+#pragma unroll
+            for (int j = 0; j < COLS / 2; ++j, d += wide) *d = w[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < COLS / 2; ++j, d += wide)
+                if (2 * j + odd < valid) *d = w[j];
         }
     } else {
+        if (!live) return;
         __nv_bfloat16* d = static_cast<__nv_bfloat16*>(p.D) + at;
 #pragma unroll
-        for (int j = 0; j < COLS; ++j)
-            if (live && j < valid) d[j * wide] = __float2bfloat16_rn(v[j]);
+        for (int j = 0; j < COLS; ++j, d += wide)
+            if (j < valid) *d = __float2bfloat16_rn(v[j]);
     }
 }
 
