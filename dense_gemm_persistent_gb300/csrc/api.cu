@@ -905,6 +905,8 @@ void wait_settings(uint64_t* wait_ns, long long* stall_after) {
     *stall_after = ov.stall_after_loads;
 }
 
+int pair_override() { return overrides_now().cta_pair; }
+
 }  // namespace host
 }  // namespace dg
 

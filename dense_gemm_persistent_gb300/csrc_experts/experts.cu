@@ -148,9 +148,15 @@ dgemm_status_t launch(const Call& c, const dg::host::Device& dev) {
     // KN: both halves of a gated product start on 16 bytes
     if (kn && gated && (N / 2) * esz % 16 != 0) return DGEMM_ERR_MISALIGNED;
     // CTA pairs (256 channels, up to 256 rows a tile) where groups are long enough to
-    // share weights between two SMs; single CTAs (128 channels, up to 64 rows) where
-    // the calls read weights for few rows each.
-    const int pair = c.R > 48 * c.E;
+    // share weights between two SMs; single CTAs (128 channels, up to 64 rows) where a
+    // call reads weights for few rows each (64 experts of 4096 x 4096: mean of 32 rows 314 us
+    // against 326, of 64 350 against 338), and where its single-CTA tiles, for groups of the
+    // mean size, are at most one wave (512 rows of 1024 x 2048: 9.4 us against 15.6; just above one
+    // wave, 512 rows of 4096 x 2048: 15.6 against 16.3).
+    const int64_t mean = (c.R + c.E - 1) / c.E, wide = gated ? c.N / 2 : c.N, step = gated ? 64 : 128;
+    const bool one_wave = (mean + 63) / 64 * std::min(c.E, c.R) * ((wide + step - 1) / step) <= dev.num_sms;
+    const int forced = dg::host::pair_override();
+    const int pair = forced >= 0 ? forced : c.R > 48 * c.E && !one_wave;
     const Variant* v = find_variant(c.type, kn, pair, c.a_rows != nullptr);
     if (!v) return DGEMM_ERR_NOT_SUPPORTED;
 

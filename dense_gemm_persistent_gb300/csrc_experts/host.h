@@ -34,6 +34,9 @@ bool encode_map(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, int r
 // a producer early (< 0: off).
 void wait_settings(uint64_t* wait_ns, long long* stall_after);
 
+// The planner override for CTA pairs: -1 none, 0 never, 1 always.
+int pair_override();
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 constexpr int kMaxDevices = 64;

@@ -17,7 +17,8 @@
  * errors return before any launch; every device-side wait is bounded and one
  * that gives up is recorded in the first DGEMM_WS_STATUS_BYTES bytes of the
  * call's workspace (or, without one, in the per-device word) for
- * dgemm_query_device_status. Base pointers of matrices must be 16-byte aligned
+ * dgemm_query_device_status. Of the planner overrides of dgemm.h, cta_pair,
+ * wait_limit_ns and stall_after_loads apply to the products. Base pointers of matrices must be 16-byte aligned
  * (DGEMM_ERR_MISALIGNED otherwise); int32 and float tables need only their
  * natural alignment.
  */

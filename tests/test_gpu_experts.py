@@ -175,6 +175,19 @@ def make(kind, g, sizes, K, N, layout="nk", gather=False, ints=False, tokens=Non
 
 
 def call(kind, a, D, layout="nk", **kw):
+    """The call as the planner has it, then with single CTAs and with CTA pairs (the last result is
+    in D): all three have the same bits, since an output's sum runs over K in the same order."""
+    outs = []
+    for pair in (-1, 0, 1):
+        out = D if pair == 1 else D.clone()
+        with dg.overrides(cta_pair=pair):
+            call_once(kind, a, out, layout, **kw)
+        outs.append(torch.nan_to_num(out.float(), nan=-12345.0))
+    assert torch.equal(outs[0], outs[2]) and torch.equal(outs[1], outs[2])
+    return D
+
+
+def call_once(kind, a, D, layout="nk", **kw):
     on = {k: (v.to(dev()) if v is not None else None) for k, v in a.items()}
     bias = kw.pop("bias", None)
     kw["bias"] = None if bias is None else bias.to(dev())
@@ -403,10 +416,13 @@ def check_int8(M, N, K, act="none", out=BF, with_bias=False, alpha=1.0, beta=0.0
     v = ref.activation(y, act)
     dv = 1.13 * dy + (v.abs() * 2.0 ** -20 if act != "none" else 0.0)
     D = torch.full((M, N), float("nan"), dtype=out, device=dev())
-    dg.dgemm_int8_scaled(A.to(dev()), B.to(dev()), sa.to(dev()), sb.to(dev()), D, C=None if C is None else C.to(dev()),
-                         alpha=alpha, beta=beta, bias=None if bias is None else bias.to(dev()), act=act)
-    assert status_ok()
-    close(D, v, dv + (v.abs() + dv) * (2.0 ** -8 if out == BF else 2.0 ** -24) + 1e-37)
+    on = lambda x: None if x is None else x.to(dev())
+    for pair in (-1, 0, 1):
+        D.fill_(float("nan"))
+        with dg.overrides(cta_pair=pair):
+            dg.dgemm_int8_scaled(on(A), on(B), on(sa), on(sb), D, C=on(C), alpha=alpha, beta=beta, bias=on(bias), act=act)
+            assert status_ok()
+        close(D, v, dv + (v.abs() + dv) * (2.0 ** -8 if out == BF else 2.0 ** -24) + 1e-37)
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 1, 16), (1, 300, 7168), (2, 129, 144), (5, 64, 1024), (8, 1000, 272), (9, 257, 528),
@@ -480,7 +496,7 @@ def test_grouped_wait_that_runs_out_is_reported(kind, sizes, gather):
             f = dg.dgemm_grouped_fp8_scaled if kind == "fp8" else dg.dgemm_grouped_int8_scaled
             f(on["A"], on["B"], on["a_scale"], on["b_scale"], on["offsets"], D, a_rows=on["a_rows"], ws=ws)
 
-    with dg.overrides(stall_after_loads=2, wait_limit_ns=20_000_000):
+    with dg.overrides(stall_after_loads=2, wait_limit_ns=20_000_000, cta_pair=1 if sizes[0] == 300 else 0):
         one()
         assert dg.dgemm_query_device_status(ws) == 6      # DGEMM_ERR_DEVICE_TIMEOUT
     assert status_ok(ws)                                  # the query cleared it; the device word is untouched
@@ -567,3 +583,37 @@ def test_grouped_depths_around_whole_slices(kind, K):
         first = slice(0, sizes[0]) if kind == "bf16" else slice(None)
         assert bool(torch.isfinite(D[first]).all())
         close(D[first], want[first], tol[first])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("layout,gather", [("nk", False), ("nk", True), ("kn", False), ("kn", True)])
+@pytest.mark.parametrize("act", ["none", "swiglu"])
+def test_grouped_more_than_one_wave(kind, layout, gather, act):
+    """Enough tiles for CTA pairs with several tiles each: long groups beside short and empty ones."""
+    if layout == "kn" and kind != "bf16":
+        pytest.skip("K x N weights are BF16")
+    sizes = [515, 0, 1, 290, 64, 33, 256, 700]
+    g = gen(91)
+    K, N = 200 if kind == "bf16" else 208, 2704
+    a = make(kind, g, sizes, K, N, layout, gather, ints=True)
+    rows = torch.arange(sum(sizes)) if a["a_rows"] is None else a["a_rows"].long()
+    wide = N // 2 if act == "swiglu" else N
+    D = torch.full((sum(sizes), wide), float("nan"), dtype=F32, device=dev())
+    call(kind, a, D, layout, act=act)
+    lo = 0
+    for e, n in enumerate(sizes):
+        b = a["B"][e].double()
+        if act == "none":
+            y = a["A"].double()[rows[lo:lo + n]] @ (b.t() if layout == "nk" else b)
+            if a["a_scale"] is not None:
+                y = y * a["a_scale"][rows[lo:lo + n]].double()[:, None] * a["b_scale"][e].double()
+            assert torch.equal(D[lo:lo + n].cpu().double(), y)
+        elif n:      # the group by itself, in few tiles: the same bits
+            pick = lambda x: x.view(torch.uint8)[rows[lo:lo + n]].view(x.dtype) if x.dtype == E4M3 else x[rows[lo:lo + n]]
+            one = dict(a, A=pick(a["A"]), B=a["B"][e:e + 1], offsets=i32([0, n]), a_rows=None)
+            if a["a_scale"] is not None:
+                one.update(a_scale=pick(a["a_scale"]), b_scale=a["b_scale"][e:e + 1])
+            alone = torch.full((n, wide), float("nan"), dtype=F32, device=dev())
+            if n > 4 or kind != "int8":      # (few int8 rows are summed in integers)
+                assert torch.equal(D[lo:lo + n], call(kind, one, alone, layout, act=act))
+        lo += n
