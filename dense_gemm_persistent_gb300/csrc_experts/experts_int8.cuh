@@ -18,9 +18,14 @@
 //   2-3     idle (they complete the first warpgroup)
 //   4-7     epilogue
 //   8-15    weight converters, one channel a thread; two teams
-//   16-23   token converters, rows by index or in order; two teams
+//   16-23   token converters, rows by index or in order; four teams
 // A converted stage is 64 K; the teams take them in turn, since a stage passes through a
-// chain of waits and conversions (~1500 clocks) longer than its MMAs (~700).
+// chain of waits and conversions (1200-1500 clocks) longer than its MMAs (~400 for a whole
+// tile). Four teams of two warps convert tokens faster than two of four: a stage's fixed
+// part, its waits and arrivals, is spread over twice as long (16384 gathered rows of 4096 x 4096
+// over 16 experts 465 us against 410, 768 rows over 64 of 2048 x 4096 128 against 121). The
+// MMA warp shares its scheduler with five others, so it takes two stages per wait
+// (133 against 128 of the latter).
 #pragma once
 
 #include "experts_common.cuh"
@@ -37,15 +42,16 @@ struct Int8Cfg {
     static constexpr int BN_CTA = BN / CTAS;
     static constexpr int KB = 128, KC = 64;              // K of a raw and of a converted stage
     static constexpr int W_RAW = 128 * KB, W_STAGES = 7 + PAIR;
-    static constexpr int AHEAD = PAIR ? 2 : 4;         // stages that a token converter team loads ahead
+    static constexpr int AHEAD = 2;                      // single CTAs: stages that a token team has copies of
     static constexpr int X_CONV = BN_CTA * KC * 2;       // a converted stage: rows here, weights in Tensor Memory
     static constexpr int A_COLS = KC / 2, C_STAGES = 4;
     static constexpr int ACC_COLS = 2 * BN;
-    static constexpr int EPI_WARPS = 4, EPI_WARP0 = 4, W_WARP0 = 8, W_TEAMS = 2, X_WARP0 = W_WARP0 + 4 * W_TEAMS, X_TEAMS = 2;
-    static constexpr int THREADS = 32 * (X_WARP0 + 4 * X_TEAMS);
+    static constexpr int EPI_WARPS = 4, EPI_WARP0 = 4, W_WARP0 = 8, W_TEAMS = 2, X_WARP0 = W_WARP0 + 4 * W_TEAMS, X_TEAMS = 4;
+    static constexpr int STAGE_ARRIVALS = 4 + 2;         // warps of a weight and of a token team
+    static constexpr int THREADS = 32 * (X_WARP0 + 2 * X_TEAMS);
     // registers per thread: at launch, and of the warpgroups after the split
     static constexpr int LAUNCH_REGS = 80, REGS_CONTROL = 48, REGS_EPILOGUE = 128, REGS_WEIGHTS = 72, REGS_TOKENS = 80;
-    static_assert(REGS_CONTROL + REGS_EPILOGUE + W_TEAMS * REGS_WEIGHTS + X_TEAMS * REGS_TOKENS <= THREADS / 128 * LAUNCH_REGS,
+    static_assert(REGS_CONTROL + REGS_EPILOGUE + W_TEAMS * REGS_WEIGHTS + X_TEAMS / 2 * REGS_TOKENS <= THREADS / 128 * LAUNCH_REGS,
                   "register split exceeds the launch allocation");
     static constexpr int TMEM_COLS = ACC_COLS + C_STAGES * A_COLS;
     static_assert(TMEM_COLS == 256 || TMEM_COLS == 512, "Tensor Memory");
@@ -55,7 +61,7 @@ struct Int8Cfg {
     static constexpr int FIXED = 1024 + BUFFERS + exchange_bytes<EPI_WARPS>() + BAR_BYTES;
     static constexpr uint32_t IDESC0 = make_idesc(0u, false, false, 128 * CTAS, 0);   // FP16 operands
     static_assert(FIXED + Schedule::bytes(DGEMM_MAX_EXPERTS) <= 232448, "shared memory");
-    static_assert((2 * W_STAGES + 2 * C_STAGES + 5) * 8 + 8 <= BAR_BYTES, "barriers fit");
+    static_assert((2 * W_STAGES + 3 * C_STAGES / 2 + 5) * 8 + 8 <= BAR_BYTES, "barriers fit");
 };
 
 // Four int8 codes to four FP16 numbers.
@@ -74,8 +80,8 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
     float* exchange = reinterpret_cast<float*>(wraw + CF::BUFFERS);
     uint64_t* w_full = reinterpret_cast<uint64_t*>(wraw + CF::BUFFERS + exchange_bytes<CF::EPI_WARPS>());
     uint64_t* w_empty = w_full + CF::W_STAGES;
-    uint64_t* full = w_empty + CF::W_STAGES;             // converted stages
-    uint64_t* done = full + CF::C_STAGES;
+    uint64_t* full = w_empty + CF::W_STAGES;             // two converted stages, of one raw stage
+    uint64_t* done = full + CF::C_STAGES / 2;            // one of them
     uint64_t* acc_full = done + CF::C_STAGES;
     uint64_t* acc_empty = acc_full + 2;
     uint64_t* drain = acc_empty + 2;
@@ -93,10 +99,8 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
             mbar_init(&w_full[s], 1);
             mbar_init(&w_empty[s], 8);                   // the teams that convert its two halves
         }
-        for (int s = 0; s < CF::C_STAGES; ++s) {
-            mbar_init(&full[s], 8 * CF::CTAS);           // a team's warps of both converters, of both CTAs
-            mbar_init(&done[s], 1);
-        }
+        for (int s = 0; s < CF::C_STAGES / 2; ++s) mbar_init(&full[s], 2 * CF::STAGE_ARRIVALS * CF::CTAS);
+        for (int s = 0; s < CF::C_STAGES; ++s) mbar_init(&done[s], 1);
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], CF::EPI_WARPS * CF::CTAS);
@@ -128,7 +132,7 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
     // converter warps: their part of converted stage g is in place ...
     auto converted = [&](uint32_t g) {
         __syncwarp();
-        uint64_t* bar = &full[g % CF::C_STAGES];
+        uint64_t* bar = &full[(g >> 1) % (CF::C_STAGES / 2)];
         if (lane == 0) {
             if (CF::PAIR && rank != 0) mbar_arrive_peer(mapa_shared(smem_u32(bar), 0));
             else mbar_arrive(bar);
@@ -181,7 +185,7 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
         // ---------------------------------------------------------------- MMA issuer
         if (rank == 0) {
             const uint64_t xd0 = smem_desc_sw128(smem_u32(conv), 16, 1024);
-            uint32_t g = 0;                              // converted stages so far
+            uint32_t g = 0;                              // raw stages so far
             int local = 0;
             const uint32_t tmem_u = __shfl_sync(kAllLanes, tmem, 0);   // (values and branches that the compiler knows to
                                                                        // be the warp's stay in uniform registers)
@@ -193,21 +197,23 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
                 tc_fence_after();
                 const uint32_t acc = tmem_u + static_cast<uint32_t>(buf * CF::BN);
                 const uint32_t idesc = CF::IDESC0 | (static_cast<uint32_t>(__shfl_sync(kAllLanes, t.n, 0) >> 3) << 17);
-                for (int kc = 0; kc < 2 * p.kstages; ++kc, ++g) {
-                    const uint32_t slot = g % CF::C_STAGES, phase = (g / CF::C_STAGES) & 1;
-                    ok = mbar_wait_warp_at<CF::PAIR>(&full[slot], phase, abort_flag, p.wait_ns);
+                for (int kb = 0; kb < p.kstages; ++kb, ++g) {
+                    const uint32_t two = g % (CF::C_STAGES / 2), phase = (g / (CF::C_STAGES / 2)) & 1;
+                    ok = mbar_wait_warp_at<CF::PAIR>(&full[two], phase, abort_flag, p.wait_ns);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t a = tmem_u + CF::ACC_COLS + slot * CF::A_COLS;
-                    const uint64_t xd = xd0 + slot * (CF::X_CONV >> 4);
+                    const uint32_t a = tmem_u + CF::ACC_COLS + two * (2 * CF::A_COLS);
+                    const uint64_t xd = xd0 + two * (2 * CF::X_CONV >> 4);
                     if (elect_one()) {
 #pragma unroll
-                        for (int k = 0; k < CF::KC / 16; ++k) {
-                            const uint32_t more = (kc > 0 || k > 0) ? 1u : 0u;
-                            mma_16_tmem_a<CF::PAIR>(acc, a + k * 8, xd + k * 2, idesc, more);
+                        for (int k = 0; k < 2 * CF::KC / 16; ++k) {
+                            const uint32_t more = (kb > 0 || k > 0) ? 1u : 0u;
+                            mma_16_tmem_a<CF::PAIR>(acc, a + k * 8, xd + (k / 4) * (CF::X_CONV >> 4) + (k % 4) * 2, idesc, more);
+                            if (k % 4 == 3) {
+                                if constexpr (CF::PAIR) mma_commit_pair(&done[2 * two + k / 4], 3);
+                                else mma_commit(&done[2 * two + k / 4]);
+                            }
                         }
-                        if constexpr (CF::PAIR) mma_commit_pair(&done[slot], 3);
-                        else mma_commit(&done[slot]);
                     }
                     __syncwarp();
                 }
@@ -250,51 +256,60 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
         const int team = (warp - CF::W_WARP0) >> 2;
         const int row = threadIdx.x & 127;                   // TMEM lane: the warp's own quarter
         const uint32_t a_base = tmem + CF::ACC_COLS + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        uint32_t g = 0;
-        int turn = team;                                     // stages until this team's next
-        for (int item = unit; ok && cur.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, t); item += units) {
-            for (int kc = 0; kc < 2 * p.kstages; ++kc, ++g) {
-                if (turn-- > 0) continue;
-                turn = CF::W_TEAMS - 1;
-                const uint32_t raw = (g >> 1) % CF::W_STAGES, half = g & 1;
-                ok = mbar_wait_warp(&w_full[raw], ((g >> 1) / CF::W_STAGES) & 1, abort_flag, p.wait_ns);
-                if (!ok) break;
-                const uint8_t* src = wraw + raw * CF::W_RAW + row * 128;
-                uint4 codes[4];
+        // The team's half of every raw stage, whatever tile it is of. The next codes are fetched before
+        // the wait for this stage's slot, or behind its store where a pair's MMAs are what takes longest
+        // (768 rows over 64 experts of 2048 x 4096 118 us against 121; 4096 x 11008 x 4096 295 against 293).
+        const int64_t tiles = static_cast<int64_t>(sched.head[1]) * p.ctiles;
+        int64_t left = tiles > unit ? (tiles - unit + units - 1) / units * p.kstages : 0;
+        const uint8_t* src = wraw + row * 128;
+        const int at = (team * 4) ^ (row & 4), low = row & 3;
+        uint4 codes[4];
+        uint32_t raw = 0, phase = 0, g = team;
+        auto fetch = [&]() {                                 // a stage's codes into registers
+            if (!mbar_wait_warp(&w_full[raw], phase, abort_flag, p.wait_ns)) return false;
+            const uint8_t* from = src + raw * CF::W_RAW;
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    codes[c] = *reinterpret_cast<const uint4*>(src + (((half * 4 + c) ^ (row & 7)) << 4));
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&w_empty[raw]);   // the codes are in registers
-                uint32_t h[32];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    int8x4_to_f16(codes[c].x, h[8 * c], h[8 * c + 1]);
-                    int8x4_to_f16(codes[c].y, h[8 * c + 2], h[8 * c + 3]);
-                    int8x4_to_f16(codes[c].z, h[8 * c + 4], h[8 * c + 5]);
-                    int8x4_to_f16(codes[c].w, h[8 * c + 6], h[8 * c + 7]);
-                }
-                ok = slot_free(g);
-                if (!ok) break;
-                tc_fence_after();
-                tmem_st32(a_base + g % CF::C_STAGES * CF::A_COLS, h);
-                tmem_st_wait();
-                tc_fence_before();
-                converted(g);
+            for (int c = 0; c < 4; ++c) codes[c] = *reinterpret_cast<const uint4*>(from + ((at + (c ^ low)) << 4));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&w_empty[raw]);
+            if (++raw == CF::W_STAGES) {
+                raw = 0;
+                phase ^= 1;
             }
+            return true;
+        };
+        if (left > 0) ok = fetch();
+        for (; ok && left > 0; --left, g += CF::W_TEAMS) {
+            uint32_t h[32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                int8x4_to_f16(codes[c].x, h[8 * c], h[8 * c + 1]);
+                int8x4_to_f16(codes[c].y, h[8 * c + 2], h[8 * c + 3]);
+                int8x4_to_f16(codes[c].z, h[8 * c + 4], h[8 * c + 5]);
+                int8x4_to_f16(codes[c].w, h[8 * c + 6], h[8 * c + 7]);
+            }
+            if (!CF::PAIR && left > 1) ok = fetch();
+            ok = ok && slot_free(g);
+            if (!ok) break;
+            tc_fence_after();
+            tmem_st32(a_base + g % CF::C_STAGES * CF::A_COLS, h);
+            tmem_st_wait();
+            tc_fence_before();
+            converted(g);
+            if (CF::PAIR && left > 1) ok = fetch();
         }
         if (!ok) fail(p, ERR_TIMEOUT_PRODUCER, abort_flag);
         __syncwarp();
     } else {
         // ---------------------------------------------------------------- token converters
-        // Four threads load and convert a row's 64 codes, 16 each; AHEAD of the team's stages are
-        // on their way before one is converted.
+        // Four threads load and convert a row's 64 codes, 16 each, 16 rows a round; the team's next
+        // stage is on its way before one is converted.
         regs_dec<CF::REGS_TOKENS>();
-        constexpr int ROUNDS = CF::BN_CTA / 32;
-        const int team = (warp - CF::X_WARP0) >> 2;
-        const int tid = threadIdx.x & 127, sub = tid >> 2, chunk = tid & 3;
+        constexpr int ROUNDS = CF::BN_CTA / 16;
+        const int team = (warp - CF::X_WARP0) >> 1;
+        const int tid = threadIdx.x & 63, sub = tid >> 2, chunk = tid & 3;
         const int at0 = ((2 * chunk) ^ (sub & 7)) << 4, at1 = ((2 * chunk + 1) ^ (sub & 7)) << 4;
-        int item = unit, kb = 0, rounds = 0, src[ROUNDS], next[ROUNDS];
+        int item = unit, kb = team >> 1, rounds = 0, src[ROUNDS], next[ROUNDS];
         Cursor ahead;
         Tile ta;                                             // the tile after the one that is loaded from
         bool more = p.kstages > 0 && ahead.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, ta), live = false;
@@ -302,7 +317,7 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
             const int xrows = ta.n / CF::CTAS, first = static_cast<int>(rank) * xrows;
 #pragma unroll
             for (int i = 0; i < ROUNDS; ++i) {
-                const int row = i * 32 + sub, r = first + row;
+                const int row = i * 16 + sub, r = first + row;
                 next[i] = -1;
                 if (row < xrows && r < ta.rows) next[i] = p.a_rows ? __ldg(p.a_rows + ta.row0 + r) : ta.row0 + r;
             }
@@ -310,123 +325,110 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
         auto advance = [&]() {                               // on to that tile
             live = more;
             if (!more) return;
-            rounds = (ta.n / CF::CTAS + 31) / 32;
+            rounds = ta.n / (16 * CF::CTAS);
 #pragma unroll
             for (int i = 0; i < ROUNDS; ++i) src[i] = next[i] < p.a_count ? next[i] : -1;
             item += units;
             more = ahead.at<CF::BN, CF::CTAS>(p, sched, item, tile_channels, ta);
             if (more) look();
         };
+        auto settle = [&]() {                                // kb past a tile's last stage is a stage of a later tile
+            while (live && kb >= p.kstages) {
+                kb -= p.kstages;
+                advance();
+            }
+        };
         if (more) look();
         advance();
+        settle();
+        const int half = (team & 1) * CF::KC + chunk * 16;
         if constexpr (CF::PAIR) {
-            // Two stages in two register sets.
-            struct Held {
-                uint4 codes[ROUNDS];
-                int rounds;                                      // 0: past the last stage
+            // A stage's codes in registers; as one is converted its registers take the next.
+            uint4 codes[ROUNDS];
+            auto load = [&](int i) {
+                const int k = kb * CF::KB + half;
+                codes[i] = make_uint4(0, 0, 0, 0);
+                if (live && src[i] >= 0 && k < p.K)
+                    codes[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(p.A) + k + static_cast<int64_t>(src[i]) * p.K));
             };
-            auto load = [&](Held& h) {                           // the team's next stage
-                h.rounds = live ? rounds : 0;
-                if (!live) return;
-                const int k = kb * CF::KB + team * CF::KC + chunk * 16;
-                const char* base = static_cast<const char*>(p.A) + k;
-    #pragma unroll
-                for (int i = 0; i < ROUNDS; ++i) {
-                    h.codes[i] = make_uint4(0, 0, 0, 0);
-                    if (src[i] >= 0 && k < p.K)
-                        h.codes[i] = __ldg(reinterpret_cast<const uint4*>(base + static_cast<int64_t>(src[i]) * p.K));
-                }
-                if (++kb == p.kstages) {
-                    kb = 0;
-                    advance();
-                }
-            };
-            uint32_t g = team;
-            auto convert = [&](const Held& h) {
-                if (!slot_free(g)) return false;
+#pragma unroll
+            for (int i = 0; i < ROUNDS; ++i) load(i);
+            for (uint32_t g = team; live; g += CF::X_TEAMS) {
+                const int now = rounds;
+                kb += CF::X_TEAMS / 2;
+                settle();
+                ok = slot_free(g);
+                if (!ok) break;
                 uint8_t* dst = conv + g % CF::C_STAGES * CF::X_CONV + sub * 128;
-    #pragma unroll
+#pragma unroll
                 for (int i = 0; i < ROUNDS; ++i) {
-                    if (i >= h.rounds) break;
-                    uint4 lo, hi;
-                    int8x4_to_f16(h.codes[i].x, lo.x, lo.y);
-                    int8x4_to_f16(h.codes[i].y, lo.z, lo.w);
-                    int8x4_to_f16(h.codes[i].z, hi.x, hi.y);
-                    int8x4_to_f16(h.codes[i].w, hi.z, hi.w);
-                    *reinterpret_cast<uint4*>(dst + i * 4096 + at0) = lo;
-                    *reinterpret_cast<uint4*>(dst + i * 4096 + at1) = hi;
+                    if (i < now) {
+                        uint4 lo, hi;
+                        int8x4_to_f16(codes[i].x, lo.x, lo.y);
+                        int8x4_to_f16(codes[i].y, lo.z, lo.w);
+                        int8x4_to_f16(codes[i].z, hi.x, hi.y);
+                        int8x4_to_f16(codes[i].w, hi.z, hi.w);
+                        *reinterpret_cast<uint4*>(dst + i * 2048 + at0) = lo;
+                        *reinterpret_cast<uint4*>(dst + i * 2048 + at1) = hi;
+                    }
+                    load(i);
                 }
                 fence_proxy_async_smem();
                 converted(g);
-                g += CF::X_TEAMS;
-                return true;
-            };
-            Held held[CF::AHEAD];
-    #pragma unroll
-            for (int i = 0; i < CF::AHEAD; ++i) load(held[i]);
-            bool left = true;
-            while (ok && left) {
-    #pragma unroll
-                for (int i = 0; i < CF::AHEAD; ++i) {
-                    left = left && held[i].rounds > 0;
-                    if (!left || !ok) break;
-                    ok = convert(held[i]);
-                    load(held[i]);
-                }
             }
         } else {
             // A thread's own places in shared memory, AHEAD stages of ROUNDS x 16 bytes: copies
             // are waited for stage by stage, where registers in flight all wait for the last.
-            // (768 rows over 64 experts of 2048 x 4096: 133 us against 151. For pairs the extra
-            // traffic and the fence behind the copies cost more: 4096 x 11008 x 4096 358 against 313.)
+            // (With two teams, 768 rows over 64 experts of 2048 x 4096: 133 us against 151. For pairs the
+            // extra traffic and the fence behind the copies cost more: 4096 x 11008 x 4096 358 against 313.)
             uint8_t* place = conv + CF::C_STAGES * CF::X_CONV + team * CF::AHEAD * CF::X_RAW + tid * 16;
             int slot_in = 0, slot_out = 0;
             auto load = [&]() {                                  // the team's next stage (an empty group past the last)
                 if (live) {
-                    const int k = kb * CF::KB + team * CF::KC + chunk * 16;
+                    const int k = kb * CF::KB + half;
                     const char* base = static_cast<const char*>(p.A) + k;
-    #pragma unroll
+#pragma unroll
                     for (int i = 0; i < ROUNDS; ++i) {
                         if (i >= rounds) break;
                         const bool read = src[i] >= 0 && k < p.K;
-                        cp_async_16(place + slot_in * CF::X_RAW + i * 2048,
+                        cp_async_16(place + slot_in * CF::X_RAW + i * 1024,
                                     read ? base + static_cast<int64_t>(src[i]) * p.K : static_cast<const char*>(p.A), read ? 16u : 0u);
                     }
-                    if (++kb == p.kstages) {
-                        kb = 0;
-                        advance();
-                    }
+                    kb += CF::X_TEAMS / 2;
+                    settle();
                 }
                 cp_async_commit();
                 if (++slot_in == CF::AHEAD) slot_in = 0;
             };
-    #pragma unroll 1
+#pragma unroll 1
             for (int i = 0; i < CF::AHEAD - 1; ++i) load();
             uint32_t g = team;
+            int n = team >> 1;
             for (int at = unit; ok && cur.at<CF::BN, CF::CTAS>(p, sched, at, tile_channels, t); at += units) {
-                const int now = (t.n / CF::CTAS + 31) / 32;
-                for (int n = 0; n < p.kstages; ++n, g += CF::X_TEAMS) {
+                const int now = t.n / (16 * CF::CTAS);
+                for (; n < p.kstages; n += CF::X_TEAMS / 2, g += CF::X_TEAMS) {
                     load();
                     cp_async_wait<CF::AHEAD - 1>();              // this stage's copies (this thread's own) have landed
                     ok = slot_free(g);
                     if (!ok) break;
                     uint8_t* dst = conv + g % CF::C_STAGES * CF::X_CONV + sub * 128;
-    #pragma unroll
+#pragma unroll
                     for (int i = 0; i < ROUNDS; ++i) {
                         if (i >= now) break;
-                        const uint4 c = *reinterpret_cast<const uint4*>(place + slot_out * CF::X_RAW + i * 2048);
+                        const uint4 c = *reinterpret_cast<const uint4*>(place + slot_out * CF::X_RAW + i * 1024);
                         uint4 lo, hi;
                         int8x4_to_f16(c.x, lo.x, lo.y);
                         int8x4_to_f16(c.y, lo.z, lo.w);
                         int8x4_to_f16(c.z, hi.x, hi.y);
                         int8x4_to_f16(c.w, hi.z, hi.w);
-                        *reinterpret_cast<uint4*>(dst + i * 4096 + at0) = lo;
-                        *reinterpret_cast<uint4*>(dst + i * 4096 + at1) = hi;
+                        *reinterpret_cast<uint4*>(dst + i * 2048 + at0) = lo;
+                        *reinterpret_cast<uint4*>(dst + i * 2048 + at1) = hi;
                     }
                     fence_proxy_async_smem();
                     converted(g);
                     if (++slot_out == CF::AHEAD) slot_out = 0;
                 }
+                n -= p.kstages;
             }
             cp_async_wait<0>();                                  // nothing of this thread's is in flight when it leaves
         }
