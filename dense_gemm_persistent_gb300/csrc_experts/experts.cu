@@ -99,16 +99,16 @@ dg::experts::Params make_params(const Call& c, const dg::host::Device& dev) {
 
 // Shared memory of the kernels of few rows: the rows, and the schedule.
 constexpr size_t kFewSharedBytes = 74 * 1024;     // three CTAs an SM
-constexpr int kFewRows = 4;
 
 // Rows of a tile of the few-rows kernel for an int8 call, 0 where the tensor-core kernel
-// takes it: the first's work grows with the rows, the second's hardly does. Over 64 experts of
-// 2048 x 4096 a mean of 4 rows took 117 us against 141, a mean of 8 169 against 171, of 12 240
-// against 174.
+// takes it: the first's work grows with the rows, the second's hardly does. One group of
+// 18432 x 7168: 25.5 us against 34.1 for a row, 32.0 against 34.2 for 4 (the instantiated most). Of
+// several groups some are longer than the mean and read their weights more than once: 64 experts of
+// 2048 x 4096, mean of 2 rows 83 us against 85, of 4 117 against 101.
 int few_rows(const Call& c) {
     if (c.type != DGEMM_GROUPED_INT8 || c.K == 0 || c.K > 131071) return 0;
     const int64_t mean = (c.R + c.E - 1) / c.E;
-    for (int rows = 1; rows <= kFewRows; rows *= 2)
+    for (int rows = 1; rows <= (c.E == 1 ? 4 : 2); rows *= 2)
         if (mean <= rows && rows * static_cast<size_t>(c.K) + dg::experts::Schedule::bytes(static_cast<int>(c.E)) <=
                                 kFewSharedBytes)
             return rows;
@@ -149,14 +149,17 @@ dgemm_status_t launch(const Call& c, const dg::host::Device& dev) {
     if (kn && gated && (N / 2) * esz % 16 != 0) return DGEMM_ERR_MISALIGNED;
     // CTA pairs (256 channels, up to 256 rows a tile) where groups are long enough to
     // share weights between two SMs; single CTAs (128 channels, up to 64 rows) where a
-    // call reads weights for few rows each (64 experts of 4096 x 4096: mean of 32 rows 314 us
-    // against 326, of 64 350 against 338), and where its single-CTA tiles, for groups of the
-    // mean size, are at most one wave (512 rows of 1024 x 2048: 9.4 us against 15.6; just above one
-    // wave, 512 rows of 4096 x 2048: 15.6 against 16.3).
+    // call reads weights for few rows each, and where its single-CTA tiles, for groups of the
+    // mean size, are at most one wave. Single against pairs, in us: BF16, 64 experts of 4096 x 4096,
+    // mean of 32 rows 323 / 332, 48 331 / 337, 64 349 / 342, 128 449 / 368 (E4M3 166 / 172, 171 / 174,
+    // 181 / 177, 238 / 192). INT8 pairs convert a weight once for 192 rows, not 64, which pays earlier: 64 experts of
+    // 2048 x 4096, mean of 16 122 / 129, 24 134 / 131, 32 143 / 133, 64 193 / 146; 32 of 4096 x 7168,
+    // mean of 24 206 / 214, 32 236 / 215. One wave: BF16 512 rows of 1024 x 2048 9.4 / 15.6, but just
+    // above it, 512 rows of 4096 x 2048, 16.3 / 15.6; INT8 256 rows of 4096 x 4096 22.8 / 25.0, 512 39.9 / 28.5.
     const int64_t mean = (c.R + c.E - 1) / c.E, wide = gated ? c.N / 2 : c.N, step = gated ? 64 : 128;
     const bool one_wave = (mean + 63) / 64 * std::min(c.E, c.R) * ((wide + step - 1) / step) <= dev.num_sms;
     const int forced = dg::host::pair_override();
-    const int pair = forced >= 0 ? forced : c.R > 48 * c.E && !one_wave;
+    const int pair = forced >= 0 ? forced : c.R > (c.type == DGEMM_GROUPED_INT8 ? 24 : 48) * c.E && !one_wave;
     const Variant* v = find_variant(c.type, kn, pair, c.a_rows != nullptr);
     if (!v) return DGEMM_ERR_NOT_SUPPORTED;
 

@@ -9,8 +9,8 @@
 // read from there serves 4 channels. At the end the lanes' sums are folded so that each
 // lane ends up with its own outputs (halving exchange: as many shuffles as sums).
 // What bounds it: HBM for one or two rows, then the dot products (4 x ROWS per 16 bytes of
-// weights). 18432 x 7168 with 1 / 2 / 4 / 8 rows took 31 / 31 / 35 / 50 us where the tensor-core
-// kernel takes 43 / 44 / 46 / 49, so tiles of 8 rows and more are left to that one.
+// weights). 18432 x 7168 with 1 / 2 / 4 rows takes 25.5 / 25.9 / 32.0 us (5.2 TB/s for one) where the
+// tensor-core kernel takes 34.2; tiles of 8 rows took 50 and are left to that one.
 #pragma once
 
 #include "experts_common.cuh"
