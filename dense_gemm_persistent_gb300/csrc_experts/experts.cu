@@ -97,22 +97,16 @@ dg::experts::Params make_params(const Call& c, const dg::host::Device& dev) {
     return p;
 }
 
-// Shared memory of the kernels of few rows: the rows, and the schedule.
+// Shared memory of the kernels of few rows.
 constexpr size_t kFewSharedBytes = 74 * 1024;     // three CTAs an SM
 
-// Rows of a tile of the few-rows kernel for an int8 call, 0 where the tensor-core kernel
-// takes it: the first's work grows with the rows, the second's hardly does. One group of
-// 18432 x 7168: 25.5 us against 34.1 for a row, 32.0 against 34.2 for 4 (the instantiated most). Of
-// several groups some are longer than the mean and read their weights more than once: 64 experts of
-// 2048 x 4096, mean of 2 rows 83 us against 85, of 4 117 against 101.
+// Most rows (1 or 2) of the few-rows kernel for an int8 call that it takes, 0 where the
+// tensor-core kernel does: one set of weights and at most two rows (18432 x 7168: 25.5 us
+// against 28.3 for one row; tiles of four took 32.0 against 28.4, and 64 experts of 2048 x 4096 with one row each
+// on average 66 against 58).
 int few_rows(const Call& c) {
-    if (c.type != DGEMM_GROUPED_INT8 || c.K == 0 || c.K > 131071) return 0;
-    const int64_t mean = (c.R + c.E - 1) / c.E;
-    for (int rows = 1; rows <= (c.E == 1 ? 4 : 2); rows *= 2)
-        if (mean <= rows && rows * static_cast<size_t>(c.K) + dg::experts::Schedule::bytes(static_cast<int>(c.E)) <=
-                                kFewSharedBytes)
-            return rows;
-    return 0;
+    if (c.type != DGEMM_GROUPED_INT8 || c.E != 1 || c.R > 2 || c.K == 0 || c.K > 131071) return 0;
+    return static_cast<size_t>(c.R) * static_cast<size_t>(c.K) <= kFewSharedBytes ? static_cast<int>(c.R) : 0;
 }
 
 dgemm_status_t launch_few(const Call& c, const dg::host::Device& dev, int rows) {
@@ -124,10 +118,8 @@ dgemm_status_t launch_few(const Call& c, const dg::host::Device& dev, int rows) 
     dg::experts::Params p = make_params(c, dev);
     const int tile_channels = p.gated ? v->tile / 2 : v->tile;
     p.ctiles = (p.wide + tile_channels - 1) / tile_channels;
-    const int64_t most_tiles = ((c.R + rows - 1) / rows + std::min(c.E, c.R)) * p.ctiles;
-    if (most_tiles > INT32_MAX / 2) return DGEMM_ERR_NOT_SUPPORTED;
-    const int grid = static_cast<int>(std::min<int64_t>(static_cast<int64_t>(dev.num_sms) * v->ctas_per_sm, most_tiles));
-    static std::atomic<unsigned char> ready[3][dg::host::kMaxDevices];
+    const int grid = std::min(dev.num_sms * v->ctas_per_sm, p.ctiles);
+    static std::atomic<unsigned char> ready[2][dg::host::kMaxDevices];
     std::atomic<unsigned char>& flag = ready[at][dev.id];
     if (!flag.load(std::memory_order_acquire)) {
         if (cudaFuncSetAttribute(v->func, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -135,7 +127,7 @@ dgemm_status_t launch_few(const Call& c, const dg::host::Device& dev, int rows) 
             return DGEMM_ERR_CUDA;
         flag.store(1, std::memory_order_release);
     }
-    const size_t smem = rows * static_cast<size_t>(c.K) + dg::experts::Schedule::bytes(p.E);
+    const size_t smem = rows * static_cast<size_t>(c.K);
     return v->launch(c.B, p, grid, smem, c.stream) == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
 }
 
@@ -152,14 +144,14 @@ dgemm_status_t launch(const Call& c, const dg::host::Device& dev) {
     // call reads weights for few rows each, and where its single-CTA tiles, for groups of the
     // mean size, are at most one wave. Single against pairs, in us: BF16, 64 experts of 4096 x 4096,
     // mean of 32 rows 323 / 332, 48 331 / 337, 64 349 / 342, 128 449 / 368 (E4M3 166 / 172, 171 / 174,
-    // 181 / 177, 238 / 192). INT8 pairs convert a weight once for 192 rows, not 64, which pays earlier: 64 experts of
-    // 2048 x 4096, mean of 16 122 / 129, 24 134 / 131, 32 143 / 133, 64 193 / 146; 32 of 4096 x 7168,
-    // mean of 24 206 / 214, 32 236 / 215. One wave: BF16 512 rows of 1024 x 2048 9.4 / 15.6, but just
-    // above it, 512 rows of 4096 x 2048, 16.3 / 15.6; INT8 256 rows of 4096 x 4096 22.8 / 25.0, 512 39.9 / 28.5.
+    // 181 / 177, 238 / 192). INT8 pairs convert a weight once for 192 rows, not 64, which pays earlier: 64 experts
+    // of 2048 x 4096, mean of 24 116 / 128, 32 128 / 130, 40 140 / 133, 64 175 / 143; 32 of 4096 x 7168, mean of
+    // 32 202 / 209, 40 225 / 212. One wave: BF16 512 rows of 1024 x 2048 9.4 / 15.6, but just above it,
+    // 512 rows of 4096 x 2048, 16.3 / 15.6; INT8 64 rows of 18432 x 7168 34.5 / 40.5, 96 54 / 43.
     const int64_t mean = (c.R + c.E - 1) / c.E, wide = gated ? c.N / 2 : c.N, step = gated ? 64 : 128;
     const bool one_wave = (mean + 63) / 64 * std::min(c.E, c.R) * ((wide + step - 1) / step) <= dev.num_sms;
     const int forced = dg::host::pair_override();
-    const int pair = forced >= 0 ? forced : c.R > (c.type == DGEMM_GROUPED_INT8 ? 24 : 48) * c.E && !one_wave;
+    const int pair = forced >= 0 ? forced : c.R > (c.type == DGEMM_GROUPED_INT8 ? 36 : 48) * c.E && !one_wave;
     const Variant* v = find_variant(c.type, kn, pair, c.a_rows != nullptr);
     if (!v) return DGEMM_ERR_NOT_SUPPORTED;
 

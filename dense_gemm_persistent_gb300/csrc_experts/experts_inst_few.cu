@@ -1,4 +1,4 @@
-// experts_inst_few.cu -- variants of the int8 products of few rows: 1, 2 or 4 a tile.
+// experts_inst_few.cu -- variants of the int8 products of one or two rows.
 #include "experts_few.cuh"
 #include "experts_kernels.h"
 #include "host.h"
@@ -22,8 +22,8 @@ FewVariant make_few() {
 }  // namespace
 
 const FewVariant* variants_few(int* count) {
-    static const FewVariant t[] = {make_few<FewCfg<1>>(), make_few<FewCfg<2>>(), make_few<FewCfg<4>>()};
-    *count = 3;
+    static const FewVariant t[] = {make_few<FewCfg<1>>(), make_few<FewCfg<2>>()};
+    *count = 2;
     return t;
 }
 

@@ -10,22 +10,23 @@
 // shared memory, its B operand. 128 K of a 256 x 192 tile of a CTA pair move 80 KB through
 // each SM's shared memory; with the converted weights there too (256 x 256 tiles) it
 // was 160 KB, 78 % of what shared memory can move in the time taken: 4096 x 11008 x 4096
-// 367 us against 333, 768 rows over 64 experts of 2048 x 4096 162 against 150. Three teams of weight
-// converters were slower (351, 159): fewer registers each.
+// 367 us against 333, 768 rows over 64 experts of 2048 x 4096 162 against 150.
 // Warps of a CTA:
 //   0       TMA producer of weight codes: 128 channels x 128 K, 128B swizzle
 //   1       MMA issuer, owner of the Tensor Memory
 //   2-3     idle (they complete the first warpgroup)
 //   4-7     epilogue
-//   8-15    weight converters, one channel a thread; two teams
-//   16-23   token converters, rows by index or in order; four teams
+//   8-..    weight converters, one channel a thread; three teams of four warps (pairs: two)
+//   then    token converters, rows by index or in order; four teams of two warps
 // A converted stage is 64 K; the teams take them in turn, since a stage passes through a
 // chain of waits and conversions (1200-1500 clocks) longer than its MMAs (~400 for a whole
 // tile). Four teams of two warps convert tokens faster than two of four: a stage's fixed
 // part, its waits and arrivals, is spread over twice as long (16384 gathered rows of 4096 x 4096
 // over 16 experts 465 us against 410, 768 rows over 64 of 2048 x 4096 128 against 121). The
 // MMA warp shares its scheduler with five others, so it takes two stages per wait
-// (133 against 128 of the latter).
+// (133 against 128 of the latter). A third team of weight converters helps single CTAs (104 against
+// 120), whose tokens need few registers; a fourth has too few (112). For pairs the registers
+// that a third takes from the token teams cost more (326 against 295 for 4096 x 11008 x 4096).
 #pragma once
 
 #include "experts_common.cuh"
@@ -46,11 +47,11 @@ struct Int8Cfg {
     static constexpr int X_CONV = BN_CTA * KC * 2;       // a converted stage: rows here, weights in Tensor Memory
     static constexpr int A_COLS = KC / 2, C_STAGES = 4;
     static constexpr int ACC_COLS = 2 * BN;
-    static constexpr int EPI_WARPS = 4, EPI_WARP0 = 4, W_WARP0 = 8, W_TEAMS = 2, X_WARP0 = W_WARP0 + 4 * W_TEAMS, X_TEAMS = 4;
+    static constexpr int EPI_WARPS = 4, EPI_WARP0 = 4, W_WARP0 = 8, W_TEAMS = PAIR ? 2 : 3, X_WARP0 = W_WARP0 + 4 * W_TEAMS, X_TEAMS = 4;
     static constexpr int STAGE_ARRIVALS = 4 + 2;         // warps of a weight and of a token team
     static constexpr int THREADS = 32 * (X_WARP0 + 2 * X_TEAMS);
     // registers per thread: at launch, and of the warpgroups after the split
-    static constexpr int LAUNCH_REGS = 80, REGS_CONTROL = 48, REGS_EPILOGUE = 128, REGS_WEIGHTS = 72, REGS_TOKENS = 80;
+    static constexpr int LAUNCH_REGS = PAIR ? 80 : 72, REGS_CONTROL = 48, REGS_EPILOGUE = 128, REGS_WEIGHTS = 72, REGS_TOKENS = PAIR ? 80 : 56;
     static_assert(REGS_CONTROL + REGS_EPILOGUE + W_TEAMS * REGS_WEIGHTS + X_TEAMS / 2 * REGS_TOKENS <= THREADS / 128 * LAUNCH_REGS,
                   "register split exceeds the launch allocation");
     static constexpr int TMEM_COLS = ACC_COLS + C_STAGES * A_COLS;
@@ -256,30 +257,28 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
         const int team = (warp - CF::W_WARP0) >> 2;
         const int row = threadIdx.x & 127;                   // TMEM lane: the warp's own quarter
         const uint32_t a_base = tmem + CF::ACC_COLS + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        // The team's half of every raw stage, whatever tile it is of. The next codes are fetched before
-        // the wait for this stage's slot, or behind its store where a pair's MMAs are what takes longest
-        // (768 rows over 64 experts of 2048 x 4096 118 us against 121; 4096 x 11008 x 4096 295 against 293).
+        // Stages are counted over all of the CTA's tiles (operands that fit in memory keep the count
+        // below 2^31). The next codes are fetched before the wait for this stage's slot, or behind
+        // its store where a pair's MMAs are what takes longest (with two teams, 768 rows over 64
+        // experts of 2048 x 4096 118 us against 121; 4096 x 11008 x 4096 295 against 293).
         const int64_t tiles = static_cast<int64_t>(sched.head[1]) * p.ctiles;
-        int64_t left = tiles > unit ? (tiles - unit + units - 1) / units * p.kstages : 0;
+        const uint32_t total = tiles > unit ? static_cast<uint32_t>((tiles - unit + units - 1) / units * 2 * p.kstages) : 0u;
         const uint8_t* src = wraw + row * 128;
-        const int at = (team * 4) ^ (row & 4), low = row & 3;
+        const int low = row & 3;
         uint4 codes[4];
-        uint32_t raw = 0, phase = 0, g = team;
-        auto fetch = [&]() {                                 // a stage's codes into registers
-            if (!mbar_wait_warp(&w_full[raw], phase, abort_flag, p.wait_ns)) return false;
+        auto fetch = [&](uint32_t g) {                       // a stage's codes into registers
+            const uint32_t n = g >> 1, raw = n % CF::W_STAGES;
+            if (!mbar_wait_warp(&w_full[raw], (n / CF::W_STAGES) & 1, abort_flag, p.wait_ns)) return false;
             const uint8_t* from = src + raw * CF::W_RAW;
+            const int at = (static_cast<int>(g & 1) * 4) ^ (row & 4);
 #pragma unroll
             for (int c = 0; c < 4; ++c) codes[c] = *reinterpret_cast<const uint4*>(from + ((at + (c ^ low)) << 4));
             __syncwarp();
             if (lane == 0) mbar_arrive(&w_empty[raw]);
-            if (++raw == CF::W_STAGES) {
-                raw = 0;
-                phase ^= 1;
-            }
             return true;
         };
-        if (left > 0) ok = fetch();
-        for (; ok && left > 0; --left, g += CF::W_TEAMS) {
+        if (static_cast<uint32_t>(team) < total) ok = fetch(team);
+        for (uint32_t g = team; ok && g < total; g += CF::W_TEAMS) {
             uint32_t h[32];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
@@ -288,7 +287,8 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
                 int8x4_to_f16(codes[c].z, h[8 * c + 4], h[8 * c + 5]);
                 int8x4_to_f16(codes[c].w, h[8 * c + 6], h[8 * c + 7]);
             }
-            if (!CF::PAIR && left > 1) ok = fetch();
+            const bool again = g + CF::W_TEAMS < total;
+            if (!CF::PAIR && again) ok = fetch(g + CF::W_TEAMS);
             ok = ok && slot_free(g);
             if (!ok) break;
             tc_fence_after();
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
             tmem_st_wait();
             tc_fence_before();
             converted(g);
-            if (CF::PAIR && left > 1) ok = fetch();
+            if (CF::PAIR && again) ok = fetch(g + CF::W_TEAMS);
         }
         if (!ok) fail(p, ERR_TIMEOUT_PRODUCER, abort_flag);
         __syncwarp();

@@ -25,9 +25,9 @@ const Variant* variants_bf16_kn(int* count);
 const Variant* variants_fp8(int* count);
 const Variant* variants_int8(int* count);
 
-// Few rows a group (int8).
+// One or two rows in all (int8).
 struct FewVariant {
-    int rows, tile, ctas_per_sm;   // rows of a tile; weight rows of a tile
+    int rows, tile, ctas_per_sm;   // most rows; weight rows of a tile
     const void* func;
     cudaError_t (*launch)(const void* B, const Params& p, int grid, size_t smem, cudaStream_t s);
 };
