@@ -20,6 +20,7 @@
 #include "dgemm_experts.h"
 #include "host.h"
 #include "ptx.cuh"
+#include "route_layout.h"
 
 namespace {
 
@@ -196,7 +197,7 @@ __device__ __forceinline__ int scan_experts(int* total, int E) {
 // placed here as well: one launch.
 template <int VPL, bool BF16>
 __global__ void __launch_bounds__(VPL <= 8 ? 1024 : 512, VPL <= 8 ? 2 : 1) route_select(const RouteParams p) {
-    extern __shared__ unsigned long long mask[];            // [E]
+    extern __shared__ __align__(16) unsigned long long mask[];            // [E]
     int* total = reinterpret_cast<int*>(mask + p.E);        // [E] (one chunk)
     int* sid = total + p.E;                                 // [CHUNK][k]
     dg::grid_dependency_wait();
@@ -239,20 +240,16 @@ __global__ void __launch_bounds__(VPL <= 8 ? 1024 : 512, VPL <= 8 ? 2 : 1) route
 // Rows of one chunk's pairs: every CTA sums the counts of the chunks before its own
 // and of all chunks (four experts a load, a thread's loads in flight together), scans
 // the totals over the experts, and places its pairs.
-constexpr int PLACE_THREADS = 1024;
+constexpr int PLACE_THREADS = dg::route::kPlaceThreads;
 constexpr int PLACE_PAIRS = CHUNK * DGEMM_MAX_TOPK / PLACE_THREADS;   // pairs of one thread, at most
 
-// Threads that share a quad of experts.
-__host__ __device__ inline int place_parts(int pitch) {
-    const int n = PLACE_THREADS / (pitch / 4);
-    return n < 1 ? 1 : n > 32 ? 32 : n;
-}
-
 __global__ void __launch_bounds__(PLACE_THREADS, 2) route_place(const RouteParams p) {
-    extern __shared__ unsigned long long mask[];            // [pitch]
-    int* before = reinterpret_cast<int*>(mask + p.pitch);   // [parts][pitch] pairs of e in earlier chunks
-    const int quads = p.pitch / 4, parts = place_parts(p.pitch);
-    int* base = before + parts * p.pitch;                   // [parts][pitch] pairs of e; then first row of e
+    extern __shared__ __align__(16) unsigned long long mask[];            // [pitch]
+    const dg::route::PlaceLayout layout(p.E);
+    char* const smem = reinterpret_cast<char*>(mask);
+    int* before = reinterpret_cast<int*>(smem + layout.before);   // [parts][pitch] pairs of e in earlier chunks
+    int* base = reinterpret_cast<int*>(smem + layout.base);       // [parts][pitch] pairs of e; then first row of e
+    const int quads = p.pitch / 4, parts = layout.parts;
     dg::grid_dependency_wait();
     if (threadIdx.x == 0) dg::grid_launch_dependents();
     const int mine = static_cast<int>(blockIdx.x);
@@ -381,7 +378,7 @@ extern "C" dgemm_status_t dgemm_route(const void* logits, dgemm_dtype_t logits_d
     p.row_token = row_token;
     p.slot_row = slot_row;
     p.counts = static_cast<uint8_t*>(ws);
-    p.pitch = (p.E + 3) / 4 * 4;
+    p.pitch = dg::route::pitch_of(p.E);
     // As many chunks as fill the last wave of two CTAs an SM, at most kMoreChunks more.
     const int64_t fewest = (T + CHUNK - 1) / CHUNK, wave = 2 * dev.num_sms;
     const int64_t want = T <= CHUNK ? 1 : std::min((fewest + wave - 1) / wave * wave, fewest + kMoreChunks);
@@ -395,7 +392,6 @@ extern "C" dgemm_status_t dgemm_route(const void* logits, dgemm_dtype_t logits_d
     else e = launch_select<32>(p, s);
     if (e != cudaSuccess) return DGEMM_ERR_CUDA;
     if (p.chunks == 1) return DGEMM_OK;
-    const size_t parts = static_cast<size_t>(place_parts(p.pitch));
-    dg::host::Launch l(static_cast<unsigned>(p.chunks), 1, PLACE_THREADS, static_cast<size_t>(p.E) * 8 + parts * p.pitch * 8, s);
+    dg::host::Launch l(static_cast<unsigned>(p.chunks), 1, PLACE_THREADS, dg::route::PlaceLayout(p.E).bytes, s);
     return cudaLaunchKernelEx(&l.cfg, route_place, p) == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
 }
