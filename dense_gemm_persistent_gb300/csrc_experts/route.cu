@@ -342,7 +342,7 @@ cudaError_t launch_select(const RouteParams& p, cudaStream_t s) {
 extern "C" size_t dgemm_route_workspace_size(int64_t T, int64_t E, int k) {
     if (route_sizes(T, E, k) != DGEMM_OK) return 0;
     const size_t chunks = static_cast<size_t>((T + CHUNK - 1) / CHUNK) + kMoreChunks;
-    return T > CHUNK ? chunks * ((static_cast<size_t>(E) + 3) / 4 * 4) : 0;
+    return T > CHUNK ? DGEMM_WS_STATUS_BYTES + chunks * static_cast<size_t>(dg::route::pitch_of(static_cast<int>(E))) : 0;
 }
 
 extern "C" dgemm_status_t dgemm_route(const void* logits, dgemm_dtype_t logits_dtype, int64_t T, int64_t E, int k,
@@ -377,7 +377,8 @@ extern "C" dgemm_status_t dgemm_route(const void* logits, dgemm_dtype_t logits_d
     p.offsets = offsets;
     p.row_token = row_token;
     p.slot_row = slot_row;
-    p.counts = static_cast<uint8_t*>(ws);
+    // behind the status word, where a call given the same workspace may have left a record
+    p.counts = need > 0 ? static_cast<uint8_t*>(ws) + DGEMM_WS_STATUS_BYTES : nullptr;
     p.pitch = dg::route::pitch_of(p.E);
     // As many chunks as fill the last wave of two CTAs an SM, at most kMoreChunks more.
     const int64_t fewest = (T + CHUNK - 1) / CHUNK, wave = 2 * dev.num_sms;

@@ -101,7 +101,8 @@ def main() -> None:
         block(X, out)
     end.record()
     torch.cuda.synchronize()
-    assert dg.dgemm_query_device_status(block.ws) == 0
+    # the block's workspace, and the per-device word of the calls without one (the router's product)
+    assert dg.dgemm_query_device_status(block.ws) == 0 and dg.dgemm_query_device_status() == 0
     sizes = block.offsets.diff().tolist()
     print(f"{a.tokens} tokens, {a.experts} experts of {a.hidden} x {a.inner}, top {a.top_k}, "
           f"{'int8' if a.int8 else 'bf16'}: {start.elapsed_time(end) / 20 * 1e3:.1f} us a call; "

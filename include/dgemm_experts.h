@@ -63,7 +63,9 @@ typedef enum {
  *              beyond offsets[E].
  *   slot_row   [T,k] int32 out: the row of each pair, -1 for id -1.
  *   ws         dgemm_route_workspace_size(T, E, k) bytes, contents arbitrary
- *              (DGEMM_ERR_WORKSPACE_TOO_SMALL with less; 0 bytes may be needed).
+ *              (DGEMM_ERR_WORKSPACE_TOO_SMALL with less; 0 bytes may be needed). Its first
+ *              DGEMM_WS_STATUS_BYTES bytes stay as they are: a status word that a product
+ *              given the same workspace has left there is kept until it is queried.
  * 1 <= k <= min(E, DGEMM_MAX_TOPK), E <= DGEMM_MAX_EXPERTS, T*k < 2^30. T == 0
  * writes zero offsets. */
 dgemm_status_t dgemm_route(const void* logits, dgemm_dtype_t logits_dtype, int64_t T, int64_t E, int k,
