@@ -28,40 +28,65 @@ _BF16 = (torch.bfloat16,)
 _CODES8 = (torch.float8_e4m3fn, torch.uint8)
 _INT8 = (torch.int8,)
 _current_raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
+_device_of = torch.Tensor.get_device   # -1 on the CPU
+_NO_DEVICE = -2                        # no tensor's device: every operand is then looked at, and refused, by name
 
 
-def _need(t, name, shape, dtypes):
+def _device(t, stream) -> int:
+    """The device of a call, by its first operand. The library launches on the current device,
+    so the operands have to live there (each is compared as it is checked), and so has a
+    stream: kernels would otherwise read another GPU's addresses."""
+    if t is None or (dev := _device_of(t)) < 0:
+        return _NO_DEVICE
+    if dev != _current_device():
+        raise ValueError(f"operands are on cuda:{dev}, the current device is cuda:{_current_device()}: "
+                         "call inside torch.cuda.device(...)")
+    if stream is not None and isinstance(stream, torch.cuda.Stream) and stream.device_index != dev:
+        raise ValueError(f"the stream is of cuda:{stream.device_index}, the operands are on cuda:{dev}")
+    return dev
+
+
+def _same_device(t, name, dev):
+    if dev >= 0 and _device_of(t) != dev:
+        raise ValueError(f"{name} is on cuda:{_device_of(t)}, the call's first operand on cuda:{dev}")
+
+
+def _need(t, name, shape, dtypes, dev):
     # the common case in few steps; anything else is looked at, and named, below
-    if t is not None and t.dtype in dtypes and t.is_cuda and (shape is None or t.shape == shape) and t.is_contiguous():
+    if (t is not None and t.dtype in dtypes and t.get_device() == dev and (shape is None or t.shape == shape)
+            and t.is_contiguous()):
         return
     if t is None:
         raise ValueError(f"{name} is required")
     _dg._require(t, name, shape, dtypes)
+    _same_device(t, name, dev)
 
 
-def _maybe(t, name, shape, dtypes):
+def _maybe(t, name, shape, dtypes, dev):
     if t is not None:
-        _need(t, name, shape, dtypes)
+        _need(t, name, shape, dtypes, dev)
 
 
-def _stream(stream, t):
-    """The raw stream: the given one, else the current one of t's device."""
-    if stream is None and t.is_cuda:
-        return _current_raw_stream(t.get_device())
+def _stream(stream, dev):
+    """The raw stream: the given one, else the current one of the call's device."""
+    if stream is None and dev >= 0:
+        return _current_raw_stream(dev)
     return _dg._stream(stream)
 
 
-def _workspace(ws):
+def _workspace(ws, dev):
     """(pointer, bytes) of the workspace tensor, or of none."""
     if ws is None:
         return None, 0
-    if not (ws.is_cuda and ws.is_contiguous()):
+    if not (ws.get_device() == dev and ws.is_contiguous()):
         _dg._require(ws, "ws")
+        _same_device(ws, "ws", dev)
     return ws.data_ptr(), ws.nbytes
 
 
-def _matrix(t, name, dtypes, dims=2):
-    _need(t, name, None, dtypes)
+def _matrix(t, name, dtypes, dev, dims=2):
+    _need(t, name, None, dtypes, dev)
     if t.dim() != dims:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {dims} dimensions")
 
@@ -87,17 +112,18 @@ def dgemm_route(logits, k, ids, weights, offsets, row_token, slot_row, *, renorm
     experts sum to 1, else they are the softmax over all. ws: uint8 workspace of
     at least dgemm_route_workspace_size(T, E, k) bytes.
     """
-    _matrix(logits, "logits", _FLOATS)
+    dev = _device(logits, stream)
+    _matrix(logits, "logits", _FLOATS, dev)
     T, E = logits.shape
     k = int(k)
-    _need(ids, "ids", (T, k), _I32)
-    _need(weights, "weights", (T, k), _F32)
-    _need(offsets, "offsets", (E + 1,), _I32)
-    _need(row_token, "row_token", (T * k,), _I32)
-    _need(slot_row, "slot_row", (T, k), _I32)
+    _need(ids, "ids", (T, k), _I32, dev)
+    _need(weights, "weights", (T, k), _F32, dev)
+    _need(offsets, "offsets", (E + 1,), _I32, dev)
+    _need(row_token, "row_token", (T * k,), _I32, dev)
+    _need(slot_row, "slot_row", (T, k), _I32, dev)
     code = _dg.load().dgemm_route(logits.data_ptr(), _float_code(logits), T, E, k, int(bool(renormalize)), ids.data_ptr(),
                                   weights.data_ptr(), offsets.data_ptr(), row_token.data_ptr(), slot_row.data_ptr(),
-                                  *_workspace(ws), _stream(stream, logits))
+                                  *_workspace(ws, dev), _stream(stream, dev))
     _dg._check(code, "dgemm_route")
 
 
@@ -111,22 +137,23 @@ def dgemm_combine(Y, slot_row, weights, out, *, add=None, stream=None):
     Y [R,H] bf16; slot_row [T,k] int32 (rows outside [0,R) add nothing); weights
     [T,k] fp32; add [T,H] bf16 or None; out [T,H] fp32 or bf16. Returns out.
     """
-    _matrix(Y, "Y", _BF16)
-    _matrix(slot_row, "slot_row", _I32)
+    dev = _device(Y, stream)
+    _matrix(Y, "Y", _BF16, dev)
+    _matrix(slot_row, "slot_row", _I32, dev)
     R, H = Y.shape
     T, k = slot_row.shape
-    _need(weights, "weights", (T, k), _F32)
-    _need(out, "out", (T, H), _FLOATS)
-    _maybe(add, "add", (T, H), _BF16)
+    _need(weights, "weights", (T, k), _F32, dev)
+    _need(out, "out", (T, H), _FLOATS, dev)
+    _maybe(add, "add", (T, H), _BF16, dev)
     code = _dg.load().dgemm_combine(Y.data_ptr(), R, slot_row.data_ptr(), weights.data_ptr(), _dg._ptr(add),
-                                    out.data_ptr(), _float_code(out), T, H, k, _stream(stream, Y))
+                                    out.data_ptr(), _float_code(out), T, H, k, _stream(stream, dev))
     _dg._check(code, "dgemm_combine")
     return out
 
 
-def _grouped_sizes(A, B, offsets, D, a_rows, b_layout, bias, act, dtypes):
-    _matrix(A, "A", dtypes)
-    _matrix(B, "B", dtypes, 3)
+def _grouped_sizes(A, B, offsets, D, a_rows, b_layout, bias, act, dtypes, dev):
+    _matrix(A, "A", dtypes, dev)
+    _matrix(B, "B", dtypes, dev, 3)
     if b_layout == "nk":
         E, N, K = B.shape
     elif b_layout == "kn":
@@ -138,14 +165,14 @@ def _grouped_sizes(A, B, offsets, D, a_rows, b_layout, bias, act, dtypes):
     count = A.shape[0]
     R = count
     if a_rows is not None:
-        _need(a_rows, "a_rows", None, _I32)
+        _need(a_rows, "a_rows", None, _I32, dev)
         if a_rows.dim() != 1:
             raise ValueError(f"a_rows has shape {tuple(a_rows.shape)}, expected one dimension")
         R = a_rows.shape[0]
     code = _act(act)
-    _need(offsets, "offsets", (E + 1,), _I32)
-    _need(D, "D", (R, N // 2 if act == "swiglu" else N), _FLOATS)
-    _maybe(bias, "bias", (E, N), _F32)
+    _need(offsets, "offsets", (E + 1,), _I32, dev)
+    _need(D, "D", (R, N // 2 if act == "swiglu" else N), _FLOATS, dev)
+    _maybe(bias, "bias", (E, N), _F32, dev)
     return E, R, N, K, count, code
 
 
@@ -159,22 +186,24 @@ def dgemm_grouped_bf16(A, B, offsets, D, *, a_rows=None, b_layout="nk", bias=Non
     gate's channels first in B). Rows outside every group are not written.
     ws: optional uint8 workspace (dgemm_grouped_workspace_size). Returns D.
     """
-    E, R, N, K, count, code = _grouped_sizes(A, B, offsets, D, a_rows, b_layout, bias, act, _BF16)
+    dev = _device(A, stream)
+    E, R, N, K, count, code = _grouped_sizes(A, B, offsets, D, a_rows, b_layout, bias, act, _BF16, dev)
     st = _dg.load().dgemm_grouped_bf16(A.data_ptr(), count, _dg._ptr(a_rows), B.data_ptr(),
                                        B_KN if b_layout == "kn" else B_NK, offsets.data_ptr(), E, D.data_ptr(),
-                                       _float_code(D), R, N, K, float(alpha), _dg._ptr(bias), code, *_workspace(ws),
-                                       _stream(stream, A))
+                                       _float_code(D), R, N, K, float(alpha), _dg._ptr(bias), code, *_workspace(ws, dev),
+                                       _stream(stream, dev))
     _dg._check(st, "dgemm_grouped_bf16")
     return D
 
 
 def _grouped_scaled(name, dtypes, Aq, Bq, a_scale, b_scale, offsets, D, a_rows, bias, act, alpha, ws, stream):
-    E, R, N, K, count, code = _grouped_sizes(Aq, Bq, offsets, D, a_rows, "nk", bias, act, dtypes)
-    _need(a_scale, "a_scale", (count,), _F32)
-    _need(b_scale, "b_scale", (E, N), _F32)
+    dev = _device(Aq, stream)
+    E, R, N, K, count, code = _grouped_sizes(Aq, Bq, offsets, D, a_rows, "nk", bias, act, dtypes, dev)
+    _need(a_scale, "a_scale", (count,), _F32, dev)
+    _need(b_scale, "b_scale", (E, N), _F32, dev)
     st = getattr(_dg.load(), name)(Aq.data_ptr(), count, _dg._ptr(a_rows), Bq.data_ptr(), a_scale.data_ptr(),
                                    b_scale.data_ptr(), offsets.data_ptr(), E, D.data_ptr(), _float_code(D), R, N, K,
-                                   float(alpha), _dg._ptr(bias), code, *_workspace(ws), _stream(stream, Aq))
+                                   float(alpha), _dg._ptr(bias), code, *_workspace(ws, dev), _stream(stream, dev))
     _dg._check(st, name)
     return D
 
@@ -203,12 +232,13 @@ def dgemm_grouped_workspace_size(type, R, E, N, K, *, act="none") -> int:
 def dgemm_int8_quantize(X, q, scale, *, stream=None):
     """Per-row int8 codes: scale [M] = max|X[m]| * (1 / 127) in fp32, q [M,K] = X / scale
     rounded to nearest even. X [M,K] bf16 or fp32. Returns (q, scale)."""
-    _matrix(X, "X", _FLOATS)
+    dev = _device(X, stream)
+    _matrix(X, "X", _FLOATS, dev)
     M, K = X.shape
-    _need(q, "q", (M, K), _INT8)
-    _need(scale, "scale", (M,), _F32)
+    _need(q, "q", (M, K), _INT8, dev)
+    _need(scale, "scale", (M,), _F32, dev)
     code = _dg.load().dgemm_int8_quantize(X.data_ptr(), _float_code(X), q.data_ptr(), scale.data_ptr(), M, K,
-                                          _stream(stream, X))
+                                          _stream(stream, dev))
     _dg._check(code, "dgemm_int8_quantize")
     return q, scale
 
@@ -221,24 +251,25 @@ def dgemm_int8_scaled(Aq, Bq, a_scale, b_scale, D, *, C=None, alpha=1.0, beta=0.
     bias [N] fp32; act in none/relu/gelu/silu. ws: optional uint8 workspace
     (dgemm_int8_workspace_size). Returns D.
     """
-    _matrix(Aq, "Aq", _INT8)
-    _matrix(Bq, "Bq", _INT8)
+    dev = _device(Aq, stream)
+    _matrix(Aq, "Aq", _INT8, dev)
+    _matrix(Bq, "Bq", _INT8, dev)
     M, K = Aq.shape
     N = Bq.shape[0]
     if Bq.shape[1] != K:
         raise ValueError(f"inner dimensions differ: Aq has K={K}, Bq has K={Bq.shape[1]}")
     if act not in ACT:
         raise ValueError(f"act must be one of {sorted(ACT)}, not {act!r}")
-    _need(a_scale, "a_scale", (M,), _F32)
-    _need(b_scale, "b_scale", (N,), _F32)
-    _need(D, "D", (M, N), _FLOATS)
+    _need(a_scale, "a_scale", (M,), _F32, dev)
+    _need(b_scale, "b_scale", (N,), _F32, dev)
+    _need(D, "D", (M, N), _FLOATS, dev)
     if beta != 0.0:   # C is read only then (and may be None otherwise)
-        _need(C, "C", (M, N), _FLOATS)
-    _maybe(bias, "bias", (N,), _F32)
+        _need(C, "C", (M, N), _FLOATS, dev)
+    _maybe(bias, "bias", (N,), _F32, dev)
     code = _dg.load().dgemm_int8_scaled(Aq.data_ptr(), Bq.data_ptr(), a_scale.data_ptr(), b_scale.data_ptr(),
                                         _dg._ptr(C), _float_code(C) if C is not None else F32, D.data_ptr(),
                                         _float_code(D), M, N, K, float(alpha), float(beta), _dg._ptr(bias), ACT[act],
-                                        *_workspace(ws), _stream(stream, Aq))
+                                        *_workspace(ws, dev), _stream(stream, dev))
     _dg._check(code, "dgemm_int8_scaled")
     return D
 
