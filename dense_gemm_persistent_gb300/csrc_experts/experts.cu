@@ -63,7 +63,9 @@ dgemm_status_t check_sizes(int type, int64_t R, int64_t E, int64_t N, int64_t K,
     if (R > INT32_MAX / 2 || N > INT32_MAX / 2 || K > INT32_MAX / 2) return DGEMM_ERR_NOT_SUPPORTED;
     const int64_t esz = type == DGEMM_GROUPED_BF16 ? 2 : 1;
     if (K * esz % 16 != 0) return DGEMM_ERR_MISALIGNED;
-    if (layout == DGEMM_B_KN && N * esz % 16 != 0) return DGEMM_ERR_MISALIGNED;
+    // K x N rows on 16 bytes, and the up half of a gated one too: tiled copies start there
+    const int64_t row = act == DGEMM_ACT_SWIGLU ? N / 2 : N;
+    if (layout == DGEMM_B_KN && row * esz % 16 != 0) return DGEMM_ERR_MISALIGNED;
     return DGEMM_OK;
 }
 
@@ -137,8 +139,6 @@ dgemm_status_t launch(const Call& c, const dg::host::Device& dev) {
     const int int8 = c.type == DGEMM_GROUPED_INT8;   // (its token rows need no map: converted on the way)
     const uint64_t esz = c.type == DGEMM_GROUPED_BF16 ? 2 : 1, sl = 128 / esz;
     const uint64_t N = static_cast<uint64_t>(c.N), K = static_cast<uint64_t>(c.K), E = static_cast<uint64_t>(c.E);
-    // KN: both halves of a gated product start on 16 bytes
-    if (kn && gated && (N / 2) * esz % 16 != 0) return DGEMM_ERR_MISALIGNED;
     // CTA pairs (256 channels, up to 256 rows a tile) where groups are long enough to
     // share weights between two SMs; single CTAs (128 channels, up to 64 rows) where a
     // call reads weights for few rows each, and where its single-CTA tiles, for groups of the

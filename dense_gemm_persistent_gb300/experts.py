@@ -183,7 +183,8 @@ def dgemm_grouped_bf16(A, B, offsets, D, *, a_rows=None, b_layout="nk", bias=Non
     A [n,K] bf16; a_rows [R] int32 or None (row r of A); B [E,N,K] ("nk") or [E,K,N]
     ("kn") bf16; offsets [E+1] int32 on the device; bias [E,N] fp32; act in
     none/relu/gelu/silu/swiglu; D [R,N] fp32 or bf16 (swiglu: [R,N/2], the
-    gate's channels first in B). Rows outside every group are not written.
+    gate's channels first in B). K is a multiple of 8; N of "kn" weights too, of 16 with
+    swiglu. Rows outside every group are not written.
     ws: optional uint8 workspace (dgemm_grouped_workspace_size). Returns D.
     """
     dev = _device(A, stream)

@@ -95,7 +95,9 @@ dgemm_status_t dgemm_combine(const void* Y, int64_t R, const int32_t* slot_row, 
  *   bias     [E,N] F32 or NULL.   act dgemm_act_t or DGEMM_ACT_SWIGLU.
  *   D        [R,N] (SWIGLU: [R,N/2]) F32 or BF16.
  *   ws       optional: DGEMM_WS_STATUS_BYTES for the call's status word.
- * K * element size must be a multiple of 16 bytes (KN: N too); N is otherwise any.
+ * K * element size must be a multiple of 16 bytes; for K x N weights N * element size too,
+ * and N/2 * element size with SWIGLU (N a multiple of 16), DGEMM_ERR_MISALIGNED otherwise;
+ * N x K weights take any N.
  * E <= DGEMM_MAX_EXPERTS. */
 dgemm_status_t dgemm_grouped_bf16(const void* A, int64_t a_count, const int32_t* a_rows, const void* B,
                                   dgemm_b_layout_t b_layout, const int32_t* offsets, int64_t E, void* D,
