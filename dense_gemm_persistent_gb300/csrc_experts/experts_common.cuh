@@ -157,6 +157,33 @@ struct Cursor {
 // ---------------------------------------------------------------- epilogue
 
 __device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.0f + __expf(-v)); }
+__device__ __forceinline__ float gelu(float v) { return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f)); }
+// max(v, 0), NaN kept (fmaxf would answer 0).
+__device__ __forceinline__ float relu(float v) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(v), "f"(0.0f));
+    return r;
+}
+
+// The switch is taken once for 32 values, so that the per-element code is straight-line.
+__device__ __forceinline__ void activate32(float (&v)[32], int act) {
+    switch (act) {
+        case DGEMM_ACT_RELU:
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = relu(v[j]);
+            break;
+        case DGEMM_ACT_GELU:
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = gelu(v[j]);
+            break;
+        case DGEMM_ACT_SILU:
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = silu(v[j]);
+            break;
+        default:
+            break;
+    }
+}
 
 // Stores one channel's COLS values, one row of D each (lanes: consecutive channels; `at`: this
 // lane's first). BF16 rows of even length: neighbouring lanes swap their packed pairs of rows,
@@ -318,7 +345,7 @@ __device__ __forceinline__ bool tile_epilogue(const Params& p, const Tile& t, ui
                     v[j] = fmaf(p.beta, x, v[j]);
                 }
             }
-            activation32(v, p.act);
+            activate32(v, p.act);
             store_columns<32>(p, at, v, live, valid);
         }
     }

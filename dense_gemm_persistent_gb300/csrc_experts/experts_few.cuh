@@ -140,8 +140,8 @@ __global__ void __launch_bounds__(CF::THREADS, CF::CTAS_PER_SM) expert_few(const
             y = silu(y) * up;
         }
         if (!stored) continue;
-        if (p.act == DGEMM_ACT_RELU) y = fmaxf(y, 0.0f);
-        else if (p.act == DGEMM_ACT_GELU) y = 0.5f * y * (1.0f + erff(y * 0.70710678118654752f));
+        if (p.act == DGEMM_ACT_RELU) y = relu(y);
+        else if (p.act == DGEMM_ACT_GELU) y = gelu(y);
         else if (p.act == DGEMM_ACT_SILU) y = silu(y);
         if (p.d_f32) static_cast<float*>(p.D)[at] = y;
         else static_cast<__nv_bfloat16*>(p.D)[at] = __float2bfloat16_rn(y);

@@ -92,7 +92,8 @@ dgemm_status_t dgemm_combine(const void* Y, int64_t R, const int32_t* slot_row, 
  *   offsets  [E+1] int32, ascending, on the device: the group sizes are not known
  *            to the host. Values are clamped into [0,R]; rows of D outside
  *            every group are not written.
- *   bias     [E,N] F32 or NULL.   act dgemm_act_t or DGEMM_ACT_SWIGLU.
+ *   bias     [E,N] F32 or NULL.   act dgemm_act_t or DGEMM_ACT_SWIGLU. NaN stays NaN
+ *            under every activation (ReLU included).
  *   D        [R,N] (SWIGLU: [R,N/2]) F32 or BF16.
  *   ws       optional: DGEMM_WS_STATUS_BYTES for the call's status word.
  * K * element size must be a multiple of 16 bytes; for K x N weights N * element size too,
