@@ -133,10 +133,14 @@ dgemm_status_t dgemm_int8_quantize(const void* X, dgemm_dtype_t x_dtype, int8_t*
 /* D = act(alpha * diag(a_scale) (Aq . Bq^T) diag(b_scale) + beta * C + bias), int8 codes.
  *   Aq [M,K], Bq [N,K] int8 (all 256 codes); a_scale [M], b_scale [N] F32;
  *   C, D [M,N] F32 or BF16 (C read only when beta != 0; may equal D); bias [N]
- *   F32 or NULL; act dgemm_act_t.
- * int8 codes are exact in BF16 and products run on the BF16 tensor cores with
+ *   F32 or NULL; act dgemm_act_t (NaN stays NaN).
+ * Arithmetic: int8 codes are exact in FP16 and products run on the FP16 tensor cores with
  * FP32 sums: the sum is the exact integer while partial sums stay below 2^24 in
- * magnitude, and rounded to 24 bits beyond that.
+ * magnitude, and rounded toward zero to 24 bits, once for each instruction of 16 terms,
+ * beyond that. One set of weights (this call, or a grouped one with E == 1) with one or
+ * two rows of at most 74 KB of codes in all (M * K <= 75776) runs on integer dot products:
+ * exact 32-bit sums (K <= 131071) rounded once to FP32. So the bits of a row whose sums
+ * pass 2^24 can depend on how many rows the call has; below 2^24 they do not.
  *   ws       optional: DGEMM_WS_STATUS_BYTES for the call's status word.
  * K must be a multiple of 16; N any. */
 dgemm_status_t dgemm_int8_scaled(const void* Aq, const void* Bq, const float* a_scale, const float* b_scale,
