@@ -11,6 +11,7 @@
 
 #include "dgemm_experts.h"
 #include "experts_kernels.h"
+#include "experts_plan.h"
 #include "host.h"
 
 namespace {
@@ -139,19 +140,9 @@ dgemm_status_t launch(const Call& c, const dg::host::Device& dev) {
     const int int8 = c.type == DGEMM_GROUPED_INT8;   // (its token rows need no map: converted on the way)
     const uint64_t esz = c.type == DGEMM_GROUPED_BF16 ? 2 : 1, sl = 128 / esz;
     const uint64_t N = static_cast<uint64_t>(c.N), K = static_cast<uint64_t>(c.K), E = static_cast<uint64_t>(c.E);
-    // CTA pairs (256 channels, up to 256 rows a tile) where groups are long enough to
-    // share weights between two SMs; single CTAs (128 channels, up to 64 rows) where a
-    // call reads weights for few rows each, and where its single-CTA tiles, for groups of the
-    // mean size, are at most one wave. Single against pairs, in us: BF16, 64 experts of 4096 x 4096,
-    // mean of 32 rows 323 / 332, 48 331 / 337, 64 349 / 342, 128 449 / 368 (E4M3 166 / 172, 171 / 174,
-    // 181 / 177, 238 / 192). INT8 pairs convert a weight once for 192 rows, not 64, which pays earlier: 64 experts
-    // of 2048 x 4096, mean of 24 116 / 128, 32 128 / 130, 40 140 / 133, 64 175 / 143; 32 of 4096 x 7168, mean of
-    // 32 202 / 209, 40 225 / 212. One wave: BF16 512 rows of 1024 x 2048 9.4 / 15.6, but just above it,
-    // 512 rows of 4096 x 2048, 16.3 / 15.6; INT8 64 rows of 18432 x 7168 34.5 / 40.5, 96 54 / 43.
-    const int64_t mean = (c.R + c.E - 1) / c.E, wide = gated ? c.N / 2 : c.N, step = gated ? 64 : 128;
-    const bool one_wave = (mean + 63) / 64 * std::min(c.E, c.R) * ((wide + step - 1) / step) <= dev.num_sms;
     const int forced = dg::host::pair_override();
-    const int pair = forced >= 0 ? forced : c.R > (c.type == DGEMM_GROUPED_INT8 ? 36 : 48) * c.E && !one_wave;
+    const int pair = forced >= 0 ? forced
+                                 : dg::experts::takes_pairs(c.R, c.E, gated ? c.N / 2 : c.N, gated ? 64 : 128, dev.num_sms);
     const Variant* v = find_variant(c.type, kn, pair, c.a_rows != nullptr);
     if (!v) return DGEMM_ERR_NOT_SUPPORTED;
 
