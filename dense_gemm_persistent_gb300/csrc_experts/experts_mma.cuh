@@ -14,7 +14,7 @@
 //
 // What bounds it: long groups the tensor pipe and the operands' way to it, short ones HBM. Gated BF16,
 // 16384 rows of 4096 x 4096 over 16 experts, takes 342-351 us with rows in order and 369-388
-// gathered (1.4-1.5 PFLOP/s); E4M3 over 32 experts 204 and 217-236; 64 gathered rows over 64 experts of
+// gathered (1.4-1.5 PFLOP/s); E4M3 over 32 experts 204 and 217-237; 64 gathered rows over 64 experts of
 // 4096 x 4096 BF16 158.
 // What the gather's choices were worth when they were made, as the other side's time over its own:
 //   cp.async, not TMA copies by index (four rows each, one per ~17 ns, 64 a stage)     1.73
