@@ -20,7 +20,8 @@ __all__ = ["dgemm_bf16", "dgemm_fp8_scaled", "dgemm_fp8_rowquant_noalloc", "dgem
            "DgemmError", "load", "lib_path",
            "dgemm_route", "dgemm_route_workspace_size", "dgemm_combine", "dgemm_grouped_bf16",
            "dgemm_grouped_fp8_scaled", "dgemm_grouped_int8_scaled", "dgemm_grouped_workspace_size",
-           "dgemm_int8_quantize", "dgemm_int8_scaled", "dgemm_int8_workspace_size"]
+           "dgemm_int8_quantize", "dgemm_int8_scaled", "dgemm_int8_workspace_size",
+           "dgemm_route_scored", "dgemm_adapter_bf16", "dgemm_adapter_add", "dgemm_adapter_workspace_size"]
 
 
 def _torch():
@@ -269,13 +270,21 @@ class overrides:
         return False
 
 
-# Routed-expert and 8-bit integer operators (imports torch on first use, as the
-# entry points above do).
+# Routed-expert and 8-bit integer operators, low-rank adapters (import torch on first
+# use, as the entry points above do).
 _EXPERTS = frozenset(name for name in __all__ if name.startswith(("dgemm_route", "dgemm_combine", "dgemm_grouped",
                                                                   "dgemm_int8")))
 
 
+_ADAPTERS = frozenset(name for name in __all__ if name.startswith("dgemm_adapter"))
+
+
 def __getattr__(name):
+    if name in _ADAPTERS:
+        from . import adapters
+        for n in _ADAPTERS:
+            globals()[n] = getattr(adapters, n)
+        return globals()[name]
     if name in _EXPERTS:
         from . import experts
         for n in _EXPERTS:

@@ -35,6 +35,11 @@ class Overrides(ctypes.Structure):
                 ("kslices", _i32), ("wait_limit_ns", _i64), ("stall_after_loads", _i64)]
 
 
+class Scoring(ctypes.Structure):
+    _fields_ = [("score", _i32), ("groups", _i32), ("groups_kept", _i32), ("group_score", _i32), ("renormalize", _i32),
+                ("weight_scale", _f32)]
+
+
 class Plan(ctypes.Structure):
     _fields_ = [("swap_ab", _i32), ("tile_m", _i32), ("tile_n", _i32), ("cta_group", _i32), ("stages", _i32),
                 ("num_tiles", _i32), ("grid", _i32), ("cooperative", _i32), ("raster_group", _i32), ("k_groups", _i32),
@@ -77,6 +82,16 @@ SIGNATURES.update({
     "dgemm_int8_scaled": (_i32, [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i64, _i64, _i64, _f32, _f32, _vp, _i32,
                                  _vp, _sz, _vp]),
     "dgemm_int8_workspace_size": (_sz, [_i64, _i64, _i64]),
+})
+# include/dgemm_scored.h and include/dgemm_adapters.h
+SIGNATURES.update({
+    "dgemm_route_scored": (_i32, [_vp, _i32, _i64, _i64, _i32, _vp, ctypes.POINTER(Scoring), _vp, _vp, _vp, _vp, _vp, _vp,
+                                  _sz, _vp]),
+    "dgemm_adapter_bf16": (_i32, [_vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _i32, _i64, _i64, _i64, _vp, _i32, _vp,
+                                  _sz, _vp]),
+    "dgemm_adapter_add": (_i32, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _vp, _i32, _vp, _i32, _i64, _i64, _i64, _vp, _i32,
+                                 _vp, _sz, _vp]),
+    "dgemm_adapter_workspace_size": (_sz, [_i64, _i64, _i64, _i64, _i64]),
 })
 NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
 WS_STATUS_BYTES = 256

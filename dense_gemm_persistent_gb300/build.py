@@ -15,13 +15,14 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 CSRC_EXPERTS = os.path.join(PKG, "csrc_experts")   # routed-expert and 8-bit integer operators
+CSRC_ADAPTERS = os.path.join(PKG, "csrc_adapters")   # low-rank adapters
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libdgemm.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC",
-                     "-I", INCLUDE, "-I", CSRC, "-I", CSRC_EXPERTS]
+                     "-I", INCLUDE, "-I", CSRC, "-I", CSRC_EXPERTS, "-I", CSRC_ADAPTERS]
 
 
 def nvcc() -> str:
@@ -32,11 +33,11 @@ def nvcc() -> str:
 
 
 def _sources():
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu"))) + sorted(glob.glob(os.path.join(CSRC_EXPERTS, "*.cu")))
+    return [f for d in (CSRC, CSRC_EXPERTS, CSRC_ADAPTERS) for f in sorted(glob.glob(os.path.join(d, "*.cu")))]
 
 
 def _deps():
-    headers = [os.path.join(d, pat) for d in (CSRC, CSRC_EXPERTS, INCLUDE) for pat in ("*.cuh", "*.h")]
+    headers = [os.path.join(d, pat) for d in (CSRC, CSRC_EXPERTS, CSRC_ADAPTERS, INCLUDE) for pat in ("*.cuh", "*.h")]
     return _sources() + [f for pat in headers for f in glob.glob(pat)] + [os.path.abspath(__file__)]
 
 

@@ -1,0 +1,181 @@
+// adapters.cu -- low-rank adapters of many requests, host side: checks, the choice of
+// a form, tensor maps and launches.
+#include <algorithm>
+#include <atomic>
+#include <cstring>
+
+#include "adapter_few.cuh"
+#include "adapter_shrink.cuh"
+#include "host.h"
+
+namespace {
+
+using dg::adapters::Few;
+using dg::adapters::Params;
+
+struct Call {
+    const void *X, *W, *A, *B;
+    const int32_t* ids;
+    const float* scale;
+    int64_t L, r;
+    const void* C;
+    dgemm_dtype_t c_dtype;
+    void* D;
+    dgemm_dtype_t d_dtype;
+    int64_t T, N, K;
+    const float* bias;
+    int act;
+    void* ws;
+    size_t ws_bytes;
+    cudaStream_t stream;
+};
+
+dgemm_status_t check_sizes(int64_t T, int64_t N, int64_t K, int64_t r, int64_t L) {
+    if (T < 0 || N < 0 || K < 0 || L < 0 || r < 1) return DGEMM_ERR_INVALID_VALUE;
+    if (L > DGEMM_MAX_ADAPTERS || r > DGEMM_MAX_ADAPTER_RANK) return DGEMM_ERR_NOT_SUPPORTED;
+    if (T > (int64_t(1) << 24) || N > INT32_MAX / 2 || K > INT32_MAX / 2) return DGEMM_ERR_NOT_SUPPORTED;
+    if (r % 8 != 0 || K % 8 != 0) return DGEMM_ERR_MISALIGNED;
+    return DGEMM_OK;
+}
+
+// A kernel's limit of dynamic shared memory, set once per device.
+bool allow_shared(std::atomic<unsigned char>* ready, int device, const void* func, int bytes) {
+    if (ready[device].load(std::memory_order_acquire)) return true;
+    if (cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    ready[device].store(1, std::memory_order_release);
+    return true;
+}
+
+dgemm_status_t launch_shrink(const Params& p, cudaStream_t s) {
+    constexpr int RB = 4;
+    dg::host::Launch l(static_cast<unsigned>(p.T) * (p.r / RB), 1, dg::adapters::SHRINK_THREADS, 0, s);
+    return cudaLaunchKernelEx(&l.cfg, dg::adapters::adapter_shrink_few<RB>, p) == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
+}
+
+dgemm_status_t launch_few(const Call& c, Params& p, const dg::host::Device& dev) {
+    constexpr int kHalf = 113 * 1024, kWhole = 232448;           // two CTAs an SM, one
+    const int fewest = (p.T + Few::MOST_COLS - 1) / Few::MOST_COLS;
+    p.width = ((p.T + fewest - 1) / fewest + 15) / 16 * 16;
+    p.tiles = (p.T + p.width - 1) / p.width;
+    const int ctiles = (p.wide + (p.gated ? 64 : 128) - 1) / (p.gated ? 64 : 128);
+    p.k_whole = p.K % Few::SL == 0;
+    p.kstages = c.W ? (p.K + Few::KS * Few::SL - 1) / (Few::KS * Few::SL) : 0;
+    const int64_t tiles = static_cast<int64_t>(p.tiles) * ctiles;
+    if (tiles > INT32_MAX / Few::MOST_SPLIT) return DGEMM_ERR_NOT_SUPPORTED;
+    p.split = 1;
+    while (p.split < Few::MOST_SPLIT && tiles * p.split * 2 <= 2 * dev.num_sms && p.kstages >= 4 * p.split) p.split *= 2;
+    const int shared = Few::smem_bytes(p.width, 3, p.split) <= kHalf ? kHalf : kWhole;
+    p.stages = p.kstages > 0 ? 2 : 0;
+    while (p.stages > 0 && p.stages < Few::MOST_STAGES && Few::smem_bytes(p.width, p.stages + 1, p.split) <= shared) ++p.stages;
+    const int smem = Few::smem_bytes(p.width, p.stages, p.split);
+    alignas(64) CUtensorMap w, x;
+    std::memset(&w, 0, sizeof w);
+    std::memset(&x, 0, sizeof x);
+    if (p.kstages > 0) {
+        const uint64_t N = p.N, K = p.K, T = p.T, sl = Few::SL, halves = p.gated ? 2 : 1, H = N / halves;
+        const uint32_t s = Few::SL, rows = p.gated ? 64 : 128, hv = static_cast<uint32_t>(halves), cols = p.width, ks = Few::KS;
+        const CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+        bool ok;
+        if (p.k_whole) {
+            // a stage's slices (and the gate and up channels of a gated tile) in one copy
+            const uint64_t dw[4] = {sl, H, halves, K / sl}, sw[3] = {K * 2, H * K * 2, 128};
+            const uint32_t bw[4] = {s, rows, hv, ks};
+            const uint64_t dx[3] = {sl, T, K / sl}, sx[2] = {K * 2, 128};
+            const uint32_t bx[3] = {s, cols, ks};
+            ok = dg::host::encode_map(&w, dt, c.W, 4, dw, sw, bw) && dg::host::encode_map(&x, dt, c.X, 3, dx, sx, bx);
+        } else {
+            const uint64_t dw[3] = {K, H, halves}, sw[2] = {K * 2, H * K * 2};
+            const uint32_t bw[3] = {s, rows, hv};
+            const uint64_t dx[2] = {K, T}, sx[1] = {K * 2};
+            const uint32_t bx[2] = {s, cols};
+            ok = dg::host::encode_map(&w, dt, c.W, 3, dw, sw, bw) && dg::host::encode_map(&x, dt, c.X, 2, dx, sx, bx);
+        }
+        if (!ok) return DGEMM_ERR_CUDA;
+    }
+    static std::atomic<unsigned char> ready[dg::host::kMaxDevices];
+    if (!allow_shared(ready, dev.id, reinterpret_cast<const void*>(&dg::adapters::adapter_few), kWhole)) return DGEMM_ERR_CUDA;
+    dg::host::Launch l(static_cast<unsigned>(tiles * p.split), 1, Few::THREADS, smem, c.stream, p.split);
+    return cudaLaunchKernelEx(&l.cfg, dg::adapters::adapter_few, w, x, p) == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
+}
+
+dgemm_status_t run_adapters(const Call& c) {
+    const dgemm_status_t st = check_sizes(c.T, c.N, c.K, c.r, c.L);
+    if (st != DGEMM_OK) return st;
+    if (c.act < DGEMM_ACT_NONE || c.act > DGEMM_ACT_SWIGLU) return DGEMM_ERR_INVALID_VALUE;
+    if (c.act == DGEMM_ACT_SWIGLU && c.N % 2 != 0) return DGEMM_ERR_INVALID_VALUE;
+    if (c.d_dtype != DGEMM_F32 && c.d_dtype != DGEMM_BF16) return DGEMM_ERR_INVALID_VALUE;
+    if (c.C && c.c_dtype != DGEMM_F32 && c.c_dtype != DGEMM_BF16) return DGEMM_ERR_INVALID_VALUE;
+    if (c.C && c.C == c.D && c.c_dtype != c.d_dtype) return DGEMM_ERR_INVALID_VALUE;
+    if (c.T == 0 || c.N == 0) return DGEMM_OK;
+    if (!c.D || !c.ids || (c.K > 0 && !c.X) || (c.K > 0 && c.L > 0 && (!c.A || !c.B))) return DGEMM_ERR_INVALID_VALUE;
+    if (!dg::host::aligned16(c.X) || !dg::host::aligned16(c.W) || !dg::host::aligned16(c.A) || !dg::host::aligned16(c.B) ||
+        !dg::host::aligned16(c.C) || !dg::host::aligned16(c.D) || !dg::host::aligned16(c.ws))
+        return DGEMM_ERR_MISALIGNED;
+    const uintptr_t natural = reinterpret_cast<uintptr_t>(c.ids) | reinterpret_cast<uintptr_t>(c.scale) |
+                              reinterpret_cast<uintptr_t>(c.bias);
+    if (natural & 3u) return DGEMM_ERR_MISALIGNED;
+    if (!c.ws || c.ws_bytes < dgemm_adapter_workspace_size(c.T, c.N, c.K, c.r, c.L)) return DGEMM_ERR_WORKSPACE_TOO_SMALL;
+    dg::host::Device dev;
+    const dgemm_status_t ds = dg::host::current_device(&dev);
+    if (ds != DGEMM_OK) return ds;
+
+    Params p{};
+    p.X = static_cast<const __nv_bfloat16*>(c.X);
+    p.low = static_cast<const __nv_bfloat16*>(c.A);
+    p.high = static_cast<const __nv_bfloat16*>(c.B);
+    p.ids = c.ids;
+    p.scale = c.scale;
+    p.V = reinterpret_cast<float*>(static_cast<char*>(c.ws) + DGEMM_WS_STATUS_BYTES);
+    p.T = static_cast<int>(c.T);
+    p.N = static_cast<int>(c.N);
+    p.K = static_cast<int>(c.K);
+    p.r = static_cast<int>(c.r);
+    p.L = c.K > 0 ? static_cast<int>(c.L) : 0;      // (without K, V is zero)
+    p.C = c.C;
+    p.c_f32 = c.c_dtype == DGEMM_F32;
+    p.D = c.D;
+    p.d_f32 = c.d_dtype == DGEMM_F32;
+    p.bias = c.bias;
+    p.act = c.act;
+    p.gated = c.act == DGEMM_ACT_SWIGLU;
+    p.wide = p.gated ? p.N / 2 : p.N;
+    p.status = dev.status;
+    p.epoch = dg::host::next_launch_epoch();
+    p.ws_status = static_cast<unsigned long long*>(c.ws);
+    dg::host::wait_settings(&p.wait_ns, &p.stall_after);
+    p.wait_first = p.L == 0;
+    if (p.L > 0) {
+        const dgemm_status_t s = launch_shrink(p, c.stream);
+        if (s != DGEMM_OK) return s;
+    }
+    return launch_few(c, p, dev);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t dgemm_adapter_workspace_size(int64_t T, int64_t N, int64_t K, int64_t r, int64_t L) {
+    if (check_sizes(T, N, K, r, L) != DGEMM_OK) return 0;
+    return DGEMM_WS_STATUS_BYTES + static_cast<size_t>(T) * static_cast<size_t>(r) * 4;
+}
+
+dgemm_status_t dgemm_adapter_bf16(const void* X, const void* W, const void* A, const void* B, const int32_t* ids,
+                                  const float* scale, int64_t L, int64_t r, void* D, dgemm_dtype_t d_dtype, int64_t T,
+                                  int64_t N, int64_t K, const float* bias, int act, void* ws, size_t ws_bytes,
+                                  dgemm_stream_t stream) {
+    if (!W && T > 0 && N > 0 && K > 0) return DGEMM_ERR_INVALID_VALUE;
+    return run_adapters(Call{X, K > 0 ? W : nullptr, A, B, ids, scale, L, r, nullptr, DGEMM_F32, D, d_dtype, T, N, K, bias, act, ws,
+                             ws_bytes, reinterpret_cast<cudaStream_t>(stream)});
+}
+
+dgemm_status_t dgemm_adapter_add(const void* X, const void* A, const void* B, const int32_t* ids, const float* scale,
+                                 int64_t L, int64_t r, const void* C, dgemm_dtype_t c_dtype, void* D,
+                                 dgemm_dtype_t d_dtype, int64_t T, int64_t N, int64_t K, const float* bias, int act,
+                                 void* ws, size_t ws_bytes, dgemm_stream_t stream) {
+    if (act == DGEMM_ACT_SWIGLU) return DGEMM_ERR_INVALID_VALUE;
+    return run_adapters(Call{X, nullptr, A, B, ids, scale, L, r, C, c_dtype, D, d_dtype, T, N, K, bias, act, ws, ws_bytes,
+                             reinterpret_cast<cudaStream_t>(stream)});
+}
+
+}  // extern "C"

@@ -1,5 +1,5 @@
-// route.cu -- dgemm_route: top-k experts of each token, their weights, and the
-// (token, slot) pairs grouped by expert.
+// route.cu -- dgemm_route and dgemm_route_scored (route_scored.cuh): top-k experts of each
+// token, their weights, and the (token, slot) pairs grouped by expert.
 //
 // Per token: p = exp(x - max x), the k largest x (equal ones lowest index
 // first), w = p / sum. Grouping is a counting sort that keeps token order: the
@@ -21,6 +21,7 @@
 #include <cfloat>
 
 #include "dgemm_experts.h"
+#include "dgemm_scored.h"
 #include "host.h"
 #include "ptx.cuh"
 #include "route_layout.h"
@@ -196,27 +197,10 @@ __device__ __forceinline__ int scan_experts(int* total, int E) {
     return all;
 }
 
-// Selects the experts of one chunk of tokens and counts them. A call of one chunk is
-// placed here as well: one launch.
-template <int VPL, bool BF16>
-__global__ void __launch_bounds__(VPL <= 8 ? 1024 : 512, VPL <= 8 ? 2 : 1) route_select(const RouteParams p) {
-    extern __shared__ __align__(16) unsigned long long mask[];            // [E]
-    int* total = reinterpret_cast<int*>(mask + p.E);        // [E] (one chunk)
-    int* sid = total + p.E;                                 // [CHUNK][k]
-    dg::grid_dependency_wait();
-    if (threadIdx.x == 0) dg::grid_launch_dependents();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int t0 = blockIdx.x * p.chunk, n = min(p.chunk, p.T - t0);
-    for (int e = threadIdx.x; e < p.E; e += blockDim.x) mask[e] = 0;
-    __syncthreads();
-    for (int i = warp; i < n; i += warps) {
-        unsigned key[VPL];
-        load_keys<VPL, BF16>(p, t0 + i, lane, key);
-        route_token<VPL, BF16>(p, t0 + i, lane, key, sid + i * p.k);
-        __syncwarp();
-        if (lane < p.k && sid[i * p.k + lane] >= 0) atomicOr(&mask[sid[i * p.k + lane]], 1ull << i);
-    }
-    __syncthreads();
+// The end of a chunk whose experts are chosen (mask: the tokens of each expert, sid: the
+// experts of each pair): its counts per expert, or where it is the only one, its rows.
+__device__ __forceinline__ void finish_chunk(const RouteParams& p, const unsigned long long* mask, int* total,
+                                             const int* sid, int t0, int n) {
     if (p.chunks > 1) {
         for (int e = threadIdx.x; e < p.pitch; e += blockDim.x)
             p.counts[static_cast<int64_t>(blockIdx.x) * p.pitch + e] =
@@ -238,6 +222,30 @@ __global__ void __launch_bounds__(VPL <= 8 ? 1024 : 512, VPL <= 8 ? 2 : 1) route
         p.slot_row[i] = row;
         if (i >= all) p.row_token[i] = -1;
     }
+}
+
+// Selects the experts of one chunk of tokens and counts them. A call of one chunk is
+// placed here as well: one launch.
+template <int VPL, bool BF16>
+__global__ void __launch_bounds__(VPL <= 8 ? 1024 : 512, VPL <= 8 ? 2 : 1) route_select(const RouteParams p) {
+    extern __shared__ __align__(16) unsigned long long mask[];            // [E]
+    int* total = reinterpret_cast<int*>(mask + p.E);        // [E] (one chunk)
+    int* sid = total + p.E;                                 // [CHUNK][k]
+    dg::grid_dependency_wait();
+    if (threadIdx.x == 0) dg::grid_launch_dependents();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int t0 = blockIdx.x * p.chunk, n = min(p.chunk, p.T - t0);
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) mask[e] = 0;
+    __syncthreads();
+    for (int i = warp; i < n; i += warps) {
+        unsigned key[VPL];
+        load_keys<VPL, BF16>(p, t0 + i, lane, key);
+        route_token<VPL, BF16>(p, t0 + i, lane, key, sid + i * p.k);
+        __syncwarp();
+        if (lane < p.k && sid[i * p.k + lane] >= 0) atomicOr(&mask[sid[i * p.k + lane]], 1ull << i);
+    }
+    __syncthreads();
+    finish_chunk(p, mask, total, sid, t0, n);
 }
 
 // Rows of one chunk's pairs: every CTA sums the counts of the chunks before its own
@@ -342,16 +350,20 @@ cudaError_t launch_select(const RouteParams& p, cudaStream_t s) {
 
 }  // namespace
 
+#include "route_scored.cuh"
+
 extern "C" size_t dgemm_route_workspace_size(int64_t T, int64_t E, int k) {
     if (route_sizes(T, E, k) != DGEMM_OK) return 0;
     const size_t chunks = static_cast<size_t>((T + CHUNK - 1) / CHUNK) + kMoreChunks;
     return T > CHUNK ? DGEMM_WS_STATUS_BYTES + chunks * static_cast<size_t>(dg::route::pitch_of(static_cast<int>(E))) : 0;
 }
 
-extern "C" dgemm_status_t dgemm_route(const void* logits, dgemm_dtype_t logits_dtype, int64_t T, int64_t E, int k,
-                                      int renormalize, int32_t* ids, float* weights, int32_t* offsets,
-                                      int32_t* row_token, int32_t* slot_row, void* ws, size_t ws_bytes,
-                                      dgemm_stream_t stream) {
+namespace {
+
+// What both routings check of their arguments, and set up for their kernels.
+dgemm_status_t prepare(RouteParams& p, dg::host::Device& dev, const void* logits, dgemm_dtype_t logits_dtype, int64_t T,
+                       int64_t E, int k, int renormalize, int32_t* ids, float* weights, int32_t* offsets,
+                       int32_t* row_token, int32_t* slot_row, void* ws, size_t ws_bytes) {
     const dgemm_status_t st = route_sizes(T, E, k);
     if (st != DGEMM_OK) return st;
     if (logits_dtype != DGEMM_F32 && logits_dtype != DGEMM_BF16) return DGEMM_ERR_INVALID_VALUE;
@@ -362,13 +374,8 @@ extern "C" dgemm_status_t dgemm_route(const void* logits, dgemm_dtype_t logits_d
     if ((natural & 3u) || !dg::host::aligned16(logits) || !dg::host::aligned16(ws)) return DGEMM_ERR_MISALIGNED;
     const size_t need = dgemm_route_workspace_size(T, E, k);
     if (need > 0 && (!ws || ws_bytes < need)) return DGEMM_ERR_WORKSPACE_TOO_SMALL;
-    dg::host::Device dev;
     const dgemm_status_t ds = dg::host::current_device(&dev);
     if (ds != DGEMM_OK) return ds;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (T == 0)
-        return cudaMemsetAsync(offsets, 0, static_cast<size_t>(E + 1) * 4, s) == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
-    RouteParams p{};
     p.logits = logits;
     p.bf16 = logits_dtype == DGEMM_BF16;
     p.T = static_cast<int>(T);
@@ -383,19 +390,83 @@ extern "C" dgemm_status_t dgemm_route(const void* logits, dgemm_dtype_t logits_d
     // behind the status word, where a call given the same workspace may have left a record
     p.counts = need > 0 ? static_cast<uint8_t*>(ws) + DGEMM_WS_STATUS_BYTES : nullptr;
     p.pitch = dg::route::pitch_of(p.E);
+    if (T == 0) return DGEMM_OK;
     // As many chunks as fill the last wave of two CTAs an SM, at most kMoreChunks more.
     const int64_t fewest = (T + CHUNK - 1) / CHUNK, wave = 2 * dev.num_sms;
     const int64_t want = T <= CHUNK ? 1 : std::min((fewest + wave - 1) / wave * wave, fewest + kMoreChunks);
     p.chunk = static_cast<int>((T + want - 1) / want);
     p.chunks = static_cast<int>((T + p.chunk - 1) / p.chunk);
+    return DGEMM_OK;
+}
+
+dgemm_status_t no_tokens(int32_t* offsets, int64_t E, cudaStream_t s) {
+    return cudaMemsetAsync(offsets, 0, static_cast<size_t>(E + 1) * 4, s) == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
+}
+
+dgemm_status_t place(const RouteParams& p, cudaStream_t s) {
+    if (p.chunks == 1) return DGEMM_OK;
+    dg::host::Launch l(static_cast<unsigned>(p.chunks), 1, PLACE_THREADS, dg::route::PlaceLayout(p.E).bytes, s);
+    return cudaLaunchKernelEx(&l.cfg, route_place, p) == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" dgemm_status_t dgemm_route(const void* logits, dgemm_dtype_t logits_dtype, int64_t T, int64_t E, int k,
+                                      int renormalize, int32_t* ids, float* weights, int32_t* offsets,
+                                      int32_t* row_token, int32_t* slot_row, void* ws, size_t ws_bytes,
+                                      dgemm_stream_t stream) {
+    RouteParams p{};
+    dg::host::Device dev;
+    const dgemm_status_t st = prepare(p, dev, logits, logits_dtype, T, E, k, renormalize, ids, weights, offsets, row_token,
+                                      slot_row, ws, ws_bytes);
+    if (st != DGEMM_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (T == 0) return no_tokens(offsets, E, s);
     cudaError_t e;
     if (E <= 64) e = launch_select<2>(p, s);
     else if (E <= 128) e = launch_select<4>(p, s);
     else if (E <= 256) e = launch_select<8>(p, s);
     else if (E <= 512) e = launch_select<16>(p, s);
     else e = launch_select<32>(p, s);
-    if (e != cudaSuccess) return DGEMM_ERR_CUDA;
-    if (p.chunks == 1) return DGEMM_OK;
-    dg::host::Launch l(static_cast<unsigned>(p.chunks), 1, PLACE_THREADS, dg::route::PlaceLayout(p.E).bytes, s);
-    return cudaLaunchKernelEx(&l.cfg, route_place, p) == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
+    return e == cudaSuccess ? place(p, s) : DGEMM_ERR_CUDA;
+}
+
+extern "C" dgemm_status_t dgemm_route_scored(const void* logits, dgemm_dtype_t logits_dtype, int64_t T, int64_t E, int k,
+                                             const float* bias, const dgemm_scoring_t* scoring, int32_t* ids,
+                                             float* weights, int32_t* offsets, int32_t* row_token, int32_t* slot_row,
+                                             void* ws, size_t ws_bytes, dgemm_stream_t stream) {
+    const dgemm_status_t sizes = route_sizes(T, E, k);
+    if (sizes != DGEMM_OK) return sizes;
+    if (!scoring) return DGEMM_ERR_INVALID_VALUE;
+    const dgemm_scoring_t c = *scoring;
+    if (c.score != DGEMM_SCORE_SOFTMAX && c.score != DGEMM_SCORE_SIGMOID) return DGEMM_ERR_INVALID_VALUE;
+    if (c.group_score != DGEMM_GROUP_MAX && c.group_score != DGEMM_GROUP_TOP2) return DGEMM_ERR_INVALID_VALUE;
+    if (c.groups < 1 || c.groups_kept < 1 || c.groups_kept > c.groups || E % c.groups != 0) return DGEMM_ERR_INVALID_VALUE;
+    if (c.groups > DGEMM_MAX_EXPERT_GROUPS) return DGEMM_ERR_NOT_SUPPORTED;
+    if (reinterpret_cast<uintptr_t>(bias) & 3u) return DGEMM_ERR_MISALIGNED;
+    ScoredParams p{};
+    dg::host::Device dev;
+    const dgemm_status_t st = prepare(p, dev, logits, logits_dtype, T, E, k, c.renormalize, ids, weights, offsets, row_token,
+                                      slot_row, ws, ws_bytes);
+    if (st != DGEMM_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (T == 0) return no_tokens(offsets, E, s);
+    p.bias = bias;
+    p.softmax = c.score == DGEMM_SCORE_SOFTMAX;
+    p.groups = c.groups_kept == c.groups ? 1 : c.groups;      // (keeping every group is having one)
+    p.per_group = p.E / p.groups;
+    p.kept = c.groups_kept;
+    p.top2 = c.group_score == DGEMM_GROUP_TOP2;
+    p.by_logit = !bias && (p.groups == 1 || !p.top2);
+    p.scale = c.weight_scale;
+    const int vpl = E <= 64 ? 2 : E <= 128 ? 4 : E <= 256 ? 8 : E <= 512 ? 16 : 32;
+    const int lanes = p.per_group % vpl == 0 ? p.per_group / vpl : 0;
+    p.lanes_per_group = (lanes & (lanes - 1)) == 0 ? lanes : 0;
+    cudaError_t e;
+    if (vpl == 2) e = launch_scored<2>(p, s);
+    else if (vpl == 4) e = launch_scored<4>(p, s);
+    else if (vpl == 8) e = launch_scored<8>(p, s);
+    else if (vpl == 16) e = launch_scored<16>(p, s);
+    else e = launch_scored<32>(p, s);
+    return e == cudaSuccess ? place(p, s) : DGEMM_ERR_CUDA;
 }

@@ -16,9 +16,11 @@ import torch
 
 import dense_gemm_persistent_gb300 as _dg
 
-from ._lib import ACT, B_KN, B_NK, BF16, F32
+from ._lib import ACT, B_KN, B_NK, BF16, F32, Scoring
 
 GROUPED_ACT = {**ACT, "swiglu": 4}
+SCORE = {"softmax": 0, "sigmoid": 1}
+GROUP_SCORE = {"max": 0, "top2": 1}
 GROUPED_TYPE = {"bf16": 0, "fp8": 1, "int8": 2}
 
 _FLOATS = (torch.float32, torch.bfloat16)
@@ -129,6 +131,39 @@ def dgemm_route(logits, k, ids, weights, offsets, row_token, slot_row, *, renorm
 
 def dgemm_route_workspace_size(T, E, k) -> int:
     return int(_dg.load().dgemm_route_workspace_size(T, E, int(k)))
+
+
+def dgemm_route_scored(logits, k, ids, weights, offsets, row_token, slot_row, *, score="sigmoid", bias=None, groups=1,
+                       groups_kept=None, group_score="top2", renormalize=True, scale=1.0, ws=None, stream=None):
+    """dgemm_route by scores: s = sigmoid or softmax of the logits, c = s + bias.
+
+    The groups_kept groups (of E / groups consecutive experts) of most worth are kept, ranked
+    by the largest c of each ("max") or the sum of its two largest ("top2"); of their
+    experts the k largest c are chosen. Weights are s at the chosen experts, divided by
+    their sum with renormalize, times scale. Equal values: lowest index first. bias [E]
+    fp32 or None; an expert whose logit or bias is -inf or NaN is never chosen.
+    groups_kept None: all. Outputs and ws as for dgemm_route.
+    """
+    dev = _device(logits, stream)
+    _matrix(logits, "logits", _FLOATS, dev)
+    T, E = logits.shape
+    k, groups = int(k), int(groups)
+    if score not in SCORE:
+        raise ValueError(f"score must be one of {sorted(SCORE)}, not {score!r}")
+    if group_score not in GROUP_SCORE:
+        raise ValueError(f"group_score must be one of {sorted(GROUP_SCORE)}, not {group_score!r}")
+    _maybe(bias, "bias", (E,), _F32, dev)
+    _need(ids, "ids", (T, k), _I32, dev)
+    _need(weights, "weights", (T, k), _F32, dev)
+    _need(offsets, "offsets", (E + 1,), _I32, dev)
+    _need(row_token, "row_token", (T * k,), _I32, dev)
+    _need(slot_row, "slot_row", (T, k), _I32, dev)
+    how = Scoring(SCORE[score], groups, groups if groups_kept is None else int(groups_kept), GROUP_SCORE[group_score],
+                  int(bool(renormalize)), float(scale))
+    code = _dg.load().dgemm_route_scored(logits.data_ptr(), _float_code(logits), T, E, k, _dg._ptr(bias), how,
+                                         ids.data_ptr(), weights.data_ptr(), offsets.data_ptr(), row_token.data_ptr(),
+                                         slot_row.data_ptr(), *_workspace(ws, dev), _stream(stream, dev))
+    _dg._check(code, "dgemm_route_scored")
 
 
 def dgemm_combine(Y, slot_row, weights, out, *, add=None, stream=None):
