@@ -30,12 +30,6 @@ struct Few {
     // (a parked tile, 64 columns of 128 floats, is never larger than two stages)
 };
 
-__device__ __forceinline__ float ld_shared_cluster_f32(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
-}
-
 __device__ __forceinline__ float activate(float v, int act) {
     switch (act) {
         case DGEMM_ACT_RELU: return experts::relu(v);

@@ -46,5 +46,294 @@ __global__ void __launch_bounds__(SHRINK_THREADS) adapter_shrink_few(const __gri
     }
 }
 
+// Many rows, on the tensor core. A tile is 128 rows of X (the MMA's rows); its columns are the
+// rows of A of every adapter that the tile's rows have, stacked, up to 256 a pass: X is read
+// once whatever the mix, and a row takes the columns of its own adapter from its accumulator. A
+// cluster of `split` CTAs shares K; the parts meet in shared memory and are added in
+// their order. Warps: 0 TMA producer, 1 MMA issuer, 2-5 accumulator to V, 6-9 for the prompt
+// form: the adapters of its token tiles, and which B_a hold numbers that are not finite
+// (those may not go through products with the zeros of other requests' rows).
+struct Shrink {
+    static constexpr int ROWS = 128, SL = 64, X_BYTES = ROWS * 128;
+    static constexpr int MOST_COLS = 256, MOST_STAGES = 8, MOST_SPLIT = 8;
+    static constexpr int EPI_WARP0 = 2, HELP_WARP0 = 6, THREADS = 320, HELPERS = 128;
+    static constexpr int TMEM_COLS = 256, WORDS = DGEMM_MAX_ADAPTERS / 32;
+    static constexpr int TABLES = 2 * WORDS * 4 + ROWS * 4 + DGEMM_MAX_ADAPTERS * 2, BAR_BYTES = 256;
+    static constexpr uint32_t IDESC0 = make_idesc(1u, false, false, 128, 0);
+    static constexpr int stage_bytes(int cols) { return X_BYTES + cols * 128; }
+    static constexpr int smem_bytes(int cols, int stages, int rank) {
+        return 1024 + stages * stage_bytes(cols) + rank * ROWS * 4 + TABLES + BAR_BYTES;
+    }
+    static_assert((2 * MOST_STAGES + 3) * 8 + 8 <= BAR_BYTES, "barriers fit");
+};
+
+__device__ __forceinline__ bool not_finite(uint32_t pair) {
+    return (pair & 0x7F80u) == 0x7F80u || (pair & 0x7F800000u) == 0x7F800000u;
+}
+__device__ __forceinline__ bool not_finite(const uint4& v) {
+    return not_finite(v.x) || not_finite(v.y) || not_finite(v.z) || not_finite(v.w);
+}
+
+// The helpers' part; `words` and `used` are theirs.
+__device__ __forceinline__ void shrink_help(const Params& p, unsigned* words, uint16_t* used, int tid) {
+    constexpr int BAR = 1;
+    auto sync = [&]() { asm volatile("barrier.cta.sync %0, %1;" ::"n"(BAR), "n"(Shrink::HELPERS) : "memory"); };
+    auto clear = [&]() {
+        for (int w = tid; w < Shrink::WORDS; w += Shrink::HELPERS) words[w] = 0;
+        sync();
+    };
+    // the adapters of the token tiles
+    for (int tile = static_cast<int>(blockIdx.x); tile < p.tiles; tile += static_cast<int>(gridDim.x)) {
+        const int row0 = tile * p.width, rows = min(p.width, p.T - row0);
+        clear();
+        mark_adapters(p, row0, rows, words, tid, Shrink::HELPERS);
+        sync();
+        int* list = p.lists + static_cast<int64_t>(tile) * kListPitch;
+        for (int i = tid; i < rows; i += Shrink::HELPERS) {
+            const int a = adapter_of(p, row0 + i);
+            if (a >= 0) list[4 + place_of(p, words, a)] = a;          // (rows of one adapter write the same)
+        }
+        if (tid == 0) list[0] = marked(p, words);
+        sync();
+    }
+    // B of every adapter in use, shared out over the launch
+    clear();
+    mark_adapters(p, 0, p.T, words, tid, Shrink::HELPERS);
+    sync();
+    for (int a = tid; a < p.L; a += Shrink::HELPERS)
+        if ((words[a >> 5] >> (a & 31)) & 1) used[place_of(p, words, a)] = static_cast<uint16_t>(a);
+    sync();
+    const int64_t per = static_cast<int64_t>(p.N) * p.r / 8, all = per * marked(p, words);
+    const int64_t i0 = all * blockIdx.x / gridDim.x, i1 = all * (blockIdx.x + 1) / gridDim.x;
+    for (int64_t i = i0; i < i1;) {
+        const int a = used[i / per];
+        const int64_t base = (i / per) * per, end = min(i1, base + per);
+        const uint4* b = reinterpret_cast<const uint4*>(p.high) + a * per - base;
+        bool bad = false;
+#pragma unroll 8
+        for (int64_t k = i + tid; k < end; k += Shrink::HELPERS) bad = not_finite(__ldg(b + k)) || bad;
+        if (bad) p.bad[a] = p.epoch;
+        i = end;
+    }
+}
+
+__global__ void __launch_bounds__(Shrink::THREADS, 1)
+    adapter_shrink_many(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmA,
+                        const __grid_constant__ Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int S = p.stages, split = p.split, stage_bytes = Shrink::X_BYTES + p.shrink_cols * 128;
+    float* park = reinterpret_cast<float*>(ring + S * stage_bytes);                    // [r][128]
+    unsigned* words = reinterpret_cast<unsigned*>(park + p.r * Shrink::ROWS);
+    unsigned* help_words = words + Shrink::WORDS;
+    int* list = reinterpret_cast<int*>(help_words + Shrink::WORDS);                    // [128] adapters of this tile
+    uint16_t* used = reinterpret_cast<uint16_t*>(list + Shrink::ROWS);
+    uint64_t* full = reinterpret_cast<uint64_t*>(used + DGEMM_MAX_ADAPTERS);
+    uint64_t* empty = full + S;
+    uint64_t* acc_full = empty + S;
+    uint64_t* acc_empty = acc_full + 1;
+    uint64_t* drain = acc_empty + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(blockIdx.x) % split, row0 = static_cast<int>(blockIdx.x) / split * Shrink::ROWS;
+    const int kb0 = static_cast<int>(static_cast<int64_t>(p.kstages) * rank / split);
+    const int kb1 = static_cast<int>(static_cast<int64_t>(p.kstages) * (rank + 1) / split);
+
+    for (int w = threadIdx.x; w < Shrink::WORDS; w += Shrink::THREADS) words[w] = 0;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(acc_full, 1);
+        mbar_init(acc_empty, 4);
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        fence_mbarrier_init();
+        tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmA);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, Shrink::TMEM_COLS);
+        tmem_relinquish();
+    }
+    __syncthreads();
+    grid_dependency_wait();
+    if (threadIdx.x == 0) grid_launch_dependents();
+    // the adapters of this tile's rows, in order; a thread of the accumulator's warps has the row that
+    // its lane of the accumulator is (a warp reads the quarter that its number says)
+    const int at = (warp & 3) * 32 + lane;
+    int mine = -1;
+    if (warp >= Shrink::EPI_WARP0 && warp < Shrink::HELP_WARP0 && row0 + at < p.T) {
+        mine = adapter_of(p, row0 + at);
+        if (mine >= 0) atomicOr(&words[mine >> 5], 1u << (mine & 31));
+    }
+    __syncthreads();
+    int slot = -1;
+    if (mine >= 0) {
+        slot = place_of(p, words, mine);
+        list[slot] = mine;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int count = marked(p, words), per_pass = p.shrink_cols / p.r, passes = (count + per_pass - 1) / per_pass;
+
+    if (warp == 0) {
+        // ---------------------------------------------------------------- TMA producer
+        const uint64_t pol = policy_evict_last();
+        uint32_t stage = 0, phase = 0;
+        int64_t issued = 0;
+        bool ok = true, stalled = false;
+        for (int pass = 0; ok && !stalled && pass < passes; ++pass) {
+            const int first = pass * per_pass, n = min(per_pass, count - first);
+            for (int kb = kb0; kb < kb1; ++kb) {
+                stalled = issued == p.stall_after;
+                if (stalled) break;
+                ok = mbar_wait_warp(&empty[stage], phase ^ 1, abort_flag, p.wait_ns);
+                if (!ok) break;
+                if (elect_one()) {
+                    uint8_t* x = ring + stage * stage_bytes;
+                    const uint32_t bar = smem_u32(&full[stage]);
+                    mbar_arrive_expect_tx(&full[stage], Shrink::X_BYTES + n * p.r * 128);
+                    tma_load_nd<false>(x, &tmX, bar, kb * Shrink::SL, row0, pol);
+                    for (int i = 0; i < n; ++i)
+                        tma_load_nd<false>(x + Shrink::X_BYTES + i * p.r * 128, &tmA, bar, kb * Shrink::SL, 0, list[first + i], pol);
+                }
+                __syncwarp();
+                ++issued;
+                if (++stage == static_cast<uint32_t>(S)) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+        }
+        if (!ok && lane == 0) experts::fail(p, ERR_TIMEOUT_PRODUCER, abort_flag);
+        for (int s = 0; s < S; ++s) {
+            const int64_t cnt = issued > s ? (issued - s + S - 1) / S : 0;
+            if (cnt > 0 && !mbar_wait_warp(&full[s], static_cast<uint32_t>((cnt - 1) & 1), nullptr, p.wait_ns) && lane == 0)
+                experts::fail(p, ERR_TIMEOUT_DRAIN, abort_flag);
+        }
+    } else if (warp == 1) {
+        // ---------------------------------------------------------------- MMA issuer
+        const uint32_t s0 = smem_u32(ring), acc = __shfl_sync(kAllLanes, tmem, 0);
+        const uint64_t xd0 = smem_desc_sw128(s0, 16, 1024), ad0 = smem_desc_sw128(s0 + Shrink::X_BYTES, 16, 1024);
+        uint32_t stage = 0, phase = 0;
+        bool ok = true;
+        for (int pass = 0; ok && pass < passes; ++pass) {
+            // (a rank of 8 may end inside a step of 16 columns: what lies there is in columns that no row takes)
+            const int n = (min(per_pass, count - pass * per_pass) * p.r + 15) / 16 * 16;
+            const uint32_t idesc = Shrink::IDESC0 | (static_cast<uint32_t>(n >> 3) << 17);
+            ok = mbar_wait_warp(acc_empty, (pass & 1) ^ 1, abort_flag, p.wait_ns);
+            if (!ok) break;
+            tc_fence_after();
+            for (int kb = kb0; kb < kb1; ++kb) {
+                ok = mbar_wait_warp(&full[stage], phase, abort_flag, p.wait_ns);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t xd = xd0 + stage * (stage_bytes >> 4), ad = ad0 + stage * (stage_bytes >> 4);
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) mma_bf16(acc, xd + k * 2, ad + k * 2, idesc, kb > kb0 || k > 0 ? 1u : 0u);
+                    mma_commit(&empty[stage]);
+                }
+                __syncwarp();
+                if (++stage == static_cast<uint32_t>(S)) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+            if (ok && elect_one()) mma_commit(acc_full);
+            __syncwarp();
+        }
+        if (elect_one()) {
+            if (!ok) experts::fail(p, ERR_TIMEOUT_MMA, abort_flag);
+            mma_commit(drain);
+            if (!mbar_wait(drain, 0, nullptr, p.wait_ns)) experts::fail(p, ERR_TIMEOUT_DRAIN, abort_flag);
+        }
+        __syncwarp();
+    } else if (warp < Shrink::HELP_WARP0) {
+        // ---------------------------------------------------------------- each row's own columns
+        const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        bool ok = true;
+        for (int pass = 0; pass < passes; ++pass) {
+            ok = mbar_wait_warp(acc_full, pass & 1, abort_flag, p.wait_ns);
+            if (!ok) break;
+            tc_fence_after();
+            const int first = pass * per_pass, n = min(per_pass, count - first);
+            for (int i = 0; i < n; ++i) {
+                const bool take = slot == first + i;
+                if (!__any_sync(kAllLanes, take)) continue;
+                for (int j = 0; j < p.r; j += 8) {
+                    uint32_t v[8];
+                    tmem_ld8(lanes + i * p.r + j, v);
+                    tmem_ld_wait();
+                    if (take) {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) park[(j + c) * Shrink::ROWS + at] = __uint_as_float(v[c]);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acc_empty);
+        }
+        if (!ok && lane == 0) experts::fail(p, ERR_TIMEOUT_EPILOGUE, abort_flag);
+    } else if (p.prompt) {
+        shrink_help(p, help_words, used, threadIdx.x - 32 * Shrink::HELP_WARP0);
+    }
+    __syncwarp();
+    if (split > 1) cluster_sync();
+    else __syncthreads();
+    // ---------------------------------------------------------------- the parts of a row together
+    if (!*abort_flag) {
+        const uint32_t parked = smem_u32(park);
+        const int groups = p.r / 8;
+        for (int i = threadIdx.x; i < (groups + split - 1) / split * Shrink::ROWS; i += Shrink::THREADS) {
+            const int r128 = i % Shrink::ROWS, g = i / Shrink::ROWS * split + rank, t = row0 + r128;
+            if (g >= groups || t >= p.T) continue;
+            const int a = adapter_of(p, t);
+            if (a < 0) continue;
+            const float scale = p.scale ? p.scale[a] : 1.0f;
+            float v[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) v[c] = 0.0f;
+            for (int s = 0; s < split; ++s) {
+                const uint32_t from = (split > 1 ? mapa_shared(parked, s) : parked) + (g * 8 * Shrink::ROWS + r128) * 4;
+#pragma unroll
+                for (int c = 0; c < 8; ++c) v[c] += ld_shared_cluster_f32(from + c * Shrink::ROWS * 4);
+            }
+            if (p.prompt) {
+                // two BF16 numbers whose sum is V up to 2^-18 of it; an infinity has no second
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float x = v[2 * c] * scale, y = v[2 * c + 1] * scale;
+                    hi[c] = pack_bf16x2(x, y);
+                    const float dx = x - bf16_lo(hi[c]), dy = y - bf16_hi(hi[c]);
+                    lo[c] = pack_bf16x2(fabsf(dx) < INFINITY ? dx : 0.0f, fabsf(dy) < INFINITY ? dy : 0.0f);
+                }
+                __nv_bfloat16* out = v_split(p, t) + g * 8;
+                *reinterpret_cast<uint4*>(out) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4*>(out + p.r) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            } else {
+                float4* out = reinterpret_cast<float4*>(p.V + static_cast<int64_t>(t) * p.r + g * 8);
+                out[0] = make_float4(v[0] * scale, v[1] * scale, v[2] * scale, v[3] * scale);
+                out[1] = make_float4(v[4] * scale, v[5] * scale, v[6] * scale, v[7] * scale);
+            }
+        }
+    }
+    tc_fence_before();
+    if (split > 1) cluster_sync();
+    else __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, Shrink::TMEM_COLS);
+    }
+}
+
 }  // namespace adapters
 }  // namespace dg

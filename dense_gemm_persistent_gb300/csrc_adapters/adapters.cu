@@ -5,13 +5,29 @@
 #include <cstring>
 
 #include "adapter_few.cuh"
+#include "adapter_mma.cuh"
 #include "adapter_shrink.cuh"
 #include "host.h"
 
 namespace {
 
 using dg::adapters::Few;
+using dg::adapters::Mma;
 using dg::adapters::Params;
+using dg::adapters::Shrink;
+
+constexpr CUtensorMapDataType kBf16 = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+constexpr int kShared = 232448;                   // a CTA's dynamic shared memory, at most
+
+// Behind the workspace's status word.
+struct Workspace {
+    size_t lists, bad, bytes;
+    Workspace(int64_t T, int64_t r, int64_t L) {
+        lists = DGEMM_WS_STATUS_BYTES + static_cast<size_t>(T) * static_cast<size_t>(r) * 4;
+        bad = lists + static_cast<size_t>((T + Mma::LEAST_WIDTH - 1) / Mma::LEAST_WIDTH) * dg::adapters::kListPitch * 4;
+        bytes = bad + static_cast<size_t>(L) * 8;
+    }
+};
 
 struct Call {
     const void *X, *W, *A, *B;
@@ -30,6 +46,9 @@ struct Call {
     cudaStream_t stream;
 };
 
+// Most rows of a call that go by tiles of 64 rows, and by FP32 units to V.
+constexpr int kMostFew = 256, kMostFewShrink = 64;
+
 dgemm_status_t check_sizes(int64_t T, int64_t N, int64_t K, int64_t r, int64_t L) {
     if (T < 0 || N < 0 || K < 0 || L < 0 || r < 1) return DGEMM_ERR_INVALID_VALUE;
     if (L > DGEMM_MAX_ADAPTERS || r > DGEMM_MAX_ADAPTER_RANK) return DGEMM_ERR_NOT_SUPPORTED;
@@ -46,56 +65,113 @@ bool allow_shared(std::atomic<unsigned char>* ready, int device, const void* fun
     return true;
 }
 
-dgemm_status_t launch_shrink(const Params& p, cudaStream_t s) {
+// V of few rows: a CTA for every four numbers.
+dgemm_status_t launch_shrink_few(const Params& p, cudaStream_t s) {
     constexpr int RB = 4;
     dg::host::Launch l(static_cast<unsigned>(p.T) * (p.r / RB), 1, dg::adapters::SHRINK_THREADS, 0, s);
     return cudaLaunchKernelEx(&l.cfg, dg::adapters::adapter_shrink_few<RB>, p) == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
 }
 
+dgemm_status_t launch_shrink_many(const Call& c, Params p, const dg::host::Device& dev) {
+    p.shrink_tiles = (p.T + Shrink::ROWS - 1) / Shrink::ROWS;
+    p.kstages = (p.K + Shrink::SL - 1) / Shrink::SL;
+    p.shrink_cols = std::min(Shrink::MOST_COLS / p.r, std::min(p.L, Shrink::ROWS)) * p.r;
+    p.split = 1;
+    while (p.split < Shrink::MOST_SPLIT && p.shrink_tiles * p.split * 2 <= dev.num_sms && p.kstages >= 4 * p.split) p.split *= 2;
+    p.stages = 2;
+    while (p.stages < Shrink::MOST_STAGES && Shrink::smem_bytes(p.shrink_cols, p.stages + 1, p.r) <= kShared) ++p.stages;
+    const int smem = Shrink::smem_bytes(p.shrink_cols, p.stages, p.r);
+    alignas(64) CUtensorMap x, a;
+    const uint64_t K = p.K, r = p.r, dx[2] = {K, static_cast<uint64_t>(p.T)}, sx[1] = {K * 2};
+    const uint64_t da[3] = {K, r, static_cast<uint64_t>(p.L)}, sa[2] = {K * 2, r * K * 2};
+    const uint32_t bx[2] = {Shrink::SL, Shrink::ROWS}, ba[3] = {Shrink::SL, static_cast<uint32_t>(p.r), 1};
+    if (!dg::host::encode_map(&x, kBf16, c.X, 2, dx, sx, bx) || !dg::host::encode_map(&a, kBf16, c.A, 3, da, sa, ba))
+        return DGEMM_ERR_CUDA;
+    static std::atomic<unsigned char> ready[dg::host::kMaxDevices];
+    if (!allow_shared(ready, dev.id, reinterpret_cast<const void*>(&dg::adapters::adapter_shrink_many), kShared))
+        return DGEMM_ERR_CUDA;
+    dg::host::Launch l(static_cast<unsigned>(p.shrink_tiles * p.split), 1, Shrink::THREADS, smem, c.stream, p.split);
+    return cudaLaunchKernelEx(&l.cfg, dg::adapters::adapter_shrink_many, x, a, p) == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
+}
+
+// The maps of X (boxes of `rows` token rows) and W (a CTA's 128 channels): with whole slices of K both slices of
+// a stage (and the gate and up channels of a gated tile) come in one copy.
+bool product_maps(const Call& c, const Params& p, CUtensorMap* w, CUtensorMap* x, int rows) {
+    const uint64_t N = p.N, K = p.K, T = p.T, sl = Few::SL, halves = p.gated ? 2 : 1, H = N / halves;
+    const uint32_t s = Few::SL, channels = p.gated ? 64 : 128, hv = static_cast<uint32_t>(halves), cols = rows, ks = Few::KS;
+    if (p.k_whole) {
+        const uint64_t dw[4] = {sl, H, halves, K / sl}, sw[3] = {K * 2, H * K * 2, 128};
+        const uint32_t bw[4] = {s, channels, hv, ks};
+        const uint64_t dx[3] = {sl, T, K / sl}, sx[2] = {K * 2, 128};
+        const uint32_t bx[3] = {s, cols, ks};
+        return dg::host::encode_map(w, kBf16, c.W, 4, dw, sw, bw) && dg::host::encode_map(x, kBf16, c.X, 3, dx, sx, bx);
+    }
+    const uint64_t dw[3] = {K, H, halves}, sw[2] = {K * 2, H * K * 2};
+    const uint32_t bw[3] = {s, channels, hv};
+    const uint64_t dx[2] = {K, T}, sx[1] = {K * 2};
+    const uint32_t bx[2] = {s, cols};
+    return dg::host::encode_map(w, kBf16, c.W, 3, dw, sw, bw) && dg::host::encode_map(x, kBf16, c.X, 2, dx, sx, bx);
+}
+
 dgemm_status_t launch_few(const Call& c, Params& p, const dg::host::Device& dev) {
-    constexpr int kHalf = 113 * 1024, kWhole = 232448;           // two CTAs an SM, one
+    constexpr int kHalf = 113 * 1024;             // two CTAs an SM
     const int fewest = (p.T + Few::MOST_COLS - 1) / Few::MOST_COLS;
     p.width = ((p.T + fewest - 1) / fewest + 15) / 16 * 16;
     p.tiles = (p.T + p.width - 1) / p.width;
     const int ctiles = (p.wide + (p.gated ? 64 : 128) - 1) / (p.gated ? 64 : 128);
-    p.k_whole = p.K % Few::SL == 0;
-    p.kstages = c.W ? (p.K + Few::KS * Few::SL - 1) / (Few::KS * Few::SL) : 0;
     const int64_t tiles = static_cast<int64_t>(p.tiles) * ctiles;
     if (tiles > INT32_MAX / Few::MOST_SPLIT) return DGEMM_ERR_NOT_SUPPORTED;
     p.split = 1;
     while (p.split < Few::MOST_SPLIT && tiles * p.split * 2 <= 2 * dev.num_sms && p.kstages >= 4 * p.split) p.split *= 2;
-    const int shared = Few::smem_bytes(p.width, 3, p.split) <= kHalf ? kHalf : kWhole;
+    const int shared = Few::smem_bytes(p.width, 3, p.split) <= kHalf ? kHalf : kShared;
     p.stages = p.kstages > 0 ? 2 : 0;
     while (p.stages > 0 && p.stages < Few::MOST_STAGES && Few::smem_bytes(p.width, p.stages + 1, p.split) <= shared) ++p.stages;
     const int smem = Few::smem_bytes(p.width, p.stages, p.split);
     alignas(64) CUtensorMap w, x;
     std::memset(&w, 0, sizeof w);
     std::memset(&x, 0, sizeof x);
-    if (p.kstages > 0) {
-        const uint64_t N = p.N, K = p.K, T = p.T, sl = Few::SL, halves = p.gated ? 2 : 1, H = N / halves;
-        const uint32_t s = Few::SL, rows = p.gated ? 64 : 128, hv = static_cast<uint32_t>(halves), cols = p.width, ks = Few::KS;
-        const CUtensorMapDataType dt = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-        bool ok;
-        if (p.k_whole) {
-            // a stage's slices (and the gate and up channels of a gated tile) in one copy
-            const uint64_t dw[4] = {sl, H, halves, K / sl}, sw[3] = {K * 2, H * K * 2, 128};
-            const uint32_t bw[4] = {s, rows, hv, ks};
-            const uint64_t dx[3] = {sl, T, K / sl}, sx[2] = {K * 2, 128};
-            const uint32_t bx[3] = {s, cols, ks};
-            ok = dg::host::encode_map(&w, dt, c.W, 4, dw, sw, bw) && dg::host::encode_map(&x, dt, c.X, 3, dx, sx, bx);
-        } else {
-            const uint64_t dw[3] = {K, H, halves}, sw[2] = {K * 2, H * K * 2};
-            const uint32_t bw[3] = {s, rows, hv};
-            const uint64_t dx[2] = {K, T}, sx[1] = {K * 2};
-            const uint32_t bx[2] = {s, cols};
-            ok = dg::host::encode_map(&w, dt, c.W, 3, dw, sw, bw) && dg::host::encode_map(&x, dt, c.X, 2, dx, sx, bx);
-        }
-        if (!ok) return DGEMM_ERR_CUDA;
-    }
+    if (p.kstages > 0 && !product_maps(c, p, &w, &x, p.width)) return DGEMM_ERR_CUDA;
     static std::atomic<unsigned char> ready[dg::host::kMaxDevices];
-    if (!allow_shared(ready, dev.id, reinterpret_cast<const void*>(&dg::adapters::adapter_few), kWhole)) return DGEMM_ERR_CUDA;
+    if (!allow_shared(ready, dev.id, reinterpret_cast<const void*>(&dg::adapters::adapter_few), kShared)) return DGEMM_ERR_CUDA;
     dg::host::Launch l(static_cast<unsigned>(tiles * p.split), 1, Few::THREADS, smem, c.stream, p.split);
     return cudaLaunchKernelEx(&l.cfg, dg::adapters::adapter_few, w, x, p) == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
+}
+
+// The token tiles of the prompt form: their width is the one with the least time by a model of waves of tiles, a tile's
+// time as its rows, at least 96 (then the weights' way to the SM is longer), and 16 more for its ends.
+void prompt_tiles(Params& p, const dg::host::Device& dev) {
+    p.ctiles = (p.wide + (p.gated ? 128 : 256) - 1) / (p.gated ? 128 : 256);
+    int64_t least = INT64_MAX;
+    for (int width = Mma::LEAST_WIDTH; width <= Mma::BN; width += Mma::Q) {
+        const int64_t tiles = (p.T + width - 1) / width, units = dev.num_sms / 2;
+        const int64_t cost = (tiles * p.ctiles + units - 1) / units * (std::max(width, 96) + 16);
+        if (cost <= least) {
+            least = cost;
+            p.width = width;
+            p.tiles = static_cast<int>(tiles);
+        }
+    }
+}
+
+dgemm_status_t launch_prompt(const Call& c, const Params& p, const dg::host::Device& dev) {
+    const int64_t items = static_cast<int64_t>(p.tiles) * p.ctiles;
+    if (items > INT32_MAX / 2) return DGEMM_ERR_NOT_SUPPORTED;
+    alignas(64) CUtensorMap w, x, b;
+    std::memset(&w, 0, sizeof w);
+    std::memset(&x, 0, sizeof x);
+    std::memset(&b, 0, sizeof b);
+    if (p.kstages > 0 && !product_maps(c, p, &w, &x, p.width / 2)) return DGEMM_ERR_CUDA;
+    if (p.L > 0) {
+        const uint64_t r = p.r, N = p.N, halves = p.gated ? 2 : 1, H = N / halves, L = p.L;
+        const uint64_t d[4] = {r, H, halves, L}, st[3] = {r * 2, H * r * 2, N * r * 2};
+        const uint32_t box[4] = {Mma::SL, p.gated ? 64u : 128u, static_cast<uint32_t>(halves), 1};
+        if (!dg::host::encode_map(&b, kBf16, c.B, 4, d, st, box)) return DGEMM_ERR_CUDA;
+    }
+    static std::atomic<unsigned char> ready[dg::host::kMaxDevices];
+    if (!allow_shared(ready, dev.id, reinterpret_cast<const void*>(&dg::adapters::adapter_mma), kShared)) return DGEMM_ERR_CUDA;
+    const int units = static_cast<int>(std::min<int64_t>(dev.num_sms / 2, items));
+    dg::host::Launch l(static_cast<unsigned>(units * 2), 1, Mma::THREADS, Mma::SMEM, c.stream, 2);
+    return cudaLaunchKernelEx(&l.cfg, dg::adapters::adapter_mma, w, x, b, p) == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
 }
 
 dgemm_status_t run_adapters(const Call& c) {
@@ -125,7 +201,10 @@ dgemm_status_t run_adapters(const Call& c) {
     p.high = static_cast<const __nv_bfloat16*>(c.B);
     p.ids = c.ids;
     p.scale = c.scale;
+    const Workspace ws(c.T, c.r, c.L);
     p.V = reinterpret_cast<float*>(static_cast<char*>(c.ws) + DGEMM_WS_STATUS_BYTES);
+    p.lists = reinterpret_cast<int*>(static_cast<char*>(c.ws) + ws.lists);
+    p.bad = reinterpret_cast<unsigned long long*>(static_cast<char*>(c.ws) + ws.bad);
     p.T = static_cast<int>(c.T);
     p.N = static_cast<int>(c.N);
     p.K = static_cast<int>(c.K);
@@ -144,11 +223,16 @@ dgemm_status_t run_adapters(const Call& c) {
     p.ws_status = static_cast<unsigned long long*>(c.ws);
     dg::host::wait_settings(&p.wait_ns, &p.stall_after);
     p.wait_first = p.L == 0;
+    p.k_whole = p.K % Few::SL == 0;
+    p.kstages = c.W ? (p.K + Few::KS * Few::SL - 1) / (Few::KS * Few::SL) : 0;
+    const int forced = dg::host::pair_override();
+    p.prompt = forced >= 0 ? forced : p.T > kMostFew;
+    if (p.prompt) prompt_tiles(p, dev);
     if (p.L > 0) {
-        const dgemm_status_t s = launch_shrink(p, c.stream);
+        const dgemm_status_t s = p.prompt || p.T > kMostFewShrink ? launch_shrink_many(c, p, dev) : launch_shrink_few(p, c.stream);
         if (s != DGEMM_OK) return s;
     }
-    return launch_few(c, p, dev);
+    return p.prompt ? launch_prompt(c, p, dev) : launch_few(c, p, dev);
 }
 
 }  // namespace
@@ -157,7 +241,7 @@ extern "C" {
 
 size_t dgemm_adapter_workspace_size(int64_t T, int64_t N, int64_t K, int64_t r, int64_t L) {
     if (check_sizes(T, N, K, r, L) != DGEMM_OK) return 0;
-    return DGEMM_WS_STATUS_BYTES + static_cast<size_t>(T) * static_cast<size_t>(r) * 4;
+    return Workspace(T, r, L).bytes;
 }
 
 dgemm_status_t dgemm_adapter_bf16(const void* X, const void* W, const void* A, const void* B, const int32_t* ids,

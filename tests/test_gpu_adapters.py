@@ -12,6 +12,16 @@ pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
 
 
+@pytest.fixture(params=[None, 0, 1], ids=["chosen", "few", "prompt"])
+def form(request):
+    """Tiles of 64 rows, the CTA pairs' tiles, or the library's choice between them."""
+    if request.param is None:
+        yield
+    else:
+        with dg.overrides(cta_pair=request.param):
+            yield
+
+
 class Problem:
     def __init__(self, T, N, K, r, L, seed=0, order="mixed", with_scale=True, with_bias=False):
         g = torch.Generator().manual_seed(seed * 1000003 + T * 7 + N * 5 + K * 3 + r + L)
@@ -78,7 +88,7 @@ SIZES = [(1, 128, 128, 8, 1), (1, 4096, 4096, 16, 8), (2, 130, 72, 8, 3), (3, 1,
 
 @pytest.mark.parametrize("T,N,K,r,L", SIZES)
 @pytest.mark.parametrize("order,act", [("mixed", "none"), ("runs", "silu"), ("one", "gelu"), ("none", "relu")])
-def test_projection(T, N, K, r, L, order, act):
+def test_projection(form, T, N, K, r, L, order, act):
     p = Problem(T, N, K, r, L, order=order, with_bias=order != "mixed", with_scale=order != "one")
     out = F32 if T % 2 else BF
     close(p.project(act, out), ref.adapters(p.X, p.A, p.B, p.ids, W=p.W, scale=p.scale, bias=p.bias, act=act, out_dtype=out))
@@ -87,14 +97,14 @@ def test_projection(T, N, K, r, L, order, act):
 @pytest.mark.parametrize("T,N,K,r,L", [(1, 256, 128, 16, 2), (20, 130, 264, 8, 7), (64, 768, 1024, 64, 20), (70, 2050, 72, 24, 3),
                                        (300, 512, 512, 16, 6), (700, 260, 320, 128, 4)])
 @pytest.mark.parametrize("out", [BF, F32])
-def test_gated_projection(T, N, K, r, L, out):
+def test_gated_projection(form, T, N, K, r, L, out):
     p = Problem(T, N, K, r, L, order="runs" if T > 64 else "mixed", with_bias=T % 3 == 1)
     close(p.project("swiglu", out), ref.adapters(p.X, p.A, p.B, p.ids, W=p.W, scale=p.scale, bias=p.bias, act="swiglu", out_dtype=out))
 
 
 @pytest.mark.parametrize("T,N,K,r,L", SIZES)
 @pytest.mark.parametrize("c,out,act", [(BF, BF, "none"), (F32, BF, "silu"), (BF, F32, "gelu"), (None, F32, "none"), (F32, F32, "relu")])
-def test_beside_another_product(T, N, K, r, L, c, out, act):
+def test_beside_another_product(form, T, N, K, r, L, c, out, act):
     p = Problem(T, N, K, r, L, seed=1, order="runs" if T > 64 else "mixed", with_bias=act == "silu")
     C = None if c is None else p.C.to(c)
     close(p.add(act, out, c), ref.adapters(p.X, p.A, p.B, p.ids, C=C, scale=p.scale, bias=p.bias, act=act, out_dtype=out))
@@ -102,7 +112,7 @@ def test_beside_another_product(T, N, K, r, L, c, out, act):
 
 @pytest.mark.parametrize("T", [5, 64, 400])
 @pytest.mark.parametrize("dtype", [BF, F32])
-def test_in_place(T, dtype):
+def test_in_place(form, T, dtype):
     for order in ("mixed", "none"):
         p = Problem(T, 300, 136, 16, 5, order=order)
         got = p.add("none", dtype, dtype, in_place=True)
@@ -112,7 +122,7 @@ def test_in_place(T, dtype):
 
 
 @pytest.mark.parametrize("T", [3, 70, 300])
-def test_no_adapters_at_all_and_no_depth(T):
+def test_no_adapters_at_all_and_no_depth(form, T):
     p = Problem(T, 264, 136, 8, 0, with_bias=True)
     close(p.project("silu"), ref.adapters(p.X, p.A, p.B, p.ids, W=p.W, bias=p.bias, act="silu"))
     close(p.add("none", F32, BF), ref.adapters(p.X, p.A, p.B, p.ids, C=p.C.to(BF), bias=p.bias, out_dtype=F32))
@@ -130,7 +140,7 @@ def test_nothing_to_do():
 
 @pytest.mark.parametrize("T,order", [(8, "mixed"), (60, "mixed"), (200, "runs"), (300, "runs"), (520, "mixed")])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
-def test_a_bad_adapter_stays_with_its_request(T, order, bad):
+def test_a_bad_adapter_stays_with_its_request(form, T, order, bad):
     p = Problem(T, 264, 256, 16, 6, order=order)
     clean = p.project(out=F32).cpu()
     clean_add = p.add(out=F32, c=F32).cpu()
@@ -150,7 +160,7 @@ def test_a_bad_adapter_stays_with_its_request(T, order, bad):
 
 
 @pytest.mark.parametrize("T", [8, 64, 300])
-def test_a_bad_row_stays_alone(T):
+def test_a_bad_row_stays_alone(form, T):
     p = Problem(T, 264, 256, 16, 6, order="one")
     clean = p.project(out=F32).cpu()
     p.X[4, 17] = float("nan")
@@ -162,7 +172,7 @@ def test_a_bad_row_stays_alone(T):
 
 
 @pytest.mark.parametrize("T,N,K,r,L,order", [(1, 512, 4096, 16, 4, "mixed"), (40, 640, 1024, 32, 9, "mixed"), (700, 520, 512, 16, 5, "runs")])
-def test_the_same_bits_every_time_on_another_stream_and_in_a_graph(T, N, K, r, L, order):
+def test_the_same_bits_every_time_on_another_stream_and_in_a_graph(form, T, N, K, r, L, order):
     p = Problem(T, N, K, r, L, order=order)
     first = p.project()
     second = p.project(ws=p.workspace(0x00))
@@ -205,7 +215,7 @@ def test_inputs_written_just_before_and_after_the_call():
 
 
 @pytest.mark.parametrize("T", [8, 600])
-def test_waits_are_bounded(T):
+def test_waits_are_bounded(form, T):
     p = Problem(T, 512, 1024, 16, 4, order="runs")
     X, W, A, B, ids, scale = p.on_gpu("X", "W", "A", "B", "ids", "scale")
     D, ws = torch.empty(T, 512, dtype=BF, device=dev()), p.workspace()
