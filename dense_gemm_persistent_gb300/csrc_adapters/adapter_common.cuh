@@ -67,12 +67,15 @@ __device__ __forceinline__ __nv_bfloat16* v_split(const Params& p, int t) {
 
 // Bits of the adapters in use among n rows, by `threads` threads that all pass; words: [128].
 __device__ __forceinline__ void mark_adapters(const Params& p, int first, int n, unsigned* words, int tid, int threads) {
-#pragma unroll 8
-    for (int i = tid; i < n; i += threads) {
-        const int a = adapter_of(p, first + i);
-        // (most are marked already: a look spares the atomic)
-        if (a >= 0 && !((*reinterpret_cast<volatile unsigned*>(words + (a >> 5)) >> (a & 31)) & 1))
-            atomicOr(&words[a >> 5], 1u << (a & 31));
+    // (loads of a batch before its marks; most are marked already, and a look spares the atomic)
+    for (int i0 = tid; i0 < n; i0 += 16 * threads) {
+        int a[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) a[k] = i0 + k * threads < n ? adapter_of(p, first + i0 + k * threads) : -1;
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+            if (a[k] >= 0 && !((*reinterpret_cast<volatile unsigned*>(words + (a[k] >> 5)) >> (a[k] & 31)) & 1))
+                atomicOr(&words[a[k] >> 5], 1u << (a[k] & 31));
     }
 }
 // The place of adapter a among the marked ones, and how many there are.

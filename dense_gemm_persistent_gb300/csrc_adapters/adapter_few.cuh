@@ -3,10 +3,9 @@
 // The output channels are the MMA's 128 rows, the token rows its columns. A cluster of
 // `split` CTAs shares a tile's K: each sums its part in Tensor Memory, parks it in its shared
 // memory, and finishes every split-th row of the tile from all parts in their order.
-// V . B_a^T runs on the FP32 units meanwhile: a thread has one channel and a row's V is the same for
-// the whole warp, so every row reads the adapter of its own and rows may be of as many
-// requests as there are. It needs V, the rest does not: only these warps wait for the launch
-// that computes it.
+// V . B_a^T runs on the FP32 units meanwhile, row by row: every row reads the adapter of its own, and
+// rows may be of as many requests as there are. It needs V, the rest does not: only these
+// warps wait for the launch that computes it.
 // Warps: 0 TMA producer, 1 MMA issuer and owner of the Tensor Memory, 2-9 epilogue.
 #pragma once
 
@@ -39,14 +38,64 @@ __device__ __forceinline__ float activate(float v, int act) {
     }
 }
 
-// V[t] . B_a[n], both r numbers.
-__device__ __forceinline__ float high_dot(const Params& p, int t, int a, int n) {
-    const uint4* b = reinterpret_cast<const uint4*>(p.high + (static_cast<int64_t>(a) * p.N + n) * p.r);
-    const float4* v = reinterpret_cast<const float4*>(p.V + static_cast<int64_t>(t) * p.r);
-    float s0 = 0.0f, s1 = 0.0f;
-#pragma unroll 4
-    for (int i = 0; i < p.r / 8; ++i) fma8(s0, s1, __ldg(b + i), v[2 * i], v[2 * i + 1]);
-    return s0 + s1;
+// V[t] . B_a^T for one row t of the tile and some of its 128 channels, by one warp: r / 8 lanes (rounded up to
+// a power of two) share a channel, so that a load of the warp is one run of memory, eight loads in
+// flight. `out`: the row's [128] results.
+struct HighItems {
+    int lanes, channels, per_row;       // lanes of a channel, channels of an item, items of a row
+    __device__ __forceinline__ explicit HighItems(int r) {
+        lanes = r <= 8 ? 1 : 1 << (32 - __clz(r / 8 - 1));
+        channels = min(128, 256 / lanes);
+        per_row = 128 / channels;
+    }
+};
+__device__ __forceinline__ void high_item(const Params& p, const HighItems& h, int t, int a, int chan0, int item, float* out) {
+    const int lane = threadIdx.x & 31, part = lane & (h.lanes - 1), first = item * h.channels + lane / h.lanes;
+    const int step = 32 / h.lanes;
+    const bool has = part < p.r / 8;
+    float4 v0 = make_float4(0, 0, 0, 0), v1 = v0;
+    if (has) {
+        const float4* v = reinterpret_cast<const float4*>(p.V + static_cast<int64_t>(t) * p.r + part * 8);
+        v0 = v[0];
+        v1 = v[1];
+    }
+    const __nv_bfloat16* b = p.high + static_cast<int64_t>(a) * p.N * p.r + part * 8;
+    uint4 w[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const int i = first + k * step, ch = chan0 + (p.gated ? i & 63 : i), n = p.gated && i >= 64 ? p.N / 2 + ch : ch;
+        w[k] = has && k * step < h.channels && ch < p.wide ? __ldg(reinterpret_cast<const uint4*>(b + static_cast<int64_t>(n) * p.r))
+                                                           : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        if (k * step >= h.channels) break;
+        float s0 = 0.0f, s1 = 0.0f;
+        fma8(s0, s1, w[k], v0, v1);
+        float s = s0 + s1;
+        for (int o = 1; o < h.lanes; o <<= 1) s += __shfl_xor_sync(kAllLanes, s, o);
+        if (part == 0) out[first + k * step] = s;
+    }
+}
+
+// The sum of a parked tile's value over the CTAs of its cluster, in their order, for COLS rows of the tile
+// (cols[i] < 0: none): every load is on its way before the first sum.
+template <int COLS>
+__device__ __forceinline__ void gather_parts(uint32_t parked, int split, const int (&cols)[COLS], int i, float (&y)[COLS]) {
+    float v[COLS][Few::MOST_SPLIT];
+#pragma unroll
+    for (int s = 0; s < Few::MOST_SPLIT; ++s) {
+        if (s >= split) break;
+        const uint32_t from = split > 1 ? mapa_shared(parked, s) : parked;
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) v[c][s] = cols[c] >= 0 ? ld_shared_cluster_f32(from + (cols[c] * 128 + i) * 4) : 0.0f;
+    }
+#pragma unroll
+    for (int s = 0; s < Few::MOST_SPLIT; ++s) {
+        if (s >= split) break;
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) y[c] = s == 0 ? v[c][0] : y[c] + v[c][s];
+    }
 }
 
 __global__ void __launch_bounds__(Few::THREADS, 1)
@@ -174,21 +223,16 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
         __syncwarp();
     } else {
         // ---------------------------------------------------------------- adapters, then this CTA's part of the sum
-        const int tid = threadIdx.x - 32 * Few::EPI_WARP0;
-        const int out = p.gated ? 64 : 128, oc = tid & (out - 1), step = Few::EPI_THREADS / out;
-        const bool live = chan0 + oc < p.wide;
         if (!p.wait_first) grid_dependency_wait();              // V, and nothing of D before the stream allows it
-        for (int q = tid / out; q < own; q += step) {
-            const int c = rank + split * q;
-            if (c >= rows) break;
-            const int a = adapter_of(p, row0 + c);
-            float y = 0.0f, up = 0.0f;
-            if (a >= 0 && live) {
-                y = high_dot(p, row0 + c, a, chan0 + oc);
-                if (p.gated) up = high_dot(p, row0 + c, a, p.N / 2 + chan0 + oc);
+        if (p.L > 0) {
+            const HighItems h(p.r);
+            for (int item = warp - Few::EPI_WARP0; item < own * h.per_row; item += Few::EPI_WARPS) {
+                const int q = item / h.per_row, c = rank + split * q;
+                if (c >= rows) break;
+                const int a = adapter_of(p, row0 + c), part = item % h.per_row;
+                if (a >= 0) high_item(p, h, row0 + c, a, chan0, part, delta + q * 128);
+                else for (int i = lane; i < h.channels; i += 32) delta[q * 128 + part * h.channels + i] = 0.0f;
             }
-            delta[q * 128 + oc] = y;
-            if (p.gated) delta[q * 128 + 64 + oc] = up;
         }
         if (p.kstages > 0) {
             const bool ok = mbar_wait_warp(acc_full, 0, abort_flag, p.wait_ns);
@@ -216,26 +260,43 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
         const int out = p.gated ? 64 : 128, oc = tid & (out - 1), step = Few::EPI_THREADS / out;
         const int ch = chan0 + oc;
         if (ch < p.wide) {
+            constexpr int COLS = 2;
             const float bias = p.bias ? __ldg(p.bias + ch) : 0.0f, bias_up = p.bias && p.gated ? __ldg(p.bias + p.N / 2 + ch) : 0.0f;
             const uint32_t parked = smem_u32(park);
-            for (int q = tid / out; q < own; q += step) {
-                const int c = rank + split * q;
-                if (c >= rows) break;
-                float y = 0.0f, up = 0.0f;
-                if (p.kstages > 0) {
-                    for (int s = 0; s < split; ++s) {
-                        const uint32_t at = split > 1 ? mapa_shared(parked, s) : parked;
-                        if (split > 1) y += ld_shared_cluster_f32(at + (c * 128 + oc) * 4);
-                        else y += park[c * 128 + oc];
-                        if (p.gated) up += split > 1 ? ld_shared_cluster_f32(at + (c * 128 + 64 + oc) * 4) : park[c * 128 + 64 + oc];
+            for (int q0 = tid / out; q0 < own; q0 += COLS * step) {
+                int cols[COLS];
+                float y[COLS], up[COLS], c_in[COLS];
+#pragma unroll
+                for (int k = 0; k < COLS; ++k) {
+                    const int q = q0 + k * step, c = rank + split * q;
+                    cols[k] = q < own && c < rows ? c : -1;
+                    y[k] = up[k] = c_in[k] = 0.0f;
+                    if (p.C && cols[k] >= 0) {
+                        const int64_t o = static_cast<int64_t>(row0 + c) * p.wide + ch;
+                        c_in[k] = p.c_f32 ? static_cast<const float*>(p.C)[o] : __bfloat162float(static_cast<const __nv_bfloat16*>(p.C)[o]);
                     }
                 }
-                const int64_t o = static_cast<int64_t>(row0 + c) * p.wide + ch;
-                if (p.C) y += p.c_f32 ? static_cast<const float*>(p.C)[o] : __bfloat162float(static_cast<const __nv_bfloat16*>(p.C)[o]);
-                y += delta[q * 128 + oc] + bias;
-                y = p.gated ? experts::silu(y) * (up + delta[q * 128 + 64 + oc] + bias_up) : activate(y, p.act);
-                if (p.d_f32) static_cast<float*>(p.D)[o] = y;
-                else static_cast<__nv_bfloat16*>(p.D)[o] = __float2bfloat16_rn(y);
+                if (p.kstages > 0) {
+                    gather_parts(parked, split, cols, oc, y);
+                    if (p.gated) gather_parts(parked, split, cols, 64 + oc, up);
+                }
+#pragma unroll
+                for (int k = 0; k < COLS; ++k) {
+                    if (cols[k] < 0) continue;
+                    const int q = q0 + k * step;
+                    float v = y[k] + c_in[k] + bias;
+                    if (p.L > 0) v += delta[q * 128 + oc];
+                    if (p.gated) {
+                        float u = up[k] + bias_up;
+                        if (p.L > 0) u += delta[q * 128 + 64 + oc];
+                        v = experts::silu(v) * u;
+                    } else {
+                        v = activate(v, p.act);
+                    }
+                    const int64_t o = static_cast<int64_t>(row0 + cols[k]) * p.wide + ch;
+                    if (p.d_f32) static_cast<float*>(p.D)[o] = v;
+                    else static_cast<__nv_bfloat16*>(p.D)[o] = __float2bfloat16_rn(v);
+                }
             }
         }
     }

@@ -116,6 +116,19 @@ __device__ __forceinline__ bool mma_epilogue(const Params& p, const MmaTile& t, 
         if (lane == 0) released();
     };
     if (part >= chunks) hand_back();
+    // C in BF16 with rows of even length is read as it is stored, two channels of one row a lane (store_columns), a
+    // chunk ahead
+    const bool c_pairs = p.C && !p.c_f32 && (p.wide & 1) == 0;
+    const int odd = lane & 1;
+    uint32_t c_next[16];
+    auto load_c = [&](int c) {
+        const int col0 = (c * 2 + part) * 32, valid = t.rows - col0;
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.C) + static_cast<int64_t>(t.row0 + col0 + odd) * p.wide + ch - odd;
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            c_next[j] = live && 2 * j + odd < valid ? *reinterpret_cast<const uint32_t*>(src + static_cast<int64_t>(2 * j) * p.wide) : 0;
+    };
+    if (c_pairs && part < chunks) load_c(0);
 #pragma unroll 1
     for (int c = 0; c * 2 + part < chunks; ++c) {
         const int col0 = (c * 2 + part) * 32;
@@ -156,13 +169,26 @@ __device__ __forceinline__ bool mma_epilogue(const Params& p, const MmaTile& t, 
             const int skip = up ? 16 : 0;
             experts::store_columns<16>(p, at + static_cast<int64_t>(skip) * p.wide, y, live, valid - skip);
         } else {
-            if (p.C && live) {
+            if (c_pairs) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const uint32_t other = __shfl_xor_sync(kAllLanes, c_next[j], 1);
+                    const uint32_t both = odd ? __byte_perm(other, c_next[j], 0x7632u) : __byte_perm(c_next[j], other, 0x5410u);
+                    v[2 * j] += bf16_lo(both);
+                    v[2 * j + 1] += bf16_hi(both);
+                }
+                if ((c + 1) * 2 + part < chunks) load_c(c + 1);
+            } else if (p.C) {
+                float more[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
-                    if (j >= valid) continue;
                     const int64_t o = at + static_cast<int64_t>(j) * p.wide;
-                    v[j] += p.c_f32 ? static_cast<const float*>(p.C)[o] : __bfloat162float(static_cast<const __nv_bfloat16*>(p.C)[o]);
+                    const bool there = live && j < valid;
+                    if (p.c_f32) more[j] = there ? static_cast<const float*>(p.C)[o] : 0.0f;
+                    else more[j] = there ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.C)[o]) : 0.0f;
                 }
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] += more[j];
             }
             experts::activate32(v, p.act);
             experts::store_columns<32>(p, at, v, live, valid);
@@ -425,7 +451,8 @@ __global__ void __launch_bounds__(Mma::THREADS, 1)
         __syncwarp();
     } else if (warp >= Mma::V_WARP0) {
         // ---------------------------------------------------------------- masked rows of V
-        // A thread has one token row of this CTA. It loads the row's numbers before the stage is free.
+        // A thread has one token row of this CTA, whose numbers it loads ahead (a row has one adapter: up to
+        // rank 64 once for the tile).
         const int row = threadIdx.x - 32 * Mma::V_WARP0;
         uint32_t stage = 0, v_phase = 0;
         int64_t done = 0;                        // stages before the tile
@@ -437,21 +464,25 @@ __global__ void __launch_bounds__(Mma::THREADS, 1)
             const int half = t.n / 2, at = static_cast<int>(rank) * half + row;
             const int own = row < half && at < t.rows && p.L > 0 ? adapter_of(p, t.row0 + at) : -1;
             const uint4* src = reinterpret_cast<const uint4*>(v_split(p, t.row0 + at));
+            uint4 v[2][8];
+            auto load = [&](int i, int vecs) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    v[0][c] = v[1][c] = make_uint4(0, 0, 0, 0);
+                    if (own >= 0 && c < vecs) {
+                        v[0][c] = __ldcg(src + i * 8 + c);
+                        v[1][c] = __ldcg(src + p.r / 8 + i * 8 + c);
+                    }
+                }
+            };
+            if (chunks_r == 1) load(0, p.r / 8);
             ta.open(p, t.tt);
             done += p.kstages;
             for (int a = ta.next(p); ok && a >= 0; a = ta.next(p)) {
                 for (int i = 0; i < chunks_r; ++i, ++done) {
                     const int vecs = min(Mma::SL, p.r - i * Mma::SL) / 8, steps = (vecs + 1) / 2;
                     stage = static_cast<uint32_t>(done % S);
-                    uint4 v[2][8];
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        v[0][c] = v[1][c] = make_uint4(0, 0, 0, 0);
-                        if (own == a && c < vecs) {
-                            v[0][c] = __ldcg(src + i * 8 + c);
-                            v[1][c] = __ldcg(src + p.r / 8 + i * 8 + c);
-                        }
-                    }
+                    if (chunks_r > 1) load(i, vecs);
                     ok = mbar_wait_warp(&v_go[stage], (v_phase >> stage) & 1, abort_flag, p.wait_ns);
                     if (!ok) break;
                     v_phase ^= 1u << stage;
@@ -460,8 +491,9 @@ __global__ void __launch_bounds__(Mma::THREADS, 1)
 #pragma unroll
                         for (int c = 0; c < 8; ++c) {
                             if (c < 2 * steps) {
-                                *reinterpret_cast<uint4*>(x + ((c ^ (row & 7)) << 4)) = v[0][c];
-                                *reinterpret_cast<uint4*>(x + slice_x + ((c ^ (row & 7)) << 4)) = v[1][c];
+                                const uint4 none = make_uint4(0, 0, 0, 0);
+                                *reinterpret_cast<uint4*>(x + ((c ^ (row & 7)) << 4)) = own == a ? v[0][c] : none;
+                                *reinterpret_cast<uint4*>(x + slice_x + ((c ^ (row & 7)) << 4)) = own == a ? v[1][c] : none;
                             }
                         }
                     }

@@ -7,7 +7,7 @@ namespace dg {
 namespace adapters {
 
 // A CTA computes RB numbers of one row: its threads share K, partial sums meet in shared memory.
-constexpr int SHRINK_THREADS = 128;
+constexpr int SHRINK_THREADS = 256;
 
 template <int RB>
 __global__ void __launch_bounds__(SHRINK_THREADS) adapter_shrink_few(const __grid_constant__ Params p) {

@@ -65,11 +65,15 @@ bool allow_shared(std::atomic<unsigned char>* ready, int device, const void* fun
     return true;
 }
 
-// V of few rows: a CTA for every four numbers.
-dgemm_status_t launch_shrink_few(const Params& p, cudaStream_t s) {
-    constexpr int RB = 4;
+// V of few rows: a CTA for some of a row's numbers.
+template <int RB>
+cudaError_t shrink_few(const Params& p, cudaStream_t s) {
     dg::host::Launch l(static_cast<unsigned>(p.T) * (p.r / RB), 1, dg::adapters::SHRINK_THREADS, 0, s);
-    return cudaLaunchKernelEx(&l.cfg, dg::adapters::adapter_shrink_few<RB>, p) == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
+    return cudaLaunchKernelEx(&l.cfg, dg::adapters::adapter_shrink_few<RB>, p);
+}
+dgemm_status_t launch_shrink_few(const Params& p, cudaStream_t s) {
+    return (static_cast<int64_t>(p.T) * p.r <= 1024 ? shrink_few<2>(p, s) : shrink_few<4>(p, s)) == cudaSuccess ? DGEMM_OK
+                                                                                                          : DGEMM_ERR_CUDA;
 }
 
 dgemm_status_t launch_shrink_many(const Call& c, Params p, const dg::host::Device& dev) {
@@ -115,15 +119,17 @@ bool product_maps(const Call& c, const Params& p, CUtensorMap* w, CUtensorMap* x
 
 dgemm_status_t launch_few(const Call& c, Params& p, const dg::host::Device& dev) {
     constexpr int kHalf = 113 * 1024;             // two CTAs an SM
-    const int fewest = (p.T + Few::MOST_COLS - 1) / Few::MOST_COLS;
+    const int most = p.kstages > 0 ? Few::MOST_COLS : 16;       // (beside another product: nothing to share, more CTAs)
+    const int fewest = (p.T + most - 1) / most;
     p.width = ((p.T + fewest - 1) / fewest + 15) / 16 * 16;
     p.tiles = (p.T + p.width - 1) / p.width;
     const int ctiles = (p.wide + (p.gated ? 64 : 128) - 1) / (p.gated ? 64 : 128);
     const int64_t tiles = static_cast<int64_t>(p.tiles) * ctiles;
     if (tiles > INT32_MAX / Few::MOST_SPLIT) return DGEMM_ERR_NOT_SUPPORTED;
     p.split = 1;
-    while (p.split < Few::MOST_SPLIT && tiles * p.split * 2 <= 2 * dev.num_sms && p.kstages >= 4 * p.split) p.split *= 2;
-    const int shared = Few::smem_bytes(p.width, 3, p.split) <= kHalf ? kHalf : kShared;
+    const bool half = Few::smem_bytes(p.width, 3, 1) <= kHalf;
+    const int shared = half ? kHalf : kShared, slots = (half ? 2 : 1) * dev.num_sms;
+    while (p.split < Few::MOST_SPLIT && tiles * p.split * 2 <= slots && p.kstages >= 4 * p.split) p.split *= 2;
     p.stages = p.kstages > 0 ? 2 : 0;
     while (p.stages > 0 && p.stages < Few::MOST_STAGES && Few::smem_bytes(p.width, p.stages + 1, p.split) <= shared) ++p.stages;
     const int smem = Few::smem_bytes(p.width, p.stages, p.split);
