@@ -32,6 +32,7 @@ struct Params : experts::Params {      // (of those: C, D, bias, N, K, wide, gat
     int shrink_tiles, shrink_cols;     // token tiles of the launch that computes V, its columns of a pass
     int split;                         // CTAs of a cluster that share a tile's K
     int stages;                        // of the ring
+    int ahead;                         // few-row form: items of B that a warp copies ahead
     int wait_first;                    // no launch of this call precedes: wait for the stream before reading anything
 };
 

@@ -1,13 +1,16 @@
 // adapter_few.cuh -- the projection with adapters for tiles of up to 64 rows.
 //
 // The output channels are the MMA's 128 rows, the token rows its columns. A cluster of
-// `split` CTAs shares a tile's K: each sums its part in Tensor Memory, parks it in its shared
-// memory, and finishes every split-th row of the tile from all parts in their order.
-// V . B_a^T runs on the FP32 units meanwhile, row by row: every row reads the adapter of its own, and
-// rows may be of as many requests as there are. It needs V, the rest does not: only these
-// warps wait for the launch that computes it.
+// `split` CTAs shares a tile's K: each sums its part in Tensor Memory and writes every split-th row of it
+// to the shared memory of the CTA that finishes those rows, from all parts in their order.
+// V . B_a^T runs on the FP32 units meanwhile, row by row: every row has the adapter of its own, and
+// rows may be of as many requests as there are. The items are some channels of one row, a run
+// of B_a that a bulk copy brings to shared memory; every warp copies its own items, some ahead. It needs
+// V, the rest does not: only these warps wait for the launch that computes it.
 // Warps: 0 TMA producer, 1 MMA issuer and owner of the Tensor Memory, 2-9 epilogue.
 #pragma once
+
+#include <type_traits>
 
 #include "adapter_common.cuh"
 
@@ -19,98 +22,133 @@ struct Few {
     static constexpr int MOST_COLS = 64, MOST_STAGES = 8, MOST_SPLIT = 8;
     static constexpr int SLICE_W = 128 * 128, W_BYTES = KS * SLICE_W;
     static constexpr int EPI_WARP0 = 2, EPI_WARPS = 8, EPI_THREADS = 32 * EPI_WARPS, THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
-    static constexpr int TMEM_COLS = 64, BAR_BYTES = 256;
+    static constexpr int MOST_AHEAD = 4, TMEM_COLS = 64, BAR_BYTES = 512;
+    // channels of an item: at most 4 KB of B
+    static __host__ __device__ constexpr int item_channels(int r) { return r <= 32 ? 64 : r <= 64 ? 32 : 16; }
     static constexpr uint32_t IDESC0 = make_idesc(1u, false, false, 128, 0);
     static constexpr int stage_bytes(int cols) { return W_BYTES + KS * cols * 128; }
-    static constexpr int smem_bytes(int cols, int stages, int split) {
-        return 1024 + stages * stage_bytes(cols) + (cols + split - 1) / split * 512 + BAR_BYTES;
+    // the ring; rows that a CTA finishes: 128 results and V; items ahead
+    static constexpr int smem_bytes(int cols, int stages, int split, int r, int ahead) {
+        return 1024 + stages * stage_bytes(cols) + (cols + split - 1) / split * (512 + r * 4) +
+               EPI_WARPS * ahead * item_channels(r) * r * 2 + BAR_BYTES;
     }
-    static_assert((2 * MOST_STAGES + 2) * 8 + 8 <= BAR_BYTES, "barriers fit");
-    // (a parked tile, 64 columns of 128 floats, is never larger than two stages)
+    static_assert((2 * MOST_STAGES + EPI_WARPS * MOST_AHEAD + 2) * 8 + 8 <= BAR_BYTES, "barriers fit");
+    // (the parts of a CTA's rows, up to 71 x 128 floats, are never more than two stages hold)
 };
 
-__device__ __forceinline__ float activate(float v, int act) {
-    switch (act) {
-        case DGEMM_ACT_RELU: return experts::relu(v);
-        case DGEMM_ACT_GELU: return experts::gelu(v);
-        case DGEMM_ACT_SILU: return experts::silu(v);
-        default: return v;
+template <int ACT>
+__device__ __forceinline__ float activate(float v) {
+    if constexpr (ACT == DGEMM_ACT_RELU) return experts::relu(v);
+    else if constexpr (ACT == DGEMM_ACT_GELU) return experts::gelu(v);
+    else if constexpr (ACT == DGEMM_ACT_SILU) return experts::silu(v);
+    else return v;
+}
+
+// The rows of a tile that a CTA finishes, one channel of D a thread: parts of the product in their order, C and
+// adapter, bias, activation, one rounding. (A copy for every activation: with the choice inside, every
+// one of them was computed for every value, 0.4 us a row.)
+template <int ACT>
+__device__ __forceinline__ void finish_rows(const Params& p, const float* parts, const float* beside, int own, int rank, int row0,
+                                            int rows, int chan0, int tid) {
+    constexpr bool GATED = ACT == DGEMM_ACT_SWIGLU;
+    constexpr int OUT = GATED ? 64 : 128, STEP = Few::EPI_THREADS / OUT;
+    const int oc = tid % OUT, ch = chan0 + oc;
+    if (ch >= p.wide) return;
+    const float bias = p.bias ? __ldg(p.bias + ch) : 0.0f, bias_up = GATED && p.bias ? __ldg(p.bias + p.N / 2 + ch) : 0.0f;
+    const int split = p.kstages > 0 ? p.split : 0;
+#pragma unroll 2
+    for (int q = tid / OUT; q < own; q += STEP) {
+        const int c = rank + p.split * q;
+        if (c >= rows) break;
+        float v = beside[q * 128 + oc] + bias, u = 0.0f;
+        if (GATED) u = beside[q * 128 + 64 + oc] + bias_up;
+        const float* from = parts + q * 128 + oc;
+        float product = 0.0f, product_up = 0.0f;
+        for (int s = 0; s < split; ++s, from += own * 128) {
+            product += from[0];
+            if (GATED) product_up += from[64];
+        }
+        v += product;
+        v = GATED ? experts::silu(v) * (u + product_up) : activate<ACT>(v);
+        const int64_t o = static_cast<int64_t>(row0 + c) * p.wide + ch;
+        if (p.d_f32) static_cast<float*>(p.D)[o] = v;
+        else static_cast<__nv_bfloat16*>(p.D)[o] = __float2bfloat16_rn(v);
     }
 }
 
-// V[t] . B_a^T for one row t of the tile and some of its 128 channels, by one warp: r / 8 lanes (rounded up to
-// a power of two) share a channel, so that a load of the warp is one run of memory, eight loads in
-// flight. `out`: the row's [128] results.
-struct HighItems {
-    int lanes, channels, per_row;       // lanes of a channel, channels of an item, items of a row
-    __device__ __forceinline__ explicit HighItems(int r) {
-        lanes = r <= 8 ? 1 : 1 << (32 - __clz(r / 8 - 1));
-        channels = min(128, 256 / lanes);
-        per_row = 128 / channels;
-    }
-};
-__device__ __forceinline__ void high_item(const Params& p, const HighItems& h, int t, int a, int chan0, int item, float* out) {
-    const int lane = threadIdx.x & 31, part = lane & (h.lanes - 1), first = item * h.channels + lane / h.lanes;
-    const int step = 32 / h.lanes;
-    const bool has = part < p.r / 8;
+// V . B_a^T of one row for CHANNELS of its channels, by one warp. L = 2^LG lanes share a channel (r / 8, rounded up to
+// a power of two); the sums over them are taken for several loads at a time, each lane ending with one
+// channel's (L - 1 shuffles for L channels, not L LG).
+// b, v: the item's B [CHANNELS][r] and V [r] in shared memory; the results are added to out.
+template <int LG>
+__device__ __forceinline__ void high_item(const __nv_bfloat16* b, const float* v, int r, float* out) {
+    constexpr int L = 1 << LG, STEP = 32 >> LG, CHANNELS = LG <= 2 ? 64 : LG == 3 ? 32 : 16;
+    constexpr int LOADS = CHANNELS / STEP, G = LOADS < L ? LOADS : L;       // of the item, of a group of sums
+    const int lane = threadIdx.x & 31, part = lane & (L - 1);
+    const bool has = part < r / 8;
     float4 v0 = make_float4(0, 0, 0, 0), v1 = v0;
     if (has) {
-        const float4* v = reinterpret_cast<const float4*>(p.V + static_cast<int64_t>(t) * p.r + part * 8);
-        v0 = v[0];
-        v1 = v[1];
+        v0 = reinterpret_cast<const float4*>(v)[2 * part];
+        v1 = reinterpret_cast<const float4*>(v)[2 * part + 1];
     }
-    const __nv_bfloat16* b = p.high + static_cast<int64_t>(a) * p.N * p.r + part * 8;
-    uint4 w[8];
+    const uint4* from = reinterpret_cast<const uint4*>(b + (lane >> LG) * r) + (has ? part : 0);
+    const int pitch = STEP * (r / 8);
+    float s[LOADS];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const int i = first + k * step, ch = chan0 + (p.gated ? i & 63 : i), n = p.gated && i >= 64 ? p.N / 2 + ch : ch;
-        w[k] = has && k * step < h.channels && ch < p.wide ? __ldg(reinterpret_cast<const uint4*>(b + static_cast<int64_t>(n) * p.r))
-                                                           : make_uint4(0, 0, 0, 0);
+    for (int k = 0; k < LOADS; ++k) {
+        const uint4 w = from[k * pitch];
+        float a0 = v0.x * bf16_lo(w.x), a1 = v0.y * bf16_hi(w.x);
+        ffma2(a0, a1, bf16_lo(w.y), bf16_hi(w.y), v0.z, v0.w);
+        ffma2(a0, a1, bf16_lo(w.z), bf16_hi(w.z), v1.x, v1.y);
+        ffma2(a0, a1, bf16_lo(w.w), bf16_hi(w.w), v1.z, v1.w);
+        s[k] = has ? a0 + a1 : 0.0f;            // (a lane without a part reads another's, whatever it holds)
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        if (k * step >= h.channels) break;
-        float s0 = 0.0f, s1 = 0.0f;
-        fma8(s0, s1, w[k], v0, v1);
-        float s = s0 + s1;
-        for (int o = 1; o < h.lanes; o <<= 1) s += __shfl_xor_sync(kAllLanes, s, o);
-        if (part == 0) out[first + k * step] = s;
+    for (int g = 0; g < LOADS; g += G) {
+#pragma unroll
+        for (int o = G / 2; o > 0; o >>= 1)
+#pragma unroll
+            for (int k = 0; k < o; ++k) {
+                const bool upper = part & o;
+                const float keep = upper ? s[g + k + o] : s[g + k], send = upper ? s[g + k] : s[g + k + o];
+                s[g + k] = keep + __shfl_xor_sync(kAllLanes, send, o);
+            }
+#pragma unroll
+        for (int o = G; o < L; o <<= 1) s[g] += __shfl_xor_sync(kAllLanes, s[g], o);
+        if (part < G) out[(g + part) * STEP + (lane >> LG)] += s[g];
+    }
+}
+__device__ __forceinline__ void high_item(int lg, const __nv_bfloat16* b, const float* v, int r, float* out) {
+    switch (lg) {
+        case 0: high_item<0>(b, v, r, out); break;
+        case 1: high_item<1>(b, v, r, out); break;
+        case 2: high_item<2>(b, v, r, out); break;
+        case 3: high_item<3>(b, v, r, out); break;
+        default: high_item<4>(b, v, r, out); break;
     }
 }
 
-// The sum of a parked tile's value over the CTAs of its cluster, in their order, for COLS rows of the tile
-// (cols[i] < 0: none): every load is on its way before the first sum.
-template <int COLS>
-__device__ __forceinline__ void gather_parts(uint32_t parked, int split, const int (&cols)[COLS], int i, float (&y)[COLS]) {
-    float v[COLS][Few::MOST_SPLIT];
-#pragma unroll
-    for (int s = 0; s < Few::MOST_SPLIT; ++s) {
-        if (s >= split) break;
-        const uint32_t from = split > 1 ? mapa_shared(parked, s) : parked;
-#pragma unroll
-        for (int c = 0; c < COLS; ++c) v[c][s] = cols[c] >= 0 ? ld_shared_cluster_f32(from + (cols[c] * 128 + i) * 4) : 0.0f;
-    }
-#pragma unroll
-    for (int s = 0; s < Few::MOST_SPLIT; ++s) {
-        if (s >= split) break;
-#pragma unroll
-        for (int c = 0; c < COLS; ++c) y[c] = s == 0 ? v[c][0] : y[c] + v[c][s];
-    }
+__device__ __forceinline__ void st_shared_cluster_f32(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-__global__ void __launch_bounds__(Few::THREADS, 1)
+__global__ void __launch_bounds__(Few::THREADS, 2)
     adapter_few(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                 const __grid_constant__ Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int S = p.stages, cols = p.width, split = p.split;
+    const int S = p.stages, cols = p.width, split = p.split, lg_split = 31 - __clz(split);
     const int slice_x = cols * 128, stage_bytes = Few::W_BYTES + Few::KS * slice_x;
     const int own = (cols + split - 1) / split;                 // rows of the tile that a CTA finishes, at most
-    float* park = reinterpret_cast<float*>(ring);               // [cols][128], once the ring has been read
-    float* delta = reinterpret_cast<float*>(ring + S * stage_bytes);           // [own][128]
-    uint64_t* full = reinterpret_cast<uint64_t*>(delta + own * 128);
+    float* parts = reinterpret_cast<float*>(ring);              // [split][own][128], once the cluster's rings have been read
+    float* beside = reinterpret_cast<float*>(ring + S * stage_bytes);          // [own][128]: C, then C + V . B_a^T
+    float* v_rows = beside + own * 128;                                         // [own][r]
+    const int channels = Few::item_channels(p.r);
+    __nv_bfloat16* slots = reinterpret_cast<__nv_bfloat16*>(v_rows + own * p.r);   // [warps][ahead][channels][r]
+    uint64_t* full = reinterpret_cast<uint64_t*>(slots + Few::EPI_WARPS * p.ahead * channels * p.r);
     uint64_t* empty = full + S;
-    uint64_t* acc_full = empty + S;
+    uint64_t* b_full = empty + S;
+    uint64_t* acc_full = b_full + Few::EPI_WARPS * p.ahead;
     uint64_t* drain = acc_full + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -122,15 +160,12 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
     const int kb0 = static_cast<int>(static_cast<int64_t>(p.kstages) * rank / split);
     const int kb1 = static_cast<int>(static_cast<int64_t>(p.kstages) * (rank + 1) / split);
 
+    // (a thread for each barrier: one after another they took 0.4 us)
+    const int bars = 2 * S + Few::EPI_WARPS * p.ahead + 2;
+    for (int b = threadIdx.x; b < bars; b += Few::THREADS) mbar_init(full + b, 1);
+    if (threadIdx.x < static_cast<unsigned>(bars)) fence_mbarrier_init();
     if (threadIdx.x == 0) {
-        for (int s = 0; s < S; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
-        }
-        mbar_init(acc_full, 1);
-        mbar_init(drain, 1);
         *abort_flag = 0;
-        fence_mbarrier_init();
         if (p.kstages > 0) {
             tma_prefetch_desc(&tmW);
             tma_prefetch_desc(&tmX);
@@ -146,7 +181,7 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
     tc_fence_after();
     if (threadIdx.x == 0) grid_launch_dependents();
     const uint32_t tmem = p.kstages > 0 ? *tmem_slot : 0;
-
+    bool summed = false;                                        // an epilogue warp: the accumulator is there
     if (warp == 0) {
         // ---------------------------------------------------------------- TMA producer
         const uint64_t pol = policy_evict_first(), pol_x = policy_evict_last();
@@ -223,86 +258,117 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
         __syncwarp();
     } else {
         // ---------------------------------------------------------------- adapters, then this CTA's part of the sum
+        const int ew = warp - Few::EPI_WARP0;
+        const int mine = p.L > 0 && rows > rank ? (rows - rank + split - 1) / split : 0;    // rows that this CTA finishes
+        const int lg_items = channels == 64 ? 1 : channels == 32 ? 2 : 3, items = mine << lg_items;
+        int of_row[2] = {-1, -1};                               // lanes: their adapters, -1 for none
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (lane + 32 * k < mine) of_row[k] = adapter_of(p, row0 + rank + split * (lane + 32 * k));
+        auto adapter = [&](int q) { return __shfl_sync(kAllLanes, q < 32 ? of_row[0] : of_row[1], q & 31); };
+        // An item's copy: the channels that there are (D's channels beyond the last have none).
+        __nv_bfloat16* my_slots = slots + ew * p.ahead * channels * p.r;
+        uint64_t* my_full = b_full + ew * p.ahead;
+        auto there = [&](int item) {
+            const int i0 = (item & ((1 << lg_items) - 1)) * channels;
+            return min(channels, p.wide - chan0 - (p.gated ? i0 & 63 : i0));
+        };
+        uint32_t pending = 0;                                   // bit s: a copy to slot s is on its way
+        auto copy = [&](int item, int slot) {
+            if (item >= items) return;
+            const int a = adapter(item >> lg_items), n = there(item);
+            if (a < 0 || n <= 0) return;
+            pending |= 1u << slot;
+            if (elect_one()) {
+                const int i0 = (item & ((1 << lg_items) - 1)) * channels;
+                const int ch = p.gated && i0 >= 64 ? p.N / 2 + chan0 + i0 - 64 : chan0 + i0;
+                mbar_arrive_expect_tx(&my_full[slot], n * p.r * 2);
+                bulk_load_1d(my_slots + slot * channels * p.r, p.high + (static_cast<int64_t>(a) * p.N + ch) * p.r, n * p.r * 2,
+                             &my_full[slot]);
+            }
+            __syncwarp();
+        };
+        for (int k = 0; k < p.ahead; ++k) copy(ew + k * Few::EPI_WARPS, k);
         if (!p.wait_first) grid_dependency_wait();              // V, and nothing of D before the stream allows it
-        if (p.L > 0) {
-            const HighItems h(p.r);
-            for (int item = warp - Few::EPI_WARP0; item < own * h.per_row; item += Few::EPI_WARPS) {
-                const int q = item / h.per_row, c = rank + split * q;
-                if (c >= rows) break;
-                const int a = adapter_of(p, row0 + c), part = item % h.per_row;
-                if (a >= 0) high_item(p, h, row0 + c, a, chan0, part, delta + q * 128);
-                else for (int i = lane; i < h.channels; i += 32) delta[q * 128 + part * h.channels + i] = 0.0f;
+        // C as the first term of the rows' sums; V of the rows
+        for (int q = ew; q < own; q += Few::EPI_WARPS) {
+            const int c = rank + split * q;
+            float first[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int64_t o = static_cast<int64_t>(row0 + c) * p.wide + chan0 + lane + 32 * k;
+                first[k] = 0.0f;
+                if (p.C && c < rows && chan0 + lane + 32 * k < p.wide)
+                    first[k] = p.c_f32 ? static_cast<const float*>(p.C)[o] : __bfloat162float(static_cast<const __nv_bfloat16*>(p.C)[o]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) beside[q * 128 + lane + 32 * k] = first[k];
+        }
+        if (mine > 0) {
+            for (int q = ew; q < mine; q += Few::EPI_WARPS)
+                if (lane < p.r / 4)         // (rows without an adapter have no V; theirs is not used)
+                    reinterpret_cast<float4*>(v_rows + q * p.r)[lane] =
+                        __ldcg(reinterpret_cast<const float4*>(p.V + static_cast<int64_t>(row0 + rank + split * q) * p.r) + lane);
+            asm volatile("barrier.cta.sync 1, %0;" ::"n"(Few::EPI_THREADS) : "memory");
+            const int lg = p.r <= 8 ? 0 : 32 - __clz(p.r / 8 - 1);
+            int slot = 0;
+            uint32_t phases = 0;            // bit s: the next parity of my_full[s]
+            bool ok = true;
+            for (int item = ew; item < items; item += Few::EPI_WARPS) {
+                const int q = item >> lg_items;
+                float* out = beside + q * 128 + (item & ((1 << lg_items) - 1)) * channels;
+                if (adapter(q) >= 0 && there(item) > 0) {
+                    ok = mbar_wait_warp(&my_full[slot], (phases >> slot) & 1, abort_flag, p.wait_ns);
+                    if (!ok) break;
+                    pending &= ~(1u << slot);
+                    phases ^= 1u << slot;
+                    high_item(lg, my_slots + slot * channels * p.r, v_rows + q * p.r, p.r, out);
+                    __syncwarp();
+                }
+                copy(item + p.ahead * Few::EPI_WARPS, slot);
+                slot = slot + 1 == p.ahead ? 0 : slot + 1;
+            }
+            if (!ok) {
+                if (lane == 0) experts::fail(p, ERR_TIMEOUT_EPILOGUE, abort_flag);
+                for (int s = 0; s < p.ahead; ++s)               // no copy is in flight when the CTA leaves
+                    if ((pending >> s) & 1) mbar_wait_warp(&my_full[s], (phases >> s) & 1, nullptr, p.wait_ns);
             }
         }
         if (p.kstages > 0) {
-            const bool ok = mbar_wait_warp(acc_full, 0, abort_flag, p.wait_ns);
-            if (ok) {
-                tc_fence_after();
-                const int quarter = warp & 3, part = (warp - Few::EPI_WARP0) >> 2;
-                for (int c = part * 16; c < cols; c += 32) {
-                    uint32_t v[16];
-                    tmem_ld16(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + c, v);
-                    tmem_ld_wait();
+            summed = mbar_wait_warp(acc_full, 0, abort_flag, p.wait_ns);
+            if (!summed && lane == 0) experts::fail(p, ERR_TIMEOUT_EPILOGUE, abort_flag);
+        }
+    }
+    __syncwarp();
+    if (split > 1) cluster_sync();               // nobody reads a ring any more
+    if (summed) {
+        tc_fence_after();
+        const int quarter = warp & 3, i = quarter * 32 + lane;
+        const uint32_t mine = smem_u32(parts) + (rank * own * 128 + i) * 4;
+        for (int c = ((warp - Few::EPI_WARP0) >> 2) * 16; c < cols; c += 32) {
+            uint32_t v[16];
+            tmem_ld16(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + c, v);
+            tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) park[(c + j) * 128 + quarter * 32 + lane] = __uint_as_float(v[j]);
-                }
-                tc_fence_before();
-            } else if (lane == 0) {
-                experts::fail(p, ERR_TIMEOUT_EPILOGUE, abort_flag);
+            for (int j = 0; j < 16; ++j) {       // (a split divides 16)
+                const uint32_t to = (split > 1 ? mapa_shared(mine, j & (split - 1)) : mine) + ((c + j) >> lg_split) * 512;
+                st_shared_cluster_f32(to, __uint_as_float(v[j]));
             }
         }
+        tc_fence_before();
     }
     if (split > 1) cluster_sync();
     else __syncthreads();
     if (warp >= Few::EPI_WARP0 && !*abort_flag) {
         // ---------------------------------------------------------------- the rows that this CTA finishes
         const int tid = threadIdx.x - 32 * Few::EPI_WARP0;
-        const int out = p.gated ? 64 : 128, oc = tid & (out - 1), step = Few::EPI_THREADS / out;
-        const int ch = chan0 + oc;
-        if (ch < p.wide) {
-            constexpr int COLS = 2;
-            const float bias = p.bias ? __ldg(p.bias + ch) : 0.0f, bias_up = p.bias && p.gated ? __ldg(p.bias + p.N / 2 + ch) : 0.0f;
-            const uint32_t parked = smem_u32(park);
-            for (int q0 = tid / out; q0 < own; q0 += COLS * step) {
-                int cols[COLS];
-                float y[COLS], up[COLS], c_in[COLS];
-#pragma unroll
-                for (int k = 0; k < COLS; ++k) {
-                    const int q = q0 + k * step, c = rank + split * q;
-                    cols[k] = q < own && c < rows ? c : -1;
-                    y[k] = up[k] = c_in[k] = 0.0f;
-                    if (p.C && cols[k] >= 0) {
-                        const int64_t o = static_cast<int64_t>(row0 + c) * p.wide + ch;
-                        c_in[k] = p.c_f32 ? static_cast<const float*>(p.C)[o] : __bfloat162float(static_cast<const __nv_bfloat16*>(p.C)[o]);
-                    }
-                }
-                if (p.kstages > 0) {
-                    gather_parts(parked, split, cols, oc, y);
-                    if (p.gated) gather_parts(parked, split, cols, 64 + oc, up);
-                }
-#pragma unroll
-                for (int k = 0; k < COLS; ++k) {
-                    if (cols[k] < 0) continue;
-                    const int q = q0 + k * step;
-                    float v = y[k] + c_in[k] + bias;
-                    if (p.L > 0) v += delta[q * 128 + oc];
-                    if (p.gated) {
-                        float u = up[k] + bias_up;
-                        if (p.L > 0) u += delta[q * 128 + 64 + oc];
-                        v = experts::silu(v) * u;
-                    } else {
-                        v = activate(v, p.act);
-                    }
-                    const int64_t o = static_cast<int64_t>(row0 + cols[k]) * p.wide + ch;
-                    if (p.d_f32) static_cast<float*>(p.D)[o] = v;
-                    else static_cast<__nv_bfloat16*>(p.D)[o] = __float2bfloat16_rn(v);
-                }
-            }
-        }
+        auto finish = [&](auto act) { finish_rows<decltype(act)::value>(p, parts, beside, own, rank, row0, rows, chan0, tid); };
+        if (p.act == DGEMM_ACT_NONE) finish(std::integral_constant<int, DGEMM_ACT_NONE>());
+        else if (p.act == DGEMM_ACT_RELU) finish(std::integral_constant<int, DGEMM_ACT_RELU>());
+        else if (p.act == DGEMM_ACT_GELU) finish(std::integral_constant<int, DGEMM_ACT_GELU>());
+        else if (p.act == DGEMM_ACT_SILU) finish(std::integral_constant<int, DGEMM_ACT_SILU>());
+        else finish(std::integral_constant<int, DGEMM_ACT_SWIGLU>());
     }
-    tc_fence_before();
-    if (split > 1) cluster_sync();
-    else __syncthreads();
     if (warp == 1 && p.kstages > 0) {
         tc_fence_after();
         tmem_dealloc(tmem, Few::TMEM_COLS);

@@ -60,20 +60,26 @@ dgemm_status_t check_sizes(int64_t T, int64_t N, int64_t K, int64_t r, int64_t L
 // A kernel's limit of dynamic shared memory, set once per device.
 bool allow_shared(std::atomic<unsigned char>* ready, int device, const void* func, int bytes) {
     if (ready[device].load(std::memory_order_acquire)) return true;
-    if (cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    if (cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess ||
+        cudaFuncSetAttribute(func, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) != cudaSuccess)
+        return false;
     ready[device].store(1, std::memory_order_release);
     return true;
 }
 
 // V of few rows: a CTA for some of a row's numbers.
 template <int RB>
-cudaError_t shrink_few(const Params& p, cudaStream_t s) {
+cudaError_t shrink_few(const Params& p, const dg::host::Device& dev, cudaStream_t s) {
+    // The same split of an SM's memory as the kernel behind it: one of another split does not start on an SM
+    // before this one has left it.
+    static std::atomic<unsigned char> ready[dg::host::kMaxDevices];
+    if (!allow_shared(ready, dev.id, reinterpret_cast<const void*>(&dg::adapters::adapter_shrink_few<RB>), 0)) return cudaErrorUnknown;
     dg::host::Launch l(static_cast<unsigned>(p.T) * (p.r / RB), 1, dg::adapters::SHRINK_THREADS, 0, s);
     return cudaLaunchKernelEx(&l.cfg, dg::adapters::adapter_shrink_few<RB>, p);
 }
-dgemm_status_t launch_shrink_few(const Params& p, cudaStream_t s) {
-    return (static_cast<int64_t>(p.T) * p.r <= 1024 ? shrink_few<2>(p, s) : shrink_few<4>(p, s)) == cudaSuccess ? DGEMM_OK
-                                                                                                          : DGEMM_ERR_CUDA;
+dgemm_status_t launch_shrink_few(const Params& p, const dg::host::Device& dev, cudaStream_t s) {
+    const cudaError_t e = static_cast<int64_t>(p.T) * p.r <= 1024 ? shrink_few<2>(p, dev, s) : shrink_few<4>(p, dev, s);
+    return e == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
 }
 
 dgemm_status_t launch_shrink_many(const Call& c, Params p, const dg::host::Device& dev) {
@@ -118,7 +124,6 @@ bool product_maps(const Call& c, const Params& p, CUtensorMap* w, CUtensorMap* x
 }
 
 dgemm_status_t launch_few(const Call& c, Params& p, const dg::host::Device& dev) {
-    constexpr int kHalf = 113 * 1024;             // two CTAs an SM
     const int most = p.kstages > 0 ? Few::MOST_COLS : 16;       // (beside another product: nothing to share, more CTAs)
     const int fewest = (p.T + most - 1) / most;
     p.width = ((p.T + fewest - 1) / fewest + 15) / 16 * 16;
@@ -127,12 +132,16 @@ dgemm_status_t launch_few(const Call& c, Params& p, const dg::host::Device& dev)
     const int64_t tiles = static_cast<int64_t>(p.tiles) * ctiles;
     if (tiles > INT32_MAX / Few::MOST_SPLIT) return DGEMM_ERR_NOT_SUPPORTED;
     p.split = 1;
-    const bool half = Few::smem_bytes(p.width, 3, 1) <= kHalf;
-    const int shared = half ? kHalf : kShared, slots = (half ? 2 : 1) * dev.num_sms;
-    while (p.split < Few::MOST_SPLIT && tiles * p.split * 2 <= slots && p.kstages >= 4 * p.split) p.split *= 2;
+    p.split = 1;
+    while (p.split < Few::MOST_SPLIT && tiles * p.split * 2 <= dev.num_sms && p.kstages >= 4 * p.split) p.split *= 2;
+    // Items of B ahead: up to 64 KB of them (a CTA's share of the memory's time), 32 KB where many rows' token slices
+    // leave no more.
+    p.ahead = p.L > 0 ? std::min(Few::MOST_AHEAD, 64 * 1024 / (Few::EPI_WARPS * Few::item_channels(p.r) * p.r * 2)) : 0;
+    auto shared = [&](int stages) { return Few::smem_bytes(p.width, stages, p.split, p.r, p.ahead); };
     p.stages = p.kstages > 0 ? 2 : 0;
-    while (p.stages > 0 && p.stages < Few::MOST_STAGES && Few::smem_bytes(p.width, p.stages + 1, p.split) <= shared) ++p.stages;
-    const int smem = Few::smem_bytes(p.width, p.stages, p.split);
+    while (p.stages > 0 && p.stages < Few::MOST_STAGES && shared(p.stages + 1) <= kShared) ++p.stages;
+    const int smem = shared(p.stages);
+    if (smem > kShared) return DGEMM_ERR_NOT_SUPPORTED;
     alignas(64) CUtensorMap w, x;
     std::memset(&w, 0, sizeof w);
     std::memset(&x, 0, sizeof x);
@@ -235,7 +244,7 @@ dgemm_status_t run_adapters(const Call& c) {
     p.prompt = forced >= 0 ? forced : p.T > kMostFew;
     if (p.prompt) prompt_tiles(p, dev);
     if (p.L > 0) {
-        const dgemm_status_t s = p.prompt || p.T > kMostFewShrink ? launch_shrink_many(c, p, dev) : launch_shrink_few(p, c.stream);
+        const dgemm_status_t s = p.prompt || p.T > kMostFewShrink ? launch_shrink_many(c, p, dev) : launch_shrink_few(p, dev, c.stream);
         if (s != DGEMM_OK) return s;
     }
     return p.prompt ? launch_prompt(c, p, dev) : launch_few(c, p, dev);
