@@ -25,13 +25,13 @@ struct Params : experts::Params {      // (of those: C, D, bias, N, K, wide, gat
     const __nv_bfloat16* high;         // B [L][N][r]
     float* V;                          // [T][r] FP32, or for the prompt form [T][2][r] BF16: V = first + second
     int* lists;                        // prompt form: [tiles][kListPitch], the adapters of a token tile: how many, which
-    unsigned long long* bad;           // prompt form: [L], this call's epoch where B_a has a number that is not finite
     int T, L, r;
     int tiles, width;                  // token tiles and their rows
     int prompt;                        // the prompt form follows
     int shrink_tiles, shrink_cols;     // token tiles of the launch that computes V, its columns of a pass
     int split;                         // CTAs of a cluster that share a tile's K
     int stages;                        // of the ring
+    int channels;                      // few-row form: of D in a tile, a multiple of 8
     int ahead;                         // few-row form: items of B that a warp copies ahead
     int wait_first;                    // no launch of this call precedes: wait for the stream before reading anything
 };
@@ -66,6 +66,13 @@ __device__ __forceinline__ __nv_bfloat16* v_split(const Params& p, int t) {
     return reinterpret_cast<__nv_bfloat16*>(p.V) + static_cast<int64_t>(t) * 2 * p.r;
 }
 
+__device__ __forceinline__ bool not_finite(uint32_t pair) {
+    return (pair & 0x7F80u) == 0x7F80u || (pair & 0x7F800000u) == 0x7F800000u;
+}
+__device__ __forceinline__ bool not_finite(const uint4& v) {
+    return not_finite(v.x) || not_finite(v.y) || not_finite(v.z) || not_finite(v.w);
+}
+
 // Bits of the adapters in use among n rows, by `threads` threads that all pass; words: [128].
 __device__ __forceinline__ void mark_adapters(const Params& p, int first, int n, unsigned* words, int tid, int threads) {
     // (loads of a batch before its marks; most are marked already, and a look spares the atomic)
@@ -89,6 +96,38 @@ __device__ __forceinline__ int marked(const Params& p, const unsigned* words) {
     int all = 0;
     for (int w = 0; w < (p.L + 31) / 32; ++w) all += __popc(words[w]);
     return all;
+}
+
+// Writes the list of a token tile of the prompt form; words: [128] in shared memory; sync() for all of the threads.
+template <class Sync>
+__device__ __forceinline__ void list_tile(const Params& p, int tile, unsigned* words, int tid, int threads, Sync sync) {
+    const int row0 = tile * p.width, rows = min(p.width, p.T - row0);
+    for (int w = tid; w < DGEMM_MAX_ADAPTERS / 32; w += threads) words[w] = 0;
+    sync();
+    mark_adapters(p, row0, rows, words, tid, threads);
+    sync();
+    int* list = p.lists + static_cast<int64_t>(tile) * kListPitch;
+    for (int i = tid; i < rows; i += threads) {
+        const int a = adapter_of(p, row0 + i);
+        if (a >= 0) list[4 + place_of(p, words, a)] = a;          // (rows of one adapter write the same)
+    }
+    if (tid == 0) list[0] = marked(p, words);
+    sync();
+}
+
+// V as the prompt form has it: two BF16 numbers whose sum is V up to 2^-18 of it (an infinity has no second).
+// Eight numbers of a row, from `at` on.
+__device__ __forceinline__ void store_v_split(const Params& p, int t, int at, const float (&v)[8]) {
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        hi[c] = pack_bf16x2(v[2 * c], v[2 * c + 1]);
+        const float dx = v[2 * c] - bf16_lo(hi[c]), dy = v[2 * c + 1] - bf16_hi(hi[c]);
+        lo[c] = pack_bf16x2(fabsf(dx) < INFINITY ? dx : 0.0f, fabsf(dy) < INFINITY ? dy : 0.0f);
+    }
+    __nv_bfloat16* out = v_split(p, t) + at;
+    *reinterpret_cast<uint4*>(out) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    *reinterpret_cast<uint4*>(out + p.r) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
 }
 
 }  // namespace adapters

@@ -1,6 +1,7 @@
 // adapter_few.cuh -- the projection with adapters for tiles of up to 64 rows.
 //
-// The output channels are the MMA's 128 rows, the token rows its columns. A cluster of
+// The output channels are the MMA's rows, up to 128 (fewer where that spreads the weights over more SMs), the token
+// rows its columns. A cluster of
 // `split` CTAs shares a tile's K: each sums its part in Tensor Memory and writes every split-th row of it
 // to the shared memory of the CTA that finishes those rows, from all parts in their order.
 // V . B_a^T runs on the FP32 units meanwhile, row by row: every row has the adapter of its own, and
@@ -52,27 +53,35 @@ __device__ __forceinline__ void finish_rows(const Params& p, const float* parts,
                                             int rows, int chan0, int tid) {
     constexpr bool GATED = ACT == DGEMM_ACT_SWIGLU;
     constexpr int OUT = GATED ? 64 : 128, STEP = Few::EPI_THREADS / OUT;
-    const int oc = tid % OUT, ch = chan0 + oc;
-    if (ch >= p.wide) return;
+    const int oc = tid % OUT, ch = chan0 + oc, mine = (rows - rank + p.split - 1) / p.split;
+    if (oc >= p.channels || ch >= p.wide) return;
     const float bias = p.bias ? __ldg(p.bias + ch) : 0.0f, bias_up = GATED && p.bias ? __ldg(p.bias + p.N / 2 + ch) : 0.0f;
     const int split = p.kstages > 0 ? p.split : 0;
-#pragma unroll 2
-    for (int q = tid / OUT; q < own; q += STEP) {
+    auto row = [&](int q, int splits) {
         const int c = rank + p.split * q;
-        if (c >= rows) break;
         float v = beside[q * 128 + oc] + bias, u = 0.0f;
         if (GATED) u = beside[q * 128 + 64 + oc] + bias_up;
         const float* from = parts + q * 128 + oc;
         float product = 0.0f, product_up = 0.0f;
-        for (int s = 0; s < split; ++s, from += own * 128) {
+        for (int s = 0; s < splits; ++s, from += own * 128) {
             product += from[0];
-            if (GATED) product_up += from[64];
+            if (GATED) product_up += from[p.channels];
         }
         v += product;
         v = GATED ? experts::silu(v) * (u + product_up) : activate<ACT>(v);
         const int64_t o = static_cast<int64_t>(row0 + c) * p.wide + ch;
         if (p.d_f32) static_cast<float*>(p.D)[o] = v;
         else static_cast<__nv_bfloat16*>(p.D)[o] = __float2bfloat16_rn(v);
+    };
+    // (the ends of the inner loop known where there is one part or none: rows then overlap)
+    if (split == 0) {
+#pragma unroll 4
+        for (int q = tid / OUT; q < mine; q += STEP) row(q, 0);
+    } else if (split == 1) {
+#pragma unroll 4
+        for (int q = tid / OUT; q < mine; q += STEP) row(q, 1);
+    } else {
+        for (int q = tid / OUT; q < mine; q += STEP) row(q, split);
     }
 }
 
@@ -156,7 +165,9 @@ __global__ void __launch_bounds__(Few::THREADS, 2)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = static_cast<int>(blockIdx.x) % split, tile = static_cast<int>(blockIdx.x) / split;
     const int row0 = (tile % p.tiles) * p.width, rows = min(p.width, p.T - row0);
-    const int chan0 = (tile / p.tiles) * (p.gated ? 64 : 128);
+    const int chan0 = (tile / p.tiles) * p.channels;
+    // bytes of a slice of W: the MMA reads 128 rows, and what lies behind the slice goes to lanes that nobody reads
+    const int slice_w = p.channels * (p.gated ? 2 : 1) * 128;
     const int kb0 = static_cast<int>(static_cast<int64_t>(p.kstages) * rank / split);
     const int kb1 = static_cast<int>(static_cast<int64_t>(p.kstages) * (rank + 1) / split);
 
@@ -197,13 +208,13 @@ __global__ void __launch_bounds__(Few::THREADS, 2)
                 uint8_t* x = w + Few::W_BYTES;
                 const uint32_t bar = smem_u32(&full[stage]);
                 const int k0 = kb * Few::KS * Few::SL;
-                mbar_arrive_expect_tx(&full[stage], stage_bytes);
+                mbar_arrive_expect_tx(&full[stage], Few::KS * (slice_w + slice_x));
                 if (p.k_whole) {
                     tma_load_nd<false>(w, &tmW, bar, 0, chan0, 0, kb * Few::KS, pol);
                     tma_load_nd<false>(x, &tmX, bar, 0, row0, kb * Few::KS, pol_x);
                 } else {
                     for (int s = 0; s < Few::KS; ++s) {
-                        tma_load_nd<false>(w + s * Few::SLICE_W, &tmW, bar, k0 + s * Few::SL, chan0, 0, pol);
+                        tma_load_nd<false>(w + s * slice_w, &tmW, bar, k0 + s * Few::SL, chan0, 0, pol);
                         tma_load_nd<false>(x + s * slice_x, &tmX, bar, k0 + s * Few::SL, row0, pol_x);
                     }
                 }
@@ -238,7 +249,7 @@ __global__ void __launch_bounds__(Few::THREADS, 2)
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < Few::KS * 4; ++k)
-                        mma_bf16(acc, wd + (k / 4) * (Few::SLICE_W >> 4) + (k % 4) * 2, xd + (k / 4) * (slice_x >> 4) + (k % 4) * 2,
+                        mma_bf16(acc, wd + (k / 4) * (slice_w >> 4) + (k % 4) * 2, xd + (k / 4) * (slice_x >> 4) + (k % 4) * 2,
                                  idesc, kb > kb0 || k > 0 ? 1u : 0u);
                     mma_commit(&empty[stage]);
                 }
@@ -271,7 +282,7 @@ __global__ void __launch_bounds__(Few::THREADS, 2)
         uint64_t* my_full = b_full + ew * p.ahead;
         auto there = [&](int item) {
             const int i0 = (item & ((1 << lg_items) - 1)) * channels;
-            return min(channels, p.wide - chan0 - (p.gated ? i0 & 63 : i0));
+            return min(channels, min(p.channels, p.wide - chan0) - (p.gated ? i0 & 63 : i0));
         };
         uint32_t pending = 0;                                   // bit s: a copy to slot s is on its way
         auto copy = [&](int item, int slot) {
@@ -298,7 +309,7 @@ __global__ void __launch_bounds__(Few::THREADS, 2)
             for (int k = 0; k < 4; ++k) {
                 const int64_t o = static_cast<int64_t>(row0 + c) * p.wide + chan0 + lane + 32 * k;
                 first[k] = 0.0f;
-                if (p.C && c < rows && chan0 + lane + 32 * k < p.wide)
+                if (p.C && c < rows && lane + 32 * k < p.channels && chan0 + lane + 32 * k < p.wide)
                     first[k] = p.c_f32 ? static_cast<const float*>(p.C)[o] : __bfloat162float(static_cast<const __nv_bfloat16*>(p.C)[o]);
             }
 #pragma unroll

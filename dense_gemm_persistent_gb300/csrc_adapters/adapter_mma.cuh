@@ -8,9 +8,10 @@
 // slices against the same slice of B_a.
 // Warps of a CTA: 0 TMA producer, 1 MMA issuer and owner of the Tensor Memory, 2-3 idle,
 // 4-11 epilogue, 12-15 write the masked rows of V.
-// A zero does not hide a number that is not finite. An adapter whose B holds one (p.bad) is left
-// out of the products, and the epilogue adds its rows' V . B_a^T by FP32 units: slow, and of its own
-// rows only.
+// A zero does not hide a number that is not finite: B_a goes through products with the zeros of other
+// requests' rows. So the last warps look at a slice of B_a before it is used, put zeros in the
+// place of what is not finite, and the epilogue adds those terms to the rows that they belong to, by FP32
+// units: slow, and of these rows only.
 #pragma once
 
 #include "adapter_common.cuh"
@@ -23,11 +24,12 @@ struct Mma {
     static constexpr int SLICE_W = 128 * 128;
     static constexpr int W_BYTES = KS * SLICE_W, STAGE = W_BYTES + KS * BN_CTA * 128, STAGES = 3;
     static constexpr int EPI_WARP0 = 4, EPI_WARPS = 8, V_WARP0 = 12, V_WARPS = 4, THREADS = 32 * (V_WARP0 + V_WARPS);
-    static constexpr int TMEM_COLS = 512, BAR_BYTES = 256;
+    static constexpr int TMEM_COLS = 512, BAR_BYTES = 512;
     static constexpr int SMEM = 1024 + STAGES * STAGE + experts::exchange_bytes<EPI_WARPS>() + BAR_BYTES;
     static constexpr uint32_t IDESC0 = make_idesc(1u, false, false, 256, 0);
     static_assert(SMEM <= 232448, "shared memory");
-    static_assert((4 * STAGES + 5) * 8 + 8 <= BAR_BYTES, "barriers fit");
+    static constexpr int MARKS = 8;      // tiles with adapters that may be between their V and their epilogue: STAGES + 2 at most
+    static_assert((4 * STAGES + 5 + MARKS) * 8 + 8 + MARKS * V_WARPS * 4 <= BAR_BYTES, "barriers fit");
 };
 
 struct MmaTile {
@@ -48,42 +50,37 @@ __device__ __forceinline__ bool mma_tile(const Params& p, int item, MmaTile& t) 
     return true;
 }
 
-// The adapters of a token tile that go through the tensor core, looked up by a whole warp 32 at a time.
+// The adapters of a token tile, looked up by a whole warp 32 at a time.
 struct TileAdapters {
     const int* list;
-    int count, base, mine;
-    unsigned good;
-    __device__ __forceinline__ void look(const Params& p) {
-        const int lane = threadIdx.x & 31;
-        mine = base + lane < count ? __ldcg(list + 4 + base + lane) : -1;
-        good = __ballot_sync(kAllLanes, mine >= 0 && __ldcg(p.bad + mine) != p.epoch);
-    }
+    int count, at, mine;
     __device__ __forceinline__ void open(const Params& p, int tt) {
         list = p.lists + static_cast<int64_t>(tt) * kListPitch;
         count = p.L > 0 ? __ldcg(list) : 0;
-        base = 0;
-        good = 0;
-        if (count > 0) look(p);
+        at = 0;
+        look();
+    }
+    __device__ __forceinline__ void look() {
+        const int i = at + static_cast<int>(threadIdx.x & 31);
+        mine = i < count ? __ldcg(list + 4 + i) : -1;
     }
     // the next one, -1 when there is none left
-    __device__ __forceinline__ int next(const Params& p) {
-        while (good == 0) {
-            base += 32;
-            if (base >= count) return -1;
-            look(p);
-        }
-        const int a = __shfl_sync(kAllLanes, mine, __ffs(good) - 1);
-        good &= good - 1;
-        return a;
+    __device__ __forceinline__ int next() {
+        if (at >= count) return -1;
+        if (at > 0 && at % 32 == 0) look();
+        return __shfl_sync(kAllLanes, mine, at++ & 31);
     }
 };
 
-// V[t] . B_a[n] from the two BF16 numbers of V.
-__device__ __forceinline__ float high_dot_split(const Params& p, int t, int a, int n) {
+// The terms of V[t] . B_a[n] whose factor of B is not finite.
+__device__ __forceinline__ float not_finite_terms(const Params& p, int t, int a, int n) {
     const __nv_bfloat16* b = p.high + (static_cast<int64_t>(a) * p.N + n) * p.r;
     const __nv_bfloat16* v = v_split(p, t);
     float s = 0.0f;
-    for (int i = 0; i < p.r; ++i) s = fmaf(__bfloat162float(v[i]) + __bfloat162float(v[p.r + i]), __bfloat162float(b[i]), s);
+    for (int i = 0; i < p.r; ++i) {
+        const float w = __bfloat162float(b[i]);
+        if (!(fabsf(w) < INFINITY)) s = fmaf(__bfloat162float(v[i]) + __bfloat162float(v[p.r + i]), w, s);
+    }
     return s;
 }
 
@@ -96,13 +93,8 @@ __device__ __forceinline__ bool mma_epilogue(const Params& p, const MmaTile& t, 
     const bool live = ch < p.wide;
     const int n = p.gated && i >= 64 ? p.N / 2 + ch : ch;    // channel of W and B
     const float bias = live && p.bias ? __ldg(p.bias + n) : 0.0f;
-    // any adapter of the tile that was left out
-    bool left_out = false;
-    const int count = p.L > 0 ? __ldcg(p.lists + static_cast<int64_t>(t.tt) * kListPitch) : 0;
-    for (int j = lane; j < count; j += 32)
-        left_out = left_out || __ldcg(p.bad + __ldcg(p.lists + static_cast<int64_t>(t.tt) * kListPitch + 4 + j)) == p.epoch;
-    left_out = __any_sync(kAllLanes, left_out);
-    bool ok = ready();
+    bool dirty = false;                                      // B of the tile had numbers that are not finite
+    bool ok = ready(&dirty);
     const int swap_id = 1 + part * 2 + (q & 1);              // barrier of warps q and q ^ 2
     if (p.gated) ok = experts::pair_all(swap_id, ok);
     if (!ok) return false;
@@ -141,12 +133,12 @@ __device__ __forceinline__ bool mma_epilogue(const Params& p, const MmaTile& t, 
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = (product ? __uint_as_float(r[j]) : 0.0f) + bias;
         }
-        if (left_out) {
+        if (dirty) {
 #pragma unroll 1
             for (int j = 0; j < 32; ++j) {
                 float more = 0.0f;
                 const int a = col0 + j < t.rows ? adapter_of(p, t.row0 + col0 + j) : -1;
-                if (a >= 0 && live && __ldcg(p.bad + a) == p.epoch) more = high_dot_split(p, t.row0 + col0 + j, a, n);
+                if (a >= 0 && live) more = not_finite_terms(p, t.row0 + col0 + j, a, n);
 #pragma unroll
                 for (int k = 0; k < 32; ++k) v[k] += k == j ? more : 0.0f;
             }
@@ -207,12 +199,14 @@ __global__ void __launch_bounds__(Mma::THREADS, 1)
     float* exchange = reinterpret_cast<float*>(ring + S * Mma::STAGE);
     uint64_t* full = reinterpret_cast<uint64_t*>(ring + S * Mma::STAGE + experts::exchange_bytes<Mma::EPI_WARPS>());
     uint64_t* empty = full + S;
-    uint64_t* v_go = empty + S;                  // a stage's token rows are free for masked rows of V (this CTA)
-    uint64_t* v_full = v_go + S;                 // they are written (both CTAs)
+    uint64_t* b_full = empty + S;                // a slice of B has landed here, and the stage's token rows are free for V
+    uint64_t* v_full = b_full + S;               // masked rows of V are written and B is finite (both CTAs)
     uint64_t* acc_full = v_full + S;
     uint64_t* acc_empty = acc_full + 2;
     uint64_t* drain = acc_empty + 2;
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    uint64_t* looked = drain + 1;                // [MARKS] the n-th tile with adapters: its slices of B have been looked at
+    int* dirty = reinterpret_cast<int*>(looked + Mma::MARKS);        // [MARKS][V_WARPS]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dirty + Mma::MARKS * Mma::V_WARPS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -225,9 +219,10 @@ __global__ void __launch_bounds__(Mma::THREADS, 1)
         for (int s = 0; s < S; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
-            mbar_init(&v_go[s], 1);
+            mbar_init(&b_full[s], 1);
             mbar_init(&v_full[s], 2 * Mma::V_WARPS);
         }
+        for (int m = 0; m < Mma::MARKS; ++m) mbar_init(&looked[m], Mma::V_WARPS);
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], Mma::EPI_WARPS * 2);
@@ -261,6 +256,7 @@ __global__ void __launch_bounds__(Mma::THREADS, 1)
         // ---------------------------------------------------------------- TMA producer
         const uint64_t pol = policy_evict_last();
         uint32_t stage = 0, phase = 0;
+        uint32_t x_phase = 0, b_phase = 0, last_b = 0;   // bit s: parity of the next use of full[s], b_full[s]; the last was b_full's
         int64_t issued = 0;
         bool ok = true, stalled = false, waited = p.wait_first;
         MmaTile t;
@@ -269,7 +265,9 @@ __global__ void __launch_bounds__(Mma::THREADS, 1)
             if (!waited) grid_dependency_wait();
             waited = true;
         };
-        auto advance = [&]() {
+        auto advance = [&](bool is_b) {
+            if (is_b) b_phase ^= 1u << stage, last_b |= 1u << stage;
+            else x_phase ^= 1u << stage, last_b &= ~(1u << stage);
             ++issued;
             if (++stage == S) {
                 stage = 0;
@@ -305,47 +303,46 @@ __global__ void __launch_bounds__(Mma::THREADS, 1)
                     }
                 }
                 __syncwarp();
-                advance();
+                advance(false);
             }
             if (!ok || stalled) break;
             if (!waited) {
                 wait_v();
                 ta.open(p, t.tt);
             }
-            for (int a = ta.next(p); ok && !stalled && a >= 0; a = ta.next(p)) {
+            for (int a = ta.next(); ok && !stalled && a >= 0; a = ta.next()) {
                 for (int i = 0; i < chunks_r; ++i) {
                     stalled = issued == p.stall_after;
                     if (stalled) break;
                     ok = mbar_wait_warp(&empty[stage], phase ^ 1, abort_flag, p.wait_ns);
                     if (!ok) break;
                     if (elect_one()) {
-                        uint8_t* w = ring + stage * Mma::STAGE;
-                        if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * Mma::SLICE_W);
-                        const uint32_t fb = mapa_shared(smem_u32(&full[stage]), 0);
-                        tma_load_nd<true>(w, &tmB, fb, i * Mma::SL, chan, 0, a, pol);
-                        mbar_arrive(&v_go[stage]);
+                        // (each CTA's own barrier: its own warps look at the slice first)
+                        mbar_arrive_expect_tx(&b_full[stage], Mma::SLICE_W);
+                        tma_load_nd<true>(ring + stage * Mma::STAGE, &tmB, smem_u32(&b_full[stage]), i * Mma::SL, chan, 0, a, pol);
                     }
                     __syncwarp();
-                    advance();
+                    advance(true);
                 }
             }
         }
         wait_v();
         if (!ok && lane == 0) experts::fail(p, ERR_TIMEOUT_PRODUCER, abort_flag);
-        // every copy issued has landed before the CTA leaves (the peer of the pair signals the leader's
-        // barriers, so it waits for the MMA's release)
+        // every copy issued has landed before the CTA leaves: its stage was released by the MMAs that read it, or, where
+        // they gave up, the barrier that it counts on says so (of the pair's peer that is the leader's)
         for (int s = 0; s < S; ++s) {
             const int64_t cnt = issued > s ? (issued - s + S - 1) / S : 0;
-            uint64_t* bar = rank != 0 ? &empty[s] : &full[s];
-            if (cnt > 0 && !mbar_wait_warp(bar, static_cast<uint32_t>((cnt - 1) & 1), nullptr, p.wait_ns) && lane == 0)
-                experts::fail(p, ERR_TIMEOUT_DRAIN, abort_flag);
+            if (cnt == 0 || mbar_wait_warp(&empty[s], static_cast<uint32_t>((cnt - 1) & 1), nullptr, p.wait_ns)) continue;
+            if (lane == 0) experts::fail(p, ERR_TIMEOUT_DRAIN, abort_flag);
+            if ((last_b >> s) & 1) mbar_wait_warp(&b_full[s], ((b_phase >> s) & 1) ^ 1, nullptr, p.wait_ns);
+            else if (rank == 0) mbar_wait_warp(&full[s], ((x_phase >> s) & 1) ^ 1, nullptr, p.wait_ns);
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------------- MMA issuer
         if (rank == 0) {
             const uint32_t s0 = smem_u32(ring), tmem_u = __shfl_sync(kAllLanes, tmem, 0);
             const uint64_t wd0 = smem_desc_sw128(s0, 16, 1024), xd0 = smem_desc_sw128(s0 + Mma::W_BYTES, 16, 1024);
-            uint32_t stage = 0, phase = 0, v_phase = 0;      // bit s of v_phase: the next parity of v_full[s]
+            uint32_t stage = 0, x_phase = 0, v_phase = 0;    // bit s: the next parity of full[s], v_full[s]
             int local = 0;
             bool ok = true, waited = p.wait_first;
             MmaTile t;
@@ -357,10 +354,7 @@ __global__ void __launch_bounds__(Mma::THREADS, 1)
             auto release = [&]() {
                 if (elect_one()) mma_commit_pair(&empty[stage], 3);
                 __syncwarp();
-                if (++stage == S) {
-                    stage = 0;
-                    phase ^= 1;
-                }
+                if (++stage == S) stage = 0;
             };
             for (int item = unit; ok && mma_tile(p, item, t); item += units, ++local) {
                 const int buf = local & 1;
@@ -374,8 +368,9 @@ __global__ void __launch_bounds__(Mma::THREADS, 1)
                     ta.open(p, t.tt);
                 }
                 for (int kb = 0; kb < p.kstages; ++kb) {
-                    ok = mbar_wait_warp(&full[stage], phase, abort_flag, p.wait_ns);
+                    ok = mbar_wait_warp(&full[stage], (x_phase >> stage) & 1, abort_flag, p.wait_ns);
                     if (!ok) break;
+                    x_phase ^= 1u << stage;
                     tc_fence_after();
                     const uint64_t wd = wd0 + stage * (Mma::STAGE >> 4), xd = xd0 + stage * (Mma::STAGE >> 4);
                     if (elect_one()) {
@@ -392,10 +387,9 @@ __global__ void __launch_bounds__(Mma::THREADS, 1)
                     ta.open(p, t.tt);
                 }
                 uint32_t more = p.kstages > 0;
-                for (int a = ta.next(p); ok && a >= 0; a = ta.next(p)) {
+                for (int a = ta.next(); ok && a >= 0; a = ta.next()) {
                     for (int i = 0; i < chunks_r; ++i) {
-                        ok = mbar_wait_warp(&full[stage], phase, abort_flag, p.wait_ns) &&
-                             mbar_wait_warp_at<true>(&v_full[stage], (v_phase >> stage) & 1, abort_flag, p.wait_ns);
+                        ok = mbar_wait_warp_at<true>(&v_full[stage], (v_phase >> stage) & 1, abort_flag, p.wait_ns);
                         if (!ok) break;
                         v_phase ^= 1u << stage;
                         tc_fence_after();
@@ -427,35 +421,39 @@ __global__ void __launch_bounds__(Mma::THREADS, 1)
     } else if (warp >= Mma::EPI_WARP0 && warp < Mma::EPI_WARP0 + Mma::EPI_WARPS) {
         // ---------------------------------------------------------------- epilogue
         const int ew = warp - Mma::EPI_WARP0;
-        int local = 0;
+        int local = 0, marks = 0;                // tiles; tiles with adapters
         bool ok = true;
         MmaTile t;
         grid_dependency_wait();
         for (int item = unit; ok && mma_tile(p, item, t); item += units, ++local) {
             const int buf = local & 1;
-            bool product = p.kstages > 0;
-            if (!product) {                      // the tile's rows may have no adapter, or only bad ones: nothing is summed
-                TileAdapters ta;
-                ta.open(p, t.tt);
-                product = ta.next(p) >= 0;
-            }
+            const bool some = p.L > 0 && __ldcg(p.lists + static_cast<int64_t>(t.tt) * kListPitch) > 0;      // rows with adapters
             ok = mma_epilogue(
-                p, t, tmem + static_cast<uint32_t>(buf * Mma::BN), product, ew, t.chan0 + static_cast<int>(rank) * (p.gated ? 64 : 128),
-                exchange, [&]() { return mbar_wait_warp(&acc_full[buf], (local >> 1) & 1, abort_flag, p.wait_ns); },
+                p, t, tmem + static_cast<uint32_t>(buf * Mma::BN), p.kstages > 0 || some, ew,
+                t.chan0 + static_cast<int>(rank) * (p.gated ? 64 : 128), exchange,
+                [&](bool* any) {
+                    if (!mbar_wait_warp(&acc_full[buf], (local >> 1) & 1, abort_flag, p.wait_ns)) return false;
+                    if (!some) return true;
+                    const int mark = marks % Mma::MARKS;
+                    if (!mbar_wait_warp(&looked[mark], (marks / Mma::MARKS) & 1, abort_flag, p.wait_ns)) return false;
+                    for (int w = 0; w < Mma::V_WARPS; ++w) *any = *any || dirty[mark * Mma::V_WARPS + w] != 0;
+                    return true;
+                },
                 [&]() {
                     if (rank != 0) mbar_arrive_cluster_relaxed(mapa_shared(smem_u32(&acc_empty[buf]), 0));
                     else mbar_arrive_relaxed(&acc_empty[buf]);
                 });
+            marks += some;
         }
         if (!ok) experts::fail(p, ERR_TIMEOUT_EPILOGUE, abort_flag);
         __syncwarp();
     } else if (warp >= Mma::V_WARP0) {
-        // ---------------------------------------------------------------- masked rows of V
+        // ---------------------------------------------------------------- masked rows of V, a look at B
         // A thread has one token row of this CTA, whose numbers it loads ahead (a row has one adapter: up to
-        // rank 64 once for the tile).
-        const int row = threadIdx.x - 32 * Mma::V_WARP0;
-        uint32_t stage = 0, v_phase = 0;
-        int64_t done = 0;                        // stages before the tile
+        // rank 64 once for the tile), and one channel of B.
+        const int row = threadIdx.x - 32 * Mma::V_WARP0, swizzle = row & 7;
+        uint32_t b_phase = 0;                    // bit s: the next parity of b_full[s]
+        int stage = 0, marks = 0;
         bool ok = true;
         MmaTile t;
         TileAdapters ta;
@@ -477,25 +475,40 @@ __global__ void __launch_bounds__(Mma::THREADS, 1)
             };
             if (chunks_r == 1) load(0, p.r / 8);
             ta.open(p, t.tt);
-            done += p.kstages;
-            for (int a = ta.next(p); ok && a >= 0; a = ta.next(p)) {
-                for (int i = 0; i < chunks_r; ++i, ++done) {
+            stage = (stage + p.kstages) % S;
+            bool found = false;
+            for (int a = ta.next(); ok && a >= 0; a = ta.next()) {
+                for (int i = 0; i < chunks_r; ++i) {
                     const int vecs = min(Mma::SL, p.r - i * Mma::SL) / 8, steps = (vecs + 1) / 2;
-                    stage = static_cast<uint32_t>(done % S);
                     if (chunks_r > 1) load(i, vecs);
-                    ok = mbar_wait_warp(&v_go[stage], (v_phase >> stage) & 1, abort_flag, p.wait_ns);
+                    ok = mbar_wait_warp(&b_full[stage], (b_phase >> stage) & 1, abort_flag, p.wait_ns);
                     if (!ok) break;
-                    v_phase ^= 1u << stage;
-                    uint8_t* x = ring + stage * Mma::STAGE + Mma::W_BYTES + row * 128;
-                    if (row < half) {
+                    b_phase ^= 1u << stage;
+                    uint8_t* w = ring + stage * Mma::STAGE + row * 128;
+                    uint8_t* x = w + Mma::W_BYTES;
+                    const uint4 none = make_uint4(0, 0, 0, 0);
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            if (c < 2 * steps) {
-                                const uint4 none = make_uint4(0, 0, 0, 0);
-                                *reinterpret_cast<uint4*>(x + ((c ^ (row & 7)) << 4)) = own == a ? v[0][c] : none;
-                                *reinterpret_cast<uint4*>(x + slice_x + ((c ^ (row & 7)) << 4)) = own == a ? v[1][c] : none;
+                    for (int c = 0; c < 8; ++c) {
+                        const int o = (c ^ swizzle) << 4;
+                        if (c < 2 * steps && row < half) {
+                            *reinterpret_cast<uint4*>(x + o) = own == a ? v[0][c] : none;
+                            *reinterpret_cast<uint4*>(x + slice_x + o) = own == a ? v[1][c] : none;
+                        }
+                    }
+                    bool bad = false;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        if (c < vecs) bad = not_finite(*reinterpret_cast<const uint4*>(w + ((c ^ swizzle) << 4))) || bad;
+                    if (bad) {
+                        for (int c = 0; c < vecs; ++c) {
+                            uint32_t* word = reinterpret_cast<uint32_t*>(w + ((c ^ swizzle) << 4));
+                            for (int k = 0; k < 4; ++k) {
+                                const uint32_t v2 = word[k];
+                                word[k] = ((v2 & 0x7F80u) == 0x7F80u ? 0u : v2 & 0xFFFFu) |
+                                          ((v2 & 0x7F800000u) == 0x7F800000u ? 0u : v2 & 0xFFFF0000u);
                             }
                         }
+                        found = true;
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -504,7 +517,17 @@ __global__ void __launch_bounds__(Mma::THREADS, 1)
                         else mbar_arrive(&v_full[stage]);
                     }
                     __syncwarp();
+                    if (++stage == S) stage = 0;
                 }
+            }
+            if (ok && ta.count > 0) {
+                const int any = __any_sync(kAllLanes, found);
+                if (lane == 0) {
+                    dirty[marks % Mma::MARKS * Mma::V_WARPS + warp - Mma::V_WARP0] = any;
+                    mbar_arrive(&looked[marks % Mma::MARKS]);
+                }
+                __syncwarp();
+                ++marks;
             }
         }
         if (!ok && lane == 0) experts::fail(p, ERR_TIMEOUT_PRODUCER, abort_flag);

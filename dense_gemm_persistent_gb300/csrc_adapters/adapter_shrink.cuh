@@ -6,15 +6,23 @@
 namespace dg {
 namespace adapters {
 
-// A CTA computes RB numbers of one row: its threads share K, partial sums meet in shared memory.
+// Few rows, by FP32 units: a CTA computes RB numbers of one row; its threads share K, partial sums meet in shared
+// memory. Its loads go out in batches of U steps, whether there are as many or not: with a remainder loop
+// most calls waited for every step. CTAs behind the rows' write the lists of the prompt form's token tiles.
 constexpr int SHRINK_THREADS = 256;
 
-template <int RB>
+template <int RB, int U>
 __global__ void __launch_bounds__(SHRINK_THREADS) adapter_shrink_few(const __grid_constant__ Params p) {
     __shared__ float part[SHRINK_THREADS / 32][RB];
+    __shared__ unsigned words[DGEMM_MAX_ADAPTERS / 32];
     grid_dependency_wait();
     if (threadIdx.x == 0) grid_launch_dependents();
-    const int blocks = p.r / RB, t = static_cast<int>(blockIdx.x) / blocks, j0 = (static_cast<int>(blockIdx.x) % blocks) * RB;
+    const int blocks = p.r / RB;
+    if (static_cast<int>(blockIdx.x) >= p.T * blocks) {
+        list_tile(p, static_cast<int>(blockIdx.x) - p.T * blocks, words, threadIdx.x, SHRINK_THREADS, []() { __syncthreads(); });
+        return;
+    }
+    const int t = static_cast<int>(blockIdx.x) / blocks, j0 = (static_cast<int>(blockIdx.x) - t * blocks) * RB;
     const int a = adapter_of(p, t);
     if (a < 0) return;
     const uint4* x = reinterpret_cast<const uint4*>(p.X + static_cast<int64_t>(t) * p.K);
@@ -23,13 +31,23 @@ __global__ void __launch_bounds__(SHRINK_THREADS) adapter_shrink_few(const __gri
     float s0[RB], s1[RB];
 #pragma unroll
     for (int j = 0; j < RB; ++j) s0[j] = s1[j] = 0.0f;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < vecs; i += SHRINK_THREADS) {
-        const uint4 xv = x[i];
-        const float4 x0 = make_float4(bf16_lo(xv.x), bf16_hi(xv.x), bf16_lo(xv.y), bf16_hi(xv.y));
-        const float4 x1 = make_float4(bf16_lo(xv.z), bf16_hi(xv.z), bf16_lo(xv.w), bf16_hi(xv.w));
+    for (int i0 = threadIdx.x; i0 < vecs; i0 += U * SHRINK_THREADS) {
+        uint4 xv[U], wv[U][RB];
 #pragma unroll
-        for (int j = 0; j < RB; ++j) fma8(s0[j], s1[j], __ldg(w + static_cast<int64_t>(j) * vecs + i), x0, x1);
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * SHRINK_THREADS;
+            const bool there = i < vecs;
+            xv[u] = there ? __ldg(x + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int j = 0; j < RB; ++j) wv[u][j] = there ? __ldg(w + static_cast<int64_t>(j) * vecs + i) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float4 x0 = make_float4(bf16_lo(xv[u].x), bf16_hi(xv[u].x), bf16_lo(xv[u].y), bf16_hi(xv[u].y));
+            const float4 x1 = make_float4(bf16_lo(xv[u].z), bf16_hi(xv[u].z), bf16_lo(xv[u].w), bf16_hi(xv[u].w));
+#pragma unroll
+            for (int j = 0; j < RB; ++j) fma8(s0[j], s1[j], wv[u][j], x0, x1);
+        }
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -42,7 +60,16 @@ __global__ void __launch_bounds__(SHRINK_THREADS) adapter_shrink_few(const __gri
     if (threadIdx.x < RB) {
         float s = 0.0f;
         for (int i = 0; i < SHRINK_THREADS / 32; ++i) s += part[i][threadIdx.x];
-        p.V[static_cast<int64_t>(t) * p.r + j0 + threadIdx.x] = p.scale ? s * p.scale[a] : s;
+        if (p.scale) s *= p.scale[a];
+        const int j = j0 + threadIdx.x;
+        if (p.prompt) {
+            const __nv_bfloat16 hi = __float2bfloat16_rn(s);
+            const float rest = s - __bfloat162float(hi);
+            v_split(p, t)[j] = hi;
+            v_split(p, t)[p.r + j] = __float2bfloat16_rn(fabsf(rest) < INFINITY ? rest : 0.0f);
+        } else {
+            p.V[static_cast<int64_t>(t) * p.r + j] = s;
+        }
     }
 }
 
@@ -51,14 +78,13 @@ __global__ void __launch_bounds__(SHRINK_THREADS) adapter_shrink_few(const __gri
 // once whatever the mix, and a row takes the columns of its own adapter from its accumulator. A
 // cluster of `split` CTAs shares K; the parts meet in shared memory and are added in
 // their order. Warps: 0 TMA producer, 1 MMA issuer, 2-5 accumulator to V, 6-9 for the prompt
-// form: the adapters of its token tiles, and which B_a hold numbers that are not finite
-// (those may not go through products with the zeros of other requests' rows).
+// form: the adapters of its token tiles.
 struct Shrink {
     static constexpr int ROWS = 128, SL = 64, X_BYTES = ROWS * 128;
     static constexpr int MOST_COLS = 256, MOST_STAGES = 8, MOST_SPLIT = 8;
     static constexpr int EPI_WARP0 = 2, HELP_WARP0 = 6, THREADS = 320, HELPERS = 128;
     static constexpr int TMEM_COLS = 256, WORDS = DGEMM_MAX_ADAPTERS / 32;
-    static constexpr int TABLES = 2 * WORDS * 4 + ROWS * 4 + DGEMM_MAX_ADAPTERS * 2, BAR_BYTES = 256;
+    static constexpr int TABLES = 2 * WORDS * 4 + ROWS * 4, BAR_BYTES = 256;
     static constexpr uint32_t IDESC0 = make_idesc(1u, false, false, 128, 0);
     static constexpr int stage_bytes(int cols) { return X_BYTES + cols * 128; }
     static constexpr int smem_bytes(int cols, int stages, int rank) {
@@ -66,56 +92,6 @@ struct Shrink {
     }
     static_assert((2 * MOST_STAGES + 3) * 8 + 8 <= BAR_BYTES, "barriers fit");
 };
-
-__device__ __forceinline__ bool not_finite(uint32_t pair) {
-    return (pair & 0x7F80u) == 0x7F80u || (pair & 0x7F800000u) == 0x7F800000u;
-}
-__device__ __forceinline__ bool not_finite(const uint4& v) {
-    return not_finite(v.x) || not_finite(v.y) || not_finite(v.z) || not_finite(v.w);
-}
-
-// The helpers' part; `words` and `used` are theirs.
-__device__ __forceinline__ void shrink_help(const Params& p, unsigned* words, uint16_t* used, int tid) {
-    constexpr int BAR = 1;
-    auto sync = [&]() { asm volatile("barrier.cta.sync %0, %1;" ::"n"(BAR), "n"(Shrink::HELPERS) : "memory"); };
-    auto clear = [&]() {
-        for (int w = tid; w < Shrink::WORDS; w += Shrink::HELPERS) words[w] = 0;
-        sync();
-    };
-    // the adapters of the token tiles
-    for (int tile = static_cast<int>(blockIdx.x); tile < p.tiles; tile += static_cast<int>(gridDim.x)) {
-        const int row0 = tile * p.width, rows = min(p.width, p.T - row0);
-        clear();
-        mark_adapters(p, row0, rows, words, tid, Shrink::HELPERS);
-        sync();
-        int* list = p.lists + static_cast<int64_t>(tile) * kListPitch;
-        for (int i = tid; i < rows; i += Shrink::HELPERS) {
-            const int a = adapter_of(p, row0 + i);
-            if (a >= 0) list[4 + place_of(p, words, a)] = a;          // (rows of one adapter write the same)
-        }
-        if (tid == 0) list[0] = marked(p, words);
-        sync();
-    }
-    // B of every adapter in use, shared out over the launch
-    clear();
-    mark_adapters(p, 0, p.T, words, tid, Shrink::HELPERS);
-    sync();
-    for (int a = tid; a < p.L; a += Shrink::HELPERS)
-        if ((words[a >> 5] >> (a & 31)) & 1) used[place_of(p, words, a)] = static_cast<uint16_t>(a);
-    sync();
-    const int64_t per = static_cast<int64_t>(p.N) * p.r / 8, all = per * marked(p, words);
-    const int64_t i0 = all * blockIdx.x / gridDim.x, i1 = all * (blockIdx.x + 1) / gridDim.x;
-    for (int64_t i = i0; i < i1;) {
-        const int a = used[i / per];
-        const int64_t base = (i / per) * per, end = min(i1, base + per);
-        const uint4* b = reinterpret_cast<const uint4*>(p.high) + a * per - base;
-        bool bad = false;
-#pragma unroll 8
-        for (int64_t k = i + tid; k < end; k += Shrink::HELPERS) bad = not_finite(__ldg(b + k)) || bad;
-        if (bad) p.bad[a] = p.epoch;
-        i = end;
-    }
-}
 
 __global__ void __launch_bounds__(Shrink::THREADS, 1)
     adapter_shrink_many(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmA,
@@ -127,8 +103,7 @@ __global__ void __launch_bounds__(Shrink::THREADS, 1)
     unsigned* words = reinterpret_cast<unsigned*>(park + p.r * Shrink::ROWS);
     unsigned* help_words = words + Shrink::WORDS;
     int* list = reinterpret_cast<int*>(help_words + Shrink::WORDS);                    // [128] adapters of this tile
-    uint16_t* used = reinterpret_cast<uint16_t*>(list + Shrink::ROWS);
-    uint64_t* full = reinterpret_cast<uint64_t*>(used + DGEMM_MAX_ADAPTERS);
+    uint64_t* full = reinterpret_cast<uint64_t*>(list + Shrink::ROWS);
     uint64_t* empty = full + S;
     uint64_t* acc_full = empty + S;
     uint64_t* acc_empty = acc_full + 1;
@@ -283,7 +258,9 @@ __global__ void __launch_bounds__(Shrink::THREADS, 1)
         }
         if (!ok && lane == 0) experts::fail(p, ERR_TIMEOUT_EPILOGUE, abort_flag);
     } else if (p.prompt) {
-        shrink_help(p, help_words, used, threadIdx.x - 32 * Shrink::HELP_WARP0);
+        for (int tile = static_cast<int>(blockIdx.x); tile < p.tiles; tile += static_cast<int>(gridDim.x))
+            list_tile(p, tile, help_words, threadIdx.x - 32 * Shrink::HELP_WARP0, Shrink::HELPERS,
+                      []() { asm volatile("barrier.cta.sync 1, %0;" ::"n"(Shrink::HELPERS) : "memory"); });
     }
     __syncwarp();
     if (split > 1) cluster_sync();
@@ -306,23 +283,14 @@ __global__ void __launch_bounds__(Shrink::THREADS, 1)
 #pragma unroll
                 for (int c = 0; c < 8; ++c) v[c] += ld_shared_cluster_f32(from + c * Shrink::ROWS * 4);
             }
-            if (p.prompt) {
-                // two BF16 numbers whose sum is V up to 2^-18 of it; an infinity has no second
-                uint32_t hi[4], lo[4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const float x = v[2 * c] * scale, y = v[2 * c + 1] * scale;
-                    hi[c] = pack_bf16x2(x, y);
-                    const float dx = x - bf16_lo(hi[c]), dy = y - bf16_hi(hi[c]);
-                    lo[c] = pack_bf16x2(fabsf(dx) < INFINITY ? dx : 0.0f, fabsf(dy) < INFINITY ? dy : 0.0f);
-                }
-                __nv_bfloat16* out = v_split(p, t) + g * 8;
-                *reinterpret_cast<uint4*>(out) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4*>(out + p.r) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            for (int c = 0; c < 8; ++c) v[c] *= scale;
+            if (p.prompt) {
+                store_v_split(p, t, g * 8, v);
             } else {
                 float4* out = reinterpret_cast<float4*>(p.V + static_cast<int64_t>(t) * p.r + g * 8);
-                out[0] = make_float4(v[0] * scale, v[1] * scale, v[2] * scale, v[3] * scale);
-                out[1] = make_float4(v[4] * scale, v[5] * scale, v[6] * scale, v[7] * scale);
+                out[0] = make_float4(v[0], v[1], v[2], v[3]);
+                out[1] = make_float4(v[4], v[5], v[6], v[7]);
             }
         }
     }

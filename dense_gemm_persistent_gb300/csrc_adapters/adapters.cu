@@ -21,11 +21,10 @@ constexpr int kShared = 232448;                   // a CTA's dynamic shared memo
 
 // Behind the workspace's status word.
 struct Workspace {
-    size_t lists, bad, bytes;
-    Workspace(int64_t T, int64_t r, int64_t L) {
+    size_t lists, bytes;
+    Workspace(int64_t T, int64_t r) {
         lists = DGEMM_WS_STATUS_BYTES + static_cast<size_t>(T) * static_cast<size_t>(r) * 4;
-        bad = lists + static_cast<size_t>((T + Mma::LEAST_WIDTH - 1) / Mma::LEAST_WIDTH) * dg::adapters::kListPitch * 4;
-        bytes = bad + static_cast<size_t>(L) * 8;
+        bytes = lists + static_cast<size_t>((T + Mma::LEAST_WIDTH - 1) / Mma::LEAST_WIDTH) * dg::adapters::kListPitch * 4;
     }
 };
 
@@ -46,8 +45,8 @@ struct Call {
     cudaStream_t stream;
 };
 
-// Most rows of a call that go by tiles of 64 rows, and by FP32 units to V.
-constexpr int kMostFew = 256, kMostFewShrink = 64;
+// Most rows of a call that go by tiles of 64 rows; most numbers of V that FP32 units compute.
+constexpr int kMostFew = 256, kMostFewShrink = 16384;
 
 dgemm_status_t check_sizes(int64_t T, int64_t N, int64_t K, int64_t r, int64_t L) {
     if (T < 0 || N < 0 || K < 0 || L < 0 || r < 1) return DGEMM_ERR_INVALID_VALUE;
@@ -68,17 +67,18 @@ bool allow_shared(std::atomic<unsigned char>* ready, int device, const void* fun
 }
 
 // V of few rows: a CTA for some of a row's numbers.
-template <int RB>
+template <int RB, int U>
 cudaError_t shrink_few(const Params& p, const dg::host::Device& dev, cudaStream_t s) {
     // The same split of an SM's memory as the kernel behind it: one of another split does not start on an SM
     // before this one has left it.
     static std::atomic<unsigned char> ready[dg::host::kMaxDevices];
-    if (!allow_shared(ready, dev.id, reinterpret_cast<const void*>(&dg::adapters::adapter_shrink_few<RB>), 0)) return cudaErrorUnknown;
-    dg::host::Launch l(static_cast<unsigned>(p.T) * (p.r / RB), 1, dg::adapters::SHRINK_THREADS, 0, s);
-    return cudaLaunchKernelEx(&l.cfg, dg::adapters::adapter_shrink_few<RB>, p);
+    if (!allow_shared(ready, dev.id, reinterpret_cast<const void*>(&dg::adapters::adapter_shrink_few<RB, U>), 0)) return cudaErrorUnknown;
+    const unsigned blocks = static_cast<unsigned>(p.T) * (p.r / RB) + (p.prompt ? p.tiles : 0);
+    dg::host::Launch l(blocks, 1, dg::adapters::SHRINK_THREADS, 0, s);
+    return cudaLaunchKernelEx(&l.cfg, dg::adapters::adapter_shrink_few<RB, U>, p);
 }
 dgemm_status_t launch_shrink_few(const Params& p, const dg::host::Device& dev, cudaStream_t s) {
-    const cudaError_t e = static_cast<int64_t>(p.T) * p.r <= 1024 ? shrink_few<2>(p, dev, s) : shrink_few<4>(p, dev, s);
+    const cudaError_t e = static_cast<int64_t>(p.T) * p.r <= 1024 ? shrink_few<2, 4>(p, dev, s) : shrink_few<4, 2>(p, dev, s);
     return e == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
 }
 
@@ -104,11 +104,11 @@ dgemm_status_t launch_shrink_many(const Call& c, Params p, const dg::host::Devic
     return cudaLaunchKernelEx(&l.cfg, dg::adapters::adapter_shrink_many, x, a, p) == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
 }
 
-// The maps of X (boxes of `rows` token rows) and W (a CTA's 128 channels): with whole slices of K both slices of
-// a stage (and the gate and up channels of a gated tile) come in one copy.
-bool product_maps(const Call& c, const Params& p, CUtensorMap* w, CUtensorMap* x, int rows) {
+// The maps of X (boxes of `rows` token rows) and W (boxes of `chan` channels of D): with whole slices of K both slices
+// of a stage (and the gate and up channels of a gated tile) come in one copy.
+bool product_maps(const Call& c, const Params& p, CUtensorMap* w, CUtensorMap* x, int rows, int chan) {
     const uint64_t N = p.N, K = p.K, T = p.T, sl = Few::SL, halves = p.gated ? 2 : 1, H = N / halves;
-    const uint32_t s = Few::SL, channels = p.gated ? 64 : 128, hv = static_cast<uint32_t>(halves), cols = rows, ks = Few::KS;
+    const uint32_t s = Few::SL, channels = chan, hv = static_cast<uint32_t>(halves), cols = rows, ks = Few::KS;
     if (p.k_whole) {
         const uint64_t dw[4] = {sl, H, halves, K / sl}, sw[3] = {K * 2, H * K * 2, 128};
         const uint32_t bw[4] = {s, channels, hv, ks};
@@ -124,16 +124,22 @@ bool product_maps(const Call& c, const Params& p, CUtensorMap* w, CUtensorMap* x
 }
 
 dgemm_status_t launch_few(const Call& c, Params& p, const dg::host::Device& dev) {
-    const int most = p.kstages > 0 ? Few::MOST_COLS : 16;       // (beside another product: nothing to share, more CTAs)
+    const int full = p.gated ? 64 : 128, ctiles = (p.wide + full - 1) / full;
+    // Rows of a tile: beside a product up to 64, which share the weights; else as many as leave a CTA for every SM.
+    int most = Few::MOST_COLS;
+    if (p.kstages == 0)
+        for (most = 16; most < Few::MOST_COLS && static_cast<int64_t>((p.T + most - 1) / most) * ctiles > dev.num_sms;) most += 16;
     const int fewest = (p.T + most - 1) / most;
     p.width = ((p.T + fewest - 1) / fewest + 15) / 16 * 16;
     p.tiles = (p.T + p.width - 1) / p.width;
-    const int ctiles = (p.wide + (p.gated ? 64 : 128) - 1) / (p.gated ? 64 : 128);
-    const int64_t tiles = static_cast<int64_t>(p.tiles) * ctiles;
-    if (tiles > INT32_MAX / Few::MOST_SPLIT) return DGEMM_ERR_NOT_SUPPORTED;
+    if (static_cast<int64_t>(p.tiles) * ctiles > INT32_MAX / Few::MOST_SPLIT / 2) return DGEMM_ERR_NOT_SUPPORTED;
     p.split = 1;
-    p.split = 1;
-    while (p.split < Few::MOST_SPLIT && tiles * p.split * 2 <= dev.num_sms && p.kstages >= 4 * p.split) p.split *= 2;
+    while (p.split < Few::MOST_SPLIT && p.tiles * ctiles * p.split * 2 <= dev.num_sms && p.kstages >= 4 * p.split) p.split *= 2;
+    // Channels of a tile: as few as fill the waves that tiles of 128 need (11008 channels: 138 CTAs of 80, not 86).
+    const int waves = (p.tiles * ctiles * p.split + dev.num_sms - 1) / dev.num_sms;
+    p.channels = std::min(full, (p.wide / std::max(1, waves * dev.num_sms / (p.tiles * p.split)) + 8) / 8 * 8);
+    p.ctiles = (p.wide + p.channels - 1) / p.channels;
+    const int64_t tiles = static_cast<int64_t>(p.tiles) * p.ctiles;
     // Items of B ahead: up to 64 KB of them (a CTA's share of the memory's time), 32 KB where many rows' token slices
     // leave no more.
     p.ahead = p.L > 0 ? std::min(Few::MOST_AHEAD, 64 * 1024 / (Few::EPI_WARPS * Few::item_channels(p.r) * p.r * 2)) : 0;
@@ -145,7 +151,7 @@ dgemm_status_t launch_few(const Call& c, Params& p, const dg::host::Device& dev)
     alignas(64) CUtensorMap w, x;
     std::memset(&w, 0, sizeof w);
     std::memset(&x, 0, sizeof x);
-    if (p.kstages > 0 && !product_maps(c, p, &w, &x, p.width)) return DGEMM_ERR_CUDA;
+    if (p.kstages > 0 && !product_maps(c, p, &w, &x, p.width, p.channels)) return DGEMM_ERR_CUDA;
     static std::atomic<unsigned char> ready[dg::host::kMaxDevices];
     if (!allow_shared(ready, dev.id, reinterpret_cast<const void*>(&dg::adapters::adapter_few), kShared)) return DGEMM_ERR_CUDA;
     dg::host::Launch l(static_cast<unsigned>(tiles * p.split), 1, Few::THREADS, smem, c.stream, p.split);
@@ -175,7 +181,7 @@ dgemm_status_t launch_prompt(const Call& c, const Params& p, const dg::host::Dev
     std::memset(&w, 0, sizeof w);
     std::memset(&x, 0, sizeof x);
     std::memset(&b, 0, sizeof b);
-    if (p.kstages > 0 && !product_maps(c, p, &w, &x, p.width / 2)) return DGEMM_ERR_CUDA;
+    if (p.kstages > 0 && !product_maps(c, p, &w, &x, p.width / 2, p.gated ? 64 : 128)) return DGEMM_ERR_CUDA;
     if (p.L > 0) {
         const uint64_t r = p.r, N = p.N, halves = p.gated ? 2 : 1, H = N / halves, L = p.L;
         const uint64_t d[4] = {r, H, halves, L}, st[3] = {r * 2, H * r * 2, N * r * 2};
@@ -216,10 +222,9 @@ dgemm_status_t run_adapters(const Call& c) {
     p.high = static_cast<const __nv_bfloat16*>(c.B);
     p.ids = c.ids;
     p.scale = c.scale;
-    const Workspace ws(c.T, c.r, c.L);
+    const Workspace ws(c.T, c.r);
     p.V = reinterpret_cast<float*>(static_cast<char*>(c.ws) + DGEMM_WS_STATUS_BYTES);
     p.lists = reinterpret_cast<int*>(static_cast<char*>(c.ws) + ws.lists);
-    p.bad = reinterpret_cast<unsigned long long*>(static_cast<char*>(c.ws) + ws.bad);
     p.T = static_cast<int>(c.T);
     p.N = static_cast<int>(c.N);
     p.K = static_cast<int>(c.K);
@@ -244,7 +249,7 @@ dgemm_status_t run_adapters(const Call& c) {
     p.prompt = forced >= 0 ? forced : p.T > kMostFew;
     if (p.prompt) prompt_tiles(p, dev);
     if (p.L > 0) {
-        const dgemm_status_t s = p.prompt || p.T > kMostFewShrink ? launch_shrink_many(c, p, dev) : launch_shrink_few(p, dev, c.stream);
+        const dgemm_status_t s = static_cast<int64_t>(p.T) * p.r > kMostFewShrink ? launch_shrink_many(c, p, dev) : launch_shrink_few(p, dev, c.stream);
         if (s != DGEMM_OK) return s;
     }
     return p.prompt ? launch_prompt(c, p, dev) : launch_few(c, p, dev);
@@ -256,7 +261,7 @@ extern "C" {
 
 size_t dgemm_adapter_workspace_size(int64_t T, int64_t N, int64_t K, int64_t r, int64_t L) {
     if (check_sizes(T, N, K, r, L) != DGEMM_OK) return 0;
-    return Workspace(T, r, L).bytes;
+    return Workspace(T, r).bytes;
 }
 
 dgemm_status_t dgemm_adapter_bf16(const void* X, const void* W, const void* A, const void* B, const int32_t* ids,
