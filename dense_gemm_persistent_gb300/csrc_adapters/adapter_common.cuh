@@ -23,7 +23,7 @@ struct Params : experts::Params {      // (of those: C, D, bias, N, K, wide, gat
     const __nv_bfloat16* X;            // [T][K]
     const __nv_bfloat16* low;          // A [L][r][K]
     const __nv_bfloat16* high;         // B [L][N][r]
-    float* V;                          // [T][r] FP32, or for the prompt form [T][2][r] BF16: V = first + second
+    __nv_bfloat16* V;                  // [T][2][r]: V = first + second
     int* lists;                        // prompt form: [tiles][kListPitch], the adapters of a token tile: how many, which
     int T, L, r;
     int tiles, width;                  // token tiles and their rows
@@ -62,9 +62,7 @@ __device__ __forceinline__ void fma8(float& s0, float& s1, const uint4& b, const
     s1 = fmaf(v1.w, bf16_hi(b.w), s1);
 }
 
-__device__ __forceinline__ __nv_bfloat16* v_split(const Params& p, int t) {
-    return reinterpret_cast<__nv_bfloat16*>(p.V) + static_cast<int64_t>(t) * 2 * p.r;
-}
+__device__ __forceinline__ __nv_bfloat16* v_row(const Params& p, int t) { return p.V + static_cast<int64_t>(t) * 2 * p.r; }
 
 __device__ __forceinline__ bool not_finite(uint32_t pair) {
     return (pair & 0x7F80u) == 0x7F80u || (pair & 0x7F800000u) == 0x7F800000u;
@@ -115,9 +113,10 @@ __device__ __forceinline__ void list_tile(const Params& p, int tile, unsigned* w
     sync();
 }
 
-// V as the prompt form has it: two BF16 numbers whose sum is V up to 2^-18 of it (an infinity has no second).
+// V goes to the tensor core as two BF16 numbers whose sum is V up to 2^-18 of it (an infinity has no second): one
+// alone would cost half of the adapter's precision, FP32 has no exact way through.
 // Eight numbers of a row, from `at` on.
-__device__ __forceinline__ void store_v_split(const Params& p, int t, int at, const float (&v)[8]) {
+__device__ __forceinline__ void store_v(const Params& p, int t, int at, const float (&v)[8]) {
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
@@ -125,7 +124,7 @@ __device__ __forceinline__ void store_v_split(const Params& p, int t, int at, co
         const float dx = v[2 * c] - bf16_lo(hi[c]), dy = v[2 * c + 1] - bf16_hi(hi[c]);
         lo[c] = pack_bf16x2(fabsf(dx) < INFINITY ? dx : 0.0f, fabsf(dy) < INFINITY ? dy : 0.0f);
     }
-    __nv_bfloat16* out = v_split(p, t) + at;
+    __nv_bfloat16* out = v_row(p, t) + at;
     *reinterpret_cast<uint4*>(out) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4*>(out + p.r) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
 }

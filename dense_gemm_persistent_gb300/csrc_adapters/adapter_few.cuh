@@ -4,10 +4,13 @@
 // rows its columns. A cluster of
 // `split` CTAs shares a tile's K: each sums its part in Tensor Memory and writes every split-th row of it
 // to the shared memory of the CTA that finishes those rows, from all parts in their order.
-// V . B_a^T runs on the FP32 units meanwhile, row by row: every row has the adapter of its own, and
-// rows may be of as many requests as there are. The items are some channels of one row, a run
-// of B_a that a bulk copy brings to shared memory; every warp copies its own items, some ahead. It needs
-// V, the rest does not: only these warps wait for the launch that computes it.
+// V . B_a^T runs on the FP32 units of the epilogue's warps meanwhile: rows may be of as many requests as there are,
+// and no row's product holds another's numbers. The rows that a CTA finishes are put in the order of
+// their adapters; an item is some channels of one adapter, a run of B_a that a bulk copy brings
+// to shared memory, for all of its rows. Every warp copies its own items, some ahead. It needs V, the rest
+// does not: only these warps wait for the launch that computes it. (Warp-wide matrix
+// instructions, m16n8k16 with V as two of the columns, were slower here: 64 rows of 11008 channels, rank
+// 64, took 104 us with them and 42 on the FP32 units, otherwise the same.)
 // Warps: 0 TMA producer, 1 MMA issuer and owner of the Tensor Memory, 2-9 epilogue.
 #pragma once
 
@@ -23,7 +26,7 @@ struct Few {
     static constexpr int MOST_COLS = 64, MOST_STAGES = 8, MOST_SPLIT = 8;
     static constexpr int SLICE_W = 128 * 128, W_BYTES = KS * SLICE_W;
     static constexpr int EPI_WARP0 = 2, EPI_WARPS = 8, EPI_THREADS = 32 * EPI_WARPS, THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
-    static constexpr int MOST_AHEAD = 4, TMEM_COLS = 64, BAR_BYTES = 512;
+    static constexpr int MOST_AHEAD = 4, TMEM_COLS = 64, BAR_BYTES = 512, GROUP_BYTES = 512;
     // channels of an item: at most 4 KB of B
     static __host__ __device__ constexpr int item_channels(int r) { return r <= 32 ? 64 : r <= 64 ? 32 : 16; }
     static constexpr uint32_t IDESC0 = make_idesc(1u, false, false, 128, 0);
@@ -31,7 +34,7 @@ struct Few {
     // the ring; rows that a CTA finishes: 128 results and V; items ahead
     static constexpr int smem_bytes(int cols, int stages, int split, int r, int ahead) {
         return 1024 + stages * stage_bytes(cols) + (cols + split - 1) / split * (512 + r * 4) +
-               EPI_WARPS * ahead * item_channels(r) * r * 2 + BAR_BYTES;
+               EPI_WARPS * ahead * item_channels(r) * r * 2 + GROUP_BYTES + BAR_BYTES;
     }
     static_assert((2 * MOST_STAGES + EPI_WARPS * MOST_AHEAD + 2) * 8 + 8 <= BAR_BYTES, "barriers fit");
     // (the parts of a CTA's rows, up to 71 x 128 floats, are never more than two stages hold)
@@ -85,55 +88,96 @@ __device__ __forceinline__ void finish_rows(const Params& p, const float* parts,
     }
 }
 
-// V . B_a^T of one row for CHANNELS of its channels, by one warp. L = 2^LG lanes share a channel (r / 8, rounded up to
-// a power of two); the sums over them are taken for several loads at a time, each lane ending with one
-// channel's (L - 1 shuffles for L channels, not L LG).
-// b, v: the item's B [CHANNELS][r] and V [r] in shared memory; the results are added to out.
+// V . B_a^T for CHANNELS channels and the `rows` rows of one adapter, by one warp. L = 2^LG lanes share a channel (r / 8,
+// rounded up to a power of two); the sums over them are taken for several loads at a time, each lane ending
+// with one channel's (L - 1 shuffles for L channels, not L LG).
+// b, v: the item's B [CHANNELS][r] and V [own][r] in shared memory; order: the rows; results are added to out [own][128].
 template <int LG>
-__device__ __forceinline__ void high_item(const __nv_bfloat16* b, const float* v, int r, float* out) {
+__device__ __forceinline__ void high_item(const __nv_bfloat16* b, const float* v, int r, const uint8_t* order, int rows, float* out) {
     constexpr int L = 1 << LG, STEP = 32 >> LG, CHANNELS = LG <= 2 ? 64 : LG == 3 ? 32 : 16;
     constexpr int LOADS = CHANNELS / STEP, G = LOADS < L ? LOADS : L;       // of the item, of a group of sums
     const int lane = threadIdx.x & 31, part = lane & (L - 1);
     const bool has = part < r / 8;
-    float4 v0 = make_float4(0, 0, 0, 0), v1 = v0;
-    if (has) {
-        v0 = reinterpret_cast<const float4*>(v)[2 * part];
-        v1 = reinterpret_cast<const float4*>(v)[2 * part + 1];
-    }
     const uint4* from = reinterpret_cast<const uint4*>(b + (lane >> LG) * r) + (has ? part : 0);
     const int pitch = STEP * (r / 8);
-    float s[LOADS];
+    uint4 w[LOADS];
 #pragma unroll
-    for (int k = 0; k < LOADS; ++k) {
-        const uint4 w = from[k * pitch];
-        float a0 = v0.x * bf16_lo(w.x), a1 = v0.y * bf16_hi(w.x);
-        ffma2(a0, a1, bf16_lo(w.y), bf16_hi(w.y), v0.z, v0.w);
-        ffma2(a0, a1, bf16_lo(w.z), bf16_hi(w.z), v1.x, v1.y);
-        ffma2(a0, a1, bf16_lo(w.w), bf16_hi(w.w), v1.z, v1.w);
-        s[k] = has ? a0 + a1 : 0.0f;            // (a lane without a part reads another's, whatever it holds)
-    }
+    for (int k = 0; k < LOADS; ++k) w[k] = from[k * pitch];
+    out += lane >> LG;
+#pragma unroll 1
+    for (int n = 0; n < rows; ++n) {
+        const int q = order[n];
+        const float4* vq = reinterpret_cast<const float4*>(v + q * r) + (has ? 2 * part : 0);
+        const float4 v0 = vq[0], v1 = vq[1];
+        float s[LOADS];
 #pragma unroll
-    for (int g = 0; g < LOADS; g += G) {
+        for (int k = 0; k < LOADS; ++k) {
+            float a0 = v0.x * bf16_lo(w[k].x), a1 = v0.y * bf16_hi(w[k].x);
+            ffma2(a0, a1, bf16_lo(w[k].y), bf16_hi(w[k].y), v0.z, v0.w);
+            ffma2(a0, a1, bf16_lo(w[k].z), bf16_hi(w[k].z), v1.x, v1.y);
+            ffma2(a0, a1, bf16_lo(w[k].w), bf16_hi(w[k].w), v1.z, v1.w);
+            s[k] = has ? a0 + a1 : 0.0f;            // (a lane without a part reads another's)
+        }
 #pragma unroll
-        for (int o = G / 2; o > 0; o >>= 1)
+        for (int g = 0; g < LOADS; g += G) {
 #pragma unroll
-            for (int k = 0; k < o; ++k) {
-                const bool upper = part & o;
-                const float keep = upper ? s[g + k + o] : s[g + k], send = upper ? s[g + k] : s[g + k + o];
-                s[g + k] = keep + __shfl_xor_sync(kAllLanes, send, o);
-            }
+            for (int o = G / 2; o > 0; o >>= 1)
 #pragma unroll
-        for (int o = G; o < L; o <<= 1) s[g] += __shfl_xor_sync(kAllLanes, s[g], o);
-        if (part < G) out[(g + part) * STEP + (lane >> LG)] += s[g];
+                for (int k = 0; k < o; ++k) {
+                    const bool upper = part & o;
+                    const float keep = upper ? s[g + k + o] : s[g + k], send = upper ? s[g + k] : s[g + k + o];
+                    s[g + k] = keep + __shfl_xor_sync(kAllLanes, send, o);
+                }
+#pragma unroll
+            for (int o = G; o < L; o <<= 1) s[g] += __shfl_xor_sync(kAllLanes, s[g], o);
+            if (part < G) out[q * 128 + (g + part) * STEP] += s[g];
+        }
     }
 }
-__device__ __forceinline__ void high_item(int lg, const __nv_bfloat16* b, const float* v, int r, float* out) {
-    switch (lg) {
-        case 0: high_item<0>(b, v, r, out); break;
-        case 1: high_item<1>(b, v, r, out); break;
-        case 2: high_item<2>(b, v, r, out); break;
-        case 3: high_item<3>(b, v, r, out); break;
-        default: high_item<4>(b, v, r, out); break;
+
+// The rows that a CTA finishes in the order of their adapters, by one warp (of[k]: the adapter of row lane + 32 k, -1: none).
+struct Grouped {
+    int count;                          // adapters
+    int adapter[Few::MOST_COLS];
+    uint8_t first[Few::MOST_COLS + 4];  // [count + 1] places in order
+    uint8_t order[Few::MOST_COLS];      // rows
+};
+__device__ __forceinline__ void group_rows(Grouped& g, const int (&of)[2], int mine) {
+    const int lane = threadIdx.x & 31;
+    int place[2] = {0, 0}, all = 0;
+    for (int j = 0; j < mine; ++j) {
+        const int a = __shfl_sync(kAllLanes, j < 32 ? of[0] : of[1], j & 31);
+        all += a >= 0;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) place[k] += a >= 0 && (a < of[k] || (a == of[k] && j < lane + 32 * k));
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        if (of[k] >= 0) {
+            g.order[place[k]] = static_cast<uint8_t>(lane + 32 * k);
+            g.adapter[place[k]] = of[k];        // (of every place first)
+        }
+    __syncwarp();
+    int a[2], before[2], groups = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int i = lane + 32 * k;
+        a[k] = i < all ? g.adapter[i] : -1;
+        const bool starts = i < all && (i == 0 || g.adapter[i - 1] != a[k]);
+        const unsigned who = __ballot_sync(kAllLanes, starts);
+        before[k] = starts ? groups + __popc(who & ((1u << lane) - 1)) : -1;
+        groups += __popc(who);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        if (before[k] >= 0) {
+            g.adapter[before[k]] = a[k];
+            g.first[before[k]] = static_cast<uint8_t>(lane + 32 * k);
+        }
+    if (lane == 0) {
+        g.first[groups] = static_cast<uint8_t>(all);
+        g.count = groups;
     }
 }
 
@@ -141,7 +185,7 @@ __device__ __forceinline__ void st_shared_cluster_f32(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
-__global__ void __launch_bounds__(Few::THREADS, 2)
+__global__ void __launch_bounds__(Few::THREADS, 1)
     adapter_few(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                 const __grid_constant__ Params p) {
     extern __shared__ uint8_t smem_raw[];
@@ -151,10 +195,11 @@ __global__ void __launch_bounds__(Few::THREADS, 2)
     const int own = (cols + split - 1) / split;                 // rows of the tile that a CTA finishes, at most
     float* parts = reinterpret_cast<float*>(ring);              // [split][own][128], once the cluster's rings have been read
     float* beside = reinterpret_cast<float*>(ring + S * stage_bytes);          // [own][128]: C, then C + V . B_a^T
-    float* v_rows = beside + own * 128;                                         // [own][r]
+    float* v_rows = beside + own * 128;                                        // [own][r]
     const int channels = Few::item_channels(p.r);
     __nv_bfloat16* slots = reinterpret_cast<__nv_bfloat16*>(v_rows + own * p.r);   // [warps][ahead][channels][r]
-    uint64_t* full = reinterpret_cast<uint64_t*>(slots + Few::EPI_WARPS * p.ahead * channels * p.r);
+    Grouped& grouped = *reinterpret_cast<Grouped*>(slots + Few::EPI_WARPS * p.ahead * channels * p.r);
+    uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(&grouped) + Few::GROUP_BYTES);
     uint64_t* empty = full + S;
     uint64_t* b_full = empty + S;
     uint64_t* acc_full = b_full + Few::EPI_WARPS * p.ahead;
@@ -271,12 +316,18 @@ __global__ void __launch_bounds__(Few::THREADS, 2)
         // ---------------------------------------------------------------- adapters, then this CTA's part of the sum
         const int ew = warp - Few::EPI_WARP0;
         const int mine = p.L > 0 && rows > rank ? (rows - rank + split - 1) / split : 0;    // rows that this CTA finishes
-        const int lg_items = channels == 64 ? 1 : channels == 32 ? 2 : 3, items = mine << lg_items;
-        int of_row[2] = {-1, -1};                               // lanes: their adapters, -1 for none
+        const int lg_items = channels == 64 ? 1 : channels == 32 ? 2 : 3;
+        if (mine > 0) {
+            if (ew == 0) {
+                int of[2] = {-1, -1};
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-            if (lane + 32 * k < mine) of_row[k] = adapter_of(p, row0 + rank + split * (lane + 32 * k));
-        auto adapter = [&](int q) { return __shfl_sync(kAllLanes, q < 32 ? of_row[0] : of_row[1], q & 31); };
+                for (int k = 0; k < 2; ++k)
+                    if (lane + 32 * k < mine) of[k] = adapter_of(p, row0 + rank + split * (lane + 32 * k));
+                group_rows(grouped, of, mine);
+            }
+            asm volatile("barrier.cta.sync 1, %0;" ::"n"(Few::EPI_THREADS) : "memory");
+        }
+        const int items = mine > 0 ? grouped.count << lg_items : 0;
         // An item's copy: the channels that there are (D's channels beyond the last have none).
         __nv_bfloat16* my_slots = slots + ew * p.ahead * channels * p.r;
         uint64_t* my_full = b_full + ew * p.ahead;
@@ -287,8 +338,8 @@ __global__ void __launch_bounds__(Few::THREADS, 2)
         uint32_t pending = 0;                                   // bit s: a copy to slot s is on its way
         auto copy = [&](int item, int slot) {
             if (item >= items) return;
-            const int a = adapter(item >> lg_items), n = there(item);
-            if (a < 0 || n <= 0) return;
+            const int a = grouped.adapter[item >> lg_items], n = there(item);
+            if (n <= 0) return;
             pending |= 1u << slot;
             if (elect_one()) {
                 const int i0 = (item & ((1 << lg_items) - 1)) * channels;
@@ -317,23 +368,32 @@ __global__ void __launch_bounds__(Few::THREADS, 2)
         }
         if (mine > 0) {
             for (int q = ew; q < mine; q += Few::EPI_WARPS)
-                if (lane < p.r / 4)         // (rows without an adapter have no V; theirs is not used)
+                if (lane < p.r / 4) {       // (rows without an adapter have no V; theirs is not used)
+                    const __nv_bfloat16* v = v_row(p, row0 + rank + split * q) + 4 * lane;
+                    const uint2 hi = __ldcg(reinterpret_cast<const uint2*>(v)), lo = __ldcg(reinterpret_cast<const uint2*>(v + p.r));
                     reinterpret_cast<float4*>(v_rows + q * p.r)[lane] =
-                        __ldcg(reinterpret_cast<const float4*>(p.V + static_cast<int64_t>(row0 + rank + split * q) * p.r) + lane);
+                        make_float4(bf16_lo(hi.x) + bf16_lo(lo.x), bf16_hi(hi.x) + bf16_hi(lo.x), bf16_lo(hi.y) + bf16_lo(lo.y),
+                                    bf16_hi(hi.y) + bf16_hi(lo.y));
+                }
             asm volatile("barrier.cta.sync 1, %0;" ::"n"(Few::EPI_THREADS) : "memory");
-            const int lg = p.r <= 8 ? 0 : 32 - __clz(p.r / 8 - 1);
             int slot = 0;
             uint32_t phases = 0;            // bit s: the next parity of my_full[s]
             bool ok = true;
             for (int item = ew; item < items; item += Few::EPI_WARPS) {
-                const int q = item >> lg_items;
-                float* out = beside + q * 128 + (item & ((1 << lg_items) - 1)) * channels;
-                if (adapter(q) >= 0 && there(item) > 0) {
+                if (there(item) > 0) {
+                    const int g = item >> lg_items, first = grouped.first[g], n = grouped.first[g + 1] - first;
                     ok = mbar_wait_warp(&my_full[slot], (phases >> slot) & 1, abort_flag, p.wait_ns);
                     if (!ok) break;
                     pending &= ~(1u << slot);
                     phases ^= 1u << slot;
-                    high_item(lg, my_slots + slot * channels * p.r, v_rows + q * p.r, p.r, out);
+                    const __nv_bfloat16* b = my_slots + slot * channels * p.r;
+                    const uint8_t* order = grouped.order + first;
+                    float* out = beside + (item & ((1 << lg_items) - 1)) * channels;
+                    if (p.r <= 8) high_item<0>(b, v_rows, p.r, order, n, out);
+                    else if (p.r <= 16) high_item<1>(b, v_rows, p.r, order, n, out);
+                    else if (p.r <= 32) high_item<2>(b, v_rows, p.r, order, n, out);
+                    else if (p.r <= 64) high_item<3>(b, v_rows, p.r, order, n, out);
+                    else high_item<4>(b, v_rows, p.r, order, n, out);
                     __syncwarp();
                 }
                 copy(item + p.ahead * Few::EPI_WARPS, slot);

@@ -75,7 +75,7 @@ struct TileAdapters {
 // The terms of V[t] . B_a[n] whose factor of B is not finite.
 __device__ __forceinline__ float not_finite_terms(const Params& p, int t, int a, int n) {
     const __nv_bfloat16* b = p.high + (static_cast<int64_t>(a) * p.N + n) * p.r;
-    const __nv_bfloat16* v = v_split(p, t);
+    const __nv_bfloat16* v = v_row(p, t);
     float s = 0.0f;
     for (int i = 0; i < p.r; ++i) {
         const float w = __bfloat162float(b[i]);
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(Mma::THREADS, 1)
         for (int item = unit; ok && mma_tile(p, item, t); item += units) {
             const int half = t.n / 2, at = static_cast<int>(rank) * half + row;
             const int own = row < half && at < t.rows && p.L > 0 ? adapter_of(p, t.row0 + at) : -1;
-            const uint4* src = reinterpret_cast<const uint4*>(v_split(p, t.row0 + at));
+            const uint4* src = reinterpret_cast<const uint4*>(v_row(p, t.row0 + at));
             uint4 v[2][8];
             auto load = [&](int i, int vecs) {
 #pragma unroll

@@ -62,14 +62,10 @@ __global__ void __launch_bounds__(SHRINK_THREADS) adapter_shrink_few(const __gri
         for (int i = 0; i < SHRINK_THREADS / 32; ++i) s += part[i][threadIdx.x];
         if (p.scale) s *= p.scale[a];
         const int j = j0 + threadIdx.x;
-        if (p.prompt) {
-            const __nv_bfloat16 hi = __float2bfloat16_rn(s);
-            const float rest = s - __bfloat162float(hi);
-            v_split(p, t)[j] = hi;
-            v_split(p, t)[p.r + j] = __float2bfloat16_rn(fabsf(rest) < INFINITY ? rest : 0.0f);
-        } else {
-            p.V[static_cast<int64_t>(t) * p.r + j] = s;
-        }
+        const __nv_bfloat16 hi = __float2bfloat16_rn(s);
+        const float rest = s - __bfloat162float(hi);
+        v_row(p, t)[j] = hi;
+        v_row(p, t)[p.r + j] = __float2bfloat16_rn(fabsf(rest) < INFINITY ? rest : 0.0f);      // (see store_v)
     }
 }
 
@@ -285,13 +281,7 @@ __global__ void __launch_bounds__(Shrink::THREADS, 1)
             }
 #pragma unroll
             for (int c = 0; c < 8; ++c) v[c] *= scale;
-            if (p.prompt) {
-                store_v_split(p, t, g * 8, v);
-            } else {
-                float4* out = reinterpret_cast<float4*>(p.V + static_cast<int64_t>(t) * p.r + g * 8);
-                out[0] = make_float4(v[0], v[1], v[2], v[3]);
-                out[1] = make_float4(v[4], v[5], v[6], v[7]);
-            }
+            store_v(p, t, g * 8, v);
         }
     }
     tc_fence_before();

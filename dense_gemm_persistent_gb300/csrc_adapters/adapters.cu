@@ -78,7 +78,11 @@ cudaError_t shrink_few(const Params& p, const dg::host::Device& dev, cudaStream_
     return cudaLaunchKernelEx(&l.cfg, dg::adapters::adapter_shrink_few<RB, U>, p);
 }
 dgemm_status_t launch_shrink_few(const Params& p, const dg::host::Device& dev, cudaStream_t s) {
-    const cudaError_t e = static_cast<int64_t>(p.T) * p.r <= 1024 ? shrink_few<2, 4>(p, dev, s) : shrink_few<4, 2>(p, dev, s);
+    // (as many CTAs as the SMs hold at once, about 4 each: more numbers a CTA beyond)
+    const int64_t numbers = static_cast<int64_t>(p.T) * p.r, at_once = 4 * dev.num_sms;
+    const cudaError_t e = numbers <= 2 * at_once   ? shrink_few<2, 4>(p, dev, s)
+                          : numbers <= 4 * at_once ? shrink_few<4, 2>(p, dev, s)
+                                                   : shrink_few<8, 2>(p, dev, s);
     return e == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
 }
 
@@ -123,7 +127,27 @@ bool product_maps(const Call& c, const Params& p, CUtensorMap* w, CUtensorMap* x
     return dg::host::encode_map(w, kBf16, c.W, 3, dw, sw, bw) && dg::host::encode_map(x, kBf16, c.X, 2, dx, sx, bx);
 }
 
+// Clusters of `split` CTAs of the few-row form that the device holds at once (a cluster lies within one part of it).
+int most_clusters(const dg::host::Device& dev, int split) {
+    static std::atomic<int> known[dg::host::kMaxDevices][Few::MOST_SPLIT + 1];
+    std::atomic<int>& n = known[dev.id][split];
+    int v = n.load(std::memory_order_acquire);
+    if (v == 0) {
+        dg::host::Launch l(static_cast<unsigned>(dev.num_sms / split * split), 1, Few::THREADS, kShared, nullptr, split);
+        l.cfg.attrs = l.attr + 1;                 // (the cluster's size alone)
+        l.cfg.numAttrs = 1;
+        if (cudaOccupancyMaxActiveClusters(&v, reinterpret_cast<const void*>(&dg::adapters::adapter_few), &l.cfg) != cudaSuccess || v < 1) {
+            cudaGetLastError();
+            v = -1;
+        }
+        n.store(v, std::memory_order_release);
+    }
+    return v;
+}
+
 dgemm_status_t launch_few(const Call& c, Params& p, const dg::host::Device& dev) {
+    static std::atomic<unsigned char> ready[dg::host::kMaxDevices];
+    if (!allow_shared(ready, dev.id, reinterpret_cast<const void*>(&dg::adapters::adapter_few), kShared)) return DGEMM_ERR_CUDA;
     const int full = p.gated ? 64 : 128, ctiles = (p.wide + full - 1) / full;
     // Rows of a tile: beside a product up to 64, which share the weights; else as many as leave a CTA for every SM.
     int most = Few::MOST_COLS;
@@ -133,27 +157,36 @@ dgemm_status_t launch_few(const Call& c, Params& p, const dg::host::Device& dev)
     p.width = ((p.T + fewest - 1) / fewest + 15) / 16 * 16;
     p.tiles = (p.T + p.width - 1) / p.width;
     if (static_cast<int64_t>(p.tiles) * ctiles > INT32_MAX / Few::MOST_SPLIT / 2) return DGEMM_ERR_NOT_SUPPORTED;
-    p.split = 1;
-    while (p.split < Few::MOST_SPLIT && p.tiles * ctiles * p.split * 2 <= dev.num_sms && p.kstages >= 4 * p.split) p.split *= 2;
-    // Channels of a tile: as few as fill the waves that tiles of 128 need (11008 channels: 138 CTAs of 80, not 86).
-    const int waves = (p.tiles * ctiles * p.split + dev.num_sms - 1) / dev.num_sms;
-    p.channels = std::min(full, (p.wide / std::max(1, waves * dev.num_sms / (p.tiles * p.split)) + 8) / 8 * 8);
+    // CTAs of a cluster that share K, and channels of a tile: the least time by a model of what a CTA reads (rows of W
+    // and X times its stages, in waves of the clusters that fit at once), the exchange of parts as 150 such units.
+    // (11008 channels: 138 CTAs of 80, not 86 of 128; 4096: 76 pairs of CTAs of 56 channels and half of K.)
+    int64_t least = INT64_MAX;
+    for (int split = 1; split <= Few::MOST_SPLIT && (split == 1 || p.kstages >= 4 * split); split *= 2) {
+        const int slots = split == 1 ? dev.num_sms : most_clusters(dev, split);
+        if (slots < 1) break;
+        const int waves = (p.tiles * ctiles + slots - 1) / slots;
+        const int channels = std::min(full, (p.wide / std::max(1, waves * slots / p.tiles) + 8) / 8 * 8);
+        const int64_t stages = (p.kstages + split - 1) / split;
+        const int64_t cost = waves * ((channels * (p.gated ? 2 : 1) + p.width) * stages + (split > 1 ? 150 : 0));
+        if (cost < least) {
+            least = cost;
+            p.split = split;
+            p.channels = channels;
+        }
+    }
     p.ctiles = (p.wide + p.channels - 1) / p.channels;
     const int64_t tiles = static_cast<int64_t>(p.tiles) * p.ctiles;
-    // Items of B ahead: up to 64 KB of them (a CTA's share of the memory's time), 32 KB where many rows' token slices
-    // leave no more.
-    p.ahead = p.L > 0 ? std::min(Few::MOST_AHEAD, 64 * 1024 / (Few::EPI_WARPS * Few::item_channels(p.r) * p.r * 2)) : 0;
+    // Items of B ahead: up to 128 KB of them, 64 beside a product; the ring has what is left.
+    const int ahead = (p.kstages > 0 ? 64 : 128) * 1024 / (Few::EPI_WARPS * Few::item_channels(p.r) * p.r * 2);
+    p.ahead = p.L > 0 ? std::min(Few::MOST_AHEAD, ahead) : 0;
     auto shared = [&](int stages) { return Few::smem_bytes(p.width, stages, p.split, p.r, p.ahead); };
     p.stages = p.kstages > 0 ? 2 : 0;
     while (p.stages > 0 && p.stages < Few::MOST_STAGES && shared(p.stages + 1) <= kShared) ++p.stages;
-    const int smem = shared(p.stages);
-    if (smem > kShared) return DGEMM_ERR_NOT_SUPPORTED;
+    const int smem = shared(p.stages);            // (two stages always fit: at most 231424 bytes, rank 128 and 64 rows)
     alignas(64) CUtensorMap w, x;
     std::memset(&w, 0, sizeof w);
     std::memset(&x, 0, sizeof x);
     if (p.kstages > 0 && !product_maps(c, p, &w, &x, p.width, p.channels)) return DGEMM_ERR_CUDA;
-    static std::atomic<unsigned char> ready[dg::host::kMaxDevices];
-    if (!allow_shared(ready, dev.id, reinterpret_cast<const void*>(&dg::adapters::adapter_few), kShared)) return DGEMM_ERR_CUDA;
     dg::host::Launch l(static_cast<unsigned>(tiles * p.split), 1, Few::THREADS, smem, c.stream, p.split);
     return cudaLaunchKernelEx(&l.cfg, dg::adapters::adapter_few, w, x, p) == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
 }
@@ -223,7 +256,7 @@ dgemm_status_t run_adapters(const Call& c) {
     p.ids = c.ids;
     p.scale = c.scale;
     const Workspace ws(c.T, c.r);
-    p.V = reinterpret_cast<float*>(static_cast<char*>(c.ws) + DGEMM_WS_STATUS_BYTES);
+    p.V = reinterpret_cast<__nv_bfloat16*>(static_cast<char*>(c.ws) + DGEMM_WS_STATUS_BYTES);
     p.lists = reinterpret_cast<int*>(static_cast<char*>(c.ws) + ws.lists);
     p.T = static_cast<int>(c.T);
     p.N = static_cast<int>(c.N);
