@@ -64,13 +64,6 @@ __device__ __forceinline__ void fma8(float& s0, float& s1, const uint4& b, const
 
 __device__ __forceinline__ __nv_bfloat16* v_row(const Params& p, int t) { return p.V + static_cast<int64_t>(t) * 2 * p.r; }
 
-__device__ __forceinline__ bool not_finite(uint32_t pair) {
-    return (pair & 0x7F80u) == 0x7F80u || (pair & 0x7F800000u) == 0x7F800000u;
-}
-__device__ __forceinline__ bool not_finite(const uint4& v) {
-    return not_finite(v.x) || not_finite(v.y) || not_finite(v.z) || not_finite(v.w);
-}
-
 // Bits of the adapters in use among n rows, by `threads` threads that all pass; words: [128].
 __device__ __forceinline__ void mark_adapters(const Params& p, int first, int n, unsigned* words, int tid, int threads) {
     // (loads of a batch before its marks; most are marked already, and a look spares the atomic)

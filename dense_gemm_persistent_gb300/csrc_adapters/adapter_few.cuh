@@ -26,7 +26,7 @@ struct Few {
     static constexpr int MOST_COLS = 64, MOST_STAGES = 8, MOST_SPLIT = 8;
     static constexpr int SLICE_W = 128 * 128, W_BYTES = KS * SLICE_W;
     static constexpr int EPI_WARP0 = 2, EPI_WARPS = 8, EPI_THREADS = 32 * EPI_WARPS, THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
-    static constexpr int MOST_AHEAD = 4, TMEM_COLS = 64, BAR_BYTES = 512, GROUP_BYTES = 512;
+    static constexpr int MOST_AHEAD = 4, TMEM_COLS = 64, BAR_BYTES = 512, GROUP_BYTES = 768;
     // channels of an item: at most 4 KB of B
     static __host__ __device__ constexpr int item_channels(int r) { return r <= 32 ? 64 : r <= 64 ? 32 : 16; }
     static constexpr uint32_t IDESC0 = make_idesc(1u, false, false, 128, 0);
@@ -135,35 +135,47 @@ __device__ __forceinline__ void high_item(const __nv_bfloat16* b, const float* v
     }
 }
 
-// The rows that a CTA finishes in the order of their adapters, by one warp (of[k]: the adapter of row lane + 32 k, -1: none).
+// The rows that a CTA finishes in the order of their adapters.
 struct Grouped {
-    int count;                          // adapters
-    int adapter[Few::MOST_COLS];
+    alignas(16) int count;              // adapters
+    alignas(16) int of[Few::MOST_COLS];             // [rows] their adapters, -1 for none
+    int adapter[Few::MOST_COLS];        // [count]
     uint8_t first[Few::MOST_COLS + 4];  // [count + 1] places in order
     uint8_t order[Few::MOST_COLS];      // rows
 };
+// By one warp: a row's place is the number of rows before it, a group starts where the adapter changes.
 __device__ __forceinline__ void group_rows(Grouped& g, const int (&of)[2], int mine) {
     const int lane = threadIdx.x & 31;
-    int place[2] = {0, 0}, all = 0;
-    for (int j = 0; j < mine; ++j) {
-        const int a = __shfl_sync(kAllLanes, j < 32 ? of[0] : of[1], j & 31);
-        all += a >= 0;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) place[k] += a >= 0 && (a < of[k] || (a == of[k] && j < lane + 32 * k));
+    for (int k = 0; k < 2; ++k) g.of[lane + 32 * k] = of[k];
+    __syncwarp();
+    int place[2] = {0, 0}, all = 0;
+    const int4* rows = reinterpret_cast<const int4*>(g.of);
+#pragma unroll 4
+    for (int j = 0; j < mine; j += 4) {
+        const int4 a4 = rows[j >> 2];
+        const int a[4] = {a4.x, a4.y, a4.z, a4.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            all += a[i] >= 0;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) place[k] += a[i] >= 0 && (a[i] < of[k] || (a[i] == of[k] && j + i < lane + 32 * k));
+        }
     }
+    int* sorted = g.adapter;
 #pragma unroll
     for (int k = 0; k < 2; ++k)
         if (of[k] >= 0) {
             g.order[place[k]] = static_cast<uint8_t>(lane + 32 * k);
-            g.adapter[place[k]] = of[k];        // (of every place first)
+            sorted[place[k]] = of[k];           // (of every place first)
         }
     __syncwarp();
     int a[2], before[2], groups = 0;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         const int i = lane + 32 * k;
-        a[k] = i < all ? g.adapter[i] : -1;
-        const bool starts = i < all && (i == 0 || g.adapter[i - 1] != a[k]);
+        a[k] = i < all ? sorted[i] : -1;
+        const bool starts = i < all && (i == 0 || sorted[i - 1] != a[k]);
         const unsigned who = __ballot_sync(kAllLanes, starts);
         before[k] = starts ? groups + __popc(who & ((1u << lane) - 1)) : -1;
         groups += __popc(who);
@@ -352,29 +364,51 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
         };
         for (int k = 0; k < p.ahead; ++k) copy(ew + k * Few::EPI_WARPS, k);
         if (!p.wait_first) grid_dependency_wait();              // V, and nothing of D before the stream allows it
-        // C as the first term of the rows' sums; V of the rows
-        for (int q = ew; q < own; q += Few::EPI_WARPS) {
-            const int c = rank + split * q;
-            float first[4];
+        // C as the first term of the rows' sums; V of the rows. (Loads of four rows at a time before the first store: one
+        // after another they took 0.7 us a row.)
+        for (int q0 = ew; q0 < own; q0 += 4 * Few::EPI_WARPS) {
+            float first[4][4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int64_t o = static_cast<int64_t>(row0 + c) * p.wide + chan0 + lane + 32 * k;
-                first[k] = 0.0f;
-                if (p.C && c < rows && lane + 32 * k < p.channels && chan0 + lane + 32 * k < p.wide)
-                    first[k] = p.c_f32 ? static_cast<const float*>(p.C)[o] : __bfloat162float(static_cast<const __nv_bfloat16*>(p.C)[o]);
+            for (int n = 0; n < 4; ++n) {
+                const int c = rank + split * (q0 + n * Few::EPI_WARPS);
+                const bool row = p.C && q0 + n * Few::EPI_WARPS < own && c < rows;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int64_t o = static_cast<int64_t>(row0 + c) * p.wide + chan0 + lane + 32 * k;
+                    first[n][k] = 0.0f;
+                    if (row && lane + 32 * k < p.channels && chan0 + lane + 32 * k < p.wide)
+                        first[n][k] = p.c_f32 ? static_cast<const float*>(p.C)[o] : __bfloat162float(static_cast<const __nv_bfloat16*>(p.C)[o]);
+                }
             }
 #pragma unroll
-            for (int k = 0; k < 4; ++k) beside[q * 128 + lane + 32 * k] = first[k];
+            for (int n = 0; n < 4; ++n)
+                if (q0 + n * Few::EPI_WARPS < own) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) beside[(q0 + n * Few::EPI_WARPS) * 128 + lane + 32 * k] = first[n][k];
+                }
         }
         if (mine > 0) {
-            for (int q = ew; q < mine; q += Few::EPI_WARPS)
-                if (lane < p.r / 4) {       // (rows without an adapter have no V; theirs is not used)
-                    const __nv_bfloat16* v = v_row(p, row0 + rank + split * q) + 4 * lane;
-                    const uint2 hi = __ldcg(reinterpret_cast<const uint2*>(v)), lo = __ldcg(reinterpret_cast<const uint2*>(v + p.r));
-                    reinterpret_cast<float4*>(v_rows + q * p.r)[lane] =
-                        make_float4(bf16_lo(hi.x) + bf16_lo(lo.x), bf16_hi(hi.x) + bf16_hi(lo.x), bf16_lo(hi.y) + bf16_lo(lo.y),
-                                    bf16_hi(hi.y) + bf16_hi(lo.y));
+            for (int q0 = ew; q0 < mine; q0 += 4 * Few::EPI_WARPS) {
+                uint2 hi[4], lo[4];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const int q = q0 + n * Few::EPI_WARPS;
+                    hi[n] = lo[n] = make_uint2(0, 0);
+                    if (q < mine && lane < p.r / 4) {       // (rows without an adapter have no V; theirs is not used)
+                        const __nv_bfloat16* v = v_row(p, row0 + rank + split * q) + 4 * lane;
+                        hi[n] = __ldcg(reinterpret_cast<const uint2*>(v));
+                        lo[n] = __ldcg(reinterpret_cast<const uint2*>(v + p.r));
+                    }
                 }
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const int q = q0 + n * Few::EPI_WARPS;
+                    if (q < mine && lane < p.r / 4)
+                        reinterpret_cast<float4*>(v_rows + q * p.r)[lane] =
+                            make_float4(bf16_lo(hi[n].x) + bf16_lo(lo[n].x), bf16_hi(hi[n].x) + bf16_hi(lo[n].x),
+                                        bf16_lo(hi[n].y) + bf16_lo(lo[n].y), bf16_hi(hi[n].y) + bf16_hi(lo[n].y));
+                }
+            }
             asm volatile("barrier.cta.sync 1, %0;" ::"n"(Few::EPI_THREADS) : "memory");
             int slot = 0;
             uint32_t phases = 0;            // bit s: the next parity of my_full[s]

@@ -7,7 +7,7 @@
 // between, and D is rounded once. V = first + second BF16 number (adapter_shrink.cuh): two
 // slices against the same slice of B_a.
 // Warps of a CTA: 0 TMA producer, 1 MMA issuer and owner of the Tensor Memory, 2-3 idle,
-// 4-11 epilogue, 12-15 write the masked rows of V.
+// 4-11 epilogue, 12-19 write the masked rows of V and look at B.
 // A zero does not hide a number that is not finite: B_a goes through products with the zeros of other
 // requests' rows. So the last warps look at a slice of B_a before it is used, put zeros in the
 // place of what is not finite, and the epilogue adds those terms to the rows that they belong to, by FP32
@@ -23,8 +23,12 @@ struct Mma {
     static constexpr int BN = kMostWidth, BN_CTA = BN / 2, LEAST_WIDTH = 64, KS = 2, SL = 64, Q = 32;
     static constexpr int SLICE_W = 128 * 128;
     static constexpr int W_BYTES = KS * SLICE_W, STAGE = W_BYTES + KS * BN_CTA * 128, STAGES = 3;
-    static constexpr int EPI_WARP0 = 4, EPI_WARPS = 8, V_WARP0 = 12, V_WARPS = 4, THREADS = 32 * (V_WARP0 + V_WARPS);
-    static constexpr int TMEM_COLS = 512, BAR_BYTES = 512;
+    static constexpr int EPI_WARP0 = 4, EPI_WARPS = 8, V_WARP0 = 12, V_WARPS = 8, THREADS = 32 * (V_WARP0 + V_WARPS);
+    // Registers: the epilogue holds a chunk, the next chunk of C and what it writes; with the launch's 96 a thread it spilled
+    // (4096 x 11008 beside another product 155 us, not 109), so the other warpgroups hand some over.
+    static constexpr int LAUNCH_REGS = 96, REGS_FIRST = 64, REGS_EPI = 128, REGS_V = 80;
+    static_assert(REGS_FIRST + 2 * REGS_EPI + 2 * REGS_V <= 5 * LAUNCH_REGS, "register split exceeds the launch allocation");
+    static constexpr int TMEM_COLS = 512, BAR_BYTES = 1024;
     static constexpr int SMEM = 1024 + STAGES * STAGE + experts::exchange_bytes<EPI_WARPS>() + BAR_BYTES;
     static constexpr uint32_t IDESC0 = make_idesc(1u, false, false, 256, 0);
     static_assert(SMEM <= 232448, "shared memory");
@@ -71,6 +75,8 @@ struct TileAdapters {
         return __shfl_sync(kAllLanes, mine, at++ & 31);
     }
 };
+
+__device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
 
 // The terms of V[t] . B_a[n] whose factor of B is not finite.
 __device__ __forceinline__ float not_finite_terms(const Params& p, int t, int a, int n) {
@@ -252,6 +258,8 @@ __global__ void __launch_bounds__(Mma::THREADS, 1)
 
     // Every role looks a tile's adapters up for itself. The slices of X and W of a role's first tile
     // need none of them: the launch that computes them may still run.
+    if (warp < Mma::EPI_WARP0) {
+    regs_dec<Mma::REGS_FIRST>();
     if (warp == 0) {
         // ---------------------------------------------------------------- TMA producer
         const uint64_t pol = policy_evict_last();
@@ -418,8 +426,10 @@ __global__ void __launch_bounds__(Mma::THREADS, 1)
             }
         }
         __syncwarp();
-    } else if (warp >= Mma::EPI_WARP0 && warp < Mma::EPI_WARP0 + Mma::EPI_WARPS) {
+    }
+    } else if (warp < Mma::EPI_WARP0 + Mma::EPI_WARPS) {
         // ---------------------------------------------------------------- epilogue
+        regs_inc<Mma::REGS_EPI>();
         const int ew = warp - Mma::EPI_WARP0;
         int local = 0, marks = 0;                // tiles; tiles with adapters
         bool ok = true;
@@ -427,6 +437,15 @@ __global__ void __launch_bounds__(Mma::THREADS, 1)
         grid_dependency_wait();
         for (int item = unit; ok && mma_tile(p, item, t); item += units, ++local) {
             const int buf = local & 1;
+            MmaTile ahead;
+            if (p.C && mma_tile(p, item + units, ahead)) {       // the next tile's C into L2: 32 channels of this warp's rows
+                const int part = ew >> 2, ch = ahead.chan0 + static_cast<int>(rank) * 128 + (ew & 3) * 32, esz = p.c_f32 ? 4 : 2;
+                for (int c = part * 32 + lane; c < ahead.rows; c += 64) {
+                    const char* at = static_cast<const char*>(p.C) + (static_cast<int64_t>(ahead.row0 + c) * p.wide + ch) * esz;
+                    if (ch < p.wide) asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+                    if (ch + 31 < p.wide) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + 31 * esz));
+                }
+            }
             const bool some = p.L > 0 && __ldcg(p.lists + static_cast<int64_t>(t.tt) * kListPitch) > 0;      // rows with adapters
             ok = mma_epilogue(
                 p, t, tmem + static_cast<uint32_t>(buf * Mma::BN), p.kstages > 0 || some, ew,
@@ -447,11 +466,12 @@ __global__ void __launch_bounds__(Mma::THREADS, 1)
         }
         if (!ok) experts::fail(p, ERR_TIMEOUT_EPILOGUE, abort_flag);
         __syncwarp();
-    } else if (warp >= Mma::V_WARP0) {
+    } else {
         // ---------------------------------------------------------------- masked rows of V, a look at B
-        // A thread has one token row of this CTA, whose numbers it loads ahead (a row has one adapter: up to
-        // rank 64 once for the tile), and one channel of B.
-        const int row = threadIdx.x - 32 * Mma::V_WARP0, swizzle = row & 7;
+        regs_dec<Mma::REGS_V>();
+        // Two threads share a token row of this CTA, one has its first numbers and one its second, and a channel of B, half of
+        // its slice each. A row's V is loaded ahead (a row has one adapter: up to rank 64 once for the tile).
+        const int row = (threadIdx.x - 32 * Mma::V_WARP0) & 127, part = (threadIdx.x - 32 * Mma::V_WARP0) >> 7, swizzle = row & 7;
         uint32_t b_phase = 0;                    // bit s: the next parity of b_full[s]
         int stage = 0, marks = 0;
         bool ok = true;
@@ -461,16 +481,13 @@ __global__ void __launch_bounds__(Mma::THREADS, 1)
         for (int item = unit; ok && mma_tile(p, item, t); item += units) {
             const int half = t.n / 2, at = static_cast<int>(rank) * half + row;
             const int own = row < half && at < t.rows && p.L > 0 ? adapter_of(p, t.row0 + at) : -1;
-            const uint4* src = reinterpret_cast<const uint4*>(v_row(p, t.row0 + at));
-            uint4 v[2][8];
+            const uint4* src = reinterpret_cast<const uint4*>(v_row(p, t.row0 + at)) + part * (p.r / 8);
+            uint4 v[8];
             auto load = [&](int i, int vecs) {
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
-                    v[0][c] = v[1][c] = make_uint4(0, 0, 0, 0);
-                    if (own >= 0 && c < vecs) {
-                        v[0][c] = __ldcg(src + i * 8 + c);
-                        v[1][c] = __ldcg(src + p.r / 8 + i * 8 + c);
-                    }
+                    v[c] = make_uint4(0, 0, 0, 0);
+                    if (own >= 0 && c < vecs) v[c] = __ldcg(src + i * 8 + c);
                 }
             };
             if (chunks_r == 1) load(0, p.r / 8);
@@ -485,22 +502,29 @@ __global__ void __launch_bounds__(Mma::THREADS, 1)
                     if (!ok) break;
                     b_phase ^= 1u << stage;
                     uint8_t* w = ring + stage * Mma::STAGE + row * 128;
-                    uint8_t* x = w + Mma::W_BYTES;
-                    const uint4 none = make_uint4(0, 0, 0, 0);
+                    uint8_t* x = w + Mma::W_BYTES + part * slice_x;
+                    const bool hit = own == a;
+                    if (row < half) {
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
-                        const int o = (c ^ swizzle) << 4;
-                        if (c < 2 * steps && row < half) {
-                            *reinterpret_cast<uint4*>(x + o) = own == a ? v[0][c] : none;
-                            *reinterpret_cast<uint4*>(x + slice_x + o) = own == a ? v[1][c] : none;
+                        for (int c = 0; c < 8; ++c)
+                            if (c < 2 * steps) *reinterpret_cast<uint4*>(x + ((c ^ swizzle) << 4)) = hit ? v[c] : make_uint4(0, 0, 0, 0);
+                    }
+                    // a number that is not finite times zero is NaN, and a sum keeps it: one operation for two numbers
+                    __nv_bfloat162 nan = __float2bfloat162_rn(0.0f);
+                    const __nv_bfloat162 zero = nan;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int at_c = c + 4 * part;
+                        if (at_c < vecs) {
+                            const uint4 b4 = *reinterpret_cast<const uint4*>(w + ((at_c ^ swizzle) << 4));
+                            nan = __hfma2(as_bf162(b4.x), zero, nan);
+                            nan = __hfma2(as_bf162(b4.y), zero, nan);
+                            nan = __hfma2(as_bf162(b4.z), zero, nan);
+                            nan = __hfma2(as_bf162(b4.w), zero, nan);
                         }
                     }
-                    bool bad = false;
-#pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        if (c < vecs) bad = not_finite(*reinterpret_cast<const uint4*>(w + ((c ^ swizzle) << 4))) || bad;
-                    if (bad) {
-                        for (int c = 0; c < vecs; ++c) {
+                    if (__hisnan(nan.x) || __hisnan(nan.y)) {
+                        for (int c = 4 * part; c < min(vecs, 4 * part + 4); ++c) {
                             uint32_t* word = reinterpret_cast<uint32_t*>(w + ((c ^ swizzle) << 4));
                             for (int k = 0; k < 4; ++k) {
                                 const uint32_t v2 = word[k];

@@ -45,8 +45,8 @@ struct Call {
     cudaStream_t stream;
 };
 
-// Most rows of a call that go by tiles of 64 rows; most numbers of V that FP32 units compute.
-constexpr int kMostFew = 256, kMostFewShrink = 16384;
+// Most numbers of V that FP32 units compute.
+constexpr int kMostFewShrink = 16384;
 
 dgemm_status_t check_sizes(int64_t T, int64_t N, int64_t K, int64_t r, int64_t L) {
     if (T < 0 || N < 0 || K < 0 || L < 0 || r < 1) return DGEMM_ERR_INVALID_VALUE;
@@ -88,19 +88,30 @@ dgemm_status_t launch_shrink_few(const Params& p, const dg::host::Device& dev, c
 
 dgemm_status_t launch_shrink_many(const Call& c, Params p, const dg::host::Device& dev) {
     p.shrink_tiles = (p.T + Shrink::ROWS - 1) / Shrink::ROWS;
-    p.kstages = (p.K + Shrink::SL - 1) / Shrink::SL;
+    p.kstages = (p.K + Shrink::KS * Shrink::SL - 1) / (Shrink::KS * Shrink::SL);
     p.shrink_cols = std::min(Shrink::MOST_COLS / p.r, std::min(p.L, Shrink::ROWS)) * p.r;
     p.split = 1;
     while (p.split < Shrink::MOST_SPLIT && p.shrink_tiles * p.split * 2 <= dev.num_sms && p.kstages >= 4 * p.split) p.split *= 2;
+    // (two stages always fit: a tile's 256 columns or less, and 128 numbers of its rows, 193 + 64 KB with rank 128, do not)
+    while (Shrink::smem_bytes(p.shrink_cols, 2, p.r) > kShared) p.shrink_cols -= p.r;
     p.stages = 2;
     while (p.stages < Shrink::MOST_STAGES && Shrink::smem_bytes(p.shrink_cols, p.stages + 1, p.r) <= kShared) ++p.stages;
     const int smem = Shrink::smem_bytes(p.shrink_cols, p.stages, p.r);
     alignas(64) CUtensorMap x, a;
-    const uint64_t K = p.K, r = p.r, dx[2] = {K, static_cast<uint64_t>(p.T)}, sx[1] = {K * 2};
+    const uint64_t K = p.K, r = p.r, T = p.T, sl = Shrink::SL;
     const uint64_t da[3] = {K, r, static_cast<uint64_t>(p.L)}, sa[2] = {K * 2, r * K * 2};
-    const uint32_t bx[2] = {Shrink::SL, Shrink::ROWS}, ba[3] = {Shrink::SL, static_cast<uint32_t>(p.r), 1};
-    if (!dg::host::encode_map(&x, kBf16, c.X, 2, dx, sx, bx) || !dg::host::encode_map(&a, kBf16, c.A, 3, da, sa, ba))
-        return DGEMM_ERR_CUDA;
+    const uint32_t ba[3] = {Shrink::SL, static_cast<uint32_t>(p.r), 1};
+    bool ok;
+    if (p.k_whole) {                              // a stage's slices in one copy
+        const uint64_t d[3] = {sl, T, K / sl}, st[2] = {K * 2, 128};
+        const uint32_t b[3] = {Shrink::SL, Shrink::ROWS, Shrink::KS};
+        ok = dg::host::encode_map(&x, kBf16, c.X, 3, d, st, b);
+    } else {
+        const uint64_t d[2] = {K, T}, st[1] = {K * 2};
+        const uint32_t b[2] = {Shrink::SL, Shrink::ROWS};
+        ok = dg::host::encode_map(&x, kBf16, c.X, 2, d, st, b);
+    }
+    if (!ok || !dg::host::encode_map(&a, kBf16, c.A, 3, da, sa, ba)) return DGEMM_ERR_CUDA;
     static std::atomic<unsigned char> ready[dg::host::kMaxDevices];
     if (!allow_shared(ready, dev.id, reinterpret_cast<const void*>(&dg::adapters::adapter_shrink_many), kShared))
         return DGEMM_ERR_CUDA;
@@ -158,7 +169,8 @@ dgemm_status_t launch_few(const Call& c, Params& p, const dg::host::Device& dev)
     p.tiles = (p.T + p.width - 1) / p.width;
     if (static_cast<int64_t>(p.tiles) * ctiles > INT32_MAX / Few::MOST_SPLIT / 2) return DGEMM_ERR_NOT_SUPPORTED;
     // CTAs of a cluster that share K, and channels of a tile: the least time by a model of what a CTA reads (rows of W
-    // and X times its stages, in waves of the clusters that fit at once), the exchange of parts as 150 such units.
+    // and X times its stages, in waves of the clusters that fit at once), a wave's ends as 1000 such units of about 4 ns, the
+    // exchange of parts as 150.
     // (11008 channels: 138 CTAs of 80, not 86 of 128; 4096: 76 pairs of CTAs of 56 channels and half of K.)
     int64_t least = INT64_MAX;
     for (int split = 1; split <= Few::MOST_SPLIT && (split == 1 || p.kstages >= 4 * split); split *= 2) {
@@ -167,7 +179,7 @@ dgemm_status_t launch_few(const Call& c, Params& p, const dg::host::Device& dev)
         const int waves = (p.tiles * ctiles + slots - 1) / slots;
         const int channels = std::min(full, (p.wide / std::max(1, waves * slots / p.tiles) + 8) / 8 * 8);
         const int64_t stages = (p.kstages + split - 1) / split;
-        const int64_t cost = waves * ((channels * (p.gated ? 2 : 1) + p.width) * stages + (split > 1 ? 150 : 0));
+        const int64_t cost = waves * ((channels * (p.gated ? 2 : 1) + p.width) * stages + 1000 + (split > 1 ? 150 : 0));
         if (cost < least) {
             least = cost;
             p.split = split;
@@ -222,7 +234,13 @@ dgemm_status_t launch_prompt(const Call& c, const Params& p, const dg::host::Dev
         if (!dg::host::encode_map(&b, kBf16, c.B, 4, d, st, box)) return DGEMM_ERR_CUDA;
     }
     static std::atomic<unsigned char> ready[dg::host::kMaxDevices];
-    if (!allow_shared(ready, dev.id, reinterpret_cast<const void*>(&dg::adapters::adapter_mma), kShared)) return DGEMM_ERR_CUDA;
+    const void* func = reinterpret_cast<const void*>(&dg::adapters::adapter_mma);
+    if (ready[dev.id].load(std::memory_order_acquire) == 0) {
+        // a register split that adds up to more than the launch holds would wait forever
+        cudaFuncAttributes fa{};
+        if (cudaFuncGetAttributes(&fa, func) != cudaSuccess || fa.numRegs < Mma::LAUNCH_REGS) return DGEMM_ERR_CUDA;
+    }
+    if (!allow_shared(ready, dev.id, func, kShared)) return DGEMM_ERR_CUDA;
     const int units = static_cast<int>(std::min<int64_t>(dev.num_sms / 2, items));
     dg::host::Launch l(static_cast<unsigned>(units * 2), 1, Mma::THREADS, Mma::SMEM, c.stream, 2);
     return cudaLaunchKernelEx(&l.cfg, dg::adapters::adapter_mma, w, x, b, p) == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
@@ -279,7 +297,12 @@ dgemm_status_t run_adapters(const Call& c) {
     p.k_whole = p.K % Few::SL == 0;
     p.kstages = c.W ? (p.K + Few::KS * Few::SL - 1) / (Few::KS * Few::SL) : 0;
     const int forced = dg::host::pair_override();
-    p.prompt = forced >= 0 ? forced : p.T > kMostFew;
+    // One wave of the few-row form's tiles, or the prompt form: on the device 128 rows of 4096 channels, every row another
+    // adapter of rank 64, 33 against 55 us, 256 rows 47 against 63 (one request: 28, 29), 384 115 against 99; of 11008
+    // channels 64 rows 37 against 49, 128 65 against 61 (one request: 48, 31).
+    const int full = p.gated ? 64 : 128;
+    const int64_t few_tiles = static_cast<int64_t>((p.T + Few::MOST_COLS - 1) / Few::MOST_COLS) * ((p.wide + full - 1) / full);
+    p.prompt = forced >= 0 ? forced : few_tiles > dev.num_sms;
     if (p.prompt) prompt_tiles(p, dev);
     if (p.L > 0) {
         const dgemm_status_t s = static_cast<int64_t>(p.T) * p.r > kMostFewShrink ? launch_shrink_many(c, p, dev) : launch_shrink_few(p, dev, c.stream);

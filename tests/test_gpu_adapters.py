@@ -41,6 +41,8 @@ class Problem:
             self.ids = torch.randint(-1, max(L, 1), (T,), generator=g).to(torch.int32)
             if order == "runs":
                 self.ids = self.ids.sort().values.roll(T // 3)
+                tail = min(T // 8, 30)      # prompts, and behind them sequences of one row
+                self.ids[T - tail:] = torch.randint(-1, max(L, 1), (tail,), generator=g).to(torch.int32)
             if T > 3:
                 self.ids[T // 2] = L            # outside: no adapter
                 self.ids[T // 3] = -2 ** 31
