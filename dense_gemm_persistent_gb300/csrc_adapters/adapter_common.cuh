@@ -37,7 +37,56 @@ struct Params : experts::Params {      // (of those: C, D, bias, N, K, wide, gat
 };
 
 constexpr int kMostWidth = 256;               // rows of a token tile of the prompt form
-constexpr int kListPitch = 4 + kMostWidth;    // [0] the count, from [4] on the adapters in order
+constexpr int kListPitch = 4 + kMostWidth;    // [0] the count, from [1] on the adapters in order
+
+// y / (1 + e^-y) by the special function unit, 2^-21 relative.
+__device__ __forceinline__ float silu(float y) {
+    float e, q;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(y * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(1.0f + e));
+    return y * q;
+}
+
+// (r0, r1) = (a0 + b0, a1 + b1) as one instruction.
+__device__ __forceinline__ void add2(float& r0, float& r1, float a0, float a1, float b0, float b1) {
+    asm("{\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(r0), "=f"(r1)
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+// Two of silu's values, the products and sums as pairs.
+__device__ __forceinline__ void silu2(float& y0, float& y1) {
+    float e0, e1, q0, q1;
+    fmul2(e0, e1, y0, y1, -1.4426950408889634f, -1.4426950408889634f);
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e0) : "f"(e0));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e1) : "f"(e1));
+    add2(e0, e1, e0, e1, 1.0f, 1.0f);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q0) : "f"(e0));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q1) : "f"(e1));
+    fmul2(y0, y1, y0, y1, q0, q1);
+}
+
+// The activation of N values: the switch is taken once for all of them.
+template <int N>
+__device__ __forceinline__ void activate(float (&v)[N], int act) {
+    switch (act) {
+        case DGEMM_ACT_RELU:
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[j] = experts::relu(v[j]);
+            break;
+        case DGEMM_ACT_GELU:
+#pragma unroll
+            for (int j = 0; j < N; ++j) v[j] = experts::gelu(v[j]);
+            break;
+        case DGEMM_ACT_SILU:
+#pragma unroll
+            for (int j = 0; j < N; j += 2) silu2(v[j], v[j + 1]);
+            break;
+        default:
+            break;
+    }
+}
 
 __device__ __forceinline__ float ld_shared_cluster_f32(uint32_t addr) {
     float v;
@@ -100,7 +149,7 @@ __device__ __forceinline__ void list_tile(const Params& p, int tile, unsigned* w
     int* list = p.lists + static_cast<int64_t>(tile) * kListPitch;
     for (int i = tid; i < rows; i += threads) {
         const int a = adapter_of(p, row0 + i);
-        if (a >= 0) list[4 + place_of(p, words, a)] = a;          // (rows of one adapter write the same)
+        if (a >= 0) list[1 + place_of(p, words, a)] = a;          // (rows of one adapter write the same)
     }
     if (tid == 0) list[0] = marked(p, words);
     sync();

@@ -41,10 +41,10 @@ struct Few {
 };
 
 template <int ACT>
-__device__ __forceinline__ float activate(float v) {
+__device__ __forceinline__ float activate_one(float v) {
     if constexpr (ACT == DGEMM_ACT_RELU) return experts::relu(v);
     else if constexpr (ACT == DGEMM_ACT_GELU) return experts::gelu(v);
-    else if constexpr (ACT == DGEMM_ACT_SILU) return experts::silu(v);
+    else if constexpr (ACT == DGEMM_ACT_SILU) return silu(v);
     else return v;
 }
 
@@ -71,7 +71,7 @@ __device__ __forceinline__ void finish_rows(const Params& p, const float* parts,
             if (GATED) product_up += from[p.channels];
         }
         v += product;
-        v = GATED ? experts::silu(v) * (u + product_up) : activate<ACT>(v);
+        v = GATED ? silu(v) * (u + product_up) : activate_one<ACT>(v);
         const int64_t o = static_cast<int64_t>(row0 + c) * p.wide + ch;
         if (p.d_f32) static_cast<float*>(p.D)[o] = v;
         else static_cast<__nv_bfloat16*>(p.D)[o] = __float2bfloat16_rn(v);

@@ -54,29 +54,57 @@ __device__ __forceinline__ bool mma_tile(const Params& p, int item, MmaTile& t) 
     return true;
 }
 
-// The adapters of a token tile, looked up by a whole warp 32 at a time.
+// The adapters of a token tile, looked up by a whole warp: one load brings the count and the first 31, and may be
+// made a tile ahead.
 struct TileAdapters {
     const int* list;
-    int count, at, mine;
-    __device__ __forceinline__ void open(const Params& p, int tt) {
-        list = p.lists + static_cast<int64_t>(tt) * kListPitch;
-        count = p.L > 0 ? __ldcg(list) : 0;
-        at = 0;
-        look();
+    int count, at, mine, ahead;
+    __device__ __forceinline__ void look_ahead(const Params& p, int tt) {
+        ahead = p.L > 0 ? __ldcg(p.lists + static_cast<int64_t>(tt) * kListPitch + (threadIdx.x & 31)) : 0;
     }
-    __device__ __forceinline__ void look() {
-        const int i = at + static_cast<int>(threadIdx.x & 31);
-        mine = i < count ? __ldcg(list + 4 + i) : -1;
+    __device__ __forceinline__ void open(const Params& p, int tt) {          // (after look_ahead of the same tile)
+        list = p.lists + static_cast<int64_t>(tt) * kListPitch;
+        mine = ahead;
+        count = __shfl_sync(kAllLanes, mine, 0);
+        at = 0;
     }
     // the next one, -1 when there is none left
     __device__ __forceinline__ int next() {
         if (at >= count) return -1;
-        if (at > 0 && at % 32 == 0) look();
-        return __shfl_sync(kAllLanes, mine, at++ & 31);
+        const int place = ++at;
+        if ((place & 31) == 0) mine = place + static_cast<int>(threadIdx.x & 31) <= count ? __ldcg(list + place + (threadIdx.x & 31)) : -1;
+        return __shfl_sync(kAllLanes, mine, place & 31);
     }
 };
 
 __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
+
+// Puts zeros in the place of numbers that are not finite in the 16-byte vectors [first, last) of a swizzled row; whether
+// there were any. Such a number times zero is NaN, and a sum keeps it: one operation for two numbers.
+__device__ __forceinline__ bool make_finite(uint8_t* row, int swizzle, int first, int last) {
+    const __nv_bfloat162 zero = __float2bfloat162_rn(0.0f);
+    __nv_bfloat162 nan[2] = {zero, zero};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const int c = first + k;
+        if (c >= last) break;
+        const uint4 b = *reinterpret_cast<const uint4*>(row + ((c ^ swizzle) << 4));
+        nan[0] = __hfma2(as_bf162(b.x), zero, nan[0]);
+        nan[1] = __hfma2(as_bf162(b.y), zero, nan[1]);
+        nan[0] = __hfma2(as_bf162(b.z), zero, nan[0]);
+        nan[1] = __hfma2(as_bf162(b.w), zero, nan[1]);
+    }
+    const __nv_bfloat162 any = __hadd2(nan[0], nan[1]);
+    if (!__hisnan(any.x) && !__hisnan(any.y)) return false;
+    for (int c = first; c < last; ++c) {
+        uint32_t* word = reinterpret_cast<uint32_t*>(row + ((c ^ swizzle) << 4));
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t v = word[k];
+            word[k] = ((v & 0x7F80u) == 0x7F80u ? 0u : v & 0xFFFFu) | ((v & 0x7F800000u) == 0x7F800000u ? 0u : v & 0xFFFF0000u);
+        }
+    }
+    return true;
+}
 
 // The terms of V[t] . B_a[n] whose factor of B is not finite.
 __device__ __forceinline__ float not_finite_terms(const Params& p, int t, int a, int n) {
@@ -162,7 +190,7 @@ __device__ __forceinline__ bool mma_epilogue(const Params& p, const MmaTile& t, 
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
                 const float x = theirs[j * 32 + lane];
-                y[j] = up ? experts::silu(x) * v[16 + j] : experts::silu(v[j]) * x;
+                y[j] = up ? silu(x) * v[16 + j] : silu(v[j]) * x;
             }
             const int skip = up ? 16 : 0;
             experts::store_columns<16>(p, at + static_cast<int64_t>(skip) * p.wide, y, live, valid - skip);
@@ -188,7 +216,7 @@ __device__ __forceinline__ bool mma_epilogue(const Params& p, const MmaTile& t, 
 #pragma unroll
                 for (int j = 0; j < 32; ++j) v[j] += more[j];
             }
-            experts::activate32(v, p.act);
+            activate(v, p.act);
             experts::store_columns<32>(p, at, v, live, valid);
         }
     }
@@ -287,6 +315,7 @@ __global__ void __launch_bounds__(Mma::THREADS, 1)
             const int x0 = t.row0 + static_cast<int>(rank) * (t.n / 2);
             if (waited || p.kstages == 0) {
                 wait_v();
+                ta.look_ahead(p, t.tt);
                 ta.open(p, t.tt);
             }
             for (int kb = 0; kb < p.kstages; ++kb) {
@@ -316,6 +345,7 @@ __global__ void __launch_bounds__(Mma::THREADS, 1)
             if (!ok || stalled) break;
             if (!waited) {
                 wait_v();
+                ta.look_ahead(p, t.tt);
                 ta.open(p, t.tt);
             }
             for (int a = ta.next(); ok && !stalled && a >= 0; a = ta.next()) {
@@ -373,6 +403,7 @@ __global__ void __launch_bounds__(Mma::THREADS, 1)
                 const uint32_t idesc = Mma::IDESC0 | (static_cast<uint32_t>(__shfl_sync(kAllLanes, t.n, 0) >> 3) << 17);
                 if (waited || p.kstages == 0) {
                     wait_v();
+                    ta.look_ahead(p, t.tt);
                     ta.open(p, t.tt);
                 }
                 for (int kb = 0; kb < p.kstages; ++kb) {
@@ -392,6 +423,7 @@ __global__ void __launch_bounds__(Mma::THREADS, 1)
                 if (!ok) break;
                 if (!waited) {
                     wait_v();
+                    ta.look_ahead(p, t.tt);
                     ta.open(p, t.tt);
                 }
                 uint32_t more = p.kstages > 0;
@@ -491,6 +523,7 @@ __global__ void __launch_bounds__(Mma::THREADS, 1)
                 }
             };
             if (chunks_r == 1) load(0, p.r / 8);
+            ta.look_ahead(p, t.tt);
             ta.open(p, t.tt);
             stage = (stage + p.kstages) % S;
             bool found = false;
@@ -509,31 +542,7 @@ __global__ void __launch_bounds__(Mma::THREADS, 1)
                         for (int c = 0; c < 8; ++c)
                             if (c < 2 * steps) *reinterpret_cast<uint4*>(x + ((c ^ swizzle) << 4)) = hit ? v[c] : make_uint4(0, 0, 0, 0);
                     }
-                    // a number that is not finite times zero is NaN, and a sum keeps it: one operation for two numbers
-                    __nv_bfloat162 nan = __float2bfloat162_rn(0.0f);
-                    const __nv_bfloat162 zero = nan;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int at_c = c + 4 * part;
-                        if (at_c < vecs) {
-                            const uint4 b4 = *reinterpret_cast<const uint4*>(w + ((at_c ^ swizzle) << 4));
-                            nan = __hfma2(as_bf162(b4.x), zero, nan);
-                            nan = __hfma2(as_bf162(b4.y), zero, nan);
-                            nan = __hfma2(as_bf162(b4.z), zero, nan);
-                            nan = __hfma2(as_bf162(b4.w), zero, nan);
-                        }
-                    }
-                    if (__hisnan(nan.x) || __hisnan(nan.y)) {
-                        for (int c = 4 * part; c < min(vecs, 4 * part + 4); ++c) {
-                            uint32_t* word = reinterpret_cast<uint32_t*>(w + ((c ^ swizzle) << 4));
-                            for (int k = 0; k < 4; ++k) {
-                                const uint32_t v2 = word[k];
-                                word[k] = ((v2 & 0x7F80u) == 0x7F80u ? 0u : v2 & 0xFFFFu) |
-                                          ((v2 & 0x7F800000u) == 0x7F800000u ? 0u : v2 & 0xFFFF0000u);
-                            }
-                        }
-                        found = true;
-                    }
+                    found = make_finite(w, swizzle, 4 * part, min(vecs, 4 * part + 4)) || found;
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) {

@@ -4,6 +4,7 @@
 #include <atomic>
 #include <cstring>
 
+#include "adapter_beside.cuh"
 #include "adapter_few.cuh"
 #include "adapter_mma.cuh"
 #include "adapter_shrink.cuh"
@@ -246,6 +247,30 @@ dgemm_status_t launch_prompt(const Call& c, const Params& p, const dg::host::Dev
     return cudaLaunchKernelEx(&l.cfg, dg::adapters::adapter_mma, w, x, b, p) == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
 }
 
+// Beside a product, BF16 in and out, rows on 16 bytes.
+dgemm_status_t launch_beside(const Call& c, const Params& p, const dg::host::Device& dev) {
+    using dg::adapters::Beside;
+    const int64_t items = static_cast<int64_t>(p.tiles) * p.ctiles;
+    if (items > INT32_MAX / 2) return DGEMM_ERR_NOT_SUPPORTED;
+    const uint64_t N = p.N, T = p.T, r = p.r, L = p.L, d[2] = {N, T}, st[1] = {N * 2};
+    const uint32_t box[2] = {Beside::SL, Beside::ROWS};
+    alignas(64) CUtensorMap cm, dm, b;
+    std::memset(&cm, 0, sizeof cm);
+    std::memset(&b, 0, sizeof b);
+    bool ok = dg::host::encode_map(&dm, kBf16, c.D, 2, d, st, box) && (!c.C || dg::host::encode_map(&cm, kBf16, c.C, 2, d, st, box));
+    if (ok && p.L > 0) {
+        const uint64_t db[4] = {r, N, 1, L}, sb[3] = {r * 2, N * r * 2, N * r * 2};
+        const uint32_t bb[4] = {Beside::SL, Beside::COLS, 1, 1};
+        ok = dg::host::encode_map(&b, kBf16, c.B, 4, db, sb, bb);
+    }
+    if (!ok) return DGEMM_ERR_CUDA;
+    static std::atomic<unsigned char> ready[dg::host::kMaxDevices];
+    if (!allow_shared(ready, dev.id, reinterpret_cast<const void*>(&dg::adapters::adapter_beside), kShared)) return DGEMM_ERR_CUDA;
+    const int ctas = static_cast<int>(std::min<int64_t>(dev.num_sms, items));
+    dg::host::Launch l(static_cast<unsigned>(ctas), 1, Beside::THREADS, Beside::SMEM, c.stream);
+    return cudaLaunchKernelEx(&l.cfg, dg::adapters::adapter_beside, cm, dm, b, p) == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
+}
+
 dgemm_status_t run_adapters(const Call& c) {
     const dgemm_status_t st = check_sizes(c.T, c.N, c.K, c.r, c.L);
     if (st != DGEMM_OK) return st;
@@ -303,12 +328,20 @@ dgemm_status_t run_adapters(const Call& c) {
     const int full = p.gated ? 64 : 128;
     const int64_t few_tiles = static_cast<int64_t>((p.T + Few::MOST_COLS - 1) / Few::MOST_COLS) * ((p.wide + full - 1) / full);
     p.prompt = forced >= 0 ? forced : few_tiles > dev.num_sms;
-    if (p.prompt) prompt_tiles(p, dev);
+    // Beside a product in BF16 whose rows TMA can copy: a form of its own (4096 x 11008 with SiLU 116 us in the general one).
+    const bool beside = p.prompt && !c.W && c.d_dtype == DGEMM_BF16 && (!c.C || c.c_dtype == DGEMM_BF16) && p.N % 8 == 0;
+    if (beside) {
+        p.width = dg::adapters::Beside::ROWS;
+        p.tiles = (p.T + p.width - 1) / p.width;
+        p.ctiles = (p.N + dg::adapters::Beside::COLS - 1) / dg::adapters::Beside::COLS;
+    } else if (p.prompt) {
+        prompt_tiles(p, dev);
+    }
     if (p.L > 0) {
         const dgemm_status_t s = static_cast<int64_t>(p.T) * p.r > kMostFewShrink ? launch_shrink_many(c, p, dev) : launch_shrink_few(p, dev, c.stream);
         if (s != DGEMM_OK) return s;
     }
-    return p.prompt ? launch_prompt(c, p, dev) : launch_few(c, p, dev);
+    return beside ? launch_beside(c, p, dev) : p.prompt ? launch_prompt(c, p, dev) : launch_few(c, p, dev);
 }
 
 }  // namespace

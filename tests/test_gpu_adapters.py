@@ -144,20 +144,23 @@ def test_nothing_to_do():
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 def test_a_bad_adapter_stays_with_its_request(form, T, order, bad):
     p = Problem(T, 264, 256, 16, 6, order=order)
-    clean = p.project(out=F32).cpu()
-    clean_add = p.add(out=F32, c=F32).cpu()
+    calls = [(lambda: p.project(out=F32).cpu(), dict(W=p.W), F32), (lambda: p.add(out=F32, c=F32).cpu(), dict(C=p.C), F32),
+             (lambda: p.add(out=BF, c=BF).cpu(), dict(C=p.C.to(BF)), BF)]
+    clean = [call() for call, _, _ in calls]
     hit = p.ids == 2
     assert bool(hit.any()) and not bool(hit.all())
     for where in ("A", "B"):
         keep = getattr(p, where).clone()
         getattr(p, where)[2, 3, 5] = bad
-        for got, was in ((p.project(out=F32).cpu(), clean), (p.add(out=F32, c=F32).cpu(), clean_add)):
+        for (call, beside, out), was in zip(calls, clean):
+            got = call()
             assert torch.equal(got[~hit], was[~hit])
-            want = ref.adapters(p.X, p.A, p.B, p.ids, **(dict(W=p.W) if was is clean else dict(C=p.C)), scale=p.scale, out_dtype=F32)[0]
+            want = ref.adapters(p.X, p.A, p.B, p.ids, **beside, scale=p.scale, out_dtype=out)[0]
             assert torch.equal(torch.isfinite(got), torch.isfinite(want))
             # one infinite factor: the same infinity (or NaN where infinities of both signs or a NaN meet)
             if where == "B":
-                assert torch.equal(torch.isnan(got), torch.isnan(want)) and torch.equal(got[torch.isinf(want)], want[torch.isinf(want)].float())
+                assert torch.equal(torch.isnan(got), torch.isnan(want))
+                assert torch.equal(got[torch.isinf(want)], want[torch.isinf(want)].to(out))
         setattr(p, where, keep)
 
 
