@@ -170,6 +170,13 @@ __device__ __forceinline__ void store_v(const Params& p, int t, int at, const fl
     *reinterpret_cast<uint4*>(out) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
     *reinterpret_cast<uint4*>(out + p.r) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
 }
+// One of them.
+__device__ __forceinline__ void store_one(const Params& p, int t, int at, float v) {
+    const __nv_bfloat16 hi = __float2bfloat16_rn(v);
+    const float rest = v - __bfloat162float(hi);
+    v_row(p, t)[at] = hi;
+    v_row(p, t)[p.r + at] = __float2bfloat16_rn(fabsf(rest) < INFINITY ? rest : 0.0f);
+}
 
 }  // namespace adapters
 }  // namespace dg

@@ -64,10 +64,7 @@ __global__ void __launch_bounds__(SHRINK_THREADS) adapter_shrink_few(const __gri
         for (int i = 0; i < SHRINK_THREADS / 32; ++i) s += part[i][threadIdx.x];
         if (p.scale) s *= p.scale[a];
         const int j = j0 + threadIdx.x;
-        const __nv_bfloat16 hi = __float2bfloat16_rn(s);
-        const float rest = s - __bfloat162float(hi);
-        v_row(p, t)[j] = hi;
-        v_row(p, t)[p.r + j] = __float2bfloat16_rn(fabsf(rest) < INFINITY ? rest : 0.0f);      // (see store_v)
+        store_one(p, t, j, s);
     }
 }
 
@@ -86,7 +83,7 @@ struct Shrink {
     static constexpr int MOST_COLS = 256, MOST_STAGES = 6, MOST_SPLIT = 8;
     static constexpr int EPI_WARP0 = 2, HELP_WARP0 = 6, THREADS = 320, HELPERS = 128;
     static constexpr int TMEM_COLS = 256, WORDS = DGEMM_MAX_ADAPTERS / 32;
-    static constexpr int FEW = 4, MOST_SINGLE = 32, BATCH = 32;      // single rows: see above; tiles looked at together
+    static constexpr int FEW = 4, MOST_SINGLE = 32, SINGLE_N = 4, BATCH = 32;      // single rows: see above; tiles looked at together
     static constexpr int TABLES = 2 * WORDS * 4 + 2 * ROWS * 4 + BATCH * 16, BAR_BYTES = 256;
     static constexpr uint32_t IDESC0 = make_idesc(1u, false, false, 128, 0);
     static constexpr int stage_bytes(int cols) { return X_BYTES + KS * cols * 128; }
@@ -102,60 +99,65 @@ __device__ __forceinline__ unsigned single_rows(int a) {
     return __ballot_sync(kAllLanes, a >= 0 && __popc(same) < Shrink::FEW);
 }
 
-// Eight numbers of V of one row by a warp.
+// Four numbers of V of one row by a warp. (Eight took twice the time: half the loads of X and A on their way.)
 __device__ __forceinline__ void single_row(const Params& p, int t, int at) {
+    constexpr int N = Shrink::SINGLE_N, U = 4;
     const int lane = threadIdx.x & 31, a = adapter_of(p, t), vecs = p.K / 8;
     const uint4* x = reinterpret_cast<const uint4*>(p.X + static_cast<int64_t>(t) * p.K);
     const uint4* w = reinterpret_cast<const uint4*>(p.low + (static_cast<int64_t>(a) * p.r + at) * p.K);
-    float s0[8], s1[8];
+    float s0[N], s1[N];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s0[j] = s1[j] = 0.0f;
-    for (int i0 = lane; i0 < vecs; i0 += 64) {
-        uint4 xv[2], wv[2][8];
+    for (int j = 0; j < N; ++j) s0[j] = s1[j] = 0.0f;
+    for (int i0 = lane; i0 < vecs; i0 += 32 * U) {
+        uint4 xv[U], wv[U][N];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < U; ++u) {
             const int i = i0 + 32 * u;
             const bool there = i < vecs;
             xv[u] = there ? __ldg(x + i) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) wv[u][j] = there ? __ldg(w + static_cast<int64_t>(j) * vecs + i) : make_uint4(0, 0, 0, 0);
+            for (int j = 0; j < N; ++j) wv[u][j] = there ? __ldg(w + static_cast<int64_t>(j) * vecs + i) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < U; ++u) {
             const float4 x0 = make_float4(bf16_lo(xv[u].x), bf16_hi(xv[u].x), bf16_lo(xv[u].y), bf16_hi(xv[u].y));
             const float4 x1 = make_float4(bf16_lo(xv[u].z), bf16_hi(xv[u].z), bf16_lo(xv[u].w), bf16_hi(xv[u].w));
 #pragma unroll
-            for (int j = 0; j < 8; ++j) fma8(s0[j], s1[j], wv[u][j], x0, x1);
+            for (int j = 0; j < N; ++j) fma8(s0[j], s1[j], wv[u][j], x0, x1);
         }
     }
     const float scale = p.scale ? p.scale[a] : 1.0f;
-    float v[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        v[j] = s0[j] + s1[j];
-        for (int o = 16; o > 0; o >>= 1) v[j] += __shfl_xor_sync(kAllLanes, v[j], o);
-        v[j] *= scale;
+    for (int j = 0; j < N; ++j) {
+        float v = s0[j] + s1[j];
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kAllLanes, v, o);
+        if (lane == 0) store_one(p, t, at + j, v * scale);
     }
-    if (lane == 0) store_v(p, t, at, v);
 }
 
-// The single rows of all tiles: an item is a row's eight numbers, the items of a tile go round the launch's warps. masks:
+// The single rows of all tiles: an item is a row's four numbers, the items of a tile go round the launch's warps. masks:
 // [BATCH][4], the single rows of a tile.
 template <class Sync>
 __device__ __forceinline__ void share_single_rows(const Params& p, uint4* masks, int warp, Sync sync) {
-    const int lane = threadIdx.x & 31, groups = p.r / 8, all = static_cast<int>(gridDim.x) * 4, me = static_cast<int>(blockIdx.x) * 4 + warp;
+    const int lane = threadIdx.x & 31, groups = p.r / Shrink::SINGLE_N, all = static_cast<int>(gridDim.x) * 4, me = static_cast<int>(blockIdx.x) * 4 + warp;
     for (int base = 0; base < p.shrink_tiles; base += Shrink::BATCH) {
-        for (int k = warp; k < Shrink::BATCH && base + k < p.shrink_tiles; k += 4) {
-            int a[4];
+        // (four tiles' rows are loaded together)
+        for (int k0 = warp; k0 < Shrink::BATCH && base + k0 < p.shrink_tiles; k0 += 16) {
+            int a[4][4];
 #pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                const int t = (base + k) * Shrink::ROWS + b * 32 + lane;
-                a[b] = t < p.T ? adapter_of(p, t) : -1;
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const int t = (base + k0 + 4 * k) * Shrink::ROWS + b * 32 + lane;
+                    a[k][b] = t < p.T ? adapter_of(p, t) : -1;
+                }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                unsigned m[4];
+#pragma unroll
+                for (int b = 0; b < 4; ++b) m[b] = single_rows(a[k][b]);
+                if (lane == 0) masks[k0 + 4 * k] = make_uint4(m[0], m[1], m[2], m[3]);
             }
-            unsigned m[4];
-#pragma unroll
-            for (int b = 0; b < 4; ++b) m[b] = single_rows(a[b]);
-            if (lane == 0) masks[k] = make_uint4(m[0], m[1], m[2], m[3]);
         }
         sync();
         const bool there = base + lane < p.shrink_tiles;
@@ -176,7 +178,7 @@ __device__ __forceinline__ void share_single_rows(const Params& p, uint4* masks,
                     j = j < c ? -1 : j - c;
                     if (j < 0) j = INT_MIN / 2;
                 }
-                single_row(p, (base + l) * Shrink::ROWS + row, item % groups * 8);
+                single_row(p, (base + l) * Shrink::ROWS + row, item % groups * Shrink::SINGLE_N);
             }
         }
         sync();
