@@ -363,9 +363,8 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
             __syncwarp();
         };
         for (int k = 0; k < p.ahead; ++k) copy(ew + k * Few::EPI_WARPS, k);
-        if (!p.wait_first) grid_dependency_wait();              // V, and nothing of D before the stream allows it
-        // C as the first term of the rows' sums; V of the rows. (Loads of four rows at a time before the first store: one
-        // after another they took 0.7 us a row.)
+        // C as the first term of the rows' sums, while V may still be under way. (Loads of four rows at a time before the
+        // first store: one after another they took 0.7 us a row.)
         for (int q0 = ew; q0 < own; q0 += 4 * Few::EPI_WARPS) {
             float first[4][4];
 #pragma unroll
@@ -387,11 +386,14 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
                     for (int k = 0; k < 4; ++k) beside[(q0 + n * Few::EPI_WARPS) * 128 + lane + 32 * k] = first[n][k];
                 }
         }
+        if (!p.wait_first) grid_dependency_wait();              // V, and nothing of D before the stream allows it
         if (mine > 0) {
-            for (int q0 = ew; q0 < mine; q0 += 4 * Few::EPI_WARPS) {
-                uint2 hi[4], lo[4];
+            {
+                constexpr int MOST = Few::MOST_COLS / Few::EPI_WARPS;       // rows of a warp: all of their loads together
+                const int q0 = ew;
+                uint2 hi[MOST], lo[MOST];
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
+                for (int n = 0; n < MOST; ++n) {
                     const int q = q0 + n * Few::EPI_WARPS;
                     hi[n] = lo[n] = make_uint2(0, 0);
                     if (q < mine && lane < p.r / 4) {       // (rows without an adapter have no V; theirs is not used)
@@ -401,7 +403,7 @@ __global__ void __launch_bounds__(Few::THREADS, 1)
                     }
                 }
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
+                for (int n = 0; n < MOST; ++n) {
                     const int q = q0 + n * Few::EPI_WARPS;
                     if (q < mine && lane < p.r / 4)
                         reinterpret_cast<float4*>(v_rows + q * p.r)[lane] =
