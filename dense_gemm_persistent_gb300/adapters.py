@@ -10,33 +10,43 @@ before the call.
 """
 from __future__ import annotations
 
+import torch
+
 import dense_gemm_persistent_gb300 as _dg
 
 from ._lib import ACT, F32
-from .experts import _BF16, _F32, _FLOATS, _I32, _act, _device, _float_code, _matrix, _maybe, _need, _stream, _workspace
+from .experts import _BF16, _F32, _FLOATS, _I32, GROUPED_ACT, _act, _device, _float_code, _matrix, _need, _stream, _workspace
+
+_bf16 = torch.bfloat16
+_SWIGLU = GROUPED_ACT["swiglu"]
 
 
 def _low_rank(X, A, B, ids, scale, dev):
-    _matrix(X, "X", _BF16, dev)
-    _matrix(A, "A", _BF16, dev, 3)
-    _matrix(B, "B", _BF16, dev, 3)
+    # the common case in few steps; anything else is looked at, and named, below
+    if not (X is not None and A is not None and B is not None and X.dtype is _bf16 and A.dtype is _bf16 and B.dtype is _bf16 and X.dim() == 2 and A.dim() == 3 and B.dim() == 3
+            and X.is_contiguous() and A.is_contiguous() and B.is_contiguous() and dev >= 0 and A.get_device() == dev
+            and B.get_device() == dev):
+        _matrix(X, "X", _BF16, dev)
+        _matrix(A, "A", _BF16, dev, 3)
+        _matrix(B, "B", _BF16, dev, 3)
     T, K = X.shape
     L, r, K2 = A.shape
+    L2, N, r2 = B.shape
     if K2 != K:
         raise ValueError(f"inner dimensions differ: X has K={K}, A has K={K2}")
-    if B.shape[0] != L or B.shape[2] != r:
+    if L2 != L or r2 != r:
         raise ValueError(f"A has shape {tuple(A.shape)}, B {tuple(B.shape)}: expected [L,r,K] and [L,N,r]")
     _need(ids, "ids", (T,), _I32, dev)
-    _maybe(scale, "scale", (L,), _F32, dev)
-    return T, K, L, r, B.shape[1]
+    if scale is not None:
+        _need(scale, "scale", (L,), _F32, dev)
+    return T, K, L, r, N
 
 
-def _apart(D, **operands):
-    """D is written while the operands are still read."""
-    lo = D.data_ptr()
-    hi = lo + D.nbytes
-    for name, t in operands.items():
-        if t is not None and t.data_ptr() < hi and lo < t.data_ptr() + t.nbytes:
+def _apart(d, d_bytes, *operands):
+    """D is written while the operands are still read: (name, address, bytes) of each."""
+    end = d + d_bytes
+    for name, p, n in operands:
+        if p and p < end and d < p + n:
             raise ValueError(f"D overlaps {name}")
 
 
@@ -54,13 +64,18 @@ def dgemm_adapter_bf16(X, W, A, B, ids, D, *, scale=None, bias=None, act="none",
     T, K, L, r, N = _low_rank(X, A, B, ids, scale, dev)
     _need(W, "W", (N, K), _BF16, dev)
     code = _act(act)
-    _need(D, "D", (T, N // 2 if act == "swiglu" else N), _FLOATS, dev)
-    _maybe(bias, "bias", (N,), _F32, dev)
-    _apart(D, X=X, W=W, A=A, B=B, ws=ws)
-    st = _dg.load().dgemm_adapter_bf16(X.data_ptr(), W.data_ptr(), A.data_ptr(), B.data_ptr(), ids.data_ptr(),
-                                       _dg._ptr(scale), L, r, D.data_ptr(), _float_code(D), T, N, K, _dg._ptr(bias), code,
-                                       *_workspace(ws, dev), _stream(stream, dev))
-    _dg._check(st, "dgemm_adapter_bf16")
+    wide = N // 2 if code == _SWIGLU else N
+    _need(D, "D", (T, wide), _FLOATS, dev)
+    if bias is not None:
+        _need(bias, "bias", (N,), _F32, dev)
+    x, w, a, b, d, dt = X.data_ptr(), W.data_ptr(), A.data_ptr(), B.data_ptr(), D.data_ptr(), _float_code(D)
+    work, work_bytes = _workspace(ws, dev)
+    _apart(d, T * wide * (4 if dt == F32 else 2), ("X", x, 2 * T * K), ("W", w, 2 * N * K), ("A", a, 2 * L * r * K),
+           ("B", b, 2 * L * N * r), ("ws", work, work_bytes))
+    st = _dg.load().dgemm_adapter_bf16(x, w, a, b, ids.data_ptr(), None if scale is None else scale.data_ptr(), L, r, d, dt, T, N, K,
+                                       None if bias is None else bias.data_ptr(), code, work, work_bytes, _stream(stream, dev))
+    if st:
+        _dg._check(st, "dgemm_adapter_bf16")
     return D
 
 
@@ -75,14 +90,20 @@ def dgemm_adapter_add(X, A, B, ids, D, *, C=None, scale=None, bias=None, act="no
     if act not in ACT:
         raise ValueError(f"act must be one of {sorted(ACT)}, not {act!r}")
     _need(D, "D", (T, N), _FLOATS, dev)
-    _maybe(C, "C", (T, N), _FLOATS, dev)
-    _maybe(bias, "bias", (N,), _F32, dev)
-    same = C is not None and C.data_ptr() == D.data_ptr() and C.dtype == D.dtype
-    _apart(D, X=X, A=A, B=B, C=None if same else C, ws=ws)
-    st = _dg.load().dgemm_adapter_add(X.data_ptr(), A.data_ptr(), B.data_ptr(), ids.data_ptr(), _dg._ptr(scale), L, r,
-                                      _dg._ptr(C), F32 if C is None else _float_code(C), D.data_ptr(), _float_code(D), T, N,
-                                      K, _dg._ptr(bias), ACT[act], *_workspace(ws, dev), _stream(stream, dev))
-    _dg._check(st, "dgemm_adapter_add")
+    if C is not None:
+        _need(C, "C", (T, N), _FLOATS, dev)
+    if bias is not None:
+        _need(bias, "bias", (N,), _F32, dev)
+    x, a, b, d, dt = X.data_ptr(), A.data_ptr(), B.data_ptr(), D.data_ptr(), _float_code(D)
+    c, ct = (None, F32) if C is None else (C.data_ptr(), _float_code(C))
+    work, work_bytes = _workspace(ws, dev)
+    _apart(d, T * N * (4 if dt == F32 else 2), ("X", x, 2 * T * K), ("A", a, 2 * L * r * K), ("B", b, 2 * L * N * r),
+           ("C", None if c == d and ct == dt else c, T * N * (4 if ct == F32 else 2)), ("ws", work, work_bytes))
+    st = _dg.load().dgemm_adapter_add(x, a, b, ids.data_ptr(), None if scale is None else scale.data_ptr(), L, r, c, ct, d, dt, T,
+                                      N, K, None if bias is None else bias.data_ptr(), ACT[act], work, work_bytes,
+                                      _stream(stream, dev))
+    if st:
+        _dg._check(st, "dgemm_adapter_add")
     return D
 
 
