@@ -4,8 +4,8 @@
 // token rows (the MMA's rows) by 128 channels (its columns); C comes by TMA, four tiles ahead, is replaced in
 // shared memory by the result and leaves by TMA. A step is one adapter of a tile: a slice of B_a, and beside it
 // the tile's rows of V with zeros for other requests' rows; two steps are on their way. A CTA has
-// an equal share of the tiles in an order where pairs of channel tiles go round the token tiles, so that
-// token tiles of many adapters are shared out too. (The prompt form of adapter_mma.cuh without its product,
+// an equal share of the tiles in an order that goes round the token tiles, so that token tiles of many
+// adapters are shared out too. (The prompt form of adapter_mma.cuh without its product,
 // channels on the MMA's rows and C and D by loads and stores of registers, took 116 us for 4096 x 11008
 // with SiLU and bias; long runs of one token tile here 222, the tile of many adapters last.)
 // As there, B_a is looked at before it is used, because a zero does not hide a number that is not finite.
@@ -21,7 +21,7 @@ namespace adapters {
 
 struct Beside {
     static constexpr int ROWS = 128, COLS = 128, SL = 64, BOX = ROWS * 128;       // a box: 64 columns of 128 rows
-    static constexpr int V_BYTES = 2 * BOX, B_STAGES = 2, B_BYTES = COLS * 128, C_STAGES = 4, C_BYTES = 2 * BOX, ACCS = 4, RUN = 2;
+    static constexpr int V_BYTES = 2 * BOX, B_STAGES = 2, B_BYTES = COLS * 128, C_STAGES = 4, C_BYTES = 2 * BOX, ACCS = 4;
     static constexpr int EPI_WARP0 = 4, EPI_WARPS = 8, EPI_TEAMS = 2, V_WARP0 = EPI_WARP0 + EPI_TEAMS * EPI_WARPS, V_WARPS = 8, THREADS = 32 * (V_WARP0 + V_WARPS);
     static constexpr int MARKS = 8;      // tiles that may be between their V or their sum and their epilogue: ACCS + B_STAGES at most
     static constexpr int BAR_BYTES = 768;
@@ -31,36 +31,27 @@ struct Beside {
     static_assert(SMEM <= 232448 && V_WARPS == 8, "shared memory; a tile's marks are one 64-bit word");
 };
 
-// A CTA's tiles, in order. (The last pair of channel tiles may be one: its place is passed over. Steps, not divisions:
-// sixteen warps take them for every tile.)
+// A CTA's tiles, in order: token tiles first, then channels. (Steps, not divisions: sixteen warps take them for every tile.)
 struct BesideTiles {
-    int left, in_run, ct0, tt, ch;       // places left; the next one's place in its run, the run's first channel tile
-    int next_tt;
+    int left, next_tt, next_ch, tt, ch;
     __device__ __forceinline__ explicit BesideTiles(const Params& p) {
-        const int64_t all = static_cast<int64_t>(p.tiles) * ((p.ctiles + Beside::RUN - 1) / Beside::RUN) * Beside::RUN;
-        const int at = static_cast<int>(all * blockIdx.x / gridDim.x), run = at / Beside::RUN;
+        const int64_t all = static_cast<int64_t>(p.tiles) * p.ctiles;
+        const int at = static_cast<int>(all * blockIdx.x / gridDim.x), column = at / p.tiles;
         left = static_cast<int>(all * (blockIdx.x + 1) / gridDim.x) - at;
-        in_run = at % Beside::RUN;
-        ct0 = run / p.tiles * Beside::RUN;
-        next_tt = run % p.tiles;
+        next_tt = at - column * p.tiles;
+        next_ch = column * Beside::COLS;
         tt = ch = 0;
     }
     __device__ __forceinline__ bool next(const Params& p) {
-        while (left > 0) {
-            const int ct = ct0 + in_run;
-            tt = next_tt;
-            ch = ct * Beside::COLS;
-            --left;
-            if (++in_run == Beside::RUN) {
-                in_run = 0;
-                if (++next_tt == p.tiles) {
-                    next_tt = 0;
-                    ct0 += Beside::RUN;
-                }
-            }
-            if (ct < p.ctiles) return true;
+        if (left == 0) return false;
+        --left;
+        tt = next_tt;
+        ch = next_ch;
+        if (++next_tt == p.tiles) {
+            next_tt = 0;
+            next_ch += Beside::COLS;
         }
-        return false;
+        return true;
     }
 };
 
@@ -357,7 +348,7 @@ __global__ void __launch_bounds__(Beside::THREADS, 1)
     } else if (warp >= Beside::V_WARP0) {
         // ---------------------------------------------------------------- masked rows of V, a look at B
         // Two threads share a token row, one has its first numbers and one its second, and a channel of B, half of its
-        // slice each. A row's V is loaded once for a run of tiles (up to rank 64).
+        // slice each. A row's V is loaded ahead (up to rank 64).
         const int row = (threadIdx.x - 32 * Beside::V_WARP0) & 127, part = (threadIdx.x - 32 * Beside::V_WARP0) >> 7, swizzle = row & 7;
         int64_t step = 0;
         int marks = 0, had = -1, own = -1;           // had: the token tile whose V is loaded

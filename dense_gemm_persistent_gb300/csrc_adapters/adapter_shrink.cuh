@@ -11,9 +11,7 @@ namespace adapters {
 // Few rows, by FP32 units: a CTA computes RB numbers of one row; its threads share K, partial sums meet in shared
 // memory. Its loads go out in batches of U steps, whether there are as many or not: with a remainder loop
 // most calls waited for every step. CTAs behind the rows' write the lists of the prompt form's token tiles.
-constexpr int SHRINK_THREADS = 256;
-
-template <int RB, int U>
+template <int RB, int U, int SHRINK_THREADS>
 __global__ void __launch_bounds__(SHRINK_THREADS) adapter_shrink_few(const __grid_constant__ Params p) {
     __shared__ float part[SHRINK_THREADS / 32][RB];
     __shared__ unsigned words[DGEMM_MAX_ADAPTERS / 32];

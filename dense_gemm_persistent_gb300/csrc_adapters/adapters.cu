@@ -68,22 +68,28 @@ bool allow_shared(std::atomic<unsigned char>* ready, int device, const void* fun
 }
 
 // V of few rows: a CTA for some of a row's numbers.
-template <int RB, int U>
+template <int RB, int U, int THREADS>
 cudaError_t shrink_few(const Params& p, const dg::host::Device& dev, cudaStream_t s) {
     // The same split of an SM's memory as the kernel behind it: one of another split does not start on an SM
     // before this one has left it.
     static std::atomic<unsigned char> ready[dg::host::kMaxDevices];
-    if (!allow_shared(ready, dev.id, reinterpret_cast<const void*>(&dg::adapters::adapter_shrink_few<RB, U>), 0)) return cudaErrorUnknown;
+    const auto kernel = dg::adapters::adapter_shrink_few<RB, U, THREADS>;
+    if (!allow_shared(ready, dev.id, reinterpret_cast<const void*>(kernel), 0)) return cudaErrorUnknown;
     const unsigned blocks = static_cast<unsigned>(p.T) * (p.r / RB) + (p.prompt ? p.tiles : 0);
-    dg::host::Launch l(blocks, 1, dg::adapters::SHRINK_THREADS, 0, s);
-    return cudaLaunchKernelEx(&l.cfg, dg::adapters::adapter_shrink_few<RB, U>, p);
+    dg::host::Launch l(blocks, 1, THREADS, 0, s);
+    return cudaLaunchKernelEx(&l.cfg, kernel, p);
+}
+// As many CTAs as the SMs hold at once, about 4 each: more numbers a CTA beyond. 256 threads share K, 128 where K is too short for
+// them (64 rows of K = 4096, rank 64: 22.7 and 26.5 us for the call; 997 rows of K = 1416, rank 8: 28.6 and 26.2).
+template <int THREADS>
+cudaError_t shrink_few(const Params& p, const dg::host::Device& dev, cudaStream_t s) {
+    const int64_t numbers = static_cast<int64_t>(p.T) * p.r, at_once = 4 * dev.num_sms;
+    return numbers <= 2 * at_once   ? shrink_few<2, 4, THREADS>(p, dev, s)
+           : numbers <= 4 * at_once ? shrink_few<4, 2, THREADS>(p, dev, s)
+                                    : shrink_few<8, 2, THREADS>(p, dev, s);
 }
 dgemm_status_t launch_shrink_few(const Params& p, const dg::host::Device& dev, cudaStream_t s) {
-    // (as many CTAs as the SMs hold at once, about 4 each: more numbers a CTA beyond)
-    const int64_t numbers = static_cast<int64_t>(p.T) * p.r, at_once = 4 * dev.num_sms;
-    const cudaError_t e = numbers <= 2 * at_once   ? shrink_few<2, 4>(p, dev, s)
-                          : numbers <= 4 * at_once ? shrink_few<4, 2>(p, dev, s)
-                                                   : shrink_few<8, 2>(p, dev, s);
+    const cudaError_t e = p.K <= 1536 ? shrink_few<128>(p, dev, s) : shrink_few<256>(p, dev, s);
     return e == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
 }
 
