@@ -46,8 +46,11 @@ struct Call {
     cudaStream_t stream;
 };
 
-// Most numbers of V that FP32 units compute.
-constexpr int kMostFewShrink = 16384;
+// V by FP32 units, every row on its own, or by the tensor core, whose launch has a longer way to its first number. FP32 / tensor
+// core in us a call of 4096 channels, every row another adapter of 32 (and one request after another): K = 4096, 256
+// rows of rank 64 43 / 74 (40 / 50); 512 of rank 16 49 / 57 (43 / 40), of rank 64 78 / 92 (70 / 57); 1024 of rank 16
+// 64 / 64 (58 / 47); K = 1024, 1024 rows of rank 16 37 / 42 (29 / 29), of rank 64 61 / 69 (50 / 39).
+bool few_for_v(int64_t T, int64_t r, int64_t K) { return T <= 256 || T * r * K <= (int64_t(1) << 25); }
 
 dgemm_status_t check_sizes(int64_t T, int64_t N, int64_t K, int64_t r, int64_t L) {
     if (T < 0 || N < 0 || K < 0 || L < 0 || r < 1) return DGEMM_ERR_INVALID_VALUE;
@@ -344,7 +347,7 @@ dgemm_status_t run_adapters(const Call& c) {
         prompt_tiles(p, dev);
     }
     if (p.L > 0) {
-        const dgemm_status_t s = static_cast<int64_t>(p.T) * p.r > kMostFewShrink ? launch_shrink_many(c, p, dev) : launch_shrink_few(p, dev, c.stream);
+        const dgemm_status_t s = few_for_v(p.T, p.r, p.K) ? launch_shrink_few(p, dev, c.stream) : launch_shrink_many(c, p, dev);
         if (s != DGEMM_OK) return s;
     }
     return beside ? launch_beside(c, p, dev) : p.prompt ? launch_prompt(c, p, dev) : launch_few(c, p, dev);
