@@ -112,11 +112,11 @@ def test_beside_another_product(form, T, N, K, r, L, c, out, act):
     close(p.add(act, out, c), ref.adapters(p.X, p.A, p.B, p.ids, C=C, scale=p.scale, bias=p.bias, act=act, out_dtype=out))
 
 
-@pytest.mark.parametrize("T", [5, 64, 400])
+@pytest.mark.parametrize("T,N", [(5, 300), (64, 304), (400, 300), (400, 304), (1100, 712)])
 @pytest.mark.parametrize("dtype", [BF, F32])
-def test_in_place(form, T, dtype):
-    for order in ("mixed", "none"):
-        p = Problem(T, 300, 136, 16, 5, order=order)
+def test_in_place(form, T, N, dtype):
+    for order in ("mixed", "none", "runs"):
+        p = Problem(T, N, 136, 16, 5, order=order)
         got = p.add("none", dtype, dtype, in_place=True)
         close(got, ref.adapters(p.X, p.A, p.B, p.ids, C=p.C.to(dtype), scale=p.scale, out_dtype=dtype))
         untouched = (p.ids < 0) | (p.ids >= 5)
@@ -231,3 +231,75 @@ def test_waits_are_bounded(form, T):
     assert dg.dgemm_query_device_status(ws) != 0
     dg.dgemm_adapter_bf16(X, W, A, B, ids, D, scale=scale, ws=ws)      # and the next call is right again
     assert dg.dgemm_query_device_status(ws) == 0 and torch.equal(D, want)
+
+
+def test_calls_on_two_streams_at_once():
+    # each with a workspace of its own
+    problems = [Problem(T, 776, 512, r, 9, seed=T, order=o) for T, r, o in ((24, 16, "mixed"), (700, 32, "runs"))]
+    want = [(p.project(), p.add()) for p in problems]
+    streams = [torch.cuda.Stream() for _ in problems]
+    held = []
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for p, s in zip(problems, streams):
+            X, W, A, B, ids, scale = p.on_gpu("X", "W", "A", "B", "ids", "scale")
+            C = p.C.to(BF).to(dev())
+            out = [torch.empty(p.sizes[0], p.sizes[1], dtype=BF, device=dev()) for _ in range(2)]
+            ws = p.workspace()
+            torch.cuda.current_stream().synchronize()
+            with torch.cuda.stream(s):
+                dg.dgemm_adapter_bf16(X, W, A, B, ids, out[0], scale=scale, ws=ws)
+                dg.dgemm_adapter_add(X, A, B, ids, out[1], C=C, scale=scale, ws=ws)
+            held.append((p, out, (X, W, A, B, ids, scale, C, ws)))
+    torch.cuda.synchronize()
+    for p, out, _ in held:
+        a, b = want[problems.index(p)]
+        assert torch.equal(out[0], a) and torch.equal(out[1], b)
+
+
+def test_the_first_call_inside_a_capture():
+    """In a process of its own: nothing has been set up when the graph is captured."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch, dense_gemm_persistent_gb300 as dg
+BF = torch.bfloat16
+mk = lambda *s: (torch.randn(*s, device="cuda") * 0.1).to(BF)
+for T, N in ((4, 256), (400, 4096), (400, 4100)):
+    X, W, A, B, C = mk(T, 512), mk(N, 512), mk(6, 16, 512), mk(6, N, 16), mk(T, N)
+    ids = torch.randint(-1, 6, (T,), dtype=torch.int32, device="cuda")
+    D, E = torch.empty_like(C), torch.empty_like(C)
+    ws = torch.empty(dg.dgemm_adapter_workspace_size(T, N, 512, 16, 6), dtype=torch.uint8, device="cuda")
+    def calls(D, E):
+        dg.dgemm_adapter_bf16(X, W, A, B, ids, D, ws=ws)
+        dg.dgemm_adapter_add(X, A, B, ids, E, C=C, ws=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        calls(D, E)
+    g.replay()
+    torch.cuda.synchronize()
+    D2, E2 = torch.empty_like(C), torch.empty_like(C)
+    calls(D2, E2)
+    torch.cuda.synchronize()
+    assert torch.equal(D, D2) and torch.equal(E, E2), (T, N)
+    assert dg.dgemm_query_device_status(ws) == 0
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=110)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("T", [64, 900])
+def test_a_workspace_of_exactly_the_size_and_what_lies_behind(form, T):
+    p = Problem(T, 520, 264, 24, 12, order="runs")
+    X, W, A, B, ids, scale = p.on_gpu("X", "W", "A", "B", "ids", "scale")
+    n = dg.dgemm_adapter_workspace_size(*p.sizes)
+    room = torch.full((n + 4096,), 0x5A, dtype=torch.uint8, device=dev())
+    D = torch.full((T + 2, 520), 7.0, dtype=BF, device=dev())
+    dg.dgemm_adapter_bf16(X, W, A, B, ids, D[1:T + 1], scale=scale, ws=room[:n])
+    close(D[1:T + 1], ref.adapters(p.X, p.A, p.B, p.ids, W=p.W, scale=p.scale))
+    assert bool((room[n:] == 0x5A).all()) and bool((D[0] == 7).all()) and bool((D[T + 1] == 7).all())
+    with pytest.raises(dg.DgemmError):
+        dg.dgemm_adapter_bf16(X, W, A, B, ids, D[1:T + 1], scale=scale, ws=room[:n - 1])
