@@ -31,6 +31,8 @@ struct Beside {
     static_assert(SMEM <= 232448 && V_WARPS == 8, "shared memory; a tile's marks are one 64-bit word");
 };
 
+constexpr int kNoAdapters = -1, kNotLooked = -2;      // of a tile, in the place of its number among those with a look at B
+
 // A CTA's tiles, in order: token tiles first, then channels. (Steps, not divisions: sixteen warps take them for every tile.)
 struct BesideTiles {
     int left, next_tt, next_ch, tt, ch;
@@ -57,7 +59,8 @@ struct BesideTiles {
 
 __global__ void __launch_bounds__(Beside::THREADS, 1)
     adapter_beside(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmD,
-                   const __grid_constant__ CUtensorMap tmB, const __grid_constant__ Params p) {
+                   const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmV,
+                   const __grid_constant__ Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* v_rows = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* b_ring = v_rows + Beside::B_STAGES * Beside::V_BYTES;
@@ -70,10 +73,10 @@ __global__ void __launch_bounds__(Beside::THREADS, 1)
     uint64_t* c_empty = c_done + Beside::C_STAGES;        // and has left
     uint64_t* acc_full = c_empty + Beside::C_STAGES;
     uint64_t* acc_empty = acc_full + Beside::ACCS;
-    uint64_t* looked = acc_empty + Beside::ACCS;          // [MARKS] the n-th tile with adapters: its slices of B have been looked at
+    uint64_t* looked = acc_empty + Beside::ACCS;          // [MARKS] the n-th tile with a look: its slices of B have been looked at
     uint64_t* drain = looked + Beside::MARKS;
     uint64_t* dirty = drain + 1;                          // [MARKS] a byte for every warp that looked
-    int* mark_of = reinterpret_cast<int*>(dirty + Beside::MARKS);   // [MARKS] which of the tiles with adapters a tile is, -1: none
+    int* mark_of = reinterpret_cast<int*>(dirty + Beside::MARKS);   // [MARKS] which of the tiles with a look at B a tile is
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mark_of + Beside::MARKS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -101,7 +104,10 @@ __global__ void __launch_bounds__(Beside::THREADS, 1)
         fence_mbarrier_init();
         if (p.C) tma_prefetch_desc(&tmC);
         tma_prefetch_desc(&tmD);
-        if (p.L > 0) tma_prefetch_desc(&tmB);
+        if (p.L > 0) {
+            tma_prefetch_desc(&tmB);
+            tma_prefetch_desc(&tmV);
+        }
     }
     if (warp == 1) {
         tmem_alloc(tmem_slot, 512);
@@ -150,8 +156,10 @@ __global__ void __launch_bounds__(Beside::THREADS, 1)
                     ok = mbar_wait_warp(&b_empty[s], static_cast<uint32_t>((b_count / Beside::B_STAGES) & 1) ^ 1, abort_flag, p.wait_ns);
                     if (!ok) break;
                     if (elect_one()) {
-                        mbar_arrive_expect_tx(&b_full[s], Beside::B_BYTES);
-                        tma_load_nd<false>(b_ring + s * Beside::B_BYTES, &tmB, smem_u32(&b_full[s]), i * Beside::SL, ch, 0, a, pol);
+                        const uint32_t bar = smem_u32(&b_full[s]);
+                        mbar_arrive_expect_tx(&b_full[s], Beside::B_BYTES + (ta.uniform ? Beside::V_BYTES : 0));
+                        tma_load_nd<false>(b_ring + s * Beside::B_BYTES, &tmB, bar, i * Beside::SL, ch, 0, a, pol);
+                        if (ta.uniform) tma_load_nd<false>(v_rows + s * Beside::V_BYTES, &tmV, bar, i * Beside::SL, tt * Beside::ROWS, 0, pol);
                     }
                     __syncwarp();
                     ++b_count;
@@ -214,10 +222,10 @@ __global__ void __launch_bounds__(Beside::THREADS, 1)
             if (!ok) break;
             if (elect_one()) {
                 mma_commit(&acc_full[buf]);
-                mark_of[local % Beside::MARKS] = more ? marks : -1;
+                mark_of[local % Beside::MARKS] = !more ? kNoAdapters : ta.uniform ? kNotLooked : marks;
                 mbar_arrive(&acc_full[buf]);
             }
-            marks += more;
+            marks += more && !ta.uniform;
             __syncwarp();
         }
         if (elect_one()) {
@@ -277,9 +285,9 @@ __global__ void __launch_bounds__(Beside::THREADS, 1)
             if (!ok) break;
             tc_fence_after();
             const int mark = mark_of[local % Beside::MARKS];
-            const bool some = mark >= 0;
+            const bool some = mark != kNoAdapters;
             bool found = false;
-            if (some) {
+            if (mark >= 0) {
                 ok = mbar_wait_warp(&looked[mark % Beside::MARKS], (mark / Beside::MARKS) & 1, abort_flag, p.wait_ns);
                 if (!ok) break;
                 found = dirty[mark % Beside::MARKS] != 0;
@@ -370,6 +378,16 @@ __global__ void __launch_bounds__(Beside::THREADS, 1)
             ta.open(p, tt);
             live = tile.next(p);
             if (live) ta.look_ahead(p, tile.tt);
+            if (ta.uniform) {                    // V comes with B
+                for (int i = 0; ok && i < chunks_r; ++i, ++step) {
+                    const int s = static_cast<int>(step % Beside::B_STAGES);
+                    ok = mbar_wait_warp(&b_full[s], static_cast<uint32_t>((step / Beside::B_STAGES) & 1), abort_flag, p.wait_ns);
+                    if (!ok) break;
+                    if (lane == 0) mbar_arrive(&ready[s]);
+                    __syncwarp();
+                }
+                continue;
+            }
             if (tt != had) {
                 own = t < p.T && p.L > 0 ? adapter_of(p, t) : -1;
                 if (chunks_r == 1) load(0, p.r / 8);

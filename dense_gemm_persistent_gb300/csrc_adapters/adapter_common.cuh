@@ -37,7 +37,9 @@ struct Params : experts::Params {      // (of those: C, D, bias, N, K, wide, gat
 };
 
 constexpr int kMostWidth = 256;               // rows of a token tile of the prompt form
-constexpr int kListPitch = 4 + kMostWidth;    // [0] the count, from [1] on the adapters in order
+constexpr int kListPitch = 4 + kMostWidth;    // [0] the count and kUniform, from [1] on the adapters in order
+constexpr int kUniform = 1 << 16;             // every row of the tile has the same adapter
+constexpr int kAdapterWords = DGEMM_MAX_ADAPTERS / 32, kWords = kAdapterWords + 4;    // a bit for every adapter; rows without one
 
 // y / (1 + e^-y) by the special function unit, 2^-21 relative.
 __device__ __forceinline__ float silu(float y) {
@@ -113,7 +115,7 @@ __device__ __forceinline__ void fma8(float& s0, float& s1, const uint4& b, const
 
 __device__ __forceinline__ __nv_bfloat16* v_row(const Params& p, int t) { return p.V + static_cast<int64_t>(t) * 2 * p.r; }
 
-// Bits of the adapters in use among n rows, by `threads` threads that all pass; words: [128].
+// Bits of the adapters in use among n rows, by `threads` threads that all pass.
 __device__ __forceinline__ void mark_adapters(const Params& p, int first, int n, unsigned* words, int tid, int threads) {
     // (loads of a batch before its marks; most are marked already, and a look spares the atomic)
     for (int i0 = tid; i0 < n; i0 += 16 * threads) {
@@ -138,11 +140,11 @@ __device__ __forceinline__ int marked(const Params& p, const unsigned* words) {
     return all;
 }
 
-// Writes the list of a token tile of the prompt form; words: [128] in shared memory; sync() for all of the threads.
+// Writes the list of a token tile of the prompt form; words: [kWords] in shared memory; sync() for all of the threads.
 template <class Sync>
 __device__ __forceinline__ void list_tile(const Params& p, int tile, unsigned* words, int tid, int threads, Sync sync) {
     const int row0 = tile * p.width, rows = min(p.width, p.T - row0);
-    for (int w = tid; w < DGEMM_MAX_ADAPTERS / 32; w += threads) words[w] = 0;
+    for (int w = tid; w < kWords; w += threads) words[w] = 0;
     sync();
     mark_adapters(p, row0, rows, words, tid, threads);
     sync();
@@ -150,8 +152,13 @@ __device__ __forceinline__ void list_tile(const Params& p, int tile, unsigned* w
     for (int i = tid; i < rows; i += threads) {
         const int a = adapter_of(p, row0 + i);
         if (a >= 0) list[1 + place_of(p, words, a)] = a;          // (rows of one adapter write the same)
+        else words[kAdapterWords] = 1;
     }
-    if (tid == 0) list[0] = marked(p, words);
+    sync();
+    if (tid == 0) {
+        const int count = marked(p, words);
+        list[0] = count | (count == 1 && words[kAdapterWords] == 0 ? kUniform : 0);
+    }
     sync();
 }
 

@@ -59,6 +59,7 @@ __device__ __forceinline__ bool mma_tile(const Params& p, int item, MmaTile& t) 
 struct TileAdapters {
     const int* list;
     int count, at, mine, ahead;
+    bool uniform;                                // one adapter, which every row has
     __device__ __forceinline__ void look_ahead(const Params& p, int tt) {
         ahead = p.L > 0 ? __ldcg(p.lists + static_cast<int64_t>(tt) * kListPitch + (threadIdx.x & 31)) : 0;
     }
@@ -66,6 +67,8 @@ struct TileAdapters {
         list = p.lists + static_cast<int64_t>(tt) * kListPitch;
         mine = ahead;
         count = __shfl_sync(kAllLanes, mine, 0);
+        uniform = (count & kUniform) != 0;
+        count &= kUniform - 1;
         at = 0;
     }
     // the next one, -1 when there is none left

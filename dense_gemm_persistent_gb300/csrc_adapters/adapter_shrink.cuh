@@ -14,7 +14,7 @@ namespace adapters {
 template <int RB, int U, int SHRINK_THREADS>
 __global__ void __launch_bounds__(SHRINK_THREADS) adapter_shrink_few(const __grid_constant__ Params p) {
     __shared__ float part[SHRINK_THREADS / 32][RB];
-    __shared__ unsigned words[DGEMM_MAX_ADAPTERS / 32];
+    __shared__ unsigned words[kWords];
     grid_dependency_wait();
     if (threadIdx.x == 0) grid_launch_dependents();
     const int blocks = p.r / RB;
@@ -80,7 +80,7 @@ struct Shrink {
     static constexpr int ROWS = 128, SL = 64, KS = 2, SLICE_X = ROWS * 128, X_BYTES = KS * SLICE_X;
     static constexpr int MOST_COLS = 256, MOST_STAGES = 6, MOST_SPLIT = 8;
     static constexpr int EPI_WARP0 = 2, HELP_WARP0 = 6, THREADS = 320, HELPERS = 128;
-    static constexpr int TMEM_COLS = 256, WORDS = DGEMM_MAX_ADAPTERS / 32;
+    static constexpr int TMEM_COLS = 256, WORDS = kWords;
     static constexpr int FEW = 4, MOST_SINGLE = 32, SINGLE_N = 4, BATCH = 32;      // single rows: see above; tiles looked at together
     static constexpr int TABLES = 2 * WORDS * 4 + 2 * ROWS * 4 + BATCH * 16, BAR_BYTES = 256;
     static constexpr uint32_t IDESC0 = make_idesc(1u, false, false, 128, 0);

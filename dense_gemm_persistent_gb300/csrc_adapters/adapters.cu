@@ -50,7 +50,7 @@ struct Call {
 // core in us a call of 4096 channels, every row another adapter of 32 (and one request after another): K = 4096, 256
 // rows of rank 64 43 / 74 (40 / 50); 512 of rank 16 49 / 57 (43 / 40), of rank 64 78 / 92 (70 / 57); 1024 of rank 16
 // 64 / 64 (58 / 47); K = 1024, 1024 rows of rank 16 37 / 42 (29 / 29), of rank 64 61 / 69 (50 / 39).
-bool few_for_v(int64_t T, int64_t r, int64_t K) { return T <= 256 || T * r * K <= (int64_t(1) << 25); }
+bool few_for_v(int64_t T, int64_t r, int64_t K) { return T <= 256 || (T <= 1024 && T * r * K <= (int64_t(1) << 25)); }
 
 dgemm_status_t check_sizes(int64_t T, int64_t N, int64_t K, int64_t r, int64_t L) {
     if (T < 0 || N < 0 || K < 0 || L < 0 || r < 1) return DGEMM_ERR_INVALID_VALUE;
@@ -263,21 +263,24 @@ dgemm_status_t launch_beside(const Call& c, const Params& p, const dg::host::Dev
     if (items > INT32_MAX / 2) return DGEMM_ERR_NOT_SUPPORTED;
     const uint64_t N = p.N, T = p.T, r = p.r, L = p.L, d[2] = {N, T}, st[1] = {N * 2};
     const uint32_t box[2] = {Beside::SL, Beside::ROWS};
-    alignas(64) CUtensorMap cm, dm, b;
+    alignas(64) CUtensorMap cm, dm, b, v;
     std::memset(&cm, 0, sizeof cm);
     std::memset(&b, 0, sizeof b);
+    std::memset(&v, 0, sizeof v);
     bool ok = dg::host::encode_map(&dm, kBf16, c.D, 2, d, st, box) && (!c.C || dg::host::encode_map(&cm, kBf16, c.C, 2, d, st, box));
     if (ok && p.L > 0) {
         const uint64_t db[4] = {r, N, 1, L}, sb[3] = {r * 2, N * r * 2, N * r * 2};
         const uint32_t bb[4] = {Beside::SL, Beside::COLS, 1, 1};
-        ok = dg::host::encode_map(&b, kBf16, c.B, 4, db, sb, bb);
+        const uint64_t dv[3] = {r, T, 2}, sv[2] = {r * 4, r * 2};         // [part][row]: the slices of a step in one copy
+        const uint32_t bv[3] = {Beside::SL, Beside::ROWS, 2};
+        ok = dg::host::encode_map(&b, kBf16, c.B, 4, db, sb, bb) && dg::host::encode_map(&v, kBf16, p.V, 3, dv, sv, bv);
     }
     if (!ok) return DGEMM_ERR_CUDA;
     static std::atomic<unsigned char> ready[dg::host::kMaxDevices];
     if (!allow_shared(ready, dev.id, reinterpret_cast<const void*>(&dg::adapters::adapter_beside), kShared)) return DGEMM_ERR_CUDA;
     const int ctas = static_cast<int>(std::min<int64_t>(dev.num_sms, items));
     dg::host::Launch l(static_cast<unsigned>(ctas), 1, Beside::THREADS, Beside::SMEM, c.stream);
-    return cudaLaunchKernelEx(&l.cfg, dg::adapters::adapter_beside, cm, dm, b, p) == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
+    return cudaLaunchKernelEx(&l.cfg, dg::adapters::adapter_beside, cm, dm, b, v, p) == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
 }
 
 dgemm_status_t run_adapters(const Call& c) {
