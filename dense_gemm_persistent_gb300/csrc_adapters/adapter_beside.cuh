@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(Beside::THREADS, 1)
         __syncwarp();
     } else if (warp == 2) {
         // ---------------------------------------------------------------- stores of finished tiles
-        // A place in the ring is free again when its store has read it: two stores may be on their way.
+        // A place in the ring is free again when its store has read it.
         int local = 0;
         bool ok = true;
         for (; ok && tile.next(p); ++local) {
@@ -248,21 +248,13 @@ __global__ void __launch_bounds__(Beside::THREADS, 1)
                 tma_store_2d(&tmD, from, ch, tt * Beside::ROWS);
                 if (ch + Beside::SL < p.N) tma_store_2d(&tmD, from + Beside::BOX, ch + Beside::SL, tt * Beside::ROWS);
                 bulk_commit();
-                if (local > 0) {
-                    bulk_wait_read<1>();
-                    mbar_arrive(&c_empty[(local - 1) % Beside::C_STAGES]);
-                }
+                bulk_wait_read<0>();
+                mbar_arrive(&c_empty[s]);
             }
             __syncwarp();
         }
         if (!ok && lane == 0) experts::fail(p, ERR_TIMEOUT_EPILOGUE, abort_flag);
-        if (lane == 0) {
-            if (ok && local > 0) {
-                bulk_wait_read<0>();
-                mbar_arrive(&c_empty[(local - 1) % Beside::C_STAGES]);
-            }
-            bulk_wait_all();                    // nothing of this CTA's memory is read when it leaves
-        }
+        if (lane == 0) bulk_wait_all();         // the results have been written when the CTA leaves
         __syncwarp();
     } else if (warp >= Beside::EPI_WARP0 && warp < Beside::V_WARP0) {
         // ---------------------------------------------------------------- epilogue

@@ -82,13 +82,13 @@ struct TileAdapters {
 
 __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
 
-// Puts zeros in the place of numbers that are not finite in the 16-byte vectors [first, last) of a swizzled row; whether
+// Puts zeros in the place of numbers that are not finite in the 16-byte vectors [first, last), four at most, of a swizzled row; whether
 // there were any. Such a number times zero is NaN, and a sum keeps it: one operation for two numbers.
 __device__ __forceinline__ bool make_finite(uint8_t* row, int swizzle, int first, int last) {
     const __nv_bfloat162 zero = __float2bfloat162_rn(0.0f);
     __nv_bfloat162 nan[2] = {zero, zero};
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
+    for (int k = 0; k < 4; ++k) {
         const int c = first + k;
         if (c >= last) break;
         const uint4 b = *reinterpret_cast<const uint4*>(row + ((c ^ swizzle) << 4));
