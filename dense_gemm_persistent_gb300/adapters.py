@@ -42,6 +42,12 @@ def _low_rank(X, A, B, ids, scale, dev):
     return T, K, L, r, N
 
 
+def _tables(ids, scale, bias, T, L, N):
+    """The small operands, for _apart."""
+    at = lambda t: None if t is None else t.data_ptr()
+    return ("ids", at(ids), 4 * T), ("scale", at(scale), 4 * L), ("bias", at(bias), 4 * N)
+
+
 def _apart(d, d_bytes, *operands):
     """D is written while the operands are still read: (name, address, bytes) of each."""
     end = d + d_bytes
@@ -71,7 +77,7 @@ def dgemm_adapter_bf16(X, W, A, B, ids, D, *, scale=None, bias=None, act="none",
     x, w, a, b, d, dt = X.data_ptr(), W.data_ptr(), A.data_ptr(), B.data_ptr(), D.data_ptr(), _float_code(D)
     work, work_bytes = _workspace(ws, dev)
     _apart(d, T * wide * (4 if dt == F32 else 2), ("X", x, 2 * T * K), ("W", w, 2 * N * K), ("A", a, 2 * L * r * K),
-           ("B", b, 2 * L * N * r), ("ws", work, work_bytes))
+           ("B", b, 2 * L * N * r), ("ws", work, work_bytes), *_tables(ids, scale, bias, T, L, N))
     st = _dg.load().dgemm_adapter_bf16(x, w, a, b, ids.data_ptr(), None if scale is None else scale.data_ptr(), L, r, d, dt, T, N, K,
                                        None if bias is None else bias.data_ptr(), code, work, work_bytes, _stream(stream, dev))
     if st:
@@ -98,7 +104,8 @@ def dgemm_adapter_add(X, A, B, ids, D, *, C=None, scale=None, bias=None, act="no
     c, ct = (None, F32) if C is None else (C.data_ptr(), _float_code(C))
     work, work_bytes = _workspace(ws, dev)
     _apart(d, T * N * (4 if dt == F32 else 2), ("X", x, 2 * T * K), ("A", a, 2 * L * r * K), ("B", b, 2 * L * N * r),
-           ("C", None if c == d and ct == dt else c, T * N * (4 if ct == F32 else 2)), ("ws", work, work_bytes))
+           ("C", None if c == d and ct == dt else c, T * N * (4 if ct == F32 else 2)), ("ws", work, work_bytes),
+           *_tables(ids, scale, bias, T, L, N))
     st = _dg.load().dgemm_adapter_add(x, a, b, ids.data_ptr(), None if scale is None else scale.data_ptr(), L, r, c, ct, d, dt, T,
                                       N, K, None if bias is None else bias.data_ptr(), ACT[act], work, work_bytes,
                                       _stream(stream, dev))

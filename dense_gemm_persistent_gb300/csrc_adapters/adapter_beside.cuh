@@ -1,16 +1,22 @@
 // adapter_beside.cuh -- many rows' adapters beside a product C, BF16 in and out: D = act(C + V . B_a^T + bias).
 //
-// Bound by the bytes of C and D, so everything else is arranged around them: one persistent CTA an SM walks tiles of 128
+// Its bytes are C and D, so everything else is arranged around them: one persistent CTA an SM walks tiles of 128
 // token rows (the MMA's rows) by 128 channels (its columns); C comes by TMA, four tiles ahead, is replaced in
 // shared memory by the result and leaves by TMA. A step is one adapter of a tile: a slice of B_a, and beside it
 // the tile's rows of V with zeros for other requests' rows; two steps are on their way. A CTA has
 // an equal share of the tiles in an order that goes round the token tiles, so that token tiles of many
-// adapters are shared out too. (The prompt form of adapter_mma.cuh without its product,
-// channels on the MMA's rows and C and D by loads and stores of registers, took 116 us for 4096 x 11008
-// with SiLU and bias; long runs of one token tile here 222, the tile of many adapters last.)
-// As there, B_a is looked at before it is used, because a zero does not hide a number that is not finite.
+// adapters are shared out too.
+// As in adapter_mma.cuh, B_a is looked at before it is used, because a zero does not hide a number that is not finite. Both the
+// zeros and the look are the work of warps of their own, and take a tile 2.3 us. Where all rows of a token tile have
+// the same adapter neither is needed: V comes by TMA as it is, and the warps only pass the step on.
+// 4096 x 11008, 8 adapters of rank 32 in runs of rows, SiLU and bias: 67-70 us with the launch that computes V (10-12 of
+// them); the bytes take 33. Of a CTA's 43 us the epilogue computes 26 (two exponentials' worth of the special function unit a
+// value, 17 of them without an activation), waits 7 for C and 6 for sums of token tiles of several adapters.
+// (Tried and measured when this form was made: that case by the prompt form of adapter_mma.cuh, which has C and D by
+// registers, 116 us; every token tile's channels in one run, the tile of many adapters last, 222; V of every tile by
+// the warps 80; sums read from Tensor Memory a part ahead, with more registers for it, 80 against 67.)
 // Warps: 0 TMA producer, 1 MMA issuer and owner of the Tensor Memory, 2 TMA stores, 3 idle, 4-11 and 12-19 epilogue
-// (every second tile each: one tile's chain of waits beside the other's, 2.7 us a tile with all sixteen on one),
+// (every second tile each: one tile's chain of waits beside the other's),
 // 20-27 masked rows of V and the look at B.
 #pragma once
 

@@ -41,7 +41,7 @@ constexpr int kListPitch = 4 + kMostWidth;    // [0] the count and kUniform, fro
 constexpr int kUniform = 1 << 16;             // every row of the tile has the same adapter
 constexpr int kAdapterWords = DGEMM_MAX_ADAPTERS / 32, kWords = kAdapterWords + 4;    // a bit for every adapter; rows without one
 
-// y / (1 + e^-y) by the special function unit, 2^-21 relative.
+// y / (1 + e^-y) by the special function unit, 2^-21 relative; below -87 the quotient is zero (at most 2e-36 off).
 __device__ __forceinline__ float silu(float y) {
     float e, q;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(y * -1.4426950408889634f));

@@ -340,7 +340,7 @@ dgemm_status_t run_adapters(const Call& c) {
     const int full = p.gated ? 64 : 128;
     const int64_t few_tiles = static_cast<int64_t>((p.T + Few::MOST_COLS - 1) / Few::MOST_COLS) * ((p.wide + full - 1) / full);
     p.prompt = forced >= 0 ? forced : few_tiles > dev.num_sms;
-    // Beside a product in BF16 whose rows TMA can copy: a form of its own (4096 x 11008 with SiLU 116 us in the general one).
+    // Beside a product in BF16 whose rows TMA can copy: a form of its own (4096 x 11008 with SiLU 67 us, in the general one 116).
     const bool beside = p.prompt && !c.W && c.d_dtype == DGEMM_BF16 && (!c.C || c.c_dtype == DGEMM_BF16) && p.N % 8 == 0;
     if (beside) {
         p.width = dg::adapters::Beside::ROWS;

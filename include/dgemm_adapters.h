@@ -15,8 +15,10 @@
  * DEVICE pointers, memory of the caller, asynchronous calls that never allocate,
  * argument errors before any launch, bounded waits that are recorded in the first
  * DGEMM_WS_STATUS_BYTES bytes of the workspace. Of the planner overrides of dgemm.h,
- * wait_limit_ns and stall_after_loads apply. A workspace serves one call at a time: calls
- * that may overlap on the GPU (two streams, two graphs) need one each.
+ * wait_limit_ns, stall_after_loads and cta_pair apply (0: the form for few rows, 1: the
+ * one for prompts; sums are in another order, so bits may differ). A workspace serves
+ * one call at a time: calls that may overlap on the GPU (two streams, two graphs) need
+ * one each.
  */
 #ifndef DGEMM_ADAPTERS_H
 #define DGEMM_ADAPTERS_H
@@ -43,10 +45,10 @@ extern "C" {
  *   D      [T,N] (SWIGLU: [T,N/2]) F32 or BF16; overlaps no operand.
  *   ws     dgemm_adapter_workspace_size(T, N, K, r, L) bytes, contents arbitrary
  *          (DGEMM_ERR_WORKSPACE_TOO_SMALL with less).
- * FP32 accumulation, one rounding to D's type. X . A_a^T is summed and scaled in FP32; on its
- * way through the tensor core it is split into two BF16 numbers, which keeps 16
- * bits of it. A row depends on its own adapter alone: NaN and infinities in another one
- * do not reach it. NaN stays NaN under every activation.
+ * FP32 accumulation, one rounding to D's type. V = scale[a] * (X . A_a^T) is summed and scaled
+ * in FP32 and kept as two BF16 numbers whose sum is V up to 2^-18 of it (a magnitude of
+ * 3.39e38 or more, that BF16 cannot hold, counts as infinite). A row depends on its own adapter alone:
+ * NaN and infinities in another one do not reach it. NaN stays NaN under every activation.
  * r and K are multiples of 8 (DGEMM_ERR_MISALIGNED otherwise), 8 <= r <= DGEMM_MAX_ADAPTER_RANK,
  * 0 <= L <= DGEMM_MAX_ADAPTERS. K == 0: every product is zero. */
 dgemm_status_t dgemm_adapter_bf16(const void* X, const void* W, const void* A, const void* B, const int32_t* ids,

@@ -161,6 +161,9 @@ def test_binding_refuses_what_the_library_would_misread(lib, fake):
     refuses("D overlaps C", add, X, A, B, ids, D, C=fake(8, 48, ptr=D.ptr + 32))
     refuses("D overlaps C", add, X, A, B, ids, D, C=fake(8, 48, dtype=f, ptr=D.ptr))
     refuses("D overlaps ws", add, X, A, B, ids, D, ws=fake(1 << 16, dtype=torch.uint8, ptr=D.ptr))
+    refuses("D overlaps ids", call, X, W, A, B, fake(8, dtype=i, ptr=D.ptr + 16), D)
+    refuses("D overlaps scale", add, X, A, B, ids, D, scale=fake(3, dtype=f, ptr=D.ptr + 16))
+    refuses("D overlaps bias", add, X, A, B, ids, D, bias=fake(48, dtype=f, ptr=D.ptr - 16))
     x, e = fake(4, 8, dtype=f), fake(4, 2, dtype=f)
     out = (fake(4, 2, dtype=i), e, fake(9, dtype=i), fake(8, dtype=i), fake(4, 2, dtype=i))
     refuses("score must be", dg.dgemm_route_scored, x, 2, *out, score="tanh")
@@ -168,3 +171,23 @@ def test_binding_refuses_what_the_library_would_misread(lib, fake):
     refuses("bias has shape", dg.dgemm_route_scored, x, 2, *out, bias=fake(9, dtype=f))
     with pytest.raises(dg.DgemmError):
         dg.dgemm_route_scored(x, 2, *out, groups=3)
+
+
+@pytest.mark.parametrize("where", ["X", "W", "A", "B", "ids", "D", "C", "scale", "bias", "ws", "logits", "balance", "offsets"])
+def test_binding_refuses_operands_of_another_device(lib, fake, where):
+    f, i = torch.float32, torch.int32
+    t = dict(X=fake(8, 64), W=fake(48, 64), A=fake(3, 16, 64), B=fake(3, 48, 16), ids=fake(8, dtype=i), D=fake(8, 48),
+             C=fake(8, 48), scale=fake(3, dtype=f), bias=fake(48, dtype=f), ws=fake(1 << 16, dtype=torch.uint8),
+             logits=fake(4, 8, dtype=f), balance=fake(8, dtype=f), offsets=fake(9, dtype=i))
+    t[where].get_device = lambda: 1
+    rest = dict(scale=t["scale"], bias=t["bias"], ws=t["ws"])
+    calls = [lambda: dg.dgemm_adapter_bf16(t["X"], t["W"], t["A"], t["B"], t["ids"], t["D"], **rest),
+             lambda: dg.dgemm_adapter_add(t["X"], t["A"], t["B"], t["ids"], t["D"], C=t["C"], **rest)]
+    if where in ("logits", "balance", "offsets"):
+        calls = [lambda: dg.dgemm_route_scored(t["logits"], 2, fake(4, 2, dtype=i), fake(4, 2, dtype=f), t["offsets"],
+                                               fake(8, dtype=i), fake(4, 2, dtype=i), bias=t["balance"])]
+    elif where in ("W", "C"):
+        calls = calls[:1] if where == "W" else calls[1:]
+    for call in calls:
+        with pytest.raises(ValueError, match="cuda:1|current device"):
+            call()
