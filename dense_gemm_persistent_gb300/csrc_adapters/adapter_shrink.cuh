@@ -81,7 +81,7 @@ struct Shrink {
     static constexpr int MOST_COLS = 256, MOST_STAGES = 6, MOST_SPLIT = 8;
     static constexpr int EPI_WARP0 = 2, HELP_WARP0 = 6, THREADS = 320, HELPERS = 128;
     static constexpr int TMEM_COLS = 256, WORDS = kWords;
-    static constexpr int FEW = 4, MOST_SINGLE = 32, SINGLE_N = 4, BATCH = 32;      // single rows: see above; tiles looked at together
+    static constexpr int FEW = 4, MOST_SINGLE = 32, SINGLE_N = 4, BATCH = 32, WINDOW = 512;      // single rows: see above; tiles looked at together, shared
     static constexpr int TABLES = 2 * WORDS * 4 + 2 * ROWS * 4 + BATCH * 16, BAR_BYTES = 256;
     static constexpr uint32_t IDESC0 = make_idesc(1u, false, false, 128, 0);
     static constexpr int stage_bytes(int cols) { return X_BYTES + KS * cols * 128; }
@@ -133,14 +133,17 @@ __device__ __forceinline__ void single_row(const Params& p, int t, int at) {
     }
 }
 
-// The single rows of all tiles: an item is a row's four numbers, the items of a tile go round the launch's warps. masks:
-// [BATCH][4], the single rows of a tile.
+// The single rows of a window of tiles: an item is a row's four numbers, the items of a tile go round the warps of the
+// window's CTAs. (Each of them looks at the window's rows: over the whole of a long launch that would grow with the
+// square of the rows.) masks: [BATCH][4], the single rows of a tile.
 template <class Sync>
 __device__ __forceinline__ void share_single_rows(const Params& p, uint4* masks, int warp, Sync sync) {
-    const int lane = threadIdx.x & 31, groups = p.r / Shrink::SINGLE_N, all = static_cast<int>(gridDim.x) * 4, me = static_cast<int>(blockIdx.x) * 4 + warp;
-    for (int base = 0; base < p.shrink_tiles; base += Shrink::BATCH) {
+    const int lane = threadIdx.x & 31, groups = p.r / Shrink::SINGLE_N;
+    const int begin = static_cast<int>(blockIdx.x) / p.split / Shrink::WINDOW * Shrink::WINDOW, end = min(begin + Shrink::WINDOW, p.shrink_tiles);
+    const int all = (end - begin) * p.split * 4, me = (static_cast<int>(blockIdx.x) - begin * p.split) * 4 + warp;
+    for (int base = begin; base < end; base += Shrink::BATCH) {
         // (four tiles' rows are loaded together)
-        for (int k0 = warp; k0 < Shrink::BATCH && base + k0 < p.shrink_tiles; k0 += 16) {
+        for (int k0 = warp; k0 < Shrink::BATCH && base + k0 < end; k0 += 16) {
             int a[4][4];
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -158,7 +161,7 @@ __device__ __forceinline__ void share_single_rows(const Params& p, uint4* masks,
             }
         }
         sync();
-        const bool there = base + lane < p.shrink_tiles;
+        const bool there = base + lane < end;
         const uint4 m = there ? masks[lane] : make_uint4(0, 0, 0, 0);
         int rows = __popc(m.x) + __popc(m.y) + __popc(m.z) + __popc(m.w);
         if (rows > Shrink::MOST_SINGLE) rows = 0;

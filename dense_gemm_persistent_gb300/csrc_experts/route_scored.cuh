@@ -433,7 +433,7 @@ __device__ __forceinline__ void route_scored_token(const ScoredParams& p, int t,
             if (m1 > kNone) size = fabsf(unordered(m1)) + (m2 > kNone ? fabsf(unordered(m2)) : 0.0f);
             size = __uint_as_float(__reduce_max_sync(kAll, __float_as_uint(size)));
             const float margin = 2.0f * off + 4.0f * Margin::kSum * size;
-            auto near = [&](unsigned a, unsigned b) { return b > kNone && unordered(a) - unordered(b) <= margin; };
+            auto near = [&](unsigned a, unsigned b) { return b > kNone && !(unordered(a) - unordered(b) > margin); };      // (inf - inf too)
             if (near(at.worth_in, at.worth_out)) {
                 // one border between two groups, and no third expert that might be one of a group's two best?
                 whole = (at.before != kAll && near(at.before, at.worth_out)) || near(at.worth_in, __reduce_max_sync(kAll, at.left));

@@ -74,6 +74,25 @@ def test_adapters_past_the_limit(T):
         assert torch.equal(D[t].cpu().double(), want_row(t, X[:, :64], A[:, :, :64], B, ids, C[t].cpu().double()).to(BF).double()), t
 
 
+@pytest.mark.parametrize("r,N", [(8, 8), (16, 40)])
+def test_many_rows(r, N):
+    """Most rows of one adapter, single rows of others between them, everywhere."""
+    T, K, L = 300001, 24, 40
+    X, A, B = small_ints(1, T, K), small_ints(2, L, r, K), small_ints(3, L, N, r)
+    g = torch.Generator().manual_seed(4)
+    ids = torch.where(torch.rand(T, generator=g) < 0.02, torch.randint(-1, L, (T,), generator=g), 7).to(torch.int32)
+    C = small_ints(6, T, N)
+    D = run(X, A, B, ids.to(dev()), T, N, C=C)
+    f = lambda x: x.cpu().double()
+    Af, Bf, Xf, Cf, own = f(A), f(B), f(X), f(C), ids.long()
+    V = torch.stack([(Xf[t] @ Af[own[t]].t()) if own[t] >= 0 else torch.zeros(r, dtype=torch.float64)
+                     for t in (own != 7).nonzero()[:, 0].tolist()])
+    want = Cf + (Xf @ Af[7].t()) @ Bf[7].t()
+    for i, t in enumerate((own != 7).nonzero()[:, 0].tolist()):
+        want[t] = Cf[t] + Bf[own[t]] @ V[i]
+    assert torch.equal(f(D), want.to(BF).double())
+
+
 def test_a_long_row():
     T, N, K, r, L = 700, 64, 3200000, 8, 2                  # X has more than 2^31 elements
     assert (T - 20) * K > TWO31

@@ -111,6 +111,14 @@ def test_masked_entries_groups_and_rows():
                 run(x, 4, score=score, bias=b, renorm=renorm)
 
 
+@pytest.mark.parametrize("kept", [1, 2, 3])
+def test_sums_of_two_that_fp32_cannot_hold(kept):
+    # every one of the first groups' sums is infinite in FP32
+    bias = torch.tensor([1.8e38, 1.8e38, 3.0e38, 3.0e38, 2.0e38, 2.9e38, 3.1e38, 3.0e38, 0.5, 0.1])
+    for b in (bias, -bias, bias.roll(4)):
+        run(torch.randn(9, 10, generator=gen(kept)), 2, bias=b, groups=5, kept=kept)
+
+
 def test_scores_that_underflow():
     x = torch.linspace(-80, -130, 64).repeat(70, 1)
     run(x, 4, bias=torch.zeros(64))
