@@ -49,7 +49,8 @@ struct Call {
 // V by FP32 units, every row on its own, or by the tensor core, whose launch has a longer way to its first number. FP32 / tensor
 // core in us a call of 4096 channels, every row another adapter of 32 (and one request after another): K = 4096, 256
 // rows of rank 64 43 / 74 (40 / 50); 512 of rank 16 49 / 57 (43 / 40), of rank 64 78 / 92 (70 / 57); 1024 of rank 16
-// 64 / 64 (58 / 47); K = 1024, 1024 rows of rank 16 37 / 42 (29 / 29), of rank 64 61 / 69 (50 / 39).
+// 64 / 64 (58 / 47); K = 1024, 1024 rows of rank 16 37 / 42 (29 / 29), of rank 64 61 / 69 (50 / 39). Beside 11008
+// channels, 4096 rows of K = 256 and rank 32: 94 / 61 (a CTA for every 8 numbers is too many).
 bool few_for_v(int64_t T, int64_t r, int64_t K) { return T <= 256 || (T <= 1024 && T * r * K <= (int64_t(1) << 25)); }
 
 dgemm_status_t check_sizes(int64_t T, int64_t N, int64_t K, int64_t r, int64_t L) {
@@ -336,7 +337,8 @@ dgemm_status_t run_adapters(const Call& c) {
     const int forced = dg::host::pair_override();
     // One wave of the few-row form's tiles, or the prompt form: on the device 128 rows of 4096 channels, every row another
     // adapter of rank 64, 33 against 55 us, 256 rows 47 against 63 (one request: 28, 29), 384 115 against 99; of 11008
-    // channels 64 rows 37 against 49, 128 65 against 61 (one request: 48, 31).
+    // channels 64 rows 37 against 49, 128 65 against 61 (one request: 48, 31). Beside a product of 11008 channels, rank 32, 200
+    // rows of one request after another 49 against 23, every row another of 48 60 against 81: only the device knows which.
     const int full = p.gated ? 64 : 128;
     const int64_t few_tiles = static_cast<int64_t>((p.T + Few::MOST_COLS - 1) / Few::MOST_COLS) * ((p.wide + full - 1) / full);
     p.prompt = forced >= 0 ? forced : few_tiles > dev.num_sms;
