@@ -3,15 +3,15 @@
 // Its bytes are C and D, so everything else is arranged around them: one persistent CTA an SM walks tiles of 128
 // token rows (the MMA's rows) by 128 channels (its columns); C comes by TMA, four tiles ahead, is replaced in
 // shared memory by the result and leaves by TMA. A step is one adapter of a tile: a slice of B_a, and beside it
-// the tile's rows of V with zeros for other requests' rows; two steps are on their way. A CTA has
+// the tile's rows of V with zeros for other requests' rows; two or three steps are on their way. A CTA has
 // an equal share of the tiles in an order that goes round the token tiles, so that token tiles of many
 // adapters are shared out too.
 // As in adapter_mma.cuh, B_a is looked at before it is used, because a zero does not hide a number that is not finite. Both the
 // zeros and the look are the work of warps of their own, and take a tile 2.3 us. Where all rows of a token tile have
 // the same adapter neither is needed: V comes by TMA as it is, and the warps only pass the step on.
-// 4096 x 11008, 8 adapters of rank 32 in runs of rows, SiLU and bias: 67-70 us with the launch that computes V (10-12 of
-// them); the bytes take 33. Of a CTA's 43 us the epilogue computes 26 (two exponentials' worth of the special function unit a
-// value, 17 of them without an activation), waits 7 for C and 6 for sums of token tiles of several adapters.
+// 4096 x 11008, 8 adapters of rank 32 in runs of rows, SiLU and bias: 64-67 us with the launch that computes V (10-12 of
+// them); the bytes take 33. The epilogue computes for 26 of a CTA's 40 us (two operations of the special function unit a
+// value; 17 without an activation); the rest are waits for C and for sums of token tiles of several adapters.
 // (Tried and measured when this form was made: that case by the prompt form of adapter_mma.cuh, which has C and D by
 // registers, 116 us; every token tile's channels in one run, the tile of many adapters last, 222; V of every tile by
 // the warps 80; sums read from Tensor Memory a part ahead, with more registers for it, 80 against 67.)
@@ -27,13 +27,22 @@ namespace adapters {
 
 struct Beside {
     static constexpr int ROWS = 128, COLS = 128, SL = 64, BOX = ROWS * 128;       // a box: 64 columns of 128 rows
-    static constexpr int V_BYTES = 2 * BOX, B_STAGES = 2, B_BYTES = COLS * 128, C_STAGES = 4, C_BYTES = 2 * BOX, ACCS = 4;
+    static constexpr int B_BYTES = COLS * 128, C_STAGES = 4, C_BYTES = 2 * BOX, ACCS = 4, MOST_B_STAGES = 3;
     static constexpr int EPI_WARP0 = 4, EPI_WARPS = 8, EPI_TEAMS = 2, V_WARP0 = EPI_WARP0 + EPI_TEAMS * EPI_WARPS, V_WARPS = 8, THREADS = 32 * (V_WARP0 + V_WARPS);
     static constexpr int MARKS = 8;      // tiles that may be between their V or their sum and their epilogue: ACCS + B_STAGES at most
     static constexpr int BAR_BYTES = 768;
-    static constexpr int SMEM = 1024 + B_STAGES * (V_BYTES + B_BYTES) + C_STAGES * C_BYTES + BAR_BYTES;
+    // Steps on their way. With rank 16 or 32 both numbers of V fit into one slice as they stand in memory (the second ones on a
+    // step of the MMA), and a third step into the memory of two: rank 32, 4096 x 11008, 8 requests in runs 66.4 -> 63.5 us, every
+    // row another of 48 705 -> 537.
+    template <bool NARROW>
+    struct Steps {
+        static constexpr int B_STAGES = NARROW ? 3 : 2, V_BYTES = NARROW ? BOX : 2 * BOX;
+        static constexpr int BYTES = B_STAGES * (V_BYTES + B_BYTES);
+    };
+    static constexpr int SMEM = 1024 + Steps<true>::BYTES + C_STAGES * C_BYTES + BAR_BYTES;
+    static_assert(Steps<true>::BYTES == Steps<false>::BYTES, "the same shared memory");
     static constexpr uint32_t IDESC = make_idesc(1u, false, false, 128, 128);
-    static_assert((3 * B_STAGES + 3 * C_STAGES + 2 * ACCS + MARKS + 1) * 8 + 8 + MARKS * (V_WARPS + 4) <= BAR_BYTES, "barriers fit");
+    static_assert((3 * MOST_B_STAGES + 3 * C_STAGES + 2 * ACCS + MARKS + 1) * 8 + 8 + MARKS * (V_WARPS + 4) <= BAR_BYTES, "barriers fit");
     static_assert(SMEM <= 232448 && V_WARPS == 8, "shared memory; a tile's marks are one 64-bit word");
 };
 
@@ -63,18 +72,20 @@ struct BesideTiles {
     }
 };
 
+template <bool NARROW>
 __global__ void __launch_bounds__(Beside::THREADS, 1)
     adapter_beside(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmD,
                    const __grid_constant__ CUtensorMap tmB, const __grid_constant__ CUtensorMap tmV,
                    const __grid_constant__ Params p) {
+    using Steps = Beside::Steps<NARROW>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* v_rows = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t* b_ring = v_rows + Beside::B_STAGES * Beside::V_BYTES;
-    uint8_t* c_ring = b_ring + Beside::B_STAGES * Beside::B_BYTES;
+    uint8_t* b_ring = v_rows + Steps::B_STAGES * Steps::V_BYTES;
+    uint8_t* c_ring = b_ring + Steps::B_STAGES * Beside::B_BYTES;
     uint64_t* b_full = reinterpret_cast<uint64_t*>(c_ring + Beside::C_STAGES * Beside::C_BYTES);
-    uint64_t* ready = b_full + Beside::B_STAGES;          // B has been looked at, V is there
-    uint64_t* b_empty = ready + Beside::B_STAGES;         // and both have been used
-    uint64_t* c_full = b_empty + Beside::B_STAGES;
+    uint64_t* ready = b_full + Steps::B_STAGES;          // B has been looked at, V is there
+    uint64_t* b_empty = ready + Steps::B_STAGES;         // and both have been used
+    uint64_t* c_full = b_empty + Steps::B_STAGES;
     uint64_t* c_done = c_full + Beside::C_STAGES;         // the result stands in C's place
     uint64_t* c_empty = c_done + Beside::C_STAGES;        // and has left
     uint64_t* acc_full = c_empty + Beside::C_STAGES;
@@ -87,10 +98,11 @@ __global__ void __launch_bounds__(Beside::THREADS, 1)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int chunks_r = (p.r + Beside::SL - 1) / Beside::SL;       // steps of one adapter
+    const int chunks_r = NARROW ? 1 : (p.r + Beside::SL - 1) / Beside::SL;       // steps of one adapter
+    const int second = NARROW ? p.r * 2 : Beside::BOX;               // bytes from a row's first numbers of V to its second
     BesideTiles tile(p);
     if (threadIdx.x == 0) {
-        for (int s = 0; s < Beside::B_STAGES; ++s) {
+        for (int s = 0; s < Steps::B_STAGES; ++s) {
             mbar_init(&b_full[s], 1);
             mbar_init(&ready[s], Beside::V_WARPS);
             mbar_init(&b_empty[s], 1);
@@ -158,14 +170,18 @@ __global__ void __launch_bounds__(Beside::THREADS, 1)
             }
             for (int a = ta.next(); ok && a >= 0; a = ta.next()) {
                 for (int i = 0; i < chunks_r; ++i) {
-                    const int s = static_cast<int>(b_count % Beside::B_STAGES);
-                    ok = mbar_wait_warp(&b_empty[s], static_cast<uint32_t>((b_count / Beside::B_STAGES) & 1) ^ 1, abort_flag, p.wait_ns);
+                    const int s = static_cast<int>(b_count % Steps::B_STAGES);
+                    ok = mbar_wait_warp(&b_empty[s], static_cast<uint32_t>((b_count / Steps::B_STAGES) & 1) ^ 1, abort_flag, p.wait_ns);
                     if (!ok) break;
                     if (elect_one()) {
                         const uint32_t bar = smem_u32(&b_full[s]);
-                        mbar_arrive_expect_tx(&b_full[s], Beside::B_BYTES + (ta.uniform ? Beside::V_BYTES : 0));
+                        mbar_arrive_expect_tx(&b_full[s], Beside::B_BYTES + (ta.uniform ? Steps::V_BYTES : 0));
                         tma_load_nd<false>(b_ring + s * Beside::B_BYTES, &tmB, bar, i * Beside::SL, ch, 0, a, pol);
-                        if (ta.uniform) tma_load_nd<false>(v_rows + s * Beside::V_BYTES, &tmV, bar, i * Beside::SL, tt * Beside::ROWS, 0, pol);
+                        if (ta.uniform) {
+                            uint8_t* to = v_rows + s * Steps::V_BYTES;
+                            if constexpr (NARROW) tma_load_nd<false>(to, &tmV, bar, 0, tt * Beside::ROWS, pol);
+                            else tma_load_nd<false>(to, &tmV, bar, i * Beside::SL, tt * Beside::ROWS, 0, pol);
+                        }
                     }
                     __syncwarp();
                     ++b_count;
@@ -179,8 +195,8 @@ __global__ void __launch_bounds__(Beside::THREADS, 1)
             if (cnt > 0 && !mbar_wait_warp(&c_full[s], static_cast<uint32_t>((cnt - 1) & 1), nullptr, p.wait_ns) && lane == 0)
                 experts::fail(p, ERR_TIMEOUT_DRAIN, abort_flag);
         }
-        for (int s = 0; s < Beside::B_STAGES; ++s) {
-            const int64_t cnt = b_count > s ? (b_count - s + Beside::B_STAGES - 1) / Beside::B_STAGES : 0;
+        for (int s = 0; s < Steps::B_STAGES; ++s) {
+            const int64_t cnt = b_count > s ? (b_count - s + Steps::B_STAGES - 1) / Steps::B_STAGES : 0;
             if (cnt > 0 && !mbar_wait_warp(&b_full[s], static_cast<uint32_t>((cnt - 1) & 1), nullptr, p.wait_ns) && lane == 0)
                 experts::fail(p, ERR_TIMEOUT_DRAIN, abort_flag);
         }
@@ -206,16 +222,16 @@ __global__ void __launch_bounds__(Beside::THREADS, 1)
             uint32_t more = 0;
             for (int a = ta.next(); ok && a >= 0; a = ta.next()) {
                 for (int i = 0; i < chunks_r; ++i) {
-                    const int s = static_cast<int>(steps_done % Beside::B_STAGES);
-                    ok = mbar_wait_warp(&ready[s], static_cast<uint32_t>((steps_done / Beside::B_STAGES) & 1), abort_flag, p.wait_ns);
+                    const int s = static_cast<int>(steps_done % Steps::B_STAGES);
+                    ok = mbar_wait_warp(&ready[s], static_cast<uint32_t>((steps_done / Steps::B_STAGES) & 1), abort_flag, p.wait_ns);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint64_t vd = vd0 + s * (Beside::V_BYTES >> 4), bd = bd0 + s * (Beside::B_BYTES >> 4);
+                    const uint64_t vd = vd0 + s * (Steps::V_BYTES >> 4), bd = bd0 + s * (Beside::B_BYTES >> 4);
                     const int steps = (min(Beside::SL, p.r - i * Beside::SL) + 15) / 16;
                     if (elect_one()) {
                         for (int part = 0; part < 2; ++part)
                             for (int k = 0; k < steps; ++k) {
-                                mma_bf16(acc, vd + part * (Beside::BOX >> 4) + k * 2, bd + k * 2, Beside::IDESC, more);
+                                mma_bf16(acc, vd + part * (second >> 4) + k * 2, bd + k * 2, Beside::IDESC, more);
                                 more = 1;
                             }
                         mma_commit(&b_empty[s]);
@@ -359,7 +375,8 @@ __global__ void __launch_bounds__(Beside::THREADS, 1)
         int64_t step = 0;
         int marks = 0, had = -1, own = -1;           // had: the token tile whose V is loaded
         bool ok = true;
-        uint4 v[8];
+        constexpr int VECS = NARROW ? 4 : 8;
+        uint4 v[VECS];
         TileAdapters ta;
         bool live = tile.next(p);
         if (live) ta.look_ahead(p, tile.tt);
@@ -368,7 +385,7 @@ __global__ void __launch_bounds__(Beside::THREADS, 1)
             const uint4* src = reinterpret_cast<const uint4*>(v_row(p, t)) + part * (p.r / 8);
             auto load = [&](int i, int vecs) {
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
+                for (int c = 0; c < VECS; ++c) {
                     v[c] = make_uint4(0, 0, 0, 0);
                     if (own >= 0 && c < vecs) v[c] = __ldcg(src + i * 8 + c);
                 }
@@ -378,8 +395,8 @@ __global__ void __launch_bounds__(Beside::THREADS, 1)
             if (live) ta.look_ahead(p, tile.tt);
             if (ta.uniform) {                    // V comes with B
                 for (int i = 0; ok && i < chunks_r; ++i, ++step) {
-                    const int s = static_cast<int>(step % Beside::B_STAGES);
-                    ok = mbar_wait_warp(&b_full[s], static_cast<uint32_t>((step / Beside::B_STAGES) & 1), abort_flag, p.wait_ns);
+                    const int s = static_cast<int>(step % Steps::B_STAGES);
+                    ok = mbar_wait_warp(&b_full[s], static_cast<uint32_t>((step / Steps::B_STAGES) & 1), abort_flag, p.wait_ns);
                     if (!ok) break;
                     if (lane == 0) mbar_arrive(&ready[s]);
                     __syncwarp();
@@ -394,17 +411,18 @@ __global__ void __launch_bounds__(Beside::THREADS, 1)
             bool found = false;
             for (int a = ta.next(); ok && a >= 0; a = ta.next()) {
                 for (int i = 0; i < chunks_r; ++i) {
-                    const int s = static_cast<int>(step % Beside::B_STAGES);
+                    const int s = static_cast<int>(step % Steps::B_STAGES);
                     const int vecs = min(Beside::SL, p.r - i * Beside::SL) / 8, steps = (vecs + 1) / 2;
                     if (chunks_r > 1) load(i, vecs);
-                    ok = mbar_wait_warp(&b_full[s], static_cast<uint32_t>((step / Beside::B_STAGES) & 1), abort_flag, p.wait_ns);
+                    ok = mbar_wait_warp(&b_full[s], static_cast<uint32_t>((step / Steps::B_STAGES) & 1), abort_flag, p.wait_ns);
                     if (!ok) break;
-                    // (B was copied after the step before the last had been used: its rows of V are free too)
-                    uint8_t* to = v_rows + s * Beside::V_BYTES + part * Beside::BOX + row * 128;
+                    // (B was copied after the stage's last step had been used: its rows of V are free too)
+                    uint8_t* to = v_rows + s * Steps::V_BYTES + (NARROW ? 0 : part * second) + row * 128;
+                    const int c0 = NARROW ? part * (second / 16) : 0;
                     const bool hit = own == a;
 #pragma unroll
-                    for (int c = 0; c < 8; ++c)
-                        if (c < 2 * steps) *reinterpret_cast<uint4*>(to + ((c ^ swizzle) << 4)) = hit ? v[c] : make_uint4(0, 0, 0, 0);
+                    for (int c = 0; c < VECS; ++c)
+                        if (c < 2 * steps) *reinterpret_cast<uint4*>(to + (((c0 + c) ^ swizzle) << 4)) = hit ? v[c] : make_uint4(0, 0, 0, 0);
                     found = make_finite(b_ring + s * Beside::B_BYTES + row * 128, swizzle, 4 * part, min(vecs, 4 * part + 4)) || found;
                     fence_proxy_async_smem();
                     __syncwarp();

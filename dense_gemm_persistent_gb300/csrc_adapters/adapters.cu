@@ -258,6 +258,7 @@ dgemm_status_t launch_prompt(const Call& c, const Params& p, const dg::host::Dev
 }
 
 // Beside a product, BF16 in and out, rows on 16 bytes.
+template <bool NARROW>
 dgemm_status_t launch_beside(const Call& c, const Params& p, const dg::host::Device& dev) {
     using dg::adapters::Beside;
     const int64_t items = static_cast<int64_t>(p.tiles) * p.ctiles;
@@ -272,16 +273,23 @@ dgemm_status_t launch_beside(const Call& c, const Params& p, const dg::host::Dev
     if (ok && p.L > 0) {
         const uint64_t db[4] = {r, N, 1, L}, sb[3] = {r * 2, N * r * 2, N * r * 2};
         const uint32_t bb[4] = {Beside::SL, Beside::COLS, 1, 1};
-        const uint64_t dv[3] = {r, T, 2}, sv[2] = {r * 4, r * 2};         // [part][row]: the slices of a step in one copy
-        const uint32_t bv[3] = {Beside::SL, Beside::ROWS, 2};
-        ok = dg::host::encode_map(&b, kBf16, c.B, 4, db, sb, bb) && dg::host::encode_map(&v, kBf16, p.V, 3, dv, sv, bv);
+        ok = dg::host::encode_map(&b, kBf16, c.B, 4, db, sb, bb);
+        if (NARROW) {                             // a row's numbers of V in one slice
+            const uint64_t dv[2] = {2 * r, T}, sv[1] = {r * 4};
+            const uint32_t bv[2] = {Beside::SL, Beside::ROWS};
+            ok = ok && dg::host::encode_map(&v, kBf16, p.V, 2, dv, sv, bv);
+        } else {                                  // [part][row]: both slices of a step in one copy
+            const uint64_t dv[3] = {r, T, 2}, sv[2] = {r * 4, r * 2};
+            const uint32_t bv[3] = {Beside::SL, Beside::ROWS, 2};
+            ok = ok && dg::host::encode_map(&v, kBf16, p.V, 3, dv, sv, bv);
+        }
     }
     if (!ok) return DGEMM_ERR_CUDA;
     static std::atomic<unsigned char> ready[dg::host::kMaxDevices];
-    if (!allow_shared(ready, dev.id, reinterpret_cast<const void*>(&dg::adapters::adapter_beside), kShared)) return DGEMM_ERR_CUDA;
+    if (!allow_shared(ready, dev.id, reinterpret_cast<const void*>(&dg::adapters::adapter_beside<NARROW>), kShared)) return DGEMM_ERR_CUDA;
     const int ctas = static_cast<int>(std::min<int64_t>(dev.num_sms, items));
     dg::host::Launch l(static_cast<unsigned>(ctas), 1, Beside::THREADS, Beside::SMEM, c.stream);
-    return cudaLaunchKernelEx(&l.cfg, dg::adapters::adapter_beside, cm, dm, b, v, p) == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
+    return cudaLaunchKernelEx(&l.cfg, dg::adapters::adapter_beside<NARROW>, cm, dm, b, v, p) == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
 }
 
 dgemm_status_t run_adapters(const Call& c) {
@@ -338,11 +346,11 @@ dgemm_status_t run_adapters(const Call& c) {
     // One wave of the few-row form's tiles, or the prompt form: on the device 128 rows of 4096 channels, every row another
     // adapter of rank 64, 33 against 55 us, 256 rows 47 against 63 (one request: 28, 29), 384 115 against 99; of 11008
     // channels 64 rows 37 against 49, 128 65 against 61 (one request: 48, 31). Beside a product of 11008 channels, rank 32, 200
-    // rows of one request after another 49 against 23, every row another of 48 60 against 81: only the device knows which.
+    // rows of one request after another 49 against 21, every row another of 48 60 against 62; 600 rows 90 and 28, 132 and 114.
     const int full = p.gated ? 64 : 128;
     const int64_t few_tiles = static_cast<int64_t>((p.T + Few::MOST_COLS - 1) / Few::MOST_COLS) * ((p.wide + full - 1) / full);
     p.prompt = forced >= 0 ? forced : few_tiles > dev.num_sms;
-    // Beside a product in BF16 whose rows TMA can copy: a form of its own (4096 x 11008 with SiLU 67 us, in the general one 116).
+    // Beside a product in BF16 whose rows TMA can copy: a form of its own (4096 x 11008 with SiLU 64 us, in the general one 116).
     const bool beside = p.prompt && !c.W && c.d_dtype == DGEMM_BF16 && (!c.C || c.c_dtype == DGEMM_BF16) && p.N % 8 == 0;
     if (beside) {
         p.width = dg::adapters::Beside::ROWS;
@@ -355,7 +363,9 @@ dgemm_status_t run_adapters(const Call& c) {
         const dgemm_status_t s = few_for_v(p.T, p.r, p.K) ? launch_shrink_few(p, dev, c.stream) : launch_shrink_many(c, p, dev);
         if (s != DGEMM_OK) return s;
     }
-    return beside ? launch_beside(c, p, dev) : p.prompt ? launch_prompt(c, p, dev) : launch_few(c, p, dev);
+    // (three steps on their way or two: see Beside::Steps)
+    if (beside) return p.r == 16 || p.r == 32 ? launch_beside<true>(c, p, dev) : launch_beside<false>(c, p, dev);
+    return p.prompt ? launch_prompt(c, p, dev) : launch_few(c, p, dev);
 }
 
 }  // namespace
