@@ -6,10 +6,10 @@
 // the tile's rows of V with zeros for other requests' rows; two or three steps are on their way. A CTA has
 // an equal share of the tiles in an order that goes round the token tiles, so that token tiles of many
 // adapters are shared out too.
-// As in adapter_mma.cuh, B_a is looked at before it is used, because a zero does not hide a number that is not finite. Both the
-// zeros and the look are the work of warps of their own, and take a tile 2.3 us. Where all rows of a token tile have
-// the same adapter neither is needed: V comes by TMA as it is, and the warps only pass the step on.
-// 4096 x 11008, 8 adapters of rank 32 in runs of rows, SiLU and bias: 64-67 us with the launch that computes V (10-12 of
+// As in adapter_mma.cuh, B_a is looked at before it is used: a zero does not hide a number that is not finite, and the two
+// numbers of V may have opposite signs. The masked rows and the look are the work of warps of their own, 2.3 us a
+// tile. Where all rows of a token tile have the same adapter V needs no zeros and comes by TMA as it is.
+// 4096 x 11008, 8 adapters of rank 32 in runs of rows, SiLU and bias: 64-68 us with the launch that computes V (10-12 of
 // them); the bytes take 33. The epilogue computes for 26 of a CTA's 40 us (two operations of the special function unit a
 // value; 17 without an activation); the rest are waits for C and for sums of token tiles of several adapters.
 // (Tried and measured when this form was made: that case by the prompt form of adapter_mma.cuh, which has C and D by
@@ -45,8 +45,6 @@ struct Beside {
     static_assert((3 * MOST_B_STAGES + 3 * C_STAGES + 2 * ACCS + MARKS + 1) * 8 + 8 + MARKS * (V_WARPS + 4) <= BAR_BYTES, "barriers fit");
     static_assert(SMEM <= 232448 && V_WARPS == 8, "shared memory; a tile's marks are one 64-bit word");
 };
-
-constexpr int kNoAdapters = -1, kNotLooked = -2;      // of a tile, in the place of its number among those with a look at B
 
 // A CTA's tiles, in order: token tiles first, then channels. (Steps, not divisions: sixteen warps take them for every tile.)
 struct BesideTiles {
@@ -90,10 +88,10 @@ __global__ void __launch_bounds__(Beside::THREADS, 1)
     uint64_t* c_empty = c_done + Beside::C_STAGES;        // and has left
     uint64_t* acc_full = c_empty + Beside::C_STAGES;
     uint64_t* acc_empty = acc_full + Beside::ACCS;
-    uint64_t* looked = acc_empty + Beside::ACCS;          // [MARKS] the n-th tile with a look: its slices of B have been looked at
+    uint64_t* looked = acc_empty + Beside::ACCS;          // [MARKS] the n-th tile with adapters: its slices of B have been looked at
     uint64_t* drain = looked + Beside::MARKS;
     uint64_t* dirty = drain + 1;                          // [MARKS] a byte for every warp that looked
-    int* mark_of = reinterpret_cast<int*>(dirty + Beside::MARKS);   // [MARKS] which of the tiles with a look at B a tile is
+    int* mark_of = reinterpret_cast<int*>(dirty + Beside::MARKS);   // [MARKS] which of the tiles with adapters a tile is, -1: none
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(mark_of + Beside::MARKS);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -244,10 +242,10 @@ __global__ void __launch_bounds__(Beside::THREADS, 1)
             if (!ok) break;
             if (elect_one()) {
                 mma_commit(&acc_full[buf]);
-                mark_of[local % Beside::MARKS] = !more ? kNoAdapters : ta.uniform ? kNotLooked : marks;
+                mark_of[local % Beside::MARKS] = more ? marks : -1;
                 mbar_arrive(&acc_full[buf]);
             }
-            marks += more && !ta.uniform;
+            marks += more;
             __syncwarp();
         }
         if (elect_one()) {
@@ -299,9 +297,9 @@ __global__ void __launch_bounds__(Beside::THREADS, 1)
             if (!ok) break;
             tc_fence_after();
             const int mark = mark_of[local % Beside::MARKS];
-            const bool some = mark != kNoAdapters;
+            const bool some = mark >= 0;
             bool found = false;
-            if (mark >= 0) {
+            if (some) {
                 ok = mbar_wait_warp(&looked[mark % Beside::MARKS], (mark / Beside::MARKS) & 1, abort_flag, p.wait_ns);
                 if (!ok) break;
                 found = dirty[mark % Beside::MARKS] != 0;
@@ -393,17 +391,7 @@ __global__ void __launch_bounds__(Beside::THREADS, 1)
             ta.open(p, tt);
             live = tile.next(p);
             if (live) ta.look_ahead(p, tile.tt);
-            if (ta.uniform) {                    // V comes with B
-                for (int i = 0; ok && i < chunks_r; ++i, ++step) {
-                    const int s = static_cast<int>(step % Steps::B_STAGES);
-                    ok = mbar_wait_warp(&b_full[s], static_cast<uint32_t>((step / Steps::B_STAGES) & 1), abort_flag, p.wait_ns);
-                    if (!ok) break;
-                    if (lane == 0) mbar_arrive(&ready[s]);
-                    __syncwarp();
-                }
-                continue;
-            }
-            if (tt != had) {
+            if (tt != had && !ta.uniform) {              // (uniform: V comes with B)
                 own = t < p.T && p.L > 0 ? adapter_of(p, t) : -1;
                 if (chunks_r == 1) load(0, p.r / 8);
                 had = tt;
@@ -413,16 +401,18 @@ __global__ void __launch_bounds__(Beside::THREADS, 1)
                 for (int i = 0; i < chunks_r; ++i) {
                     const int s = static_cast<int>(step % Steps::B_STAGES);
                     const int vecs = min(Beside::SL, p.r - i * Beside::SL) / 8, steps = (vecs + 1) / 2;
-                    if (chunks_r > 1) load(i, vecs);
+                    if (chunks_r > 1 && !ta.uniform) load(i, vecs);
                     ok = mbar_wait_warp(&b_full[s], static_cast<uint32_t>((step / Steps::B_STAGES) & 1), abort_flag, p.wait_ns);
                     if (!ok) break;
-                    // (B was copied after the stage's last step had been used: its rows of V are free too)
-                    uint8_t* to = v_rows + s * Steps::V_BYTES + (NARROW ? 0 : part * second) + row * 128;
-                    const int c0 = NARROW ? part * (second / 16) : 0;
-                    const bool hit = own == a;
+                    if (!ta.uniform) {
+                        // (B was copied after the stage's last step had been used: its rows of V are free too)
+                        uint8_t* to = v_rows + s * Steps::V_BYTES + (NARROW ? 0 : part * second) + row * 128;
+                        const int c0 = NARROW ? part * (second / 16) : 0;
+                        const bool hit = own == a;
 #pragma unroll
-                    for (int c = 0; c < VECS; ++c)
-                        if (c < 2 * steps) *reinterpret_cast<uint4*>(to + (((c0 + c) ^ swizzle) << 4)) = hit ? v[c] : make_uint4(0, 0, 0, 0);
+                        for (int c = 0; c < VECS; ++c)
+                            if (c < 2 * steps) *reinterpret_cast<uint4*>(to + (((c0 + c) ^ swizzle) << 4)) = hit ? v[c] : make_uint4(0, 0, 0, 0);
+                    }
                     found = make_finite(b_ring + s * Beside::B_BYTES + row * 128, swizzle, 4 * part, min(vecs, 4 * part + 4)) || found;
                     fence_proxy_async_smem();
                     __syncwarp();

@@ -164,6 +164,28 @@ def test_a_bad_adapter_stays_with_its_request(form, T, order, bad):
         setattr(p, where, keep)
 
 
+@pytest.mark.parametrize("T,K,r", [(256, 256, 16), (400, 64, 32), (300, 128, 24), (520, 64, 128)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_a_bad_adapter_that_whole_tiles_share(form, T, K, r, bad):
+    # V = +-1 and +-1.01 (not a BF16 number): its rest is 0 or has the other sign, and the infinity stays what it is
+    p = Problem(T, 264, K, r, 6, order="none")
+    p.ids[:] = 2
+    p.ids[T // 256 * 256:] = 4
+    p.X[:] = 0
+    p.X[:, 0] = torch.tensor([1.0, -1.0, 1.0078125, -1.0078125] * T)[:T].to(BF)
+    p.A[:] = 0
+    p.A[:, :, 0] = 1.0
+    p.A[:, r // 2:, 0] = 1.0078125
+    p.scale[:] = 1.0
+    p.B[2, 5, 3] = p.B[2, 200, r - 1] = bad
+    for got, beside, out in ((p.project(out=F32).cpu(), dict(W=p.W), F32), (p.add(out=BF, c=BF).cpu(), dict(C=p.C.to(BF)), BF),
+                             (p.add(out=F32, c=BF).cpu(), dict(C=p.C.to(BF)), F32)):
+        want = ref.adapters(p.X, p.A, p.B, p.ids, **beside, scale=p.scale, out_dtype=out)[0]
+        assert torch.equal(torch.isnan(got), torch.isnan(want))
+        assert torch.equal(got[torch.isinf(want)], want[torch.isinf(want)].to(out))
+        assert torch.equal(torch.isfinite(got), torch.isfinite(want))
+
+
 @pytest.mark.parametrize("T", [8, 64, 300])
 def test_a_bad_row_stays_alone(form, T):
     p = Problem(T, 264, 256, 16, 6, order="one")
