@@ -325,3 +325,23 @@ def test_a_workspace_of_exactly_the_size_and_what_lies_behind(form, T):
     assert bool((room[n:] == 0x5A).all()) and bool((D[0] == 7).all()) and bool((D[T + 1] == 7).all())
     with pytest.raises(dg.DgemmError):
         dg.dgemm_adapter_bf16(X, W, A, B, ids, D[1:T + 1], scale=scale, ws=room[:n - 1])
+
+
+@pytest.mark.parametrize("T,N,K,r", [(60, 136, 64, 8), (260, 264, 72, 16), (1100, 200, 128, 32), (700, 136, 64, 72)])
+def test_the_most_adapters_and_tables_on_four_bytes(form, T, N, K, r):
+    # every row another of 4096: hundreds in a token tile; ids, scale and bias start on any element
+    p = Problem(T, N, K, r, 4096, with_bias=True)
+    p.ids[4:] = (torch.arange(T - 4, dtype=torch.int32) * 1361 + 7) % 4096
+    X, W, A, B, C = p.on_gpu("X", "W", "A", "B", "C")
+    shift = lambda t: torch.cat([t[:1], t]).to(dev())[1:]
+    ids, scale, bias = shift(p.ids), shift(p.scale), shift(p.bias)
+    assert ids.data_ptr() % 16 == 4
+    for C_, out in ((None, BF), (C.to(BF), BF), (C, F32)):
+        D, ws = torch.empty(T, N, dtype=out, device=dev()), p.workspace()
+        if C_ is None:
+            dg.dgemm_adapter_bf16(X, W, A, B, ids, D, scale=scale, bias=bias, act="silu", ws=ws)
+        else:
+            dg.dgemm_adapter_add(X, A, B, ids, D, C=C_, scale=scale, bias=bias, act="silu", ws=ws)
+        assert status_ok(ws)
+        beside = dict(W=p.W) if C_ is None else dict(C=C_.cpu())
+        close(D, ref.adapters(p.X, p.A, p.B, p.ids, **beside, scale=p.scale, bias=p.bias, act="silu", out_dtype=out))
