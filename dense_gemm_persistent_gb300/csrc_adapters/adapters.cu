@@ -6,6 +6,7 @@
 
 #include "adapter_beside.cuh"
 #include "adapter_few.cuh"
+#include "adapter_forms.h"
 #include "adapter_mma.cuh"
 #include "adapter_shrink.cuh"
 #include "host.h"
@@ -261,6 +262,7 @@ dgemm_status_t launch_prompt(const Call& c, const Params& p, const dg::host::Dev
 template <bool NARROW>
 dgemm_status_t launch_beside(const Call& c, const Params& p, const dg::host::Device& dev) {
     using dg::adapters::Beside;
+    if (p.gated) return DGEMM_ERR_NOT_SUPPORTED;          // (D's map has rows of N channels)
     const int64_t items = static_cast<int64_t>(p.tiles) * p.ctiles;
     if (items > INT32_MAX / 2) return DGEMM_ERR_NOT_SUPPORTED;
     const uint64_t N = p.N, T = p.T, r = p.r, L = p.L, d[2] = {N, T}, st[1] = {N * 2};
@@ -351,7 +353,7 @@ dgemm_status_t run_adapters(const Call& c) {
     const int64_t few_tiles = static_cast<int64_t>((p.T + Few::MOST_COLS - 1) / Few::MOST_COLS) * ((p.wide + full - 1) / full);
     p.prompt = forced >= 0 ? forced : few_tiles > dev.num_sms;
     // Beside a product in BF16 whose rows TMA can copy: a form of its own (4096 x 11008 with SiLU 64 us, in the general one 116).
-    const bool beside = p.prompt && !c.W && c.d_dtype == DGEMM_BF16 && (!c.C || c.c_dtype == DGEMM_BF16) && p.N % 8 == 0;
+    const bool beside = dg::adapters::beside_form(p.prompt, c.W != nullptr, p.gated, p.d_f32, c.C && p.c_f32, p.N);
     if (beside) {
         p.width = dg::adapters::Beside::ROWS;
         p.tiles = (p.T + p.width - 1) / p.width;
