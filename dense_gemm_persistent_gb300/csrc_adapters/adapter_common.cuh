@@ -23,7 +23,7 @@ struct Params : experts::Params {      // (of those: C, D, bias, N, K, wide, gat
     const __nv_bfloat16* X;            // [T][K]
     const __nv_bfloat16* low;          // A [L][r][K]
     const __nv_bfloat16* high;         // B [L][N][r]
-    __nv_bfloat16* V;                  // [T][2][r]: V = first + second
+    void* V;                           // prompt form: BF16 [T][2][r], V = first + second; else float [T][r]
     int* lists;                        // prompt form: [tiles][kListPitch], the adapters of a token tile: how many, which
     int T, L, r;
     int tiles, width;                  // token tiles and their rows
@@ -113,7 +113,11 @@ __device__ __forceinline__ void fma8(float& s0, float& s1, const uint4& b, const
     s1 = fmaf(v1.w, bf16_hi(b.w), s1);
 }
 
-__device__ __forceinline__ __nv_bfloat16* v_row(const Params& p, int t) { return p.V + static_cast<int64_t>(t) * 2 * p.r; }
+// Row t of V: of the prompt form, and of the few-row form.
+__device__ __forceinline__ __nv_bfloat16* v_row(const Params& p, int t) {
+    return static_cast<__nv_bfloat16*>(p.V) + static_cast<int64_t>(t) * 2 * p.r;
+}
+__device__ __forceinline__ float* v_row_f32(const Params& p, int t) { return static_cast<float*>(p.V) + static_cast<int64_t>(t) * p.r; }
 
 // Bits of the adapters in use among n rows, by `threads` threads that all pass.
 __device__ __forceinline__ void mark_adapters(const Params& p, int first, int n, unsigned* words, int tid, int threads) {
@@ -162,10 +166,18 @@ __device__ __forceinline__ void list_tile(const Params& p, int tile, unsigned* w
     sync();
 }
 
-// V goes to the tensor core as two BF16 numbers whose sum is V up to 2^-18 of it (an infinity has no second): one
-// alone would cost half of the adapter's precision, FP32 has no exact way through.
+// The few-row form multiplies V by B on FP32 units and has it in FP32. To the tensor core it goes as two BF16 numbers, in
+// the same bytes: a BF16 number has 8 significant bits, so that the first leaves up to 2^-8 of V and the second up to
+// 2^-9 of that, V up to 2^-17 in all (an infinity has no second). One alone would cost half of the
+// adapter's precision, FP32 has no exact way through.
 // Eight numbers of a row, from `at` on.
 __device__ __forceinline__ void store_v(const Params& p, int t, int at, const float (&v)[8]) {
+    if (!p.prompt) {
+        float4* out = reinterpret_cast<float4*>(v_row_f32(p, t) + at);
+        out[0] = make_float4(v[0], v[1], v[2], v[3]);
+        out[1] = make_float4(v[4], v[5], v[6], v[7]);
+        return;
+    }
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
@@ -179,6 +191,10 @@ __device__ __forceinline__ void store_v(const Params& p, int t, int at, const fl
 }
 // One of them.
 __device__ __forceinline__ void store_one(const Params& p, int t, int at, float v) {
+    if (!p.prompt) {
+        v_row_f32(p, t)[at] = v;
+        return;
+    }
     const __nv_bfloat16 hi = __float2bfloat16_rn(v);
     const float rest = v - __bfloat162float(hi);
     v_row(p, t)[at] = hi;

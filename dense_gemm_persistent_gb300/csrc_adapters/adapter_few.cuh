@@ -406,24 +406,18 @@ __global__ void __launch_bounds__(65536 / 128, 1)
         if (mine > 0) {
             {
                 const int q0 = ew;                          // rows of a warp: all of their loads together
-                uint2 hi[MOST], lo[MOST];
+                float4 v[MOST];
 #pragma unroll
                 for (int n = 0; n < MOST; ++n) {
                     const int q = q0 + n * Few::EPI_WARPS;
-                    hi[n] = lo[n] = make_uint2(0, 0);
-                    if (q < mine && lane < p.r / 4) {       // (rows without an adapter have no V; theirs is not used)
-                        const __nv_bfloat16* v = v_row(p, row0 + rank + split * q) + 4 * lane;
-                        hi[n] = __ldcg(reinterpret_cast<const uint2*>(v));
-                        lo[n] = __ldcg(reinterpret_cast<const uint2*>(v + p.r));
-                    }
+                    v[n] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (q < mine && lane < p.r / 4)         // (rows without an adapter have no V; theirs is not used)
+                        v[n] = __ldcg(reinterpret_cast<const float4*>(v_row_f32(p, row0 + rank + split * q)) + lane);
                 }
 #pragma unroll
                 for (int n = 0; n < MOST; ++n) {
                     const int q = q0 + n * Few::EPI_WARPS;
-                    if (q < mine && lane < p.r / 4)
-                        reinterpret_cast<float4*>(v_rows + q * p.r)[lane] =
-                            make_float4(bf16_lo(hi[n].x) + bf16_lo(lo[n].x), bf16_hi(hi[n].x) + bf16_hi(lo[n].x),
-                                        bf16_lo(hi[n].y) + bf16_lo(lo[n].y), bf16_hi(hi[n].y) + bf16_hi(lo[n].y));
+                    if (q < mine && lane < p.r / 4) reinterpret_cast<float4*>(v_rows + q * p.r)[lane] = v[n];
                 }
             }
             asm volatile("barrier.cta.sync 1, %0;" ::"n"(Few::EPI_THREADS) : "memory");

@@ -322,7 +322,7 @@ dgemm_status_t run_adapters(const Call& c) {
     p.ids = c.ids;
     p.scale = c.scale;
     const Workspace ws(c.T, c.r);
-    p.V = reinterpret_cast<__nv_bfloat16*>(static_cast<char*>(c.ws) + DGEMM_WS_STATUS_BYTES);
+    p.V = static_cast<char*>(c.ws) + DGEMM_WS_STATUS_BYTES;
     p.lists = reinterpret_cast<int*>(static_cast<char*>(c.ws) + ws.lists);
     p.T = static_cast<int>(c.T);
     p.N = static_cast<int>(c.N);

@@ -46,8 +46,9 @@ extern "C" {
  *   ws     dgemm_adapter_workspace_size(T, N, K, r, L) bytes, contents arbitrary
  *          (DGEMM_ERR_WORKSPACE_TOO_SMALL with less).
  * FP32 accumulation, one rounding to D's type. V = scale[a] * (X . A_a^T) is summed and scaled
- * in FP32 and kept as two BF16 numbers whose sum is V up to 2^-18 of it (a magnitude of
- * 3.39e38 or more, that BF16 cannot hold, counts as infinite). A row depends on its own adapter alone:
+ * in FP32. The form for few rows keeps it so; the one for prompts keeps two BF16 numbers
+ * whose sum is V up to 2^-17 of it (a magnitude of 3.39e38 or more, that BF16 cannot hold,
+ * counts as infinite there). A row depends on its own adapter alone:
  * NaN and infinities in another one do not reach it. NaN stays NaN under every activation.
  * r and K are multiples of 8 (DGEMM_ERR_MISALIGNED otherwise), 8 <= r <= DGEMM_MAX_ADAPTER_RANK,
  * 0 <= L <= DGEMM_MAX_ADAPTERS. K == 0: every product is zero. */
