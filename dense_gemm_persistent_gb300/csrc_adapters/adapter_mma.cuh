@@ -9,8 +9,8 @@
 // Warps of a CTA: 0 TMA producer, 1 MMA issuer and owner of the Tensor Memory, 2-3 idle,
 // 4-11 epilogue, 12-19 write the masked rows of V and look at B.
 // A zero does not hide a number that is not finite: B_a goes through products with the zeros of other
-// requests' rows. So the last warps look at a slice of B_a before it is used, put zeros in the
-// place of what is not finite, and the epilogue adds those terms to the rows that they belong to, by FP32
+// requests' rows. So the last warps look at a slice of B_a before it is used, put finite numbers in the
+// place of what is not, and the epilogue adds those terms to the rows that they belong to, by FP32
 // units: slow, and of these rows only.
 #pragma once
 
@@ -82,8 +82,11 @@ struct TileAdapters {
 
 __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
 
-// Puts zeros in the place of numbers that are not finite in the 16-byte vectors [first, last), four at most, of a swizzled row; whether
-// there were any. Such a number times zero is NaN, and a sum keeps it: one operation for two numbers.
+// Replaces the numbers that are not finite in the 16-byte vectors [first, last), four at most, of a swizzled row; whether
+// there were any. Such a number times zero is NaN, and a sum keeps it: one operation for two numbers. An infinity becomes the
+// smallest normal number of its sign, not zero: where the row's own V is infinite too, the product is then the
+// infinity that it has to be (with a zero it would be NaN, which nothing added later takes back). Of a finite V it
+// leaves 2^-126 of it, 4 at most, in a sum that not_finite_terms makes infinite or NaN.
 __device__ __forceinline__ bool make_finite(uint8_t* row, int swizzle, int first, int last) {
     const __nv_bfloat162 zero = __float2bfloat162_rn(0.0f);
     __nv_bfloat162 nan[2] = {zero, zero};
@@ -102,8 +105,11 @@ __device__ __forceinline__ bool make_finite(uint8_t* row, int swizzle, int first
     for (int c = first; c < last; ++c) {
         uint32_t* word = reinterpret_cast<uint32_t*>(row + ((c ^ swizzle) << 4));
         for (int k = 0; k < 4; ++k) {
-            const uint32_t v = word[k];
-            word[k] = ((v & 0x7F80u) == 0x7F80u ? 0u : v & 0xFFFFu) | ((v & 0x7F800000u) == 0x7F800000u ? 0u : v & 0xFFFF0000u);
+            const uint32_t v = word[k], lo = v & 0xFFFFu, hi = v & 0xFFFF0000u;
+            // (an infinity: 2^-126 with its sign; NaN: 0)
+            const uint32_t in_lo = (v & 0x7Fu) == 0 ? (v & 0x8000u) | 0x0080u : 0u;
+            const uint32_t in_hi = (v & 0x7F0000u) == 0 ? (v & 0x80000000u) | 0x00800000u : 0u;
+            word[k] = ((v & 0x7F80u) == 0x7F80u ? in_lo : lo) | ((v & 0x7F800000u) == 0x7F800000u ? in_hi : hi);
         }
     }
     return true;
