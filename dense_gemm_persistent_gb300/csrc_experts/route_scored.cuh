@@ -424,7 +424,8 @@ __device__ __forceinline__ void route_scored_token(const ScoredParams& p, int t,
             }
         }
         if (lane >= p.groups) m1 = m2 = kNone;
-        const unsigned worth = p.top2 && m2 > kNone ? ordered(unordered(m1) + unordered(m2) + 0.0f) : m1;
+        // (two finite numbers: a sum below FP32's range is the lowest there is, not kNone; the margin then sends it to FP64)
+        const unsigned worth = p.top2 && m2 > kNone ? ordered(fmaxf(unordered(m1) + unordered(m2), -FLT_MAX) + 0.0f) : m1;
         const Border at = keep_groups(p, worth);
         unsigned kept = at.kept;
         if (!BY_LOGIT && at.out) {
