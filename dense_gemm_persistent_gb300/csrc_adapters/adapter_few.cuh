@@ -36,9 +36,26 @@ struct Few {
         return 1024 + stages * stage_bytes(cols) + (cols + split - 1) / split * (512 + r * 4) +
                EPI_WARPS * ahead * item_channels(r) * r * 2 + GROUP_BYTES + BAR_BYTES;
     }
+    // Items of B that a warp copies ahead: up to 128 KB of them in a CTA, 64 beside a product; the ring has what is left.
+    static __host__ __device__ constexpr int items_ahead(int r, bool product) {
+        const int n = (product ? 64 : 128) * 1024 / (EPI_WARPS * item_channels(r) * r * 2);
+        return n < MOST_AHEAD ? n : MOST_AHEAD;
+    }
+    // the most that two stages need, or none
+    static __host__ __device__ constexpr int most_bytes() {
+        int most = 0;
+        for (int r = 8; r <= DGEMM_MAX_ADAPTER_RANK; r += 8) {
+            const int with = smem_bytes(MOST_COLS, 2, 1, r, items_ahead(r, true)), without = smem_bytes(MOST_COLS, 0, 1, r, items_ahead(r, false));
+            most = with > most ? with : most;
+            most = without > most ? without : most;
+        }
+        return most;
+    }
     static_assert((2 * MOST_STAGES + EPI_WARPS * MOST_AHEAD + 2) * 8 + 8 <= BAR_BYTES, "barriers fit");
-    // (the parts of a CTA's rows, up to 71 x 128 floats, are never more than two stages hold)
+    // (a split divides the columns, a multiple of 16: all parts of a CTA's rows are MOST_COLS rows of 128 floats)
+    static_assert(MOST_COLS * 512 <= 2 * (W_BYTES + KS * 16 * 128), "two stages hold the parts of a CTA's rows");
 };
+static_assert(Few::most_bytes() <= 232448, "two stages always fit");
 
 template <int ACT>
 __device__ __forceinline__ float activate_one(float v) {

@@ -183,7 +183,7 @@ dgemm_status_t launch_few(const Call& c, Params& p, const dg::host::Device& dev)
     // CTAs of a cluster that share K, and channels of a tile: the least time by a model of what a CTA reads (rows of W
     // and X times its stages, in waves of the clusters that fit at once), a wave's ends as 1000 such units of about 4 ns, the
     // exchange of parts as 150.
-    // (11008 channels: 138 CTAs of 80, not 86 of 128; 4096: 76 pairs of CTAs of 56 channels and half of K.)
+    // (K = 4096: 11008 channels 138 CTAs of 80, not 86 of 128; 4096 channels 35 clusters of 4 CTAs, 120 channels and a quarter of K.)
     int64_t least = INT64_MAX;
     for (int split = 1; split <= Few::MOST_SPLIT && (split == 1 || p.kstages >= 4 * split); split *= 2) {
         const int slots = split == 1 ? dev.num_sms : most_clusters(dev, split);
@@ -200,13 +200,11 @@ dgemm_status_t launch_few(const Call& c, Params& p, const dg::host::Device& dev)
     }
     p.ctiles = (p.wide + p.channels - 1) / p.channels;
     const int64_t tiles = static_cast<int64_t>(p.tiles) * p.ctiles;
-    // Items of B ahead: up to 128 KB of them, 64 beside a product; the ring has what is left.
-    const int ahead = (p.kstages > 0 ? 64 : 128) * 1024 / (Few::EPI_WARPS * Few::item_channels(p.r) * p.r * 2);
-    p.ahead = p.L > 0 ? std::min(Few::MOST_AHEAD, ahead) : 0;
+    p.ahead = p.L > 0 ? Few::items_ahead(p.r, p.kstages > 0) : 0;
     auto shared = [&](int stages) { return Few::smem_bytes(p.width, stages, p.split, p.r, p.ahead); };
     p.stages = p.kstages > 0 ? 2 : 0;
     while (p.stages > 0 && p.stages < Few::MOST_STAGES && shared(p.stages + 1) <= kShared) ++p.stages;
-    const int smem = shared(p.stages);            // (two stages always fit: at most 231424 bytes, rank 128 and 64 rows)
+    const int smem = shared(p.stages);            // (two stages always fit: Few::most_bytes)
     alignas(64) CUtensorMap w, x;
     std::memset(&w, 0, sizeof w);
     std::memset(&x, 0, sizeof x);
