@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(Beside::THREADS, 1)
             live = tile.next(p);
             if (live) ta.look_ahead(p, tile.tt);
             if (p.C) {
-                stalled = c_count == p.stall_after;
+                stalled = c_count + b_count == p.stall_after;
                 if (stalled) break;
                 const int s = static_cast<int>(c_count % Beside::C_STAGES);
                 ok = mbar_wait_warp(&c_empty[s], static_cast<uint32_t>((c_count / Beside::C_STAGES) & 1) ^ 1, abort_flag, p.wait_ns);
@@ -166,8 +166,10 @@ __global__ void __launch_bounds__(Beside::THREADS, 1)
                 __syncwarp();
                 ++c_count;
             }
-            for (int a = ta.next(); ok && a >= 0; a = ta.next()) {
+            for (int a = ta.next(); ok && !stalled && a >= 0; a = ta.next()) {
                 for (int i = 0; i < chunks_r; ++i) {
+                    stalled = c_count + b_count == p.stall_after;
+                    if (stalled) break;
                     const int s = static_cast<int>(b_count % Steps::B_STAGES);
                     ok = mbar_wait_warp(&b_empty[s], static_cast<uint32_t>((b_count / Steps::B_STAGES) & 1) ^ 1, abort_flag, p.wait_ns);
                     if (!ok) break;
