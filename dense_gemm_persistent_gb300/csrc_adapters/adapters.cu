@@ -84,8 +84,11 @@ cudaError_t shrink_few(const Params& p, const dg::host::Device& dev, cudaStream_
     dg::host::Launch l(blocks, 1, THREADS, 0, s);
     return cudaLaunchKernelEx(&l.cfg, kernel, p);
 }
-// As many CTAs as the SMs hold at once, about 4 each: more numbers a CTA beyond. 256 threads share K, 128 where K is too short for
-// them (64 rows of K = 4096, rank 64: 22.7 and 26.5 us for the call; 997 rows of K = 1416, rank 8: 28.6 and 26.2).
+// As many CTAs as the SMs hold at once, about 4 each: more numbers a CTA beyond. 256 threads share K, 128 where one batch of
+// theirs (two loads of 8 numbers) is all of it, up to 2048: more threads would leave half of a batch empty. 128 / 256 threads in
+// us a call: K = 512, 1024, 2048, 2560, 4096; 64 rows of rank 64, 4096 channels 29.9 / 31.0, 25.2 / 26.5, 21.9 / 22.6, 25.2 /
+// 24.6, 27.7 / 26.7; 512 rows of rank 32, 2048 channels 19.6 / 24.5, 21.2 / 25.9, 22.4 / 28.4, 26.6 / 26.6, 33.6 / 33.4.
+// (997 rows of rank 8, in long runs, would take 128 beyond too: 4096 33.0 / 37.7.)
 template <int THREADS>
 cudaError_t shrink_few(const Params& p, const dg::host::Device& dev, cudaStream_t s) {
     const int64_t numbers = static_cast<int64_t>(p.T) * p.r, at_once = 4 * dev.num_sms;
@@ -94,7 +97,7 @@ cudaError_t shrink_few(const Params& p, const dg::host::Device& dev, cudaStream_
                                     : shrink_few<8, 2, THREADS>(p, dev, s);
 }
 dgemm_status_t launch_shrink_few(const Params& p, const dg::host::Device& dev, cudaStream_t s) {
-    const cudaError_t e = p.K <= 1536 ? shrink_few<128>(p, dev, s) : shrink_few<256>(p, dev, s);
+    const cudaError_t e = p.K <= 2048 ? shrink_few<128>(p, dev, s) : shrink_few<256>(p, dev, s);
     return e == cudaSuccess ? DGEMM_OK : DGEMM_ERR_CUDA;
 }
 
