@@ -51,7 +51,8 @@ extern "C" {
  * counts as infinite there). A row depends on its own adapter alone:
  * NaN and infinities in another one do not reach it. NaN stays NaN under every activation.
  * r and K are multiples of 8 (DGEMM_ERR_MISALIGNED otherwise), 8 <= r <= DGEMM_MAX_ADAPTER_RANK,
- * 0 <= L <= DGEMM_MAX_ADAPTERS. K == 0: every product is zero. */
+ * 0 <= L <= DGEMM_MAX_ADAPTERS, T <= 2^24, N and K below 2^30 (DGEMM_ERR_NOT_SUPPORTED
+ * beyond). K == 0: every product is zero. */
 dgemm_status_t dgemm_adapter_bf16(const void* X, const void* W, const void* A, const void* B, const int32_t* ids,
                                   const float* scale, int64_t L, int64_t r, void* D, dgemm_dtype_t d_dtype, int64_t T,
                                   int64_t N, int64_t K, const float* bias, int act, void* ws, size_t ws_bytes,

@@ -1,10 +1,13 @@
 """The choice of the kernel that writes N channels of D beside a product (adapter_beside.cuh),
-on the CPU: never for a gated D, which has half of them."""
+on the CPU: never for a gated D, which has half of them. And the largest sizes that both calls take."""
 import itertools
 import os
 import re
 import shutil
 import subprocess
+
+import dense_gemm_persistent_gb300 as dg
+from dense_gemm_persistent_gb300 import build
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 CSRC = os.path.join(ROOT, "dense_gemm_persistent_gb300", "csrc_adapters")
@@ -37,3 +40,11 @@ def test_the_launches_follow_the_rule():
     assert re.findall(r"const bool beside = (.*);", text) == [
         "dg::adapters::beside_form(p.prompt, c.W != nullptr, p.gated, p.d_f32, c.C && p.c_f32, p.N)"]
     assert len(re.findall(r"launch_beside<\w+>\(c, p, dev\)", text)) == text.count("if (beside) return") * 2 == 2
+
+
+def test_the_limits_that_the_header_states():
+    build.build()
+    size = dg.dgemm_adapter_workspace_size
+    assert size(1 << 24, 8, 8, 8, 1) > 0 and size((1 << 24) + 1, 8, 8, 8, 1) == 0
+    assert size(1, (1 << 30) - 1, 8, 8, 1) > 0 and size(1, 1 << 30, 8, 8, 1) == 0
+    assert size(1, 8, (1 << 30) - 8, 8, 1) > 0 and size(1, 8, 1 << 30, 8, 1) == 0
