@@ -83,8 +83,8 @@ struct TileAdapters {
 __device__ __forceinline__ __nv_bfloat162 as_bf162(uint32_t w) { return *reinterpret_cast<const __nv_bfloat162*>(&w); }
 
 // Replaces the numbers that are not finite in the 16-byte vectors [first, last), four at most, of a swizzled row; whether
-// there were any. Such a number times zero is NaN, and a sum keeps it: one operation for two numbers. An infinity becomes the
-// smallest normal number of its sign, not zero: where the row's own V is infinite too, the product is then the
+// there were any. Such a number times zero is NaN, and a sum keeps it: one operation for two numbers. In its place comes the
+// smallest normal number of its sign, not zero: where the row's own V is infinite and B too, the product is then the
 // infinity that it has to be (with a zero it would be NaN, which nothing added later takes back). Of a finite V it
 // leaves 2^-126 of it, 4 at most, in a sum that not_finite_terms makes infinite or NaN.
 __device__ __forceinline__ bool make_finite(uint8_t* row, int swizzle, int first, int last) {
@@ -105,11 +105,9 @@ __device__ __forceinline__ bool make_finite(uint8_t* row, int swizzle, int first
     for (int c = first; c < last; ++c) {
         uint32_t* word = reinterpret_cast<uint32_t*>(row + ((c ^ swizzle) << 4));
         for (int k = 0; k < 4; ++k) {
-            const uint32_t v = word[k], lo = v & 0xFFFFu, hi = v & 0xFFFF0000u;
-            // (an infinity: 2^-126 with its sign; NaN: 0)
-            const uint32_t in_lo = (v & 0x7Fu) == 0 ? (v & 0x8000u) | 0x0080u : 0u;
-            const uint32_t in_hi = (v & 0x7F0000u) == 0 ? (v & 0x80000000u) | 0x00800000u : 0u;
-            word[k] = ((v & 0x7F80u) == 0x7F80u ? in_lo : lo) | ((v & 0x7F800000u) == 0x7F800000u ? in_hi : hi);
+            const uint32_t v = word[k];             // (the sign and the exponent's last bit)
+            word[k] = ((v & 0x7F80u) == 0x7F80u ? v & 0x8080u : v & 0xFFFFu) |
+                      ((v & 0x7F800000u) == 0x7F800000u ? v & 0x80800000u : v & 0xFFFF0000u);
         }
     }
     return true;
