@@ -9,7 +9,7 @@
 // As in adapter_mma.cuh, B_a is looked at before it is used: a zero does not hide a number that is not finite, and the two
 // numbers of V may have opposite signs. The masked rows and the look are the work of warps of their own, 2.3 us a
 // tile. Where all rows of a token tile have the same adapter V needs no zeros and comes by TMA as it is.
-// 4096 x 11008, 8 adapters of rank 32 in runs of rows, SiLU and bias: 64-68 us with the launch that computes V (10-12 of
+// 4096 x 11008, 8 adapters of rank 32 in runs of rows, SiLU and bias: 64-67 us with the launch that computes V (10-12 of
 // them); the bytes take 33. The epilogue computes for 26 of a CTA's 40 us (two operations of the special function unit a
 // value; 17 without an activation); the rest are waits for C and for sums of token tiles of several adapters.
 // (Tried and measured when this form was made: that case by the prompt form of adapter_mma.cuh, which has C and D by
@@ -32,8 +32,8 @@ struct Beside {
     static constexpr int MARKS = 8;      // tiles that may be between their V or their sum and their epilogue: ACCS + B_STAGES at most
     static constexpr int BAR_BYTES = 768;
     // Steps on their way. With rank 16 or 32 both numbers of V fit into one slice as they stand in memory (the second ones on a
-    // step of the MMA), and a third step into the memory of two: rank 32, 4096 x 11008, 8 requests in runs 66.4 -> 63.5 us, every
-    // row another of 48 705 -> 537.
+    // step of the MMA), and a third step into the memory of two: rank 32, 4096 x 11008, 8 requests in runs 71 -> 66 us, every
+    // row another of 48 747 -> 547.
     template <bool NARROW>
     struct Steps {
         static constexpr int B_STAGES = NARROW ? 3 : 2, V_BYTES = NARROW ? BOX : 2 * BOX;
