@@ -514,18 +514,29 @@ __device__ __forceinline__ void route_scored_token(const ScoredParams& p, int t,
             float xn = __shfl_down_sync(kAll, xj, 1), bn = __shfl_down_sync(kAll, bj, 1);
             int next_id = __shfl_down_sync(kAll, my_id, 1);
             if (lane == n - 1) xn = xe, bn = be, next_id = behind_id;
-            if (__any_sync(kAll, tight && !(xj == xn && bj == bn && my_id < next_id))) {
-                bool all = n >= 32;
-                if (!all && more) {           // is the one behind apart from the next?
-                    __syncwarp();
-                    const unsigned behind2 = pick.take(lane, won);
-                    __syncwarp();
-                    const int id2 = static_cast<int>(won->y);
-                    if (near(behind, behind2)) all = !(logit_at(p, t, id2) == xe && bias_at(p, id2) == be && behind_id < id2);
-                }
+            const bool open = __any_sync(kAll, tight && !(xj == xn && bj == bn && my_id < next_id));
+            // Who else may be among the first k? What is near the last of them: what is not lies below all of them.
+            const unsigned last = __shfl_sync(kAll, my_key, n - 1);
+            const bool one = near(last, behind);
+            bool several = false, all = open && one && n >= 32;
+            if (one) {
+                __syncwarp();
+                several = near(last, pick.take(lane, won));
+                __syncwarp();
+            }
+            if (several && !open) {       // in order as they are if all of them are the last one's equals
+                const float xl = __shfl_sync(kAll, xj, n - 1), bl = __shfl_sync(kAll, bj, n - 1);
+                auto differs = [&](int e) { return !(logit_at(p, t, e) == xl && bias_at(p, e) == bl); };
+                bool other = differs(static_cast<int>(won->y));
+#pragma unroll
+                for (int i = 0; i < VPL; ++i)
+                    if (near(last, pick.key[i])) other = other || differs(lane * VPL + (pick.PLACE - (pick.key[i] & pick.PLACE)));
+                all = __any_sync(kAll, other);
+            }
+            if (all || open) {
                 const double inv = inverse_sum();
-                if (all) my_id = choose64<VPL>(p, t, lane, xmax, inv);
-                else my_id = order64(p, t, lane == n && more ? behind_id : my_id, more ? n + 1 : n, n, lane, xmax, inv);
+                if (all || several) my_id = choose64<VPL>(p, t, lane, xmax, inv);
+                else my_id = order64(p, t, lane == n && one ? behind_id : my_id, one ? n + 1 : n, n, lane, xmax, inv);
                 xj = my_id >= 0 ? logit_at(p, t, my_id) : 0.0f;
             }
         }

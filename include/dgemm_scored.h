@@ -48,8 +48,9 @@ typedef struct {
  *   (a sum of sigmoid scores below 2^-126 counts as 2^-126); 0 for id -1. Without
  *   renormalize, or beside a chosen logit above -20, a score below 2^-126 may count as 0.
  * The order is that of the values in FP64: where FP32 values are too near to tell, the
- * token is decided again (values that FP64 cannot tell apart are equal). Without a bias, and with no groups or groups
- * ranked by their largest value, the order of the logits decides.
+ * token is decided again (values that FP64 cannot tell apart are equal). Without a bias,
+ * and with all groups kept or groups ranked by their largest value, the order of the logits
+ * decides.
  *   logits   [T,E] F32 or BF16. An expert whose logit or bias is -inf or NaN is never
  *            chosen and has no part in the softmax; +inf counts as the largest finite number.
  *   bias     [E] F32 or NULL (all 0).
